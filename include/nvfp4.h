@@ -359,6 +359,110 @@ int nvfp4_gemm_batched(const nvfp4_gemm_problem* problems, int32_t count, int64_
                        void* stream);
 
 /*
+ * Element types of operands that may be bf16 or fp32.
+ */
+enum { NVFP4_BF16 = 0, NVFP4_F32 = 1 };
+
+/*
+ * MoE router: the step in front of the grouped GEMMs ("The Moment of Recalibration",
+ * magik.net, Input Knowledge: 256 experts, top-8 routing). For token t with logits l_te, routed
+ * when valid[t] != 0 and some l_te is above -inf:
+ *   p_te = exp(l_te) / sum_e exp(l_te); the k largest l_te are selected, ties to the lower
+ *   expert; an expert whose logit is -inf is never selected (its slot: index -1, weight 0);
+ *   weights p at the selected experts, with `renormalize` divided by their sum.
+ * Load-balance loss over the n routed tokens, with c_e selections of expert e and
+ * P_e = (1/n) sum_t p_te:  L = E sum_e (c_e / (n k)) P_e  (0 when n = 0; 1 when balanced).
+ *   logits          device [T, E], bf16 or fp32 (logits_type NVFP4_BF16 / NVFP4_F32). Logits of a
+ *                   token with valid[t] == 0 are not read; NaN or +inf in a routed token's row
+ *                   makes that row's weights, mean_prob and the loss NaN, and nothing else
+ *   valid           device u8 [T] (0: padding token) or NULL (all valid)
+ *   topk_idx        int32 [T, k] written, largest logit first; -1 in empty slots
+ *   topk_w          fp32 [T, k] written
+ *   slot_row        int32 [T, k] written: the routed row of each slot, -1 in empty slots
+ *   counts          int32 [E] written: rows per expert
+ *   expert_offsets  int32 [E + 1] written: exclusive prefix sums of counts, as the grouped GEMMs
+ *                   read them. offsets[E] = T k when every slot is filled
+ *   row_token       int32 [T k] written: token of each routed row, rows sorted by expert, then
+ *                   token; -1 from offsets[E] on
+ *   mean_prob       fp32 [E] written: P_e;  balance_loss fp32 [1];  routed_tokens int32 [1]: n
+ *   workspace       nvfp4_moe_route_workspace_bytes(T, E) bytes, 16-byte aligned
+ * E <= NVFP4_MOE_MAX_EXPERTS, k <= min(E, NVFP4_MOE_MAX_TOPK), T k < 2^31. Results repeat bit for
+ * bit. T == 0 writes zero counts, offsets, means and loss.
+ */
+#define NVFP4_MOE_MAX_EXPERTS 1024
+#define NVFP4_MOE_MAX_TOPK 32
+size_t nvfp4_moe_route_workspace_bytes(int64_t T, int32_t E);
+int nvfp4_moe_route(const void* logits, int32_t logits_type, const uint8_t* valid, int64_t T, int32_t E, int32_t k,
+                    int32_t renormalize, int32_t* topk_idx, float* topk_w, int32_t* slot_row, int32_t* counts,
+                    int32_t* expert_offsets, int32_t* row_token, float* mean_prob, float* balance_loss,
+                    int32_t* routed_tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of nvfp4_moe_route's logits from the gradients of the weights and of the balance
+ * loss. The selection and the counts carry no gradient. With
+ * G_te = dL E c_e / (k n^2), plus dw_ts at the selected experts (plain weights):
+ *   dl_te = p_te (G_te - sum_i p_ti G_ti);
+ * renormalised weights add w_ts (dw_ts - sum_r w_tr dw_tr) at the selected experts instead.
+ *   logits, valid, T, E, k, renormalize   as in the forward call
+ *   topk_idx, topk_w, counts, routed_tokens  its outputs
+ *   d_w       fp32 [T, k] or NULL (no gradient from the weights); read at filled slots only
+ *   d_loss    device fp32 [1] or NULL (no gradient from the loss)
+ *   d_logits  [T, E], type as logits, written (zeros in rows that are not routed)
+ */
+int nvfp4_moe_route_backward(const void* logits, int32_t logits_type, const uint8_t* valid, int64_t T, int32_t E,
+                             int32_t k, int32_t renormalize, const int32_t* topk_idx, const float* topk_w,
+                             const int32_t* counts, const int32_t* routed_tokens, const float* d_w,
+                             const float* d_loss, void* d_logits, void* stream);
+
+/*
+ * FP8 tensors with a scale for each block of 128: E4M3 codes and one fp32 scale per block,
+ * value = code * scale; s = amax_block / 448 (1 for a block of zeros), code = E4M3_rn_satfinite(x / s),
+ * every step one IEEE fp32 operation. Two forms of blocks:
+ *   block_rows 1     1 x 128 along the row (activations, gradients); scales [ceil(K/128)][rows]
+ *   block_rows 128   128 x 128 (weights); scales [ceil(rows/128)][ceil(K/128)], row-major
+ * Last blocks may be partial. K % 16 == 0.
+ *   x          device bf16 [M_x, K], 16-byte aligned
+ *   row_token  NULL (then M == M_x), or device int32 [M]: row r is quantised from
+ *              x[row_token[r]] (the router's row lists: gathers and quantises in one pass); an
+ *              index outside [0, M_x) gives a row of zeros with scale 1
+ *   q, s       codes [M, K] and scales; NULL, NULL when not wanted
+ *   qt, st     codes and scales of the transpose, or NULL, NULL: codes [K, M'] with M' = M rounded
+ *              up to a multiple of 16 (columns past M written 0), blocks 1 x 128 along its rows,
+ *              i.e. along M (st [ceil(M/128)][K]); for block_rows 128 the same blocks and codes
+ *              (st [ceil(K/128)][ceil(M/128)]). The operands of a layer's gradients: with
+ *              y = x W^T, dx = dy W reads q(dy) and qt(W), dW = dy^T x reads qt(dy) and qt(x).
+ */
+int nvfp4_fp8_quantize(const uint16_t* x, int64_t M_x, int64_t K, int32_t block_rows, const int32_t* row_token,
+                       int64_t M, uint8_t* q, float* s, uint8_t* qt, float* st, void* stream);
+
+/*
+ * FP8 GEMM y = a b^T on such tensors, each block of 128 of K summed on the tensor cores and
+ * scaled into an fp32 sum:  y[m, n] = sum_c sa[c, m] sb(c, n) sum_{k in block c} a[m, k] b[n, k].
+ *   a, sa   codes [M, K], scales [ceil(K/128)][M] (block_rows 1)
+ *   b, sb   codes [N, K], scales by b_block_rows (128: weights; 1: a second activation, for dW)
+ *   y       [M, N] row-major, bf16 or fp32 (y_type NVFP4_BF16 / NVFP4_F32), 16-byte aligned
+ * K % 16 == 0; any M >= 0, N >= 1. dev_status as for nvfp4_gemm.
+ */
+int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int32_t b_block_rows,
+                   void* y, int32_t y_type, int64_t M, int64_t N, int64_t K, int32_t* dev_status, void* stream);
+
+/*
+ * Grouped (MoE) FP8 GEMM: rows expert_offsets[e] .. expert_offsets[e+1]-1 of a times expert e's
+ * weight. As nvfp4_grouped_gemm, except that expert_offsets[E] may be below M_total (a router
+ * with padding tokens): rows from there on are neither read nor written.
+ *   a, sa           codes [M_total, K], scales [ceil(K/128)][M_total]
+ *   b, sb           codes [E, N, K], scales [E][ceil(N/128)][ceil(K/128)]
+ *   expert_offsets  device int32 [E+1], 0 = offsets[0] <= ... <= offsets[E] <= M_total; checked on the
+ *                   device (NVFP4_ERR_BAD_OFFSETS in *dev_status, y untouched)
+ *   y               bf16 [M_total, N]
+ *   workspace       nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K) bytes, 256-byte aligned
+ */
+size_t nvfp4_fp8_grouped_gemm_workspace_bytes(int32_t E, int64_t M_total, int64_t N, int64_t K);
+int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
+                           const int32_t* expert_offsets, int32_t E, int64_t M_total, int64_t N, int64_t K,
+                           uint16_t* y, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
  * Elementwise device encoders used by the quantiser, for exhaustive checks:
  * fp32 -> E2M1 code (round to nearest even, saturating, sign kept) and
  * fp32 -> E4M3FN code (round to nearest even, saturating to +-448).

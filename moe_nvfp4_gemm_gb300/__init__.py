@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -47,7 +48,9 @@ EXPORTS = ["nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_amax_workspace_byt
            "nvfp4_encode_e4m3", "nvfp4_tune", "nvfp4_last_launch_count",
            "nvfp4_sparse_meta_bytes", "nvfp4_scale_bytes_b32", "nvfp4_prune_pairs", "nvfp4_quantize_b32",
            "nvfp4_sparse_gemm", "nvfp4_grouped_sparse_gemm", "nvfp4_gemm_batched",
-           "nvfp4_grouped_gemm_swiglu_quantize_out"]
+           "nvfp4_grouped_gemm_swiglu_quantize_out",
+           "nvfp4_moe_route_workspace_bytes", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_fp8_quantize",
+           "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm_workspace_bytes", "nvfp4_fp8_grouped_gemm"]
 
 
 class NVFP4Error(RuntimeError):
@@ -124,6 +127,18 @@ def lib():
             L.nvfp4_gemm_batched.argtypes = [_vp, _i32, _i64, _vp, _vp]
             L.nvfp4_grouped_gemm_swiglu_quantize_out.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64,
                                                                  _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp, _vp]
+            L.nvfp4_moe_route_workspace_bytes.restype = _sz
+            L.nvfp4_moe_route_workspace_bytes.argtypes = [_i64, _i32]
+            L.nvfp4_moe_route.argtypes = [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _sz, _vp]
+            L.nvfp4_moe_route_backward.argtypes = [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                                   _vp, _vp, _vp]
+            L.nvfp4_fp8_quantize.argtypes = [_vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
+            L.nvfp4_fp8_gemm.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp]
+            L.nvfp4_fp8_grouped_gemm_workspace_bytes.restype = _sz
+            L.nvfp4_fp8_grouped_gemm_workspace_bytes.argtypes = [_i32, _i64, _i64, _i64]
+            L.nvfp4_fp8_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _sz, _vp,
+                                                 _vp]
             L.nvfp4_last_launch_count.restype = ctypes.c_int
             _lib = L
     return _lib
@@ -434,6 +449,180 @@ def nvfp4_grouped_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, expert_offsets, 
            lib().nvfp4_grouped_sparse_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_c), _ptr(sfb_c), _ptr(meta),
                                            _ptr(gb), _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
                                            _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)))
+    return y
+
+
+NVFP4_BF16 = 0
+NVFP4_F32 = 1
+NVFP4_MOE_MAX_EXPERTS = 1024
+NVFP4_MOE_MAX_TOPK = 32
+_FLOAT_TYPES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32}
+
+
+class MoeRouting(NamedTuple):
+    """What nvfp4_moe_route returns (T tokens, k slots each, E experts)."""
+    topk_idx: torch.Tensor        # int32 [T, k]: selected experts, -1 in empty slots
+    topk_w: torch.Tensor          # fp32 [T, k]: their weights
+    slot_row: torch.Tensor        # int32 [T, k]: routed row of each slot, -1 in empty slots
+    counts: torch.Tensor          # int32 [E]: rows per expert
+    expert_offsets: torch.Tensor  # int32 [E + 1]: as the grouped GEMMs read them
+    row_token: torch.Tensor       # int32 [T * k]: token of each routed row, -1 past the last
+    mean_prob: torch.Tensor       # fp32 [E]: mean probability over the routed tokens
+    balance_loss: torch.Tensor    # fp32 [1]
+    routed_tokens: torch.Tensor   # int32 [1]
+
+
+def _route_inputs(logits, valid):
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype in _FLOAT_TYPES
+            and logits.is_contiguous() and logits.dim() == 2):
+        raise TypeError("logits must be a contiguous CUDA tensor [T, E] of torch.bfloat16 or torch.float32")
+    if valid is not None and not (isinstance(valid, torch.Tensor) and valid.is_cuda and valid.is_contiguous()
+                                  and valid.dtype in (torch.bool, torch.uint8) and valid.numel() == logits.shape[0]):
+        raise TypeError("valid must be a contiguous CUDA tensor [T] of torch.bool or torch.uint8")
+    return logits.shape
+
+
+def nvfp4_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().nvfp4_moe_route_workspace_bytes(T, E))
+
+
+def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, valid=None, workspace=None,
+                    stream=None) -> MoeRouting:
+    """Softmax router: top-k experts and weights of each token, per-expert counts and offsets, the
+    expert-sorted row lists that the grouped GEMMs read, and the load-balance loss."""
+    T, E = _route_inputs(logits, valid)
+    dev = logits.device
+    n = T * max(k, 0)
+    ints = torch.empty(3 * n + 2 * E + 2, dtype=torch.int32, device=dev)
+    idx, slot_row, row_token, counts, offsets, routed = ints.split([n, n, n, E, E + 1, 1])
+    floats = torch.empty(n + E + 1, dtype=torch.float32, device=dev)
+    w, mean, loss = floats.split([n, E, 1])
+    if workspace is None:
+        workspace = torch.empty(nvfp4_moe_route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+    _check("nvfp4_moe_route",
+           lib().nvfp4_moe_route(_ptr(logits), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
+                                 _ptr(idx), _ptr(w), _ptr(slot_row), _ptr(counts), _ptr(offsets), _ptr(row_token),
+                                 _ptr(mean), _ptr(loss), _ptr(routed), _ptr(workspace), workspace.numel(),
+                                 _stream(stream)))
+    return MoeRouting(idx.view(T, k), w.view(T, k), slot_row.view(T, k), counts, offsets, row_token, mean, loss, routed)
+
+
+def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None, d_loss=None,
+                             renormalize: bool = False, valid=None, d_logits=None, stream=None) -> torch.Tensor:
+    """Gradient of nvfp4_moe_route's logits (arguments as in that call) from the gradients of the
+    weights topk_w (d_w, fp32 [T, k]) and of the balance loss (d_loss, fp32 [1])."""
+    T, E = _route_inputs(logits, valid)
+    k = routing.topk_idx.shape[1]
+    for t, dt, shape, n in ((routing.topk_idx, torch.int32, (T, k), "topk_idx"),
+                            (routing.topk_w, torch.float32, (T, k), "topk_w"),
+                            (routing.counts, torch.int32, (E,), "counts"),
+                            (routing.routed_tokens, torch.int32, (1,), "routed_tokens"),
+                            (d_w, torch.float32, (T, k), "d_w"), (d_loss, torch.float32, (1,), "d_loss")):
+        if t is not None:
+            _cuda(t, dt, n)
+            if tuple(t.shape) != shape:
+                raise TypeError(f"{n} must have shape {shape}")
+    d_logits = torch.empty_like(logits) if d_logits is None else _cuda(d_logits, logits.dtype, "d_logits")
+    _check("nvfp4_moe_route_backward",
+           lib().nvfp4_moe_route_backward(_ptr(logits), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
+                                          int(renormalize), _ptr(routing.topk_idx), _ptr(routing.topk_w),
+                                          _ptr(routing.counts), _ptr(routing.routed_tokens), _ptr(d_w), _ptr(d_loss),
+                                          _ptr(d_logits), _stream(stream)))
+    return d_logits
+
+
+def _fp8(t, name):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in (torch.float8_e4m3fn, torch.uint8)
+            and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous CUDA tensor of torch.float8_e4m3fn (or uint8 codes)")
+    return t
+
+
+def _holds(t, n, name):
+    if t.numel() < n:
+        raise TypeError(f"{name} holds {t.numel()} elements, needs {n}")
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, row_token=None, transposed: bool = False, stream=None):
+    """bf16 [M, K] -> (codes float8_e4m3fn [M, K], scales fp32), one scale per 1 x 128 block along K
+    (scales [K/128, M]) or, with block_rows=128, per 128 x 128 block (scales [M/128, K/128]; sizes
+    rounded up). row_token (int32): quantise the rows x[row_token]. transposed: also return the
+    codes [K, M rounded up to 16] and scales of the transpose, blocks along M."""
+    _cuda(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise TypeError("x must be [M, K]")
+    M_x, K = x.shape
+    M = M_x
+    if row_token is not None:
+        _cuda(row_token, torch.int32, "row_token")
+        M = row_token.numel()
+    dev = x.device
+    square = block_rows == 128
+    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    s = torch.empty((_blocks(M), _blocks(K)) if square else (_blocks(K), M), dtype=torch.float32, device=dev)
+    qt = st = None
+    if transposed:
+        qt = torch.empty((K, (M + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=dev)
+        st = torch.empty((_blocks(K), _blocks(M)) if square else (_blocks(M), K), dtype=torch.float32, device=dev)
+    _check("nvfp4_fp8_quantize",
+           lib().nvfp4_fp8_quantize(_ptr(x), M_x, K, block_rows, _ptr(row_token), M, _ptr(q), _ptr(s), _ptr(qt),
+                                    _ptr(st), _stream(stream)))
+    return (q, s, qt, st) if transposed else (q, s)
+
+
+def nvfp4_fp8_gemm(a, sa, b, sb, M: int, N: int, K: int, b_block_rows: int = 128, out_dtype=torch.bfloat16, y=None,
+                   dev_status=None, stream=None):
+    """y = a b^T [M, N] in bf16 or fp32 from E4M3 codes a [M, K], b [N, K] and their block scales
+    (see nvfp4_fp8_quantize; b_block_rows: rows of b that share a scale, 128 or 1)."""
+    _fp8(a, "a")
+    _fp8(b, "b")
+    _cuda(sa, torch.float32, "sa")
+    _cuda(sb, torch.float32, "sb")
+    if out_dtype not in _FLOAT_TYPES:
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    _holds(a, M * K, "a")
+    _holds(b, N * K, "b")
+    _holds(sa, _blocks(K) * M, "sa")
+    _holds(sb, _blocks(K) * (N if b_block_rows == 1 else _blocks(N)), "sb")
+    y = torch.empty((M, N), dtype=out_dtype, device=a.device) if y is None else _cuda(y, out_dtype, "y")
+    _holds(y, M * N, "y")
+    _check("nvfp4_fp8_gemm",
+           lib().nvfp4_fp8_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), b_block_rows, _ptr(y), _FLOAT_TYPES[out_dtype],
+                                M, N, K, _ptr(dev_status), _stream(stream)))
+    return y
+
+
+def nvfp4_fp8_grouped_gemm_workspace_bytes(E: int, M_total: int, N: int, K: int) -> int:
+    return int(lib().nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K))
+
+
+def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N: int, K: int, y=None,
+                           workspace=None, dev_status=None, stream=None):
+    """Per-expert y[rows of e] = a[rows of e] b_e^T (bf16 [M_total, N]) from E4M3 codes a [M_total, K],
+    b [E, N, K] and their block scales; rows sorted by expert, rows past expert_offsets[E] untouched."""
+    _fp8(a, "a")
+    _fp8(b, "b")
+    _cuda(sa, torch.float32, "sa")
+    _cuda(sb, torch.float32, "sb")
+    _cuda(expert_offsets, torch.int32, "expert_offsets")
+    _holds(a, M_total * K, "a")
+    _holds(b, E * N * K, "b")
+    _holds(sa, _blocks(K) * M_total, "sa")
+    _holds(sb, E * _blocks(N) * _blocks(K), "sb")
+    _holds(expert_offsets, E + 1, "expert_offsets")
+    y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else _cuda(y, torch.bfloat16, "y")
+    _holds(y, M_total * N, "y")
+    if workspace is None:
+        workspace = torch.empty(max(1, nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K)), dtype=torch.uint8,
+                                device=a.device)
+    _check("nvfp4_fp8_grouped_gemm",
+           lib().nvfp4_fp8_grouped_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(expert_offsets), E, M_total, N, K,
+                                        _ptr(y), _ptr(workspace), workspace.numel(), _ptr(dev_status),
+                                        _stream(stream)))
     return y
 
 

@@ -881,6 +881,186 @@ int nvfp4_grouped_gemm_swiglu_quantize_out(const uint8_t* a, const uint8_t* sfa,
                       workspace_bytes, dev_status, stream, 1, nullptr, 0, nullptr, q_out, sf_out, g_out);
 }
 
+// ---- MoE router --------------------------------------------------------------------------------
+
+static int check_route(int64_t T, int32_t E, int32_t k, int32_t logits_type) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E) return NVFP4_ERR_INVALID_ARG;
+  if (logits_type != NVFP4_BF16 && logits_type != NVFP4_F32) return NVFP4_ERR_INVALID_ARG;
+  if (E > NVFP4_MOE_MAX_EXPERTS || k > NVFP4_MOE_MAX_TOPK || T > kMaxDim || T * k > kMaxDim)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return NVFP4_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool aligned_logits(const void* p, int32_t type) {
+  return (reinterpret_cast<uintptr_t>(p) & (type == NVFP4_BF16 ? 1u : 3u)) == 0;
+}
+
+size_t nvfp4_moe_route_workspace_bytes(int64_t T, int32_t E) {
+  if (T <= 0 || E <= 0) return 0;
+  return static_cast<size_t>(route_blocks(T)) * (2 * static_cast<size_t>(E) + 1) * 4;
+}
+
+int nvfp4_moe_route(const void* logits, int32_t logits_type, const uint8_t* valid, int64_t T, int32_t E, int32_t k,
+                    int32_t renormalize, int32_t* topk_idx, float* topk_w, int32_t* slot_row, int32_t* counts,
+                    int32_t* expert_offsets, int32_t* row_token, float* mean_prob, float* balance_loss,
+                    int32_t* routed_tokens, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  int rc = check_route(T, E, k, logits_type);
+  if (rc) return rc;
+  if (!counts || !expert_offsets || !mean_prob || !balance_loss || !routed_tokens) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_idx || !topk_w || !slot_row || !row_token)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned_logits(logits, logits_type) || !aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(slot_row) ||
+      !aligned4(counts) || !aligned4(expert_offsets) || !aligned4(row_token) || !aligned4(mean_prob) ||
+      !aligned4(balance_loss) || !aligned4(routed_tokens))
+    return NVFP4_ERR_ALIGNMENT;
+  const size_t need = nvfp4_moe_route_workspace_bytes(T, E);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  rc = device_info(d);
+  if (rc) return rc;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.valid = valid;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.bf16 = logits_type == NVFP4_BF16;
+  a.renorm = renormalize != 0;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.slot_row = slot_row;
+  a.counts = counts;
+  a.expert_offsets = expert_offsets;
+  a.row_token = row_token;
+  a.mean_prob = mean_prob;
+  a.loss = balance_loss;
+  a.routed_tokens = routed_tokens;
+  a.ws_hist = static_cast<int32_t*>(workspace);
+  a.ws_psum = reinterpret_cast<float*>(a.ws_hist + static_cast<int64_t>(route_blocks(T)) * (E + 1));
+  int launches = 0;
+  rc = from_cuda(launch_moe_route(a, static_cast<cudaStream_t>(stream), &launches));
+  g_last_launches = launches;
+  return rc;
+}
+
+int nvfp4_moe_route_backward(const void* logits, int32_t logits_type, const uint8_t* valid, int64_t T, int32_t E,
+                             int32_t k, int32_t renormalize, const int32_t* topk_idx, const float* topk_w,
+                             const int32_t* counts, const int32_t* routed_tokens, const float* d_w,
+                             const float* d_loss, void* d_logits, void* stream) {
+  g_last_launches = 0;
+  int rc = check_route(T, E, k, logits_type);
+  if (rc) return rc;
+  if (T == 0) return NVFP4_OK;
+  if (!logits || !topk_idx || !topk_w || !counts || !routed_tokens || !d_logits) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned_logits(logits, logits_type) || !aligned_logits(d_logits, logits_type) || !aligned4(topk_idx) ||
+      !aligned4(topk_w) || !aligned4(counts) || !aligned4(routed_tokens) || !aligned4(d_w) || !aligned4(d_loss))
+    return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  rc = device_info(d);
+  if (rc) return rc;
+  RouteBwdArgs a = {};
+  a.logits = logits;
+  a.valid = valid;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.bf16 = logits_type == NVFP4_BF16;
+  a.renorm = renormalize != 0;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.counts = counts;
+  a.routed_tokens = routed_tokens;
+  a.d_w = d_w;
+  a.d_loss = d_loss;
+  a.d_logits = d_logits;
+  rc = from_cuda(launch_moe_route_bwd(a, d.sms, static_cast<cudaStream_t>(stream)));
+  g_last_launches = 1;
+  return rc;
+}
+
+// ---- FP8 with a scale for each block of 128 ------------------------------------------------------
+
+int nvfp4_fp8_quantize(const uint16_t* x, int64_t M_x, int64_t K, int32_t block_rows, const int32_t* row_token,
+                       int64_t M, uint8_t* q, float* s, uint8_t* qt, float* st, void* stream) {
+  g_last_launches = 0;
+  if (M_x < 0 || K < 0 || M < 0 || (block_rows != 1 && block_rows != 128)) return NVFP4_ERR_INVALID_ARG;
+  if (!row_token && M != M_x) return NVFP4_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M_x > kMaxDim || M > kMaxDim || K > kMaxDim ||
+      ((M + 127) / 128) * ((K + 127) / 128) > kMaxDim)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0 || K == 0) return NVFP4_OK;
+  if ((M_x > 0 && !x) || (!q && !qt) || (q && !s) || (qt && !st)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(qt) || !aligned4(s) || !aligned4(st) || !aligned4(row_token))
+    return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  int rc = device_info(d);
+  if (rc) return rc;
+  Fp8QuantArgs a = {x, row_token, M_x, M, K, q, s, qt, st};
+  rc = from_cuda(launch_fp8_quantize(a, block_rows, static_cast<cudaStream_t>(stream)));
+  g_last_launches = 1;
+  return rc;
+}
+
+static int check_fp8_shape(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N <= 0 || K <= 0) return NVFP4_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return NVFP4_OK;
+}
+
+int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int32_t b_block_rows,
+                   void* y, int32_t y_type, int64_t M, int64_t N, int64_t K, int32_t* dev_status, void* stream) {
+  g_last_launches = 0;
+  (void)dev_status;
+  int rc = check_fp8_shape(M, N, K);
+  if (rc) return rc;
+  if ((b_block_rows != 1 && b_block_rows != 128) || (y_type != NVFP4_BF16 && y_type != NVFP4_F32))
+    return NVFP4_ERR_INVALID_ARG;
+  if (M == 0) return NVFP4_OK;
+  if (!a || !sa || !b || !sb || !y) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(y) || !aligned4(sa) || !aligned4(sb)) return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  rc = device_info(d);
+  if (rc) return rc;
+  Fp8GemmArgs p = {a, sa, b, sb, nullptr, y, M, N, K, b_block_rows, y_type == NVFP4_F32};
+  rc = from_cuda(launch_fp8_gemm(p, 1, static_cast<cudaStream_t>(stream)));
+  g_last_launches = 1;
+  return rc;
+}
+
+size_t nvfp4_fp8_grouped_gemm_workspace_bytes(int32_t E, int64_t M_total, int64_t N, int64_t K) {
+  (void)N;
+  (void)K;
+  if (E <= 0 || M_total < 0) return 0;
+  return 256;
+}
+
+int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
+                           const int32_t* expert_offsets, int32_t E, int64_t M_total, int64_t N, int64_t K,
+                           uint16_t* y, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  g_last_launches = 0;
+  int rc = check_fp8_shape(M_total, N, K);
+  if (E <= 0) return NVFP4_ERR_INVALID_ARG;
+  if (rc) return rc;
+  if (static_cast<int64_t>(E) * N > kMaxDim || E > 16384 || M_total > (int64_t(1) << 30))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (M_total == 0) return NVFP4_OK;
+  if (!a || !sa || !b || !sb || !expert_offsets || !y) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(y) || !aligned4(sa) || !aligned4(sb) || !aligned4(expert_offsets))
+    return NVFP4_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K))
+    return NVFP4_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  rc = device_info(d);
+  if (rc) return rc;
+  Fp8GemmArgs p = {a, sa, b, sb, expert_offsets, y, M_total, N, K, 128, 0, static_cast<int32_t*>(workspace), dev_status};
+  rc = from_cuda(launch_fp8_gemm(p, E, static_cast<cudaStream_t>(stream)));
+  g_last_launches = 2;
+  return rc;
+}
+
 }  // extern "C"
 
 // ---- allocation-free grouped GEMM ------------------------------------------------------------

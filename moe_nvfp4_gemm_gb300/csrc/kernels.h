@@ -124,6 +124,73 @@ cudaError_t launch_grouped_prep(const int32_t* offsets, const int32_t* row_token
                                 int kc4, int tile_rows, const uint8_t* sfx,
                                 int32_t* n_tiles, int4* tiles, uint8_t* slabs, int32_t* status, int grid,
                                 cudaStream_t st, const uint8_t* x_tok = nullptr, uint8_t* xg = nullptr);
+
+// ---- MoE router ---------------------------------------------------------------------------
+constexpr int kRouteBlocks = 304;  // most CTAs that share the tokens (two per SM)
+struct RouteArgs {
+  const void* logits;     // [T, E], fp32 or bf16
+  const uint8_t* valid;   // [T] or null
+  int64_t T;
+  int E, k;
+  int bf16, renorm;
+  int vec;                // rows can be read a lane's values at a time
+  int32_t* topk_idx;      // [T, k]
+  float* topk_w;          // [T, k]
+  int32_t* slot_row;      // [T, k]
+  int32_t* counts;        // [E]
+  int32_t* expert_offsets;  // [E + 1]
+  int32_t* row_token;     // [T * k]
+  float* mean_prob;       // [E]
+  float* loss;            // [1]
+  int32_t* routed_tokens;  // [1]
+  int32_t* ws_hist;       // [blocks][E + 1]
+  float* ws_psum;         // [blocks][E]
+};
+struct RouteBwdArgs {
+  const void* logits;
+  const uint8_t* valid;
+  int64_t T;
+  int E, k;
+  int bf16, renorm;
+  int vec;
+  const int32_t* topk_idx;
+  const float* topk_w;
+  const int32_t* counts;
+  const int32_t* routed_tokens;
+  const float* d_w;       // [T, k] or null
+  const float* d_loss;    // [1] or null
+  void* d_logits;         // [T, E], the logits' type
+};
+int route_blocks(int64_t T);
+cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches);
+cudaError_t launch_moe_route_bwd(RouteBwdArgs a, int sms, cudaStream_t st);
+
+// ---- FP8 block-128 operators --------------------------------------------------------------
+struct Fp8QuantArgs {
+  const uint16_t* x;         // bf16 [M_x, K]
+  const int32_t* row_token;  // [M] rows of x, or null (row r)
+  int64_t M_x, M, K;
+  uint8_t* q;                // [M, K] or null
+  float* s;                  // [ceil(K/128), M], square blocks [ceil(M/128), ceil(K/128)]
+  uint8_t* qt;               // [K, M rounded up to 16] or null
+  float* st;                 // [ceil(M/128), K], square blocks [ceil(K/128), ceil(M/128)]
+};
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int block_rows, cudaStream_t st);
+
+struct Fp8GemmArgs {
+  const uint8_t* a;
+  const float* sa;
+  const uint8_t* b;
+  const float* sb;
+  const int32_t* offsets;  // grouped: [E + 1]
+  void* y;
+  int64_t M, N, K;
+  int b_rows;              // rows of b that share a scale: 128 or 1
+  int f32;                 // y fp32 instead of bf16
+  int32_t* ok;             // grouped: workspace word, 1 when the offsets are well formed
+  int32_t* status;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& p, int E, cudaStream_t st);
 int stream_smem_bytes(int stages, int x_rows, int recv_bytes, bool sparse = false);
 // shared memory after the ring for one tile's token indices (and with qout the epilogue's
 // NVFP4 transpose tiles, 1 KB per epilogue warp)

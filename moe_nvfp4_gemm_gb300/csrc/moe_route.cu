@@ -1,0 +1,551 @@
+// MoE router: softmax over the experts, top-k selection, per-expert counts, rows sorted by
+// expert, the load-balance loss, and the gradient of the logits.
+//
+// For token t with logits l_te (e < E), routed when it is valid and some l_te > -inf:
+//   p_te = exp(l_te - max) / sum;  the k largest l_te are selected, ties to the lowest expert,
+//   an expert at -inf never (its slot holds -1 and weight 0);
+//   w_ts = p at the selected experts, optionally divided by their sum.
+// With n routed tokens, c_e selections of expert e and P_e = (1/n) sum_t p_te:
+//   balance loss L = E sum_e (c_e / (n k)) P_e.
+// A routed row's place is offsets[e] + the number of earlier (token, slot) pairs that chose e,
+// in (token, slot) order, so the order does not depend on how the work was split. Counts are
+// integers and every floating sum runs in a fixed order: results repeat bit for bit.
+#include <stdint.h>
+
+#include "kernels.h"
+#include "nvfp4_quant.cuh"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+constexpr int kRouteThreads = 256;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr float kLog2E = 1.4426950408889634f;
+
+DEVI float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Order-preserving map of fp32 onto uint32; 0 is below every float's key.
+DEVI uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);  // -0 and +0 tie
+  return u ^ ((u & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
+}
+DEVI float key_value(uint32_t key) { return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu)); }
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+
+DEVI float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// One row's logits: lane holds experts lane * VPL + j; experts >= E read as -inf.
+template <int VPL, bool BF16>
+DEVI void load_row(const void* logits, int64_t row, int E, bool vec, int lane, float (&v)[VPL]) {
+  if (vec) {  // E == 32 * VPL, rows aligned to a lane's bytes
+    if (BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(logits) + row * E + lane * VPL;
+      if constexpr (VPL >= 8) {
+#pragma unroll
+        for (int j = 0; j < VPL; j += 8) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + j));
+          v[j] = bf16lo(w.x), v[j + 1] = bf16hi(w.x), v[j + 2] = bf16lo(w.y), v[j + 3] = bf16hi(w.y);
+          v[j + 4] = bf16lo(w.z), v[j + 5] = bf16hi(w.z), v[j + 6] = bf16lo(w.w), v[j + 7] = bf16hi(w.w);
+        }
+      } else if constexpr (VPL >= 2) {
+#pragma unroll
+        for (int j = 0; j < VPL; j += 2) {
+          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p + j));
+          v[j] = bf16lo(w), v[j + 1] = bf16hi(w);
+        }
+      } else {
+        v[0] = __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+      }
+    } else {
+      const float* p = static_cast<const float*>(logits) + row * E + lane * VPL;
+      if constexpr (VPL >= 4) {
+#pragma unroll
+        for (int j = 0; j < VPL; j += 4) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(p + j));
+          v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) v[j] = __ldg(p + j);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int e = lane * VPL + j;
+      v[j] = __uint_as_float(0xFF800000u);
+      if (e < E)
+        v[j] = BF16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(logits) + row * E + e)) << 16)
+                    : __ldg(static_cast<const float*>(logits) + row * E + e);
+    }
+  }
+}
+
+// The CTA's tokens [t0, t1): selection and weights to global memory; the per-expert
+// selection counts (and at [E] the routed tokens) to hist, the sums of p to psum (per-warp
+// slices, added in warp order). Ends with a CTA barrier.
+template <int VPL, bool BF16>
+DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, float* psum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, k = a.k;
+  for (int e = threadIdx.x; e <= E; e += kRouteThreads) hist[e] = 0;
+  __syncthreads();
+  float acc[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) acc[j] = 0.0f;
+  int routed = 0;
+  for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) {
+    float v[VPL];
+    uint32_t key[VPL];
+    const bool valid = !a.valid || __ldg(a.valid + t) != 0;
+    uint32_t top = 0;  // largest key of the row
+    if (valid) {
+      load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        key[j] = order_key(v[j]);
+        m = max(m, key[j]);
+      }
+      top = __reduce_max_sync(0xffffffffu, m);
+    }
+    int my_idx = -1;
+    float my_w = 0.0f;
+    if (top > kKeyNegInf) {
+      const float mx = key_value(top);
+      float sum = 0.0f, e[VPL];
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        e[j] = ex2((v[j] - mx) * kLog2E);
+        sum += e[j];
+      }
+      sum = warp_sum(sum);
+      const float inv = __frcp_rn(sum);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) acc[j] += e[j] * inv;
+      ++routed;
+      // k rounds: the largest remaining key; ties to the lowest lane, then the lowest j
+      uint32_t my_key = 0;
+      for (int s = 0; s < k; ++s) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
+        const uint32_t best = __reduce_max_sync(0xffffffffu, m);
+        if (best <= kKeyNegInf) break;
+        const int w = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
+        int at = -1;
+        if (lane == w) {
+#pragma unroll
+          for (int j = VPL - 1; j >= 0; --j)
+            if (key[j] == best) at = j;
+#pragma unroll
+          for (int j = 0; j < VPL; ++j)
+            if (j == at) key[j] = 0;
+        }
+        at = __shfl_sync(0xffffffffu, at, w);
+        if (lane == s) {
+          my_idx = w * VPL + at;
+          my_key = best;
+        }
+      }
+      const float es = my_idx >= 0 ? ex2((key_value(my_key) - mx) * kLog2E) : 0.0f;
+      my_w = a.renorm ? es / warp_sum(es) : es * inv;
+      if (my_idx >= 0) atomicAdd(&hist[my_idx], 1);
+    }
+    if (lane < k) {
+      a.topk_idx[t * k + lane] = my_idx;
+      a.topk_w[t * k + lane] = my_w;
+    }
+  }
+  if (lane == 0) atomicAdd(&hist[E], routed);
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    if (lane * VPL + j < E) psum[warp * E + lane * VPL + j] = acc[j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    float s = 0.0f;
+    for (int w = 0; w < kRouteWarps; ++w) s += psum[w * E + e];
+    psum[e] = s;
+  }
+  __syncthreads();
+}
+
+// Exclusive scan of counts[E] into offs[E + 1] (shared memory); all threads of the CTA.
+DEVI void scan_counts(const int32_t* counts, int E, int32_t* offs) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int c = e0 + lane < E ? counts[e0 + lane] : 0;
+      int s = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+      }
+      if (e0 + lane < E) offs[e0 + lane] = base + s - c;
+      base += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) offs[E] = base;
+  }
+  __syncthreads();
+}
+
+// Rows of the CTA's tokens: base[e] (shared) is the first row of expert e that this CTA
+// fills. Each warp owns a contiguous range of the tokens: its selections per expert are
+// counted first, then every token's k slots take consecutive places (a token's experts
+// are distinct, so its lanes never meet). wcnt: [kRouteWarps][E] in shared memory.
+DEVI void place_rows(const RouteArgs& a, int64_t t0, int64_t t1, const int32_t* base, int32_t* wcnt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, k = a.k;
+  for (int i = threadIdx.x; i < kRouteWarps * E; i += kRouteThreads) wcnt[i] = 0;
+  __syncthreads();
+  const int64_t per = (t1 - t0 + kRouteWarps - 1) / kRouteWarps;
+  const int64_t w0 = min(t1, t0 + warp * per), w1 = min(t1, w0 + per);
+  int32_t* mine = wcnt + warp * E;
+  for (int64_t i = w0 * k + lane; i < w1 * k; i += 32) {
+    const int e = a.topk_idx[i];
+    if (e >= 0) atomicAdd(&mine[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    int s = base[e];
+    for (int w = 0; w < kRouteWarps; ++w) {
+      const int c = wcnt[w * E + e];
+      wcnt[w * E + e] = s;
+      s += c;
+    }
+  }
+  __syncthreads();
+  for (int64_t t = w0; t < w1; ++t) {
+    if (lane < k) {
+      const int e = a.topk_idx[t * k + lane];
+      int row = -1;
+      if (e >= 0) {
+        row = mine[e]++;
+        a.row_token[row] = static_cast<int32_t>(t);
+      }
+      a.slot_row[t * k + lane] = row;
+    }
+    __syncwarp();
+  }
+}
+
+// Writes what one CTA writes for all: offsets and the balance loss (n routed tokens).
+DEVI void finish_route(const RouteArgs& a, const int32_t* counts, const float* mean, int n, const int32_t* offs) {
+  for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) a.expert_offsets[e] = offs[e];
+  if (threadIdx.x < 32) {
+    float s = 0.0f;
+    for (int e = threadIdx.x; e < a.E; e += 32) s += static_cast<float>(counts[e]) * mean[e];
+    s = warp_sum(s);
+    if (threadIdx.x == 0)
+      a.loss[0] = n > 0 ? static_cast<float>(a.E) * s / (static_cast<float>(n) * static_cast<float>(a.k)) : 0.0f;
+  }
+}
+
+DEVI void route_chunk(const RouteArgs& a, int64_t& t0, int64_t& t1) {
+  const int64_t per = (a.T + gridDim.x - 1) / gridDim.x;
+  t0 = min(a.T, static_cast<int64_t>(blockIdx.x) * per);
+  t1 = min(a.T, t0 + per);
+}
+
+// Stage 1: every CTA routes its tokens; counts and sums of p per CTA to the workspace.
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(kRouteThreads) k_moe_route(const RouteArgs a) {
+  extern __shared__ int32_t sh[];
+  int32_t* hist = sh;
+  float* psum = reinterpret_cast<float*>(sh + a.E + 1);
+  int64_t t0, t1;
+  route_chunk(a, t0, t1);
+  route_rows<VPL, BF16>(a, t0, t1, hist, psum);
+  for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
+    a.ws_hist[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + e] = hist[e];
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.ws_psum[static_cast<int64_t>(blockIdx.x) * a.E + e] = psum[e];
+}
+
+// Stage 2: one CTA per 32 experts. ws_hist becomes each CTA's exclusive prefix; totals to
+// counts, means of p to mean_prob. Warps own contiguous runs of the `blocks` rows.
+__global__ void __launch_bounds__(kRouteThreads) k_moe_scan(const RouteArgs a, int blocks) {
+  __shared__ int32_t part[kRouteWarps][32];
+  __shared__ float fpart[kRouteWarps][32];
+  __shared__ int32_t npart[kRouteWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, e = blockIdx.x * 32 + lane;
+  const int per = (blocks + kRouteWarps - 1) / kRouteWarps;
+  const int b0 = min(blocks, warp * per), b1 = min(blocks, b0 + per);
+  int c = 0, n = 0;
+  float s = 0.0f;
+  if (e < E)
+    for (int b = b0; b < b1; ++b) {
+      c += a.ws_hist[static_cast<int64_t>(b) * (E + 1) + e];
+      s += a.ws_psum[static_cast<int64_t>(b) * E + e];
+    }
+  for (int b = b0 + lane; b < b1; b += 32) n += a.ws_hist[static_cast<int64_t>(b) * (E + 1) + E];
+  n = __reduce_add_sync(0xffffffffu, n);
+  part[warp][lane] = c;
+  fpart[warp][lane] = s;
+  if (lane == 0) npart[warp] = n;
+  __syncthreads();
+  int before = 0, total = 0;
+  n = 0;
+  s = 0.0f;
+  for (int w = 0; w < kRouteWarps; ++w) {
+    if (w < warp) before += part[w][lane];
+    total += part[w][lane];
+    s += fpart[w][lane];
+    n += npart[w];
+  }
+  if (e < E) {
+    for (int b = b0; b < b1; ++b) {
+      int32_t* h = a.ws_hist + static_cast<int64_t>(b) * (E + 1) + e;
+      const int v = *h;
+      *h = before;
+      before += v;
+    }
+    if (warp == 0) {
+      a.counts[e] = total;
+      a.mean_prob[e] = n > 0 ? s / static_cast<float>(n) : 0.0f;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.routed_tokens[0] = n;
+}
+
+// Stage 3: every CTA places its tokens' rows.
+__global__ void __launch_bounds__(kRouteThreads) k_moe_place(const RouteArgs a) {
+  extern __shared__ int32_t sh[];
+  int32_t* offs = sh;                // [E + 1]
+  int32_t* base = offs + a.E + 1;    // [E]
+  int32_t* wcnt = base + a.E;        // [kRouteWarps][E]
+  scan_counts(a.counts, a.E, offs);
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
+    base[e] = offs[e] + a.ws_hist[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + e];
+  int64_t t0, t1;
+  route_chunk(a, t0, t1);
+  place_rows(a, t0, t1, base, wcnt);
+  // rows that no selection fills
+  for (int64_t r = offs[a.E] + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x; r < a.T * a.k;
+       r += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+    a.row_token[r] = -1;
+  if (blockIdx.x == 0) finish_route(a, a.counts, a.mean_prob, a.routed_tokens[0], offs);
+}
+
+// All stages in one CTA, for few tokens: no workspace, one launch.
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(kRouteThreads) k_moe_route_one(const RouteArgs a) {
+  extern __shared__ int32_t sh[];
+  int32_t* hist = sh;                                       // [E + 1]
+  int32_t* offs = hist + a.E + 1;                           // [E + 1]
+  float* psum = reinterpret_cast<float*>(offs + a.E + 1);   // [kRouteWarps][E], then the means
+  route_rows<VPL, BF16>(a, 0, a.T, hist, psum);
+  scan_counts(hist, a.E, offs);
+  const int n = hist[a.E];
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+    psum[e] = n > 0 ? psum[e] / static_cast<float>(n) : 0.0f;
+    a.mean_prob[e] = psum[e];
+    a.counts[e] = hist[e];
+  }
+  if (threadIdx.x == 0) a.routed_tokens[0] = n;
+  __syncthreads();
+  finish_route(a, hist, psum, n, offs);
+  for (int64_t r = offs[a.E] + threadIdx.x; r < a.T * a.k; r += kRouteThreads) a.row_token[r] = -1;
+  __syncthreads();  // psum's memory is reused
+  place_rows(a, 0, a.T, offs, reinterpret_cast<int32_t*>(psum));
+}
+
+// ---- gradient of the logits ------------------------------------------------------------------
+//
+// G_te = dL E c_e / (k n^2) from the balance loss (its counts carry no gradient), plus dw_ts at
+// the selected experts when the weights are plain; d l_te = p_te (G_te - sum_i p_ti G_ti).
+// Renormalised weights are a softmax over the selected logits alone: they add
+// w_s (dw_s - sum_r w_r dw_r) at expert idx_s instead. Unrouted tokens get zeros.
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(kRouteThreads) k_moe_route_bwd(const RouteBwdArgs a) {
+  extern __shared__ float shf[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, k = a.k;
+  float* spot = shf + warp * (32 * VPL);  // this warp's sparse part of the row, zero between rows
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) spot[lane * VPL + j] = 0.0f;
+  __syncwarp();
+  const float n = static_cast<float>(a.routed_tokens[0]);
+  const float scale = (a.d_loss && n > 0.0f) ? __ldg(a.d_loss) * static_cast<float>(E) / (static_cast<float>(k) * n * n) : 0.0f;
+  float g[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int e = lane * VPL + j;
+    g[j] = e < E ? scale * static_cast<float>(__ldg(a.counts + e)) : 0.0f;
+  }
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T;
+       t += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
+    float v[VPL], d[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
+    float mx = __uint_as_float(0xFF800000u);
+    const bool valid = !a.valid || __ldg(a.valid + t) != 0;
+    if (valid) {
+      load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) mx = fmaxf(mx, v[j]);
+      mx = key_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
+    }
+    if (mx > __uint_as_float(0xFF800000u)) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        v[j] = ex2((v[j] - mx) * kLog2E);
+        sum += v[j];
+      }
+      const float inv = __frcp_rn(warp_sum(sum));
+      int idx = -1;
+      if (a.d_w) {
+        float dw = 0.0f, w = 0.0f;
+        if (lane < k) {
+          idx = __ldg(a.topk_idx + t * k + lane);
+          if (idx >= E) idx = -1;
+          if (idx >= 0) {
+            dw = __ldg(a.d_w + t * k + lane);
+            w = __ldg(a.topk_w + t * k + lane);
+          }
+        }
+        if (a.renorm) dw = w * (dw - warp_sum(w * dw));
+        if (idx >= 0) spot[idx] = dw;
+        __syncwarp();
+      }
+      float dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        v[j] *= inv;
+        d[j] = spot[lane * VPL + j];
+        const float G = a.renorm ? g[j] : g[j] + d[j];
+        dot += v[j] * G;
+      }
+      dot = warp_sum(dot);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const float G = a.renorm ? g[j] : g[j] + d[j];
+        d[j] = v[j] * (G - dot) + (a.renorm ? d[j] : 0.0f);
+      }
+      __syncwarp();
+      if (idx >= 0) spot[idx] = 0.0f;
+      __syncwarp();
+    }
+    if (a.vec) {
+      if (BF16) {
+        uint16_t* o = static_cast<uint16_t*>(a.d_logits) + t * E + lane * VPL;
+        if constexpr (VPL >= 8) {
+#pragma unroll
+          for (int j = 0; j < VPL; j += 8)
+            *reinterpret_cast<uint4*>(o + j) = make_uint4(pack_bf16x2(d[j], d[j + 1]), pack_bf16x2(d[j + 2], d[j + 3]),
+                                                          pack_bf16x2(d[j + 4], d[j + 5]), pack_bf16x2(d[j + 6], d[j + 7]));
+        } else if constexpr (VPL >= 2) {
+#pragma unroll
+          for (int j = 0; j < VPL; j += 2) *reinterpret_cast<uint32_t*>(o + j) = pack_bf16x2(d[j], d[j + 1]);
+        } else {
+          o[0] = static_cast<uint16_t>(pack_bf16x2(d[0], 0.0f) & 0xFFFFu);
+        }
+      } else {
+        float* o = static_cast<float*>(a.d_logits) + t * E + lane * VPL;
+        if constexpr (VPL >= 4) {
+#pragma unroll
+          for (int j = 0; j < VPL; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) o[j] = d[j];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const int e = lane * VPL + j;
+        if (e < E) {
+          if (BF16)
+            static_cast<uint16_t*>(a.d_logits)[t * E + e] = static_cast<uint16_t>(pack_bf16x2(d[j], 0.0f) & 0xFFFFu);
+          else
+            static_cast<float*>(a.d_logits)[t * E + e] = d[j];
+        }
+      }
+    }
+  }
+}
+
+// ---- host launchers ----------------------------------------------------------------------------
+
+// Values per lane: the smallest power of two that covers E (E <= 1024).
+static int route_vpl(int E) {
+  int v = 1;
+  while (v * 32 < E) v <<= 1;
+  return v;
+}
+
+static bool route_vec(const void* p, int E, int bf16) {
+  const int v = route_vpl(E);
+  const int lane_bytes = v * (bf16 ? 2 : 4) < 16 ? v * (bf16 ? 2 : 4) : 16;
+  return E == 32 * v && reinterpret_cast<uintptr_t>(p) % lane_bytes == 0;
+}
+
+#define ROUTE_DISPATCH(call)                                      \
+  switch (route_vpl(a.E) * 2 + (a.bf16 ? 1 : 0)) {                \
+    case 2: call(1, false); break;                                \
+    case 3: call(1, true); break;                                 \
+    case 4: call(2, false); break;                                \
+    case 5: call(2, true); break;                                 \
+    case 8: call(4, false); break;                                \
+    case 9: call(4, true); break;                                 \
+    case 16: call(8, false); break;                               \
+    case 17: call(8, true); break;                                \
+    case 32: call(16, false); break;                              \
+    case 33: call(16, true); break;                               \
+    case 64: call(32, false); break;                              \
+    default: call(32, true); break;                               \
+  }
+
+// Tokens up to which one CTA does all the stages in one launch.
+constexpr int kRouteOneTokens = 64;
+
+int route_blocks(int64_t T) {
+  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps;
+  return static_cast<int>(b < kRouteBlocks ? b : kRouteBlocks);
+}
+
+cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches) {
+  a.vec = route_vec(a.logits, a.E, a.bf16);
+  const int E = a.E;
+  if (a.T <= kRouteOneTokens) {
+    const int smem = (2 * (E + 1) + kRouteWarps * E) * 4;
+    *launches = 1;
+#define CALL(V, B) k_moe_route_one<V, B><<<1, kRouteThreads, smem, st>>>(a)
+    ROUTE_DISPATCH(CALL)
+#undef CALL
+    return cudaGetLastError();
+  }
+  const int blocks = route_blocks(a.T);
+  const int smem = (E + 1 + kRouteWarps * E) * 4;
+  *launches = 3;
+#define CALL(V, B) k_moe_route<V, B><<<blocks, kRouteThreads, smem, st>>>(a)
+  ROUTE_DISPATCH(CALL)
+#undef CALL
+  k_moe_scan<<<(E + 31) / 32, kRouteThreads, 0, st>>>(a, blocks);
+  k_moe_place<<<blocks, kRouteThreads, (2 * E + 1 + kRouteWarps * E) * 4, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_moe_route_bwd(RouteBwdArgs a, int sms, cudaStream_t st) {
+  a.vec = route_vec(a.logits, a.E, a.bf16) && route_vec(a.d_logits, a.E, a.bf16);
+  const int64_t want = (a.T + kRouteWarps - 1) / kRouteWarps;
+  const int grid = static_cast<int>(want < 8 * sms ? want : 8 * sms);
+  const int smem = kRouteWarps * 32 * route_vpl(a.E) * 4;
+#define CALL(V, B) k_moe_route_bwd<V, B><<<grid, kRouteThreads, smem, st>>>(a)
+  ROUTE_DISPATCH(CALL)
+#undef CALL
+  return cudaGetLastError();
+}
+
+}  // namespace nvfp4
