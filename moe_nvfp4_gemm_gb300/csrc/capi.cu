@@ -123,14 +123,15 @@ int encode_sf(CUtensorMap* m, const void* base, uint64_t chunks) {
 
 // bf16 output [rows, cols] (cols contiguous) for TMA stores: boxes of 64 columns
 // (128 bytes, 128-byte swizzle) x 32 rows; elements outside the tensor are not written.
-int encode_out(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols) {
+// With f32: fp32 output, boxes of 32 columns (128 bytes) x 32 rows.
+int encode_out(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols, bool f32 = false) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return NVFP4_ERR_CUDA;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, 32};
+  cuuint64_t strides[1] = {cols * (f32 ? 4 : 2)};
+  cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
@@ -167,6 +168,8 @@ int pow2_at_least(int v) {
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxFp8Dim = int64_t(1) << 30;
+constexpr int64_t kFp8MinTileRows = 32;  // smallest token tile of the grouped FP8 kernels
 
 }  // namespace
 
@@ -1005,35 +1008,69 @@ int nvfp4_fp8_quantize(const uint16_t* x, int64_t M_x, int64_t K, int32_t block_
 
 static int check_fp8_shape(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N <= 0 || K <= 0) return NVFP4_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  // 2^30: the kernels index rows and columns with 32-bit integers, with headroom for a tile
+  if (K % 16 != 0 || M > kMaxFp8Dim || N > kMaxFp8Dim || K > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
+}
+
+// Launches the pair kernel on `tiles` 256 x 256 tiles (grouped: at most that many).
+static int run_fp8_pair(const uint8_t* a, const uint8_t* b, int64_t b_rows_total, const Fp8GemmArgs& p, int64_t tiles,
+                        int sms, cudaStream_t st) {
+  CUtensorMap tmA, tmB, tmY;
+  int rc;
+  if ((rc = encode_2d(&tmA, a, p.M, p.K, 128))) return rc;
+  if ((rc = encode_2d(&tmB, b, b_rows_total, p.K, 128))) return rc;
+  tmY = tmA;  // unused when y's rows are not 16-byte aligned
+  if (p.N % (p.f32 ? 4 : 8) == 0 && (rc = encode_out(&tmY, p.y, p.M, p.N, p.f32 != 0))) return rc;
+  int64_t pairs = (g_tune.dense_grid ? g_tune.dense_grid : sms) / 2;
+  if (pairs > tiles) pairs = tiles;
+  if (pairs < 1) pairs = 1;
+  return from_cuda(launch_fp8_gemm_pair(tmA, tmB, tmY, p, static_cast<int>(2 * pairs), st));
 }
 
 int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int32_t b_block_rows,
                    void* y, int32_t y_type, int64_t M, int64_t N, int64_t K, int32_t* dev_status, void* stream) {
   g_last_launches = 0;
-  (void)dev_status;
   int rc = check_fp8_shape(M, N, K);
   if (rc) return rc;
   if ((b_block_rows != 1 && b_block_rows != 128) || (y_type != NVFP4_BF16 && y_type != NVFP4_F32))
     return NVFP4_ERR_INVALID_ARG;
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (tiles > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return NVFP4_OK;
   if (!a || !sa || !b || !sb || !y) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(b) || !aligned16(y) || !aligned4(sa) || !aligned4(sb)) return NVFP4_ERR_ALIGNMENT;
   DevInfo d;
   rc = device_info(d);
   if (rc) return rc;
-  Fp8GemmArgs p = {a, sa, b, sb, nullptr, y, M, N, K, b_block_rows, y_type == NVFP4_F32};
-  rc = from_cuda(launch_fp8_gemm(p, 1, static_cast<cudaStream_t>(stream)));
+  Fp8GemmArgs p = {};
+  p.sa = sa;
+  p.sb = sb;
+  p.y = y;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.b_rows = b_block_rows;
+  p.f32 = y_type == NVFP4_F32;
+  p.status = dev_status;
+  p.watchdog_ns = watchdog_ns();
+  p.drop_stage = g_tune.withhold_stage;
+  rc = run_fp8_pair(a, b, N, p, tiles, d.sms, static_cast<cudaStream_t>(stream));
   g_last_launches = 1;
   return rc;
 }
 
+// Tiles of at most kFp8TileRows rows of one expert each.
+static int64_t fp8_max_tiles(int32_t E, int64_t M_total, int64_t tile_rows) {
+  return (M_total + tile_rows - 1) / tile_rows + E;
+}
+
+// [0] the tile count, [16..) the tile list; sized for the smallest tiles.
 size_t nvfp4_fp8_grouped_gemm_workspace_bytes(int32_t E, int64_t M_total, int64_t N, int64_t K) {
   (void)N;
   (void)K;
   if (E <= 0 || M_total < 0) return 0;
-  return 256;
+  return static_cast<size_t>(16 + fp8_max_tiles(E, M_total, kFp8MinTileRows) * 16);
 }
 
 int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
@@ -1043,7 +1080,8 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   int rc = check_fp8_shape(M_total, N, K);
   if (E <= 0) return NVFP4_ERR_INVALID_ARG;
   if (rc) return rc;
-  if (static_cast<int64_t>(E) * N > kMaxDim || E > 16384 || M_total > (int64_t(1) << 30))
+  const int64_t max_tiles = fp8_max_tiles(E, M_total, kFp8MinTileRows);
+  if (E > 16384 || static_cast<int64_t>(E) * N > kMaxFp8Dim || max_tiles * ((N + 127) / 128) > kMaxFp8Dim)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (M_total == 0) return NVFP4_OK;
   if (!a || !sa || !b || !sb || !expert_offsets || !y) return NVFP4_ERR_INVALID_ARG;
@@ -1055,8 +1093,28 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   DevInfo d;
   rc = device_info(d);
   if (rc) return rc;
-  Fp8GemmArgs p = {a, sa, b, sb, expert_offsets, y, M_total, N, K, 128, 0, static_cast<int32_t*>(workspace), dev_status};
-  rc = from_cuda(launch_fp8_gemm(p, E, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t* n_tiles = static_cast<int32_t*>(workspace);
+  int4* tiles = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + 16);
+  Fp8GemmArgs p = {};
+  p.sa = sa;
+  p.sb = sb;
+  p.y = y;
+  p.M = M_total;
+  p.N = N;
+  p.K = K;
+  p.b_rows = 128;
+  p.tiles = tiles;
+  p.n_tiles = n_tiles;
+  p.E = E;
+  p.max_tiles = static_cast<int>(fp8_max_tiles(E, M_total, 256));
+  p.status = dev_status;
+  p.watchdog_ns = watchdog_ns();
+  p.drop_stage = g_tune.withhold_stage;
+  rc = from_cuda(launch_fp8_tiles(expert_offsets, E, static_cast<int>(M_total), 256, tiles, n_tiles, dev_status, st));
+  g_last_launches = 1;
+  if (rc) return rc;
+  rc = run_fp8_pair(a, b, static_cast<int64_t>(E) * N, p, fp8_max_tiles(E, M_total, 256) * ((N + 255) / 256), d.sms, st);
   g_last_launches = 2;
   return rc;
 }

@@ -1,5 +1,16 @@
-// FP8 block-scaled products: y[m, n] = sum_c sa[c, m] sb(c, n) sum_{k in block c} a[m, k] b[n, k],
-// a, b E4M3, c running over blocks of 128 of K, sb one scale per 128 rows of b or per row.
+// FP8 block-scaled tile GEMM: y[m, n] = sum_c sa[c, m] sb(c, n) sum_{k in block c} a[m, k] b[n, k],
+// a, b E4M3, c running over blocks of 128 of K, sb one scale per 128 rows of b or one per row.
+//
+// The tensor core sums one block of 128 (four K = 32 MMAs) from zero into a TMEM buffer; the
+// epilogue warps read the 256 x 256 block sums back and add them, times their scales, to the
+// result, which stays in their registers (fp32) for the whole of K. So each block sum meets
+// its two fp32 scales exactly once, and two TMEM buffers (all 512 columns) let the MMA of block
+// c + 1 run while block c is read.
+//
+// One CTA pair (cta_group::2) per 256 x 256 tile of y: per block of K each CTA loads 128 rows of a
+// and of b (32 KB by TMA, 128-byte swizzle) and the pair's MMAs take 512 cycles at the full rate;
+// each CTA's eight epilogue warps (lane quarter x column half) need 4 x (tcgen05.ld of 32 columns +
+// 16 packed fma) per block in that time.
 #include <stdint.h>
 
 #include "kernels.h"
@@ -8,79 +19,450 @@
 
 namespace nvfp4 {
 
-// Grouped: 0 = offsets[0] <= ... <= offsets[E] <= M; the verdict goes to *ok for the product.
-__global__ void __launch_bounds__(256) k_fp8_check_offsets(const int32_t* __restrict__ offsets, int E, int64_t M,
-                                                           int32_t* ok, int32_t* status) {
-  bool good = offsets[0] == 0 && offsets[E] <= M;
-  for (int e = threadIdx.x; e < E; e += 256) good = good && offsets[e] <= offsets[e + 1];
-  good = __syncthreads_and(good) != 0;
-  if (threadIdx.x == 0) {
-    *ok = good;
-    if (!good) report_status(status, kStatusBadOffsets);
+struct Fp8PairCfg {
+  // warps 0-3: producer, MMA issuer, two idle; warps 4-11: epilogue. 384 x 168 registers at
+  // launch; the epilogue takes what the first warpgroup gives up: 128 x 72 + 256 x 216 = 384 x 168.
+  static constexpr int THREADS = 384;
+  static constexpr int CONTROL_REGS = 72, EPILOGUE_REGS = 216;
+  static_assert(128 * CONTROL_REGS + 256 * EPILOGUE_REGS <= 384 * 168, "register shares");
+  static constexpr int TILE_BYTES = 128 * 128;
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int STAGES = 5;
+  static constexpr int OUT_BYTES = 8 * 4096;  // one 32-row x 128-byte store box per epilogue warp
+  static constexpr int SCALE_BYTES = 8 * 2 * 512;  // per warp: two buffers of 128 column scales
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 1024 + 256;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+struct Fp8Tile {
+  int m0, m_end;  // rows of a and y: [m0, m_end)
+  int b_row;      // first row of b
+  int n0;         // first column of y
+  const float* sb;
+};
+
+// Everything that the previous kernel in the stream may have written (tile list, scales) is read
+// with plain loads: this kernel starts while that one may still run (programmatic dependent
+// launch), so the data is not read-only for the kernel's life, as the non-coherent path (__ldg)
+// requires; a plain load stays behind griddep_wait.
+template <bool GROUPED>
+DEVI Fp8Tile fp8_tile(const Fp8GemmArgs& p, int t, int mt, int nt, int kbs) {
+  Fp8Tile r;
+  const int N = static_cast<int>(p.N);
+  if (GROUPED) {
+    int4 d = p.tiles[t / nt];
+    d.x = min(max(d.x, 0), p.E - 1);
+    d.y = min(max(d.y, 0), static_cast<int>(p.M) - 1);
+    d.z = min(max(d.z, 0), static_cast<int>(p.M) - d.y);
+    r.n0 = (t % nt) * 256;
+    r.m0 = d.y;
+    r.m_end = d.y + d.z;
+    r.b_row = d.x * N + r.n0;
+    r.sb = p.sb + static_cast<int64_t>(d.x) * ((N + 127) / 128) * kbs;
+  } else {
+    r.m0 = (t % mt) * 256;
+    r.n0 = (t / mt) * 256;
+    r.m_end = static_cast<int>(p.M);
+    r.b_row = r.n0;
+    r.sb = p.sb;
   }
+  return r;
 }
 
-// One CTA per 64 x 64 tile of y (grouped: of one expert's rows), 4 x 4 outputs per thread; each
-// 128-block's sum in fp32, then scaled into the fp32 result.
-__global__ void __launch_bounds__(256) k_fp8_gemm(const Fp8GemmArgs p) {
-  __shared__ float as[32][65], bs[32][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int e = blockIdx.z;
-  const int64_t N = p.N, K = p.K;
-  if (p.offsets && *p.ok == 0) return;
-  const int64_t r_begin = p.offsets ? p.offsets[e] : 0, r_end = p.offsets ? p.offsets[e + 1] : p.M;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const uint8_t* b = p.b + e * N * K;
-  const int64_t kbs = (K + 127) / 128;
-  const float* sb = p.sb + e * ((N + 127) / 128) * kbs;
-  for (int64_t m0 = r_begin + static_cast<int64_t>(blockIdx.y) * 64; m0 < r_end; m0 += static_cast<int64_t>(gridDim.y) * 64) {
-    float acc[4][4] = {};
-    for (int64_t c = 0; c < kbs; ++c) {
-      float part[4][4] = {};
-      for (int64_t k0 = c * 128; k0 < min(K, c * 128 + 128); k0 += 32) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-          const int r = i >> 5, kk = i & 31;
-          as[kk][r] = (m0 + r < r_end && k0 + kk < K) ? e4m3_decode(p.a[(m0 + r) * K + k0 + kk]) : 0.0f;
-          bs[kk][r] = (n0 + r < N && k0 + kk < K) ? e4m3_decode(b[(n0 + r) * K + k0 + kk]) : 0.0f;
-        }
-        __syncthreads();
-        for (int kk = 0; kk < 32; ++kk)
+// A warp's 32 rows x 128 bytes of results to y, through its 4 KB box (16-byte chunk c of row r at
+// chunk c ^ (r % 8)): by a TMA store (whole tiles), or row by row with plain stores where y's
+// rows are not 16-byte aligned or the box reaches past the tile's rows.
+template <bool F32>
+DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, const uint32_t (&w)[32], const CUtensorMap* tmY, bool by_tma,
+                        int row0, int m_end, int col0, int N) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) bulk_wait_group_read0();  // the previous box has left the buffer
+  __syncwarp();
+  const uint32_t row_addr = smem_u32(buf) + lane * 128;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[i][j] += as[kk][ty * 4 + i] * bs[kk][tx * 4 + j];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-          if (m < r_end && n < N)
-            acc[i][j] += part[i][j] * (p.sa[c * p.M + m] * (p.b_rows == 1 ? sb[c * N + n] : sb[(n >> 7) * kbs + c]));
-        }
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
+                 "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+  if (by_tma) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tmY, buf, col0, row0);
+      bulk_commit_group();
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-        if (m < r_end && n < N) {
-          if (p.f32)
-            static_cast<float*>(p.y)[m * N + n] = acc[i][j];
-          else
-            static_cast<uint16_t*>(p.y)[m * N + n] = static_cast<uint16_t>(pack_bf16x2(acc[i][j], 0.0f) & 0xFFFFu);
-        }
+  } else {
+    __syncwarp();
+    const int rows = min(32, m_end - row0);
+    for (int r = 0; r < rows; ++r) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+      const int64_t at = static_cast<int64_t>(row0 + r) * N + col0;
+      if (F32) {
+        if (col0 + lane < N) static_cast<float*>(p.y)[at + lane] = __uint_as_float(v);
+      } else {
+        uint16_t* y = static_cast<uint16_t*>(p.y) + at + 2 * lane;
+        if (col0 + 2 * lane < N) y[0] = static_cast<uint16_t>(v & 0xFFFFu);
+        if (col0 + 2 * lane + 1 < N) y[1] = static_cast<uint16_t>(v >> 16);
       }
+    }
+    __syncwarp();
   }
 }
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& p, int E, cudaStream_t st) {
-  if (p.offsets) k_fp8_check_offsets<<<1, 256, 0, st>>>(p.offsets, E, p.M, p.ok, p.status);
-  const int64_t mt = (p.M + 63) / 64;
-  dim3 grid(static_cast<unsigned>((p.N + 63) / 64), static_cast<unsigned>(E > 1 ? (mt / E + 1) : (mt < 65535 ? mt : 65535)),
-            static_cast<unsigned>(E));
-  k_fp8_gemm<<<grid, 256, 0, st>>>(p);
+// COLSCALE: one scale per row of b (a column of y), staged per warp in shared memory and applied
+// before the row scale; otherwise one per 128 rows of b, which a warp's 128 columns share.
+template <bool COLSCALE, bool GROUPED, bool F32>
+__global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
+    k_fp8_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Fp8GemmArgs p) {
+  using C = Fp8PairCfg;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* out_buf = smem + STAGES * C::STAGE_BYTES;
+  float* scale_buf = reinterpret_cast<float*>(out_buf + C::OUT_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_buf + C::OUT_BYTES + C::SCALE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;  // [2]
+  uint64_t* tempty = tfull + 2;      // [2]
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t wd = p.watchdog_ns;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 16);  // one elected lane per epilogue warp, both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmY);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either signals the other
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // set-up overlaps the previous kernel; every memory access waits for it
+
+  const int M = static_cast<int>(p.M), N = static_cast<int>(p.N);
+  const int nt = (N + 255) / 256;
+  const int mt = (M + 255) / 256;
+  const int KB = static_cast<int>((p.K + 127) / 128);
+  const int tiles = GROUPED ? min(max(p.n_tiles[0], 0), p.max_tiles) * nt : mt * nt;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (warp >= 4) {
+    regs_inc<C::EPILOGUE_REGS>();
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    uint8_t* box = out_buf + (warp - 4) * 4096;
+    float* cs = scale_buf + (warp - 4) * 256;
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+    const bool aligned_rows = N % (F32 ? 4 : 8) == 0;
+    int buf = 0;
+    uint32_t bph = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += npairs) {
+      const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+      const int row0 = tl.m0 + rank * 128 + q * 32, row = row0 + lane;
+      const int col0 = tl.n0 + h * 128;
+      const bool row_ok = row < tl.m_end;
+      const float* sa = p.sa + row;
+      const float* sb = COLSCALE ? tl.sb + col0 + lane : tl.sb + static_cast<int64_t>(col0 >> 7) * KB;
+      // the scales of a block of K: this row's, and the warp's column block's (or its four of 128)
+      auto row_scale = [&](int kb) { return row_ok && kb < KB ? sa[static_cast<int64_t>(kb) * M] : 0.0f; };
+      auto block_scale = [&](int kb) { return kb < KB && col0 < N ? sb[kb] : 0.0f; };
+      auto col_scale = [&](int kb, int i) {
+        return kb < KB && col0 + lane + 32 * i < N ? sb[static_cast<int64_t>(kb) * N + 32 * i] : 0.0f;
+      };
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      // loaded two blocks ahead of their use
+      float ra = row_scale(0), rb = row_scale(1), ca[4], cb[4];
+      if (COLSCALE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ca[i] = col_scale(0, i), cb[i] = col_scale(1, i);
+      } else {
+        ca[0] = block_scale(0), cb[0] = block_scale(1);
+      }
+      for (int kb = 0; kb < KB; ++kb) {
+        const float rs = COLSCALE ? ra : ra * ca[0];
+        const uint64_t rs2 = f2(rs, rs);
+        if (COLSCALE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cs[buf * 128 + lane + 32 * i] = ca[i];
+          __syncwarp();
+        }
+        ra = rb;
+        rb = row_scale(kb + 2);
+        if (COLSCALE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ca[i] = cb[i], cb[i] = col_scale(kb + 2, i);
+        } else {
+          ca[0] = cb[0];
+          cb[0] = block_scale(kb + 2);
+        }
+        if (!mbar_wait_warp(&tfull[buf], bph, abort_flag, wd)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + h * 128;
+        uint32_t r[2][32];
+        tmem_ld32(taddr, r[0]);
+        tmem_ld_wait32(r[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t* cur = r[c & 1];
+          if (c < 3) {
+            tmem_ld32(taddr + 32 * (c + 1), r[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive_cluster(tempty_leader[buf]);
+            __syncwarp();
+          }
+          if (COLSCALE) {
+            const float4* cv = reinterpret_cast<const float4*>(cs + buf * 128 + 32 * c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 v = cv[j];
+              const uint64_t x0 = f2_mul(f2(__uint_as_float(cur[4 * j]), __uint_as_float(cur[4 * j + 1])), f2(v.x, v.y));
+              const uint64_t x1 = f2_mul(f2(__uint_as_float(cur[4 * j + 2]), __uint_as_float(cur[4 * j + 3])), f2(v.z, v.w));
+              acc[16 * c + 2 * j] = f2_fma(x0, rs2, acc[16 * c + 2 * j]);
+              acc[16 * c + 2 * j + 1] = f2_fma(x1, rs2, acc[16 * c + 2 * j + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[16 * c + j] = f2_fma(f2(__uint_as_float(cur[2 * j]), __uint_as_float(cur[2 * j + 1])), rs2, acc[16 * c + j]);
+          }
+          if (c < 3) tmem_ld_wait32(r[(c + 1) & 1]);
+        }
+        buf ^= 1;
+        bph ^= buf == 0;
+      }
+      if (!ok) break;
+      // results to y; a grouped tile that ends inside the box's rows must not touch the next expert's
+      const bool by_tma = aligned_rows && (!GROUPED || row0 + 32 <= tl.m_end);
+      if (row0 < tl.m_end) {
+#pragma unroll
+        for (int b = 0; b < (F32 ? 4 : 2); ++b) {
+          const int c0 = col0 + b * (F32 ? 32 : 64);
+          if (c0 < N) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float lo, hi;
+              if (F32) {
+                f2_split(acc[16 * b + (j >> 1)], lo, hi);
+                w[j] = __float_as_uint((j & 1) ? hi : lo);
+              } else {
+                f2_split(acc[32 * b + j], lo, hi);
+                w[j] = pack_bf16x2(lo, hi);
+              }
+            }
+            fp8_store_box<F32>(p, box, w, &tmY, by_tma, row0, tl.m_end, c0, N);
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group0();  // this warp's stores are complete before the CTA exits
+    __syncwarp();
+  } else {
+  regs_dec<C::CONTROL_REGS>();
+  if (warp == 0) {
+    const uint64_t pol = policy_evict_last();
+    int s = 0;
+    uint32_t ph = 0;
+    int issued_phase[STAGES];
+    for (int i = 0; i < STAGES; ++i) issued_phase[i] = -1;
+    int issued = 0;
+    for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+      const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag, wd)) break;
+        // test hook: the first CTA withholds its expect-tx arrival and loads
+        const bool withheld = blockIdx.x == 0 && ++issued == p.drop_stage;
+        if (!withheld && elect_one()) {
+          uint8_t* st = smem + s * C::STAGE_BYTES;
+          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+          tma_load_2d_pair(st, &tmA, bar, kb * 128, tl.m0 + rank * 128, pol);
+          tma_load_2d_pair(st + C::TILE_BYTES, &tmB, bar, kb * 128, tl.b_row + rank * 128, pol);
+        }
+        __syncwarp();
+        issued_phase[s] = ph;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    griddep_launch_dependents();
+    // The even CTA's full barriers count both CTAs' bytes: let them all land.
+    if (leader)
+      for (int i = 0; i < STAGES; ++i)
+        if (issued_phase[i] >= 0) {
+          volatile int32_t dummy = 0;
+          mbar_wait_warp(&full[i], issued_phase[i], &dummy, wd);
+        }
+  } else if (warp == 1) {
+    if (leader) {
+      const uint32_t idesc = idesc_e4m3(256, 256);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, bph = 0;
+      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_warp(&tempty[buf], bph ^ 1, abort_flag, wd)) break;
+          if (!mbar_wait_warp(&full[s], ph, abort_flag, wd)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t a_addr = smem_u32(smem + s * C::STAGE_BYTES);
+            const uint64_t adesc = desc_sw128(a_addr), bdesc = desc_sw128(a_addr + C::TILE_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f8_pair(tmem + buf * 256, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0);
+            tc_commit_pair(&empty[s], 3);
+            tc_commit_pair(&tfull[buf], 3);
+          }
+          __syncwarp();
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          buf ^= 1;
+          bph ^= buf == 0;
+        }
+      }
+      if (elect_one()) tc_commit_pair(drain, 1);
+      __syncwarp();
+      volatile int32_t dummy = 0;
+      mbar_wait_warp(drain, 0, &dummy, wd);
+    }
+  }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still read its shared memory or signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) report_status(p.status, kStatusTimeout);
+}
+
+// ---- grouped preparation ------------------------------------------------------------------------
+
+// One CTA: checks 0 = offsets[0] <= ... <= offsets[E] <= M and lists the token tiles, (expert, first
+// row, rows) with at most tile_rows rows of one expert each; experts without rows get none.
+// Malformed offsets are reported and leave an empty list.
+__global__ void __launch_bounds__(1024) k_fp8_tiles(const int32_t* offsets, int E, int M, int tile_rows, int4* tiles,
+                                                    int32_t* n_tiles, int32_t* status) {
+  __shared__ int32_t wsum[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // thread i owns a contiguous run of experts
+  const int per = (E + 1023) / 1024;
+  const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
+  bool good = true;
+  int mine = 0;
+  if (threadIdx.x == 0) good = offsets[0] == 0 && offsets[E] <= M;
+  for (int e = e0; e < e1; ++e) {
+    const int a = offsets[e], b = offsets[e + 1];
+    good = good && a >= 0 && a <= b && b <= M;
+    if (good) mine += (b - a + tile_rows - 1) / tile_rows;
+  }
+  good = __syncthreads_and(good) != 0;
+  if (!good) {
+    if (threadIdx.x == 0) {
+      *n_tiles = 0;
+      report_status(status, kStatusBadOffsets);
+    }
+    return;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += wsum[w];
+    total += wsum[w];
+  }
+  int at = before + incl - mine;
+  for (int e = e0; e < e1; ++e) {
+    const int a = offsets[e], b = offsets[e + 1];
+    for (int r = a; r < b; r += tile_rows) tiles[at++] = make_int4(e, r, min(tile_rows, b - r), 0);
+  }
+  if (threadIdx.x == 0) *n_tiles = total;
+}
+
+// ---- host launchers -------------------------------------------------------------------------------
+
+cudaError_t launch_fp8_tiles(const int32_t* offsets, int E, int M, int tile_rows, int4* tiles, int32_t* n_tiles,
+                             int32_t* status, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_fp8_tiles, offsets, E, M, tile_rows, tiles, n_tiles, status);
+}
+
+cudaError_t launch_fp8_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmY,
+                                 const Fp8GemmArgs& p, int grid, cudaStream_t st) {
+  void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Fp8GemmArgs);
+  if (p.tiles)
+    kernel = k_fp8_gemm_pair<false, true, false>;
+  else if (p.b_rows == 1)
+    kernel = p.f32 ? k_fp8_gemm_pair<true, false, true> : k_fp8_gemm_pair<true, false, false>;
+  else
+    kernel = p.f32 ? k_fp8_gemm_pair<false, false, true> : k_fp8_gemm_pair<false, false, false>;
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Fp8PairCfg::THREADS);
+  cfg.dynamicSmemBytes = Fp8PairCfg::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmY, p);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

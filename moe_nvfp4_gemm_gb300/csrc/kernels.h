@@ -178,19 +178,25 @@ struct Fp8QuantArgs {
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int block_rows, cudaStream_t st);
 
 struct Fp8GemmArgs {
-  const uint8_t* a;
   const float* sa;
-  const uint8_t* b;
   const float* sb;
-  const int32_t* offsets;  // grouped: [E + 1]
   void* y;
   int64_t M, N, K;
   int b_rows;              // rows of b that share a scale: 128 or 1
   int f32;                 // y fp32 instead of bf16
-  int32_t* ok;             // grouped: workspace word, 1 when the offsets are well formed
+  const int4* tiles;       // grouped: (expert, first row, rows, -), else null
+  const int32_t* n_tiles;
+  int E, max_tiles;
   int32_t* status;
+  uint64_t watchdog_ns;    // limit of every pipeline wait
+  int drop_stage;          // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
 };
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& p, int E, cudaStream_t st);
+cudaError_t launch_fp8_tiles(const int32_t* offsets, int E, int M, int tile_rows, int4* tiles, int32_t* n_tiles,
+                             int32_t* status, cudaStream_t st);
+// grid: an even number of CTAs (two per 256 x 256 tile in flight)
+cudaError_t launch_fp8_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmY,
+                                 const Fp8GemmArgs& p, int grid, cudaStream_t st);
+
 int stream_smem_bytes(int stages, int x_rows, int recv_bytes, bool sparse = false);
 // shared memory after the ring for one tile's token indices (and with qout the epilogue's
 // NVFP4 transpose tiles, 1 KB per epilogue warp)
