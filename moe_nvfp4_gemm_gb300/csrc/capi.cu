@@ -1055,7 +1055,22 @@ int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const fl
   p.status = dev_status;
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
-  rc = run_fp8_pair(a, b, N, p, tiles, d.sms, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int max_m = g_tune.stream_max_m == 0 ? 128 : g_tune.stream_max_m;
+  if (M <= max_m) {
+    const int64_t ntw = (N + 127) / 128, kb = (K + 127) / 128;
+    int64_t split = g_tune.stream_split ? g_tune.stream_split : 2 * int64_t(d.sms) / ntw;
+    split = split < 1 ? 1 : (split > 8 ? 8 : split);
+    if (split > kb) split = kb;
+    p.split = static_cast<int>(split);
+    p.l2_prefetch = stream_l2_prefetch(ntw * split, d.sms, 16384);
+    CUtensorMap tmW, tmX;
+    if ((rc = encode_2d(&tmW, b, N, K, 128))) return rc;
+    if ((rc = encode_2d(&tmX, a, M, K, 32))) return rc;
+    rc = from_cuda(launch_fp8_stream(tmW, tmX, p, M <= 32 ? 32 : (M <= 64 ? 64 : 128), d.sms, st));
+  } else {
+    rc = run_fp8_pair(a, b, N, p, tiles, d.sms, st);
+  }
   g_last_launches = 1;
   return rc;
 }
@@ -1106,15 +1121,26 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   p.b_rows = 128;
   p.tiles = tiles;
   p.n_tiles = n_tiles;
-  p.E = E;
-  p.max_tiles = static_cast<int>(fp8_max_tiles(E, M_total, 256));
+  // Token tiles: experts with few rows each go to the streaming kernel, in tiles that most
+  // experts fit in once (an expert with more rows streams its weights once per tile).
+  const int64_t mean = (M_total + E - 1) / E;
+  const bool tile_kernel = mean > 512;
+  const int tile_rows = tile_kernel ? 256 : (mean <= 12 ? 32 : (mean <= 28 ? 64 : (mean <= 72 ? 128 : 256)));
+  p.max_tiles = static_cast<int>(fp8_max_tiles(E, M_total, tile_rows));
   p.status = dev_status;
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
-  rc = from_cuda(launch_fp8_tiles(expert_offsets, E, static_cast<int>(M_total), 256, tiles, n_tiles, dev_status, st));
+  rc = from_cuda(launch_fp8_tiles(expert_offsets, E, static_cast<int>(M_total), tile_rows, tiles, n_tiles, dev_status, st));
   g_last_launches = 1;
   if (rc) return rc;
-  rc = run_fp8_pair(a, b, static_cast<int64_t>(E) * N, p, fp8_max_tiles(E, M_total, 256) * ((N + 255) / 256), d.sms, st);
+  if (tile_kernel) {
+    rc = run_fp8_pair(a, b, static_cast<int64_t>(E) * N, p, p.max_tiles * ((N + 255) / 256), d.sms, st);
+  } else {
+    CUtensorMap tmW, tmX;
+    if ((rc = encode_2d(&tmW, b, static_cast<uint64_t>(E) * N, K, 128))) return rc;
+    if ((rc = encode_2d(&tmX, a, M_total, K, 32))) return rc;
+    rc = from_cuda(launch_fp8_stream(tmW, tmX, p, tile_rows, d.sms, st));
+  }
   g_last_launches = 2;
   return rc;
 }

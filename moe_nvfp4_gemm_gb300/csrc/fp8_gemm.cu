@@ -50,10 +50,7 @@ DEVI Fp8Tile fp8_tile(const Fp8GemmArgs& p, int t, int mt, int nt, int kbs) {
   Fp8Tile r;
   const int N = static_cast<int>(p.N);
   if (GROUPED) {
-    int4 d = p.tiles[t / nt];
-    d.x = min(max(d.x, 0), p.E - 1);
-    d.y = min(max(d.y, 0), static_cast<int>(p.M) - 1);
-    d.z = min(max(d.z, 0), static_cast<int>(p.M) - d.y);
+    const int4 d = p.tiles[t / nt];
     r.n0 = (t % nt) * 256;
     r.m0 = d.y;
     r.m_end = d.y + d.z;
@@ -164,7 +161,7 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
   const int nt = (N + 255) / 256;
   const int mt = (M + 255) / 256;
   const int KB = static_cast<int>((p.K + 127) / 128);
-  const int tiles = GROUPED ? min(max(p.n_tiles[0], 0), p.max_tiles) * nt : mt * nt;
+  const int tiles = GROUPED ? p.n_tiles[0] * nt : mt * nt;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
   if (warp >= 4) {

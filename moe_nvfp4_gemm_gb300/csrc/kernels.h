@@ -186,11 +186,16 @@ struct Fp8GemmArgs {
   int f32;                 // y fp32 instead of bf16
   const int4* tiles;       // grouped: (expert, first row, rows, -), else null
   const int32_t* n_tiles;
-  int E, max_tiles;
+  int max_tiles;           // grouped: most tiles the list can hold
   int32_t* status;
   uint64_t watchdog_ns;    // limit of every pipeline wait
   int drop_stage;          // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
+  int split;               // streaming kernel, dense: cluster size along K
+  int stages;              // streaming kernel: ring depth (set by its launcher)
+  int l2_prefetch;         // streaming kernel, dense: blocks of K prefetched into L2 at entry
 };
+cudaError_t launch_fp8_stream(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int tile_rows,
+                              int sms, cudaStream_t st);
 cudaError_t launch_fp8_tiles(const int32_t* offsets, int E, int M, int tile_rows, int4* tiles, int32_t* n_tiles,
                              int32_t* status, cudaStream_t st);
 // grid: an even number of CTAs (two per 256 x 256 tile in flight)
