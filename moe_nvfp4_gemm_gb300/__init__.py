@@ -80,6 +80,8 @@ class GemmProblem(ctypes.Structure):
 def lib():
     """The loaded libnvfp4.so; raises if it was not built (no fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -144,13 +146,13 @@ def lib():
     return _lib
 
 
-def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t):  # an int: every entry point's argtypes convert it to the pointer
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _check(fn, rc):

@@ -900,8 +900,8 @@ static bool aligned_logits(const void* p, int32_t type) {
 }
 
 size_t nvfp4_moe_route_workspace_bytes(int64_t T, int32_t E) {
-  if (T <= 0 || E <= 0) return 0;
-  return static_cast<size_t>(route_blocks(T)) * (2 * static_cast<size_t>(E) + 1) * 4;
+  if (T <= 0 || E <= 0 || E > NVFP4_MOE_MAX_EXPERTS) return 0;
+  return static_cast<size_t>(route_blocks(T, E)) * (2 * static_cast<size_t>(E) + 1) * 4;
 }
 
 int nvfp4_moe_route(const void* logits, int32_t logits_type, const uint8_t* valid, int64_t T, int32_t E, int32_t k,
@@ -941,7 +941,7 @@ int nvfp4_moe_route(const void* logits, int32_t logits_type, const uint8_t* vali
   a.loss = balance_loss;
   a.routed_tokens = routed_tokens;
   a.ws_hist = static_cast<int32_t*>(workspace);
-  a.ws_psum = reinterpret_cast<float*>(a.ws_hist + static_cast<int64_t>(route_blocks(T)) * (E + 1));
+  a.ws_psum = reinterpret_cast<float*>(a.ws_hist + static_cast<int64_t>(route_blocks(T, E)) * (E + 1));
   int launches = 0;
   rc = from_cuda(launch_moe_route(a, static_cast<cudaStream_t>(stream), &launches));
   g_last_launches = launches;
@@ -995,7 +995,7 @@ int nvfp4_fp8_quantize(const uint16_t* x, int64_t M_x, int64_t K, int32_t block_
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (M == 0 || K == 0) return NVFP4_OK;
   if ((M_x > 0 && !x) || (!q && !qt) || (q && !s) || (qt && !st)) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(q) || !aligned16(qt) || !aligned4(s) || !aligned4(st) || !aligned4(row_token))
+  if (!aligned16(x) || !aligned16(q) || !aligned16(qt) || !aligned4(s) || !aligned16(st) || !aligned4(row_token))
     return NVFP4_ERR_ALIGNMENT;
   DevInfo d;
   int rc = device_info(d);
@@ -1124,8 +1124,8 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   // Token tiles: experts with few rows each go to the streaming kernel, in tiles that most
   // experts fit in once (an expert with more rows streams its weights once per tile).
   const int64_t mean = (M_total + E - 1) / E;
-  const bool tile_kernel = mean > 512;
-  const int tile_rows = tile_kernel ? 256 : (mean <= 12 ? 32 : (mean <= 28 ? 64 : (mean <= 72 ? 128 : 256)));
+  const bool tile_kernel = mean > 72;
+  const int tile_rows = tile_kernel ? 256 : (mean <= 12 ? 32 : (mean <= 28 ? 64 : 128));
   p.max_tiles = static_cast<int>(fp8_max_tiles(E, M_total, tile_rows));
   p.status = dev_status;
   p.watchdog_ns = watchdog_ns();

@@ -15,29 +15,50 @@ namespace nvfp4 {
 
 constexpr int kFp8QuantThreads = 256;  // 16 groups of 8 rows x 16 groups of 8 columns
 
-// Eight E4M3 codes of v / s (element j in byte j), for s with y = RN(1 / s).
-DEVI uint2 e4m3_codes8(const uint4& w, const float (&s)[8], const float (&y)[8], bool fast) {
+// Eight E4M3 codes of v / s (element j in byte j): element pair j divided by (s.x, s.y)[j], for
+// y = RN(1 / s). FAST: x / s correctly rounded by the two fma corrections of div_rn_by, two
+// elements at a time (they lose the sign of a zero, so the signs are put back on the codes).
+template <bool FAST>
+DEVI uint2 e4m3_codes8(const uint4& w, const float2 (&s)[4], const float2 (&y)[4]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint16_t h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float lo = bf16lo(u[j]), hi = bf16hi(u[j]);
     float a, b;
-    if (fast) {
-      // x / s correctly rounded by the two fma corrections of div_rn_by, two elements at a time
-      const uint64_t xx = f2(lo, hi), yy = f2(y[2 * j], y[2 * j + 1]), nd = f2(-s[2 * j], -s[2 * j + 1]);
+    if (FAST) {
+      const uint64_t xx = f2(lo, hi), yy = f2(y[j].x, y[j].y), nd = f2(-s[j].x, -s[j].y);
       const uint64_t q0 = f2_mul(xx, yy);
       const uint64_t q1 = f2_fma(f2_fma(q0, nd, xx), yy, q0);
       f2_split(f2_fma(f2_fma(q1, nd, xx), yy, q1), a, b);
-      a = with_sign_of(a, lo);
-      b = with_sign_of(b, hi);
     } else {
-      a = __fdiv_rn(lo, s[2 * j]);
-      b = __fdiv_rn(hi, s[2 * j + 1]);
+      a = __fdiv_rn(lo, s[j].x);
+      b = __fdiv_rn(hi, s[j].y);
     }
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[j]) : "f"(b), "f"(a));
   }
-  return make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+  uint2 c = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+  if (FAST) {  // bytes 1 and 3 of two input words hold four signs
+    c.x = (c.x & 0x7F7F7F7Fu) | (__byte_perm(u[0], u[1], 0x7531) & 0x80808080u);
+    c.y = (c.y & 0x7F7F7F7Fu) | (__byte_perm(u[2], u[3], 0x7531) & 0x80808080u);
+  }
+  return c;
+}
+
+DEVI uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Columns c0 .. c3 of four rows' code words (byte = column) as words (byte = row).
+DEVI void transpose4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_t (&c)[4]) {
+  const uint32_t t0 = __byte_perm(r0, r1, 0x5140), t1 = __byte_perm(r2, r3, 0x5140);
+  const uint32_t t2 = __byte_perm(r0, r1, 0x7362), t3 = __byte_perm(r2, r3, 0x7362);
+  c[0] = __byte_perm(t0, t1, 0x5410);
+  c[1] = __byte_perm(t0, t1, 0x7632);
+  c[2] = __byte_perm(t2, t3, 0x5410);
+  c[3] = __byte_perm(t2, t3, 0x7632);
 }
 
 DEVI float fp8_block_scale(float amax) { return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f); }
@@ -50,139 +71,132 @@ DEVI bool fp8_fast(float s) { return s >= 8.077935669463161e-28f && s <= 1e30f; 
 // One CTA = one 128 x 128 tile of x; thread (ty, tx) holds rows ty*8 .. +7, columns tx*8 .. +7
 // (eight 16-byte loads in flight, a warp reads two 256-byte runs per load).
 //   SQUARE: one scale for the tile, otherwise one for each row (q) and each column (qt).
+// A row's maximum meets in its 16 lanes by recursive halving (each lane ends with the row tx / 2),
+// so that a warp computes its 16 rows' scales (an IEEE division and a reciprocal, ~40 instructions)
+// once, not once per row; the tile's 128 column scales are computed by one thread each.
 // qt goes through shared memory as bytes [column][row]; rows >= M and columns >= K read as 0, so
 // the padding columns of qt (up to the next multiple of 16 rows) are written 0.
 template <bool SQUARE, bool TRANSPOSED>
 __global__ void __launch_bounds__(kFp8QuantThreads) k_fp8_quantize(const Fp8QuantArgs a) {
   __shared__ __align__(16) uint8_t tile[TRANSPOSED ? 128 * 128 : 16];
-  __shared__ __align__(16) uint32_t colmax[8][64];  // per warp: |x| maxima of column pairs
-  __shared__ float rowscale[128];
+  __shared__ __align__(16) uint32_t colmax[TRANSPOSED || SQUARE ? 8 : 1][64];  // per warp: |x| maxima of column pairs
+  __shared__ __align__(16) float colscale[2][TRANSPOSED && !SQUARE ? 128 : 1];  // scale, reciprocal
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const int kbs = static_cast<int>((a.K + 127) / 128);
   const int64_t mb = blockIdx.x / kbs;
   const int kb = static_cast<int>(blockIdx.x % kbs);
   const int64_t m0 = mb * 128, k0 = static_cast<int64_t>(kb) * 128;
   const int64_t col = k0 + tx * 8;
+  const bool col_ok = col < a.K;  // K is a multiple of 16: a group of 8 columns is whole
   uint4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = m0 + ty * 8 + i;
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < a.M && col < a.K) {  // K is a multiple of 16: a group of 8 columns is whole
+    if (r < a.M && col_ok) {
       int64_t src = r;
       if (a.row_token) src = __ldg(a.row_token + r);
       if (src >= 0 && src < a.M_x) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + src * a.K + col));
     }
   }
-  float rs[8];  // SQUARE: the tile's scale in rs[0]
-  uint32_t cm[4] = {0u, 0u, 0u, 0u};
+  uint32_t rm[8], cm[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t u[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu};
-    uint32_t m2 = u[0];
-#pragma unroll
-    for (int j = 1; j < 4; ++j) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(u[j]));
+    rm[i] = max_bf16x2(max_bf16x2(u[0], u[1]), max_bf16x2(u[2], u[3]));
     if (TRANSPOSED || SQUARE) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) asm("max.bf16x2 %0, %0, %1;" : "+r"(cm[j]) : "r"(u[j]));
-    }
-    if (!SQUARE) {
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        const uint32_t w = __shfl_xor_sync(0xffffffffu, m2, o);
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w));
-      }
-      rs[i] = fp8_block_scale(fmaxf(bf16lo(m2), bf16hi(m2)));
-      if (tx == 0) rowscale[ty * 8 + i] = rs[i];
+      for (int j = 0; j < 4; ++j) cm[j] = max_bf16x2(cm[j], u[j]);
     }
   }
-  float cs[8];
+  float rs = 1.0f;  // SQUARE: the tile's scale, otherwise that of row ty*8 + tx/2
+  if (!SQUARE) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {  // lanes 2 o apart exchange the halves of their rows
+      const bool up = (tx & (2 * o)) != 0;
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        const uint32_t give = up ? rm[i] : rm[i + o], keep = up ? rm[i + o] : rm[i];
+        rm[i] = max_bf16x2(keep, __shfl_xor_sync(0xffffffffu, give, 2 * o));
+      }
+    }
+    rm[0] = max_bf16x2(rm[0], __shfl_xor_sync(0xffffffffu, rm[0], 1));
+    rs = fp8_block_scale(fmaxf(bf16lo(rm[0]), bf16hi(rm[0])));
+    const int64_t r = m0 + ty * 8 + (tx >> 1);
+    if (a.q && (tx & 1) == 0 && r < a.M) a.s[static_cast<int64_t>(kb) * a.M + r] = rs;
+  }
   if (TRANSPOSED || SQUARE) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = __shfl_xor_sync(0xffffffffu, cm[j], 16);
-      asm("max.bf16x2 %0, %0, %1;" : "+r"(cm[j]) : "r"(w));
-    }
+    for (int j = 0; j < 4; ++j) cm[j] = max_bf16x2(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
     if (lane < 16) *reinterpret_cast<uint4*>(&colmax[warp][tx * 4]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+    __syncthreads();
   }
-  __syncthreads();
   if (SQUARE) {
     uint32_t m2 = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(colmax[w][lane]));
-      asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(colmax[w][lane + 32]));
-    }
+    for (int w = 0; w < 8; ++w) m2 = max_bf16x2(m2, max_bf16x2(colmax[w][lane], colmax[w][lane + 32]));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint32_t w = __shfl_xor_sync(0xffffffffu, m2, o);
-      asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w));
-    }
-    rs[0] = fp8_block_scale(fmaxf(bf16lo(m2), bf16hi(m2)));
+    for (int o = 16; o > 0; o >>= 1) m2 = max_bf16x2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    rs = fp8_block_scale(fmaxf(bf16lo(m2), bf16hi(m2)));
     if (tid == 0) {
       const int64_t mbs = (a.M + 127) / 128;
-      if (a.q) a.s[mb * kbs + kb] = rs[0];
-      if (TRANSPOSED) a.st[kb * mbs + mb] = rs[0];
+      if (a.q) a.s[mb * kbs + kb] = rs;
+      if (TRANSPOSED) a.st[kb * mbs + mb] = rs;
     }
-  } else {
-    if (a.q && tid < 128 && m0 + tid < a.M) a.s[static_cast<int64_t>(kb) * a.M + m0 + tid] = rowscale[tid];
-    if (TRANSPOSED) {
-      uint32_t m2[4] = {0u, 0u, 0u, 0u};
+  } else if (TRANSPOSED) {
+    if (tid < 64) {  // column pair tid
+      uint32_t m2 = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const uint4 c = *reinterpret_cast<const uint4*>(&colmax[w][tx * 4]);
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m2[0]) : "r"(c.x));
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m2[1]) : "r"(c.y));
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m2[2]) : "r"(c.z));
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m2[3]) : "r"(c.w));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cs[2 * j] = fp8_block_scale(bf16lo(m2[j]));
-        cs[2 * j + 1] = fp8_block_scale(bf16hi(m2[j]));
-      }
-      if (ty == 0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < a.K) a.st[mb * a.K + col + j] = cs[j];
-      }
+      for (int w = 0; w < 8; ++w) m2 = max_bf16x2(m2, colmax[w][tid]);
+      const float s0 = fp8_block_scale(bf16lo(m2)), s1 = fp8_block_scale(bf16hi(m2));
+      *reinterpret_cast<float2*>(&colscale[0][2 * tid]) = make_float2(s0, s1);
+      *reinterpret_cast<float2*>(&colscale[1][2 * tid]) = make_float2(__frcp_rn(s0), __frcp_rn(s1));
+      if (k0 + 2 * tid < a.K) *reinterpret_cast<float2*>(a.st + mb * a.K + k0 + 2 * tid) = make_float2(s0, s1);
     }
+    __syncthreads();
   }
   uint2 codes[8];
   if (a.q || SQUARE) {
+    const float ry = __frcp_rn(rs);
+    const bool fast = __all_sync(0xffffffffu, fp8_fast(rs));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = SQUARE ? rs[0] : rs[i];
-      const float y = __frcp_rn(s);
-      const float ss[8] = {s, s, s, s, s, s, s, s}, yy[8] = {y, y, y, y, y, y, y, y};
-      codes[i] = e4m3_codes8(v[i], ss, yy, fp8_fast(s));
+      const float s = SQUARE ? rs : __shfl_sync(0xffffffffu, rs, (lane & 16) + 2 * i);
+      const float y = SQUARE ? ry : __shfl_sync(0xffffffffu, ry, (lane & 16) + 2 * i);
+      const float2 ss[4] = {{s, s}, {s, s}, {s, s}, {s, s}}, yy[4] = {{y, y}, {y, y}, {y, y}, {y, y}};
+      codes[i] = fast ? e4m3_codes8<true>(v[i], ss, yy) : e4m3_codes8<false>(v[i], ss, yy);
       const int64_t r = m0 + ty * 8 + i;
-      if (a.q && r < a.M && col < a.K) *reinterpret_cast<uint2*>(a.q + r * a.K + col) = codes[i];
+      if (a.q && r < a.M && col_ok) *reinterpret_cast<uint2*>(a.q + r * a.K + col) = codes[i];
     }
   }
   if (TRANSPOSED) {
     if (!SQUARE) {
-      float y[8];
+      float2 cs[4], cy[4];
       bool fast = true;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = __frcp_rn(cs[j]);
-        fast = fast && fp8_fast(cs[j]);
+      for (int j = 0; j < 4; j += 2) {
+        const float4 s4 = *reinterpret_cast<const float4*>(&colscale[0][tx * 8 + 2 * j]);
+        const float4 y4 = *reinterpret_cast<const float4*>(&colscale[1][tx * 8 + 2 * j]);
+        cs[j] = make_float2(s4.x, s4.y), cs[j + 1] = make_float2(s4.z, s4.w);
+        cy[j] = make_float2(y4.x, y4.y), cy[j + 1] = make_float2(y4.z, y4.w);
+        fast = fast && fp8_fast(s4.x) && fp8_fast(s4.y) && fp8_fast(s4.z) && fp8_fast(s4.w);
       }
+      fast = __all_sync(0xffffffffu, fast);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) codes[i] = e4m3_codes8(v[i], cs, y, fast);
+      for (int i = 0; i < 8; ++i) codes[i] = fast ? e4m3_codes8<true>(v[i], cs, cy) : e4m3_codes8<false>(v[i], cs, cy);
     }
     // 8 x 8 byte transpose: column tx*8 + j gets rows ty*8 .. +7 as one 8-byte unit, unit ty
     // stored at ty ^ tx so that a warp's 32 units of one j cover all banks
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t w[2] = {0u, 0u};
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[8], top[4], bot[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t half = j < 4 ? codes[i].x : codes[i].y;
-        w[i >> 2] |= ((half >> (8 * (j & 3))) & 0xFFu) << (8 * (i & 3));
-      }
-      *reinterpret_cast<uint2*>(tile + (tx * 8 + j) * 128 + ((ty ^ tx) << 3)) = make_uint2(w[0], w[1]);
+      for (int i = 0; i < 8; ++i) w[i] = h == 0 ? codes[i].x : codes[i].y;
+      transpose4(w[0], w[1], w[2], w[3], top);
+      transpose4(w[4], w[5], w[6], w[7], bot);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint2*>(tile + (tx * 8 + h * 4 + j) * 128 + ((ty ^ tx) << 3)) = make_uint2(top[j], bot[j]);
     }
     __syncthreads();
     const int64_t ldt = (a.M + 15) / 16 * 16;

@@ -161,7 +161,7 @@ struct RouteBwdArgs {
   const float* d_loss;    // [1] or null
   void* d_logits;         // [T, E], the logits' type
 };
-int route_blocks(int64_t T);
+int route_blocks(int64_t T, int E);
 cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches);
 cudaError_t launch_moe_route_bwd(RouteBwdArgs a, int sms, cudaStream_t st);
 

@@ -18,8 +18,8 @@
 
 namespace nvfp4 {
 
-constexpr int kRouteThreads = 256;
-constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kPlaceThreads = 256;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
 constexpr float kLog2E = 1.4426950408889634f;
 
 DEVI float ex2(float x) {
@@ -35,6 +35,9 @@ DEVI uint32_t order_key(float v) {
 }
 DEVI float key_value(uint32_t key) { return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu)); }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+
+// log2 of exp(v - max)
+DEVI float route_arg(float v, float mx) { return (v - mx) * kLog2E; }
 
 DEVI float warp_sum(float v) {
 #pragma unroll
@@ -89,25 +92,105 @@ DEVI void load_row(const void* logits, int64_t row, int E, bool vec, int lane, f
   }
 }
 
+// Warps per CTA of the routing kernels: 16, but 8 for more than 256 experts (registers, and the
+// per-warp sums of p in shared memory).
+template <int VPL>
+struct RouteCfg {
+  static constexpr int WARPS = VPL <= 8 ? 16 : 8;
+  static constexpr int THREADS = 32 * WARPS;
+};
+
+// The k largest of a warp's 32 * VPL keys (lane holds experts lane * VPL + j), in order, ties to
+// the lower expert: lane s < k returns slot s's expert (-1: none above -inf) and key.
+//
+// The k-th largest of the 32 lane maxima bounds the k-th largest key from below, so the selected
+// experts are among the few keys (typically k and one or two) that reach it. Those candidates are
+// compacted into `cand` and each counts the candidates that precede it, which is its slot: about
+// 150 instructions for 256 experts and k = 8, against 400 for k rounds of a maximum over all keys.
+// With more than 32 candidates (many equal logits) the rounds are run.
+template <int VPL>
+DEVI void warp_top_k(uint32_t (&key)[VPL], int k, uint64_t* cand, int& out_idx, uint32_t& out_key) {
+  const int lane = threadIdx.x & 31;
+  uint32_t lane_max = 0;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) lane_max = max(lane_max, key[j]);
+  uint32_t bound = 0, left = lane_max;
+  for (int s = 0; s < k; ++s) {  // equal maxima leave together: the bound is then lower, and still one
+    bound = __reduce_max_sync(0xffffffffu, left);
+    if (left == bound) left = 0;
+  }
+  bound = max(bound, kKeyNegInf + 1);
+  int n = 0;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const bool c = key[j] >= bound;
+    const uint32_t m = __ballot_sync(0xffffffffu, c);
+    const int at = n + __popc(m & below);
+    // the key in the high half, the complement of the expert in the low half: one comparison orders both
+    if (c && at < 32) cand[at] = static_cast<uint64_t>(key[j]) << 32 | static_cast<uint32_t>(~(lane * VPL + j));
+    n += __popc(m);
+  }
+  out_idx = -1;
+  out_key = 0;
+  __syncwarp();
+  if (n <= 32) {
+    const uint64_t mine = lane < n ? cand[lane] : 0;
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += cand[i] > mine;
+    __syncwarp();
+    if (lane < n) cand[rank] = mine;
+    __syncwarp();
+    if (lane < min(n, k)) {
+      out_key = static_cast<uint32_t>(cand[lane] >> 32);
+      out_idx = static_cast<int>(~static_cast<uint32_t>(cand[lane]));
+    }
+    __syncwarp();
+    return;
+  }
+  for (int s = 0; s < k; ++s) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
+    const uint32_t best = __reduce_max_sync(0xffffffffu, m);
+    if (best <= kKeyNegInf) break;
+    const int w = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
+    int at = -1;
+    if (lane == w) {
+#pragma unroll
+      for (int j = VPL - 1; j >= 0; --j)
+        if (key[j] == best) at = j;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (j == at) key[j] = 0;
+    }
+    at = __shfl_sync(0xffffffffu, at, w);
+    if (lane == s) {
+      out_idx = w * VPL + at;
+      out_key = best;
+    }
+  }
+}
+
 // The CTA's tokens [t0, t1): selection and weights to global memory; the per-expert
 // selection counts (and at [E] the routed tokens) to hist, the sums of p to psum (per-warp
-// slices, added in warp order). Ends with a CTA barrier.
+// slices, added in warp order). Ends with a CTA barrier. One warp per token.
 template <int VPL, bool BF16>
-DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, float* psum) {
+DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, float* psum, uint64_t* cand) {
+  constexpr int WARPS = RouteCfg<VPL>::WARPS, THREADS = RouteCfg<VPL>::THREADS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k;
-  for (int e = threadIdx.x; e <= E; e += kRouteThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e <= E; e += THREADS) hist[e] = 0;
   __syncthreads();
   float acc[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) acc[j] = 0.0f;
   int routed = 0;
-  for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) {
+  for (int64_t t = t0 + warp; t < t1; t += WARPS) {
     float v[VPL];
     uint32_t key[VPL];
-    const bool valid = !a.valid || __ldg(a.valid + t) != 0;
     uint32_t top = 0;  // largest key of the row
-    if (valid) {
+    if (!a.valid || __ldg(a.valid + t) != 0) {
       load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
       uint32_t m = 0;
 #pragma unroll
@@ -120,43 +203,19 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
     int my_idx = -1;
     float my_w = 0.0f;
     if (top > kKeyNegInf) {
-      const float mx = key_value(top);
-      float sum = 0.0f, e[VPL];
+      float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        e[j] = ex2((v[j] - mx) * kLog2E);
-        sum += e[j];
+        v[j] = ex2(route_arg(v[j], key_value(top)));
+        sum += v[j];
       }
-      sum = warp_sum(sum);
-      const float inv = __frcp_rn(sum);
+      const float inv = __frcp_rn(warp_sum(sum));
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) acc[j] += e[j] * inv;
+      for (int j = 0; j < VPL; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
       ++routed;
-      // k rounds: the largest remaining key; ties to the lowest lane, then the lowest j
-      uint32_t my_key = 0;
-      for (int s = 0; s < k; ++s) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
-        const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-        if (best <= kKeyNegInf) break;
-        const int w = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
-        int at = -1;
-        if (lane == w) {
-#pragma unroll
-          for (int j = VPL - 1; j >= 0; --j)
-            if (key[j] == best) at = j;
-#pragma unroll
-          for (int j = 0; j < VPL; ++j)
-            if (j == at) key[j] = 0;
-        }
-        at = __shfl_sync(0xffffffffu, at, w);
-        if (lane == s) {
-          my_idx = w * VPL + at;
-          my_key = best;
-        }
-      }
-      const float es = my_idx >= 0 ? ex2((key_value(my_key) - mx) * kLog2E) : 0.0f;
+      uint32_t my_key;
+      warp_top_k<VPL>(key, k, cand + warp * 32, my_idx, my_key);
+      const float es = my_idx >= 0 ? ex2(route_arg(key_value(my_key), key_value(top))) : 0.0f;
       my_w = a.renorm ? es / warp_sum(es) : es * inv;
       if (my_idx >= 0) atomicAdd(&hist[my_idx], 1);
     }
@@ -170,9 +229,9 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
   for (int j = 0; j < VPL; ++j)
     if (lane * VPL + j < E) psum[warp * E + lane * VPL + j] = acc[j];
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < E; e += THREADS) {
     float s = 0.0f;
-    for (int w = 0; w < kRouteWarps; ++w) s += psum[w * E + e];
+    for (int w = 0; w < WARPS; ++w) s += psum[w * E + e];
     psum[e] = s;
   }
   __syncthreads();
@@ -200,48 +259,51 @@ DEVI void scan_counts(const int32_t* counts, int E, int32_t* offs) {
 }
 
 // Rows of the CTA's tokens: base[e] (shared) is the first row of expert e that this CTA
-// fills. Each warp owns a contiguous range of the tokens: its selections per expert are
-// counted first, then every token's k slots take consecutive places (a token's experts
-// are distinct, so its lanes never meet). wcnt: [kRouteWarps][E] in shared memory.
+// fills. Each warp owns a contiguous range of the (token, slot) pairs: its selections per expert
+// are counted first, then 32 pairs at a time take their places: the pairs of one expert in the
+// step find one another (match), and count the ones before them. wcnt: [WARPS][E] in shared
+// memory.
+template <int WARPS>
 DEVI void place_rows(const RouteArgs& a, int64_t t0, int64_t t1, const int32_t* base, int32_t* wcnt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k;
-  for (int i = threadIdx.x; i < kRouteWarps * E; i += kRouteThreads) wcnt[i] = 0;
+  for (int i = threadIdx.x; i < WARPS * E; i += 32 * WARPS) wcnt[i] = 0;
   __syncthreads();
-  const int64_t per = (t1 - t0 + kRouteWarps - 1) / kRouteWarps;
-  const int64_t w0 = min(t1, t0 + warp * per), w1 = min(t1, w0 + per);
+  const int64_t per = ((t1 - t0) * k + WARPS - 1) / WARPS;
+  const int64_t p0 = min(t1 * k, t0 * k + warp * per), p1 = min(t1 * k, p0 + per);
   int32_t* mine = wcnt + warp * E;
-  for (int64_t i = w0 * k + lane; i < w1 * k; i += 32) {
+  for (int64_t i = p0 + lane; i < p1; i += 32) {
     const int e = a.topk_idx[i];
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < E; e += 32 * WARPS) {
     int s = base[e];
-    for (int w = 0; w < kRouteWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const int c = wcnt[w * E + e];
       wcnt[w * E + e] = s;
       s += c;
     }
   }
   __syncthreads();
-  for (int64_t t = w0; t < w1; ++t) {
-    if (lane < k) {
-      const int e = a.topk_idx[t * k + lane];
-      int row = -1;
-      if (e >= 0) {
-        row = mine[e]++;
-        a.row_token[row] = static_cast<int32_t>(t);
-      }
-      a.slot_row[t * k + lane] = row;
-    }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int64_t i0 = p0; i0 < p1; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const int e = i < p1 ? a.topk_idx[i] : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    int row = -1;
+    if (e >= 0) row = mine[e] + __popc(same & below);
     __syncwarp();
+    if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
+    __syncwarp();
+    if (e >= 0) a.row_token[row] = static_cast<int32_t>(i / k);
+    if (i < p1) a.slot_row[i] = row;
   }
 }
 
 // Writes what one CTA writes for all: offsets and the balance loss (n routed tokens).
 DEVI void finish_route(const RouteArgs& a, const int32_t* counts, const float* mean, int n, const int32_t* offs) {
-  for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) a.expert_offsets[e] = offs[e];
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_offsets[e] = offs[e];
   if (threadIdx.x < 32) {
     float s = 0.0f;
     for (int e = threadIdx.x; e < a.E; e += 32) s += static_cast<float>(counts[e]) * mean[e];
@@ -259,36 +321,46 @@ DEVI void route_chunk(const RouteArgs& a, int64_t& t0, int64_t& t1) {
 
 // Stage 1: every CTA routes its tokens; counts and sums of p per CTA to the workspace.
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kRouteThreads) k_moe_route(const RouteArgs a) {
-  extern __shared__ int32_t sh[];
-  int32_t* hist = sh;
-  float* psum = reinterpret_cast<float*>(sh + a.E + 1);
+__global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route(const RouteArgs a) {
+  extern __shared__ __align__(16) uint64_t sh64[];
+  uint64_t* cand = sh64;  // [WARPS][32]
+  int32_t* hist = reinterpret_cast<int32_t*>(cand + RouteCfg<VPL>::WARPS * 32);  // [E + 1]
+  float* psum = reinterpret_cast<float*>(hist + a.E + 1);                          // [WARPS][E]
+  griddep_launch_dependents();
   int64_t t0, t1;
   route_chunk(a, t0, t1);
-  route_rows<VPL, BF16>(a, t0, t1, hist, psum);
-  for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
+  route_rows<VPL, BF16>(a, t0, t1, hist, psum, cand);
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x)
     a.ws_hist[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + e] = hist[e];
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.ws_psum[static_cast<int64_t>(blockIdx.x) * a.E + e] = psum[e];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.ws_psum[static_cast<int64_t>(blockIdx.x) * a.E + e] = psum[e];
 }
 
 // Stage 2: one CTA per 32 experts. ws_hist becomes each CTA's exclusive prefix; totals to
-// counts, means of p to mean_prob. Warps own contiguous runs of the `blocks` rows.
-__global__ void __launch_bounds__(kRouteThreads) k_moe_scan(const RouteArgs a, int blocks) {
-  __shared__ int32_t part[kRouteWarps][32];
-  __shared__ float fpart[kRouteWarps][32];
-  __shared__ int32_t npart[kRouteWarps];
+// counts, means of p to mean_prob. Warps own contiguous runs of the `blocks` rows (at most
+// kScanRun each, all loaded at once). Reads what stage 1 wrote, which may still run when this kernel
+// starts: plain loads behind the dependency wait.
+constexpr int kScanWarps = 32;
+constexpr int kScanRun = (kRouteBlocks + kScanWarps - 1) / kScanWarps;
+__global__ void __launch_bounds__(kScanWarps * 32) k_moe_scan(const RouteArgs a, int blocks) {
+  __shared__ int32_t part[kScanWarps][32];
+  __shared__ float fpart[kScanWarps][32];
+  __shared__ int32_t npart[kScanWarps];
+  griddep_wait();
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, e = blockIdx.x * 32 + lane;
-  const int per = (blocks + kRouteWarps - 1) / kRouteWarps;
+  const int per = (blocks + kScanWarps - 1) / kScanWarps;
   const int b0 = min(blocks, warp * per), b1 = min(blocks, b0 + per);
-  int c = 0, n = 0;
+  int32_t h[kScanRun];
   float s = 0.0f;
-  if (e < E)
-    for (int b = b0; b < b1; ++b) {
-      c += a.ws_hist[static_cast<int64_t>(b) * (E + 1) + e];
-      s += a.ws_psum[static_cast<int64_t>(b) * E + e];
-    }
-  for (int b = b0 + lane; b < b1; b += 32) n += a.ws_hist[static_cast<int64_t>(b) * (E + 1) + E];
+  int c = 0, n = 0;
+#pragma unroll
+  for (int i = 0; i < kScanRun; ++i) {
+    h[i] = (e < E && b0 + i < b1) ? a.ws_hist[static_cast<int64_t>(b0 + i) * (E + 1) + e] : 0;
+    if (e < E && b0 + i < b1) s += a.ws_psum[static_cast<int64_t>(b0 + i) * E + e];
+    c += h[i];
+  }
+  if (b0 + lane < b1) n = a.ws_hist[static_cast<int64_t>(b0 + lane) * (E + 1) + E];
   n = __reduce_add_sync(0xffffffffu, n);
   part[warp][lane] = c;
   fpart[warp][lane] = s;
@@ -297,19 +369,20 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_scan(const RouteArgs a, i
   int before = 0, total = 0;
   n = 0;
   s = 0.0f;
-  for (int w = 0; w < kRouteWarps; ++w) {
-    if (w < warp) before += part[w][lane];
-    total += part[w][lane];
+  for (int w = 0; w < kScanWarps; ++w) {
+    const int v = part[w][lane];
+    if (w < warp) before += v;
+    total += v;
     s += fpart[w][lane];
     n += npart[w];
   }
   if (e < E) {
-    for (int b = b0; b < b1; ++b) {
-      int32_t* h = a.ws_hist + static_cast<int64_t>(b) * (E + 1) + e;
-      const int v = *h;
-      *h = before;
-      before += v;
-    }
+#pragma unroll
+    for (int i = 0; i < kScanRun; ++i)
+      if (b0 + i < b1) {
+        a.ws_hist[static_cast<int64_t>(b0 + i) * (E + 1) + e] = before;
+        before += h[i];
+      }
     if (warp == 0) {
       a.counts[e] = total;
       a.mean_prob[e] = n > 0 ? s / static_cast<float>(n) : 0.0f;
@@ -319,35 +392,38 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_scan(const RouteArgs a, i
 }
 
 // Stage 3: every CTA places its tokens' rows.
-__global__ void __launch_bounds__(kRouteThreads) k_moe_place(const RouteArgs a) {
+__global__ void __launch_bounds__(kPlaceThreads) k_moe_place(const RouteArgs a) {
   extern __shared__ int32_t sh[];
   int32_t* offs = sh;                // [E + 1]
   int32_t* base = offs + a.E + 1;    // [E]
-  int32_t* wcnt = base + a.E;        // [kRouteWarps][E]
+  int32_t* wcnt = base + a.E;        // [kPlaceWarps][E]
+  griddep_wait();
   scan_counts(a.counts, a.E, offs);
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
+  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads)
     base[e] = offs[e] + a.ws_hist[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + e];
   int64_t t0, t1;
   route_chunk(a, t0, t1);
-  place_rows(a, t0, t1, base, wcnt);
+  place_rows<kPlaceWarps>(a, t0, t1, base, wcnt);
   // rows that no selection fills
-  for (int64_t r = offs[a.E] + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x; r < a.T * a.k;
-       r += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+  for (int64_t r = offs[a.E] + static_cast<int64_t>(blockIdx.x) * kPlaceThreads + threadIdx.x; r < a.T * a.k;
+       r += static_cast<int64_t>(gridDim.x) * kPlaceThreads)
     a.row_token[r] = -1;
   if (blockIdx.x == 0) finish_route(a, a.counts, a.mean_prob, a.routed_tokens[0], offs);
 }
 
 // All stages in one CTA, for few tokens: no workspace, one launch.
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kRouteThreads) k_moe_route_one(const RouteArgs a) {
-  extern __shared__ int32_t sh[];
-  int32_t* hist = sh;                                       // [E + 1]
-  int32_t* offs = hist + a.E + 1;                           // [E + 1]
-  float* psum = reinterpret_cast<float*>(offs + a.E + 1);   // [kRouteWarps][E], then the means
-  route_rows<VPL, BF16>(a, 0, a.T, hist, psum);
+__global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route_one(const RouteArgs a) {
+  constexpr int WARPS = RouteCfg<VPL>::WARPS;
+  extern __shared__ __align__(16) uint64_t sh64[];
+  uint64_t* cand = sh64;                                      // [WARPS][32]
+  int32_t* hist = reinterpret_cast<int32_t*>(cand + WARPS * 32);  // [E + 1]
+  int32_t* offs = hist + a.E + 1;                             // [E + 1]
+  float* psum = reinterpret_cast<float*>(offs + a.E + 1);     // [WARPS][E], then the means
+  route_rows<VPL, BF16>(a, 0, a.T, hist, psum, cand);
   scan_counts(hist, a.E, offs);
   const int n = hist[a.E];
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     psum[e] = n > 0 ? psum[e] / static_cast<float>(n) : 0.0f;
     a.mean_prob[e] = psum[e];
     a.counts[e] = hist[e];
@@ -355,9 +431,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_one(const RouteArgs
   if (threadIdx.x == 0) a.routed_tokens[0] = n;
   __syncthreads();
   finish_route(a, hist, psum, n, offs);
-  for (int64_t r = offs[a.E] + threadIdx.x; r < a.T * a.k; r += kRouteThreads) a.row_token[r] = -1;
+  for (int64_t r = offs[a.E] + threadIdx.x; r < a.T * a.k; r += blockDim.x) a.row_token[r] = -1;
   __syncthreads();  // psum's memory is reused
-  place_rows(a, 0, a.T, offs, reinterpret_cast<int32_t*>(psum));
+  place_rows<WARPS>(a, 0, a.T, offs, reinterpret_cast<int32_t*>(psum));
 }
 
 // ---- gradient of the logits ------------------------------------------------------------------
@@ -366,8 +442,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_one(const RouteArgs
 // the selected experts when the weights are plain; d l_te = p_te (G_te - sum_i p_ti G_ti).
 // Renormalised weights are a softmax over the selected logits alone: they add
 // w_s (dw_s - sum_r w_r dw_r) at expert idx_s instead. Unrouted tokens get zeros.
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kRouteThreads) k_moe_route_bwd(const RouteBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) k_moe_route_bwd(const RouteBwdArgs a) {
   extern __shared__ float shf[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k;
@@ -383,8 +461,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_bwd(const RouteBwdA
     const int e = lane * VPL + j;
     g[j] = e < E ? scale * static_cast<float>(__ldg(a.counts + e)) : 0.0f;
   }
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kBwdWarps + warp; t < a.T;
+       t += static_cast<int64_t>(gridDim.x) * kBwdWarps) {
     float v[VPL], d[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
@@ -507,42 +585,60 @@ static bool route_vec(const void* p, int E, int bf16) {
     default: call(32, true); break;                               \
   }
 
-// Tokens up to which one CTA does all the stages in one launch.
-constexpr int kRouteOneTokens = 64;
+// Tokens up to which one CTA does all the stages in one launch: two tokens a warp (32 tokens of 256
+// experts: see the figures at the launcher).
+constexpr int kRouteOneTokens = 32;
 
-int route_blocks(int64_t T) {
-  const int64_t b = (T + kRouteWarps - 1) / kRouteWarps;
+static int route_warps(int E) { return route_vpl(E) <= 8 ? 16 : 8; }
+
+int route_blocks(int64_t T, int E) {
+  const int64_t b = (T + route_warps(E) - 1) / route_warps(E);
   return static_cast<int>(b < kRouteBlocks ? b : kRouteBlocks);
 }
 
 cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches) {
   a.vec = route_vec(a.logits, a.E, a.bf16);
-  const int E = a.E;
+  const int E = a.E, warps = route_warps(E), threads = 32 * warps;
   if (a.T <= kRouteOneTokens) {
-    const int smem = (2 * (E + 1) + kRouteWarps * E) * 4;
+    const int smem = warps * 256 + (2 * (E + 1) + warps * E) * 4;
     *launches = 1;
-#define CALL(V, B) k_moe_route_one<V, B><<<1, kRouteThreads, smem, st>>>(a)
+#define CALL(V, B) k_moe_route_one<V, B><<<1, threads, smem, st>>>(a)
     ROUTE_DISPATCH(CALL)
 #undef CALL
     return cudaGetLastError();
   }
-  const int blocks = route_blocks(a.T);
-  const int smem = (E + 1 + kRouteWarps * E) * 4;
+  const int blocks = route_blocks(a.T, E);
+  const int smem = warps * 256 + (E + 1 + warps * E) * 4;
   *launches = 3;
-#define CALL(V, B) k_moe_route<V, B><<<blocks, kRouteThreads, smem, st>>>(a)
+#define CALL(V, B) k_moe_route<V, B><<<blocks, threads, smem, st>>>(a)
   ROUTE_DISPATCH(CALL)
 #undef CALL
-  k_moe_scan<<<(E + 31) / 32, kRouteThreads, 0, st>>>(a, blocks);
-  k_moe_place<<<blocks, kRouteThreads, (2 * E + 1 + kRouteWarps * E) * 4, st>>>(a);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the later stages' launches overlap the stage before; each waits for it before reading
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((E + 31) / 32);
+  cfg.blockDim = dim3(kScanWarps * 32);
+  e = cudaLaunchKernelEx(&cfg, k_moe_scan, a, blocks);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kPlaceThreads);
+  cfg.dynamicSmemBytes = (2 * E + 1 + kPlaceWarps * E) * 4;
+  return cudaLaunchKernelEx(&cfg, k_moe_place, a);
 }
 
 cudaError_t launch_moe_route_bwd(RouteBwdArgs a, int sms, cudaStream_t st) {
   a.vec = route_vec(a.logits, a.E, a.bf16) && route_vec(a.d_logits, a.E, a.bf16);
-  const int64_t want = (a.T + kRouteWarps - 1) / kRouteWarps;
+  const int64_t want = (a.T + kBwdWarps - 1) / kBwdWarps;
   const int grid = static_cast<int>(want < 8 * sms ? want : 8 * sms);
-  const int smem = kRouteWarps * 32 * route_vpl(a.E) * 4;
-#define CALL(V, B) k_moe_route_bwd<V, B><<<grid, kRouteThreads, smem, st>>>(a)
+  const int smem = kBwdWarps * 32 * route_vpl(a.E) * 4;
+#define CALL(V, B) k_moe_route_bwd<V, B><<<grid, kBwdThreads, smem, st>>>(a)
   ROUTE_DISPATCH(CALL)
 #undef CALL
   return cudaGetLastError();

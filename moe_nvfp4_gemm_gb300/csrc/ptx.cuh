@@ -86,6 +86,18 @@ DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uin
   }
 }
 
+// Warp-collective wait for hand-offs that normally complete within a microsecond: a short uniform
+// loop (one try_wait and one vote when the phase is already complete), the clock not read before
+// 128 failed polls, since its read alone costs the warp several hundred cycles.
+DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns);
+DEVI bool mbar_poll_warp(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 128; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
+}
+
 // Warp-collective wait: every lane polls, the result is the same in all lanes.
 DEVI bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
