@@ -151,8 +151,10 @@ def _ptr(t):  # an int: every entry point's argtypes convert it to the pointer
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without the Stream object (3 us of a small call's host time)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(fn, rc):
@@ -493,20 +495,30 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
     """Softmax router: top-k experts and weights of each token, per-expert counts and offsets, the
     expert-sorted row lists that the grouped GEMMs read, and the load-balance loss."""
     T, E = _route_inputs(logits, valid)
-    dev = logits.device
     n = T * max(k, 0)
-    ints = torch.empty(3 * n + 2 * E + 2, dtype=torch.int32, device=dev)
-    idx, slot_row, row_token, counts, offsets, routed = ints.split([n, n, n, E, E + 1, 1])
-    floats = torch.empty(n + E + 1, dtype=torch.float32, device=dev)
-    w, mean, loss = floats.split([n, E, 1])
-    if workspace is None:
-        workspace = torch.empty(nvfp4_moe_route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+    ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
+    # one allocation: the outputs as consecutive 4-byte words, then the workspace
+    at_w, at_slot, at_row = n, 2 * n, 3 * n
+    at_counts = 4 * n
+    at_off = at_counts + E
+    at_mean = at_off + E + 1
+    at_loss = at_mean + E
+    at_routed = at_loss + 1
+    at_ws = (at_routed + 1 + 3) // 4 * 4
+    buf = torch.empty(at_ws + (ws_bytes // 4 if workspace is None else 0), dtype=torch.int32, device=logits.device)
+    p = buf.data_ptr()
+    ws = p + 4 * at_ws if workspace is None else workspace.data_ptr()
     _check("nvfp4_moe_route",
-           lib().nvfp4_moe_route(_ptr(logits), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
-                                 _ptr(idx), _ptr(w), _ptr(slot_row), _ptr(counts), _ptr(offsets), _ptr(row_token),
-                                 _ptr(mean), _ptr(loss), _ptr(routed), _ptr(workspace), workspace.numel(),
-                                 _stream(stream)))
-    return MoeRouting(idx.view(T, k), w.view(T, k), slot_row.view(T, k), counts, offsets, row_token, mean, loss, routed)
+           lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
+                                 p, p + 4 * at_w, p + 4 * at_slot, p + 4 * at_counts, p + 4 * at_off, p + 4 * at_row,
+                                 p + 4 * at_mean, p + 4 * at_loss, p + 4 * at_routed, ws,
+                                 ws_bytes if workspace is None else workspace.numel(), _stream(stream)))
+    real = buf.view(torch.float32)
+    per, row = (T, k), (k, 1)
+    return MoeRouting(buf.as_strided(per, row, 0), real.as_strided(per, row, at_w), buf.as_strided(per, row, at_slot),
+                      buf.as_strided((E,), (1,), at_counts), buf.as_strided((E + 1,), (1,), at_off),
+                      buf.as_strided((n,), (1,), at_row), real.as_strided((E,), (1,), at_mean),
+                      real.as_strided((1,), (1,), at_loss), buf.as_strided((1,), (1,), at_routed))
 
 
 def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None, d_loss=None,
