@@ -15,36 +15,49 @@ namespace nvfp4 {
 
 constexpr int kFp8QuantThreads = 256;  // 16 groups of 8 rows x 16 groups of 8 columns
 
-// Eight E4M3 codes of v / s (element j in byte j): element pair j divided by (s.x, s.y)[j], for
-// y = RN(1 / s). FAST: x / s correctly rounded by the two fma corrections of div_rn_by, two
-// elements at a time (they lose the sign of a zero, so the signs are put back on the codes).
+// 1 / s as an unevaluated sum hi + lo, hi rounded down and lo >= 0 the rounded rest (its remainder
+// 1 - s hi is exact): hi + lo is within 2^-46 of 1 / s.
+struct Reciprocal {
+  float hi, lo;
+};
+DEVI Reciprocal fp8_reciprocal(float s) {
+  Reciprocal y;
+  y.hi = __frcp_rd(s);
+  y.lo = __fmul_rn(__fmaf_rn(-s, y.hi, 1.0f), y.hi);
+  return y;
+}
+
+// Eight E4M3 codes of v / s (element j in byte j), element pair j divided by s[j] (two scales).
+// FAST: RN(x hi + RN(x lo)) is RN(x / s) for a bf16 x and s = RN(amax / 448) of a bf16 amax >= |x|:
+// the sum is within 2^-46 of x / s, and no such quotient lies that close to the middle of two
+// floats without being rounded alike (checked for all pairs of significands and all exponents that
+// reach a code). x lo has x's sign, so that a zero keeps its own.
 template <bool FAST>
-DEVI uint2 e4m3_codes8(const uint4& w, const float2 (&s)[4], const float2 (&y)[4]) {
+DEVI uint2 e4m3_codes8(const uint4& w, const float2 (&s)[4], const float2 (&hi)[4], const float2 (&lo)[4]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint16_t h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float lo = bf16lo(u[j]), hi = bf16hi(u[j]);
+    const float xl = bf16lo(u[j]), xh = bf16hi(u[j]);
     float a, b;
     if (FAST) {
-      const uint64_t xx = f2(lo, hi), yy = f2(y[j].x, y[j].y), nd = f2(-s[j].x, -s[j].y);
-      const uint64_t q0 = f2_mul(xx, yy);
-      const uint64_t q1 = f2_fma(f2_fma(q0, nd, xx), yy, q0);
-      f2_split(f2_fma(f2_fma(q1, nd, xx), yy, q1), a, b);
+      const uint64_t xx = f2(xl, xh);
+      f2_split(f2_fma(xx, f2(hi[j].x, hi[j].y), f2_mul(xx, f2(lo[j].x, lo[j].y))), a, b);
     } else {
-      a = __fdiv_rn(lo, s[j].x);
-      b = __fdiv_rn(hi, s[j].y);
+      a = __fdiv_rn(xl, s[j].x);
+      b = __fdiv_rn(xh, s[j].y);
     }
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[j]) : "f"(b), "f"(a));
   }
-  uint2 c = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
-  if (FAST) {  // bytes 1 and 3 of two input words hold four signs
-    c.x = (c.x & 0x7F7F7F7Fu) | (__byte_perm(u[0], u[1], 0x7531) & 0x80808080u);
-    c.y = (c.y & 0x7F7F7F7Fu) | (__byte_perm(u[2], u[3], 0x7531) & 0x80808080u);
-  }
-  return c;
+  return make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
 }
 
+// max(|a|, |b|) of two bf16 pairs; the sign bits of the result are to be ignored.
+DEVI uint32_t maxabs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 DEVI uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -63,10 +76,9 @@ DEVI void transpose4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_
 
 DEVI float fp8_block_scale(float amax) { return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f); }
 
-// Where the corrections are exact or cannot change a code: with 2^-90 <= s <= 1e30, an element
-// of magnitude >= 2^-102 has an exact remainder (see div_rn_by), and a smaller one a quotient
-// below 2^-12, less than half the smallest code's 2^-9: its code is 0 (with x's sign) either way.
-DEVI bool fp8_fast(float s) { return s >= 8.077935669463161e-28f && s <= 1e30f; }
+// Scales for which the two-part reciprocal holds: hi, lo, the products that matter (quotients from
+// 2^-11 on) and lo's remainder all stay clear of underflow; smaller quotients have code 0 anyway.
+DEVI bool fp8_fast(float s) { return s >= 8.077935669463161e-28f && s <= 1.8446744073709552e19f; }  // 2^-90, 2^64
 
 // One CTA = one 128 x 128 tile of x; thread (ty, tx) holds rows ty*8 .. +7, columns tx*8 .. +7
 // (eight 16-byte loads in flight, a warp reads two 256-byte runs per load).
@@ -77,10 +89,10 @@ DEVI bool fp8_fast(float s) { return s >= 8.077935669463161e-28f && s <= 1e30f; 
 // qt goes through shared memory as bytes [column][row]; rows >= M and columns >= K read as 0, so
 // the padding columns of qt (up to the next multiple of 16 rows) are written 0.
 template <bool SQUARE, bool TRANSPOSED>
-__global__ void __launch_bounds__(kFp8QuantThreads) k_fp8_quantize(const Fp8QuantArgs a) {
+__global__ void __launch_bounds__(kFp8QuantThreads, TRANSPOSED ? 4 : 5) k_fp8_quantize(const Fp8QuantArgs a) {
   __shared__ __align__(16) uint8_t tile[TRANSPOSED ? 128 * 128 : 16];
   __shared__ __align__(16) uint32_t colmax[TRANSPOSED || SQUARE ? 8 : 1][64];  // per warp: |x| maxima of column pairs
-  __shared__ __align__(16) float colscale[2][TRANSPOSED && !SQUARE ? 128 : 1];  // scale, reciprocal
+  __shared__ __align__(16) float colscale[3][TRANSPOSED && !SQUARE ? 128 : 1];  // scale, its reciprocal's parts
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const int kbs = static_cast<int>((a.K + 127) / 128);
   const int64_t mb = blockIdx.x / kbs;
@@ -99,14 +111,14 @@ __global__ void __launch_bounds__(kFp8QuantThreads) k_fp8_quantize(const Fp8Quan
       if (src >= 0 && src < a.M_x) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + src * a.K + col));
     }
   }
-  uint32_t rm[8], cm[4] = {0u, 0u, 0u, 0u};
+  uint32_t rm[8], cm[4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t u[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu};
-    rm[i] = max_bf16x2(max_bf16x2(u[0], u[1]), max_bf16x2(u[2], u[3]));
+    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    rm[i] = maxabs_bf16x2(maxabs_bf16x2(u[0], u[1]), maxabs_bf16x2(u[2], u[3])) & 0x7FFF7FFFu;
     if (TRANSPOSED || SQUARE) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cm[j] = max_bf16x2(cm[j], u[j]);
+      for (int j = 0; j < 4; ++j) cm[j] = i == 0 ? u[j] : maxabs_bf16x2(cm[j], u[j]);
     }
   }
   float rs = 1.0f;  // SQUARE: the tile's scale, otherwise that of row ty*8 + tx/2
@@ -127,7 +139,8 @@ __global__ void __launch_bounds__(kFp8QuantThreads) k_fp8_quantize(const Fp8Quan
   }
   if (TRANSPOSED || SQUARE) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cm[j] = max_bf16x2(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+    for (int j = 0; j < 4; ++j)
+      cm[j] = maxabs_bf16x2(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16)) & 0x7FFF7FFFu;
     if (lane < 16) *reinterpret_cast<uint4*>(&colmax[warp][tx * 4]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
     __syncthreads();
   }
@@ -150,40 +163,48 @@ __global__ void __launch_bounds__(kFp8QuantThreads) k_fp8_quantize(const Fp8Quan
       for (int w = 0; w < 8; ++w) m2 = max_bf16x2(m2, colmax[w][tid]);
       const float s0 = fp8_block_scale(bf16lo(m2)), s1 = fp8_block_scale(bf16hi(m2));
       *reinterpret_cast<float2*>(&colscale[0][2 * tid]) = make_float2(s0, s1);
-      *reinterpret_cast<float2*>(&colscale[1][2 * tid]) = make_float2(__frcp_rn(s0), __frcp_rn(s1));
+      const Reciprocal y0 = fp8_reciprocal(s0), y1 = fp8_reciprocal(s1);
+      *reinterpret_cast<float2*>(&colscale[1][2 * tid]) = make_float2(y0.hi, y1.hi);
+      *reinterpret_cast<float2*>(&colscale[2][2 * tid]) = make_float2(y0.lo, y1.lo);
       if (k0 + 2 * tid < a.K) *reinterpret_cast<float2*>(a.st + mb * a.K + k0 + 2 * tid) = make_float2(s0, s1);
     }
     __syncthreads();
   }
   uint2 codes[8];
   if (a.q || SQUARE) {
-    const float ry = __frcp_rn(rs);
+    const Reciprocal ry = fp8_reciprocal(rs);
     const bool fast = __all_sync(0xffffffffu, fp8_fast(rs));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = SQUARE ? rs : __shfl_sync(0xffffffffu, rs, (lane & 16) + 2 * i);
-      const float y = SQUARE ? ry : __shfl_sync(0xffffffffu, ry, (lane & 16) + 2 * i);
-      const float2 ss[4] = {{s, s}, {s, s}, {s, s}, {s, s}}, yy[4] = {{y, y}, {y, y}, {y, y}, {y, y}};
-      codes[i] = fast ? e4m3_codes8<true>(v[i], ss, yy) : e4m3_codes8<false>(v[i], ss, yy);
+      auto of_row = [&](float x) {
+        const float f = SQUARE ? x : __shfl_sync(0xffffffffu, x, (lane & 16) + 2 * i);
+        return make_float2(f, f);
+      };
+      const float2 s = of_row(rs), hi = of_row(ry.hi), lo = of_row(ry.lo);
+      const float2 ss[4] = {s, s, s, s}, hh[4] = {hi, hi, hi, hi}, ll[4] = {lo, lo, lo, lo};
+      codes[i] = fast ? e4m3_codes8<true>(v[i], ss, hh, ll) : e4m3_codes8<false>(v[i], ss, hh, ll);
       const int64_t r = m0 + ty * 8 + i;
       if (a.q && r < a.M && col_ok) *reinterpret_cast<uint2*>(a.q + r * a.K + col) = codes[i];
     }
   }
   if (TRANSPOSED) {
     if (!SQUARE) {
-      float2 cs[4], cy[4];
+      float2 cs[4], hi[4], lo[4];
       bool fast = true;
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
         const float4 s4 = *reinterpret_cast<const float4*>(&colscale[0][tx * 8 + 2 * j]);
-        const float4 y4 = *reinterpret_cast<const float4*>(&colscale[1][tx * 8 + 2 * j]);
+        const float4 h4 = *reinterpret_cast<const float4*>(&colscale[1][tx * 8 + 2 * j]);
+        const float4 l4 = *reinterpret_cast<const float4*>(&colscale[2][tx * 8 + 2 * j]);
         cs[j] = make_float2(s4.x, s4.y), cs[j + 1] = make_float2(s4.z, s4.w);
-        cy[j] = make_float2(y4.x, y4.y), cy[j + 1] = make_float2(y4.z, y4.w);
+        hi[j] = make_float2(h4.x, h4.y), hi[j + 1] = make_float2(h4.z, h4.w);
+        lo[j] = make_float2(l4.x, l4.y), lo[j + 1] = make_float2(l4.z, l4.w);
         fast = fast && fp8_fast(s4.x) && fp8_fast(s4.y) && fp8_fast(s4.z) && fp8_fast(s4.w);
       }
       fast = __all_sync(0xffffffffu, fast);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) codes[i] = fast ? e4m3_codes8<true>(v[i], cs, cy) : e4m3_codes8<false>(v[i], cs, cy);
+      for (int i = 0; i < 8; ++i)
+        codes[i] = fast ? e4m3_codes8<true>(v[i], cs, hi, lo) : e4m3_codes8<false>(v[i], cs, hi, lo);
     }
     // 8 x 8 byte transpose: column tx*8 + j gets rows ty*8 .. +7 as one 8-byte unit, unit ty
     // stored at ty ^ tx so that a warp's 32 units of one j cover all banks
