@@ -20,7 +20,7 @@
 namespace nvfp4 {
 
 struct Fp8PairCfg {
-  // warps 0-3: producer, MMA issuer, two idle; warps 4-11: epilogue. 384 x 168 registers at
+  // warps 0-3: producer, MMA issuer, waiter, one idle; warps 4-11: epilogue. 384 x 168 registers at
   // launch; the epilogue takes what the first warpgroup gives up: 128 x 72 + 256 x 216 = 384 x 168.
   static constexpr int THREADS = 384;
   static constexpr int CONTROL_REGS = 72, EPILOGUE_REGS = 216;
@@ -29,10 +29,14 @@ struct Fp8PairCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int STAGES = 5;
   static constexpr int OUT_BYTES = 8 * 4096;  // one 32-row x 128-byte store box per epilogue warp
-  static constexpr int SCALE_BYTES = 8 * 2 * 512;  // per warp: two buffers of 128 column scales
+  // per epilogue warp: DEPTH slots of 32 row scales and 128 column scales (or one block's)
+  static constexpr int DEPTH = 4, SCALES = 160;
+  static constexpr int SCALE_BYTES = 8 * DEPTH * SCALES * 4;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 1024 + 256;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
+
+constexpr uint32_t kFp8HandoffBarrier = 1;  // waiter and MMA warp
 
 struct Fp8Tile {
   int m0, m_end;  // rows of a and y: [m0, m_end)
@@ -67,8 +71,8 @@ DEVI Fp8Tile fp8_tile(const Fp8GemmArgs& p, int t, int mt, int nt, int kbs) {
 }
 
 // A warp's 32 rows x 128 bytes of results to y, through its 4 KB box (16-byte chunk c of row r at
-// chunk c ^ (r % 8)): by a TMA store (whole tiles), or row by row with plain stores where y's
-// rows are not 16-byte aligned or the box reaches past the tile's rows.
+// chunk c ^ (r % 8)): by a TMA store (whole boxes), or with plain stores where y's rows are
+// not 16-byte aligned (a row at a time) or a grouped tile ends inside the box (four rows at a time).
 template <bool F32>
 DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, const uint32_t (&w)[32], const CUtensorMap* tmY, bool by_tma,
                         int row0, int m_end, int col0, int N) {
@@ -91,6 +95,18 @@ DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, const uint32_t (&w)[
   } else {
     __syncwarp();
     const int rows = min(32, m_end - row0);
+    constexpr int PER16 = F32 ? 4 : 8;  // values per 16 bytes
+    if (N % PER16 == 0) {  // four rows at a time, 16 bytes a lane
+      const int c = lane & 7;
+      if (col0 + c * PER16 < N)
+        for (int r = lane >> 3; r < rows; r += 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+          uint8_t* y = static_cast<uint8_t*>(p.y) + (static_cast<int64_t>(row0 + r) * N + col0 + c * PER16) * (16 / PER16);
+          *reinterpret_cast<uint4*>(y) = v;
+        }
+      __syncwarp();
+      return;
+    }
     for (int r = 0; r < rows; ++r) {
       const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
       const int64_t at = static_cast<int64_t>(row0 + r) * N + col0;
@@ -168,7 +184,7 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
     regs_inc<C::EPILOGUE_REGS>();
     const int q = warp & 3, h = (warp - 4) >> 2;
     uint8_t* box = out_buf + (warp - 4) * 4096;
-    float* cs = scale_buf + (warp - 4) * 256;
+    float* cs = scale_buf + (warp - 4) * C::DEPTH * C::SCALES;
     const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
     const bool aligned_rows = N % (F32 ? 4 : 8) == 0;
     int buf = 0;
@@ -178,43 +194,39 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
       const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
       const int row0 = tl.m0 + rank * 128 + q * 32, row = row0 + lane;
       const int col0 = tl.n0 + h * 128;
-      const bool row_ok = row < tl.m_end;
-      const float* sa = p.sa + row;
-      const float* sb = COLSCALE ? tl.sb + col0 + lane : tl.sb + static_cast<int64_t>(col0 >> 7) * KB;
-      // the scales of a block of K: this row's, and the warp's column block's (or its four of 128)
-      auto row_scale = [&](int kb) { return row_ok && kb < KB ? sa[static_cast<int64_t>(kb) * M] : 0.0f; };
-      auto block_scale = [&](int kb) { return kb < KB && col0 < N ? sb[kb] : 0.0f; };
-      auto col_scale = [&](int kb, int i) {
-        return kb < KB && col0 + lane + 32 * i < N ? sb[static_cast<int64_t>(kb) * N + 32 * i] : 0.0f;
+      // The scales of a block of K reach shared memory by cp.async, DEPTH blocks ahead of their use
+      // (a register held for a later block would make the loop wait for its load one block after
+      // issuing it: L2's latency then paces every block). Rows and columns past the tile's copy a
+      // scale inside it; their sums are not stored.
+      const float* sa = p.sa + min(row, tl.m_end - 1);
+      const float* sb = COLSCALE ? tl.sb : tl.sb + static_cast<int64_t>(min(col0, N - 1) >> 7) * KB;
+      auto fetch_scales = [&](int kb) {
+        const int k = min(kb, KB - 1);
+        float* d = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
+        cp_async4(d + lane, sa + static_cast<int64_t>(k) * M);
+        if (COLSCALE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async4(d + 32 + lane + 32 * i, sb + static_cast<int64_t>(k) * N + min(col0 + lane + 32 * i, N - 1));
+        } else if (lane == 0) {
+          cp_async4(d + 32, sb + k);
+        }
+        cp_async_commit();
       };
-      uint64_t acc[64];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      // loaded two blocks ahead of their use
-      float ra = row_scale(0), rb = row_scale(1), ca[4], cb[4];
-      if (COLSCALE) {
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ca[i] = col_scale(0, i), cb[i] = col_scale(1, i);
-      } else {
-        ca[0] = block_scale(0), cb[0] = block_scale(1);
-      }
+      for (int kb = 0; kb < C::DEPTH - 1; ++kb) fetch_scales(kb);
+#pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
-        const float rs = COLSCALE ? ra : ra * ca[0];
+        __syncwarp();  // the slot that is filled now has been read by all lanes
+        fetch_scales(kb + C::DEPTH - 1);
+        cp_async_wait<C::DEPTH - 1>();
+        __syncwarp();
+        const float* sc = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
+        const float rs = COLSCALE ? sc[lane] : sc[lane] * sc[32];
         const uint64_t rs2 = f2(rs, rs);
-        if (COLSCALE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cs[buf * 128 + lane + 32 * i] = ca[i];
-          __syncwarp();
-        }
-        ra = rb;
-        rb = row_scale(kb + 2);
-        if (COLSCALE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ca[i] = cb[i], cb[i] = col_scale(kb + 2, i);
-        } else {
-          ca[0] = cb[0];
-          cb[0] = block_scale(kb + 2);
-        }
         if (!mbar_wait_warp(&tfull[buf], bph, abort_flag, wd)) {
           ok = false;
           break;
@@ -233,28 +245,28 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (elect_one()) mbar_arrive_cluster(tempty_leader[buf]);
-            __syncwarp();
           }
           if (COLSCALE) {
-            const float4* cv = reinterpret_cast<const float4*>(cs + buf * 128 + 32 * c);
+            const float4* cv = reinterpret_cast<const float4*>(sc + 32 + 32 * c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float4 v = cv[j];
-              const uint64_t x0 = f2_mul(f2(__uint_as_float(cur[4 * j]), __uint_as_float(cur[4 * j + 1])), f2(v.x, v.y));
-              const uint64_t x1 = f2_mul(f2(__uint_as_float(cur[4 * j + 2]), __uint_as_float(cur[4 * j + 3])), f2(v.z, v.w));
-              acc[16 * c + 2 * j] = f2_fma(x0, rs2, acc[16 * c + 2 * j]);
-              acc[16 * c + 2 * j + 1] = f2_fma(x1, rs2, acc[16 * c + 2 * j + 1]);
+              float* a = acc + 32 * c + 4 * j;
+              a[0] = fmaf(__uint_as_float(cur[4 * j]) * v.x, rs, a[0]);
+              a[1] = fmaf(__uint_as_float(cur[4 * j + 1]) * v.y, rs, a[1]);
+              a[2] = fmaf(__uint_as_float(cur[4 * j + 2]) * v.z, rs, a[2]);
+              a[3] = fmaf(__uint_as_float(cur[4 * j + 3]) * v.w, rs, a[3]);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[16 * c + j] = f2_fma(f2(__uint_as_float(cur[2 * j]), __uint_as_float(cur[2 * j + 1])), rs2, acc[16 * c + j]);
+            for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(cur[j]), rs, acc[32 * c + j]);
           }
           if (c < 3) tmem_ld_wait32(r[(c + 1) & 1]);
         }
         buf ^= 1;
         bph ^= buf == 0;
       }
+      cp_async_wait<0>();
       if (!ok) break;
       // results to y; a grouped tile that ends inside the box's rows must not touch the next expert's
       const bool by_tma = aligned_rows && (!GROUPED || row0 + 32 <= tl.m_end);
@@ -268,10 +280,10 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
             for (int j = 0; j < 32; ++j) {
               float lo, hi;
               if (F32) {
-                f2_split(acc[16 * b + (j >> 1)], lo, hi);
-                w[j] = __float_as_uint((j & 1) ? hi : lo);
+                lo = hi = acc[32 * b + j];
+                w[j] = __float_as_uint(lo);
               } else {
-                f2_split(acc[32 * b + j], lo, hi);
+                lo = acc[64 * b + 2 * j], hi = acc[64 * b + 2 * j + 1];
                 w[j] = pack_bf16x2(lo, hi);
               }
             }
@@ -288,8 +300,7 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
     const uint64_t pol = policy_evict_last();
     int s = 0;
     uint32_t ph = 0;
-    int issued_phase[STAGES];
-    for (int i = 0; i < STAGES; ++i) issued_phase[i] = -1;
+    uint32_t used = 0, phases = 0;  // per stage: requested at all, phase of the last request
     int issued = 0;
     for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
       const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
@@ -305,7 +316,8 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
           tma_load_2d_pair(st + C::TILE_BYTES, &tmB, bar, kb * 128, tl.b_row + rank * 128, pol);
         }
         __syncwarp();
-        issued_phase[s] = ph;
+        used |= 1u << s;
+        phases = (phases & ~(1u << s)) | ph << s;
         if (++s == STAGES) {
           s = 0;
           ph ^= 1;
@@ -316,30 +328,53 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
     // The even CTA's full barriers count both CTAs' bytes: let them all land.
     if (leader)
       for (int i = 0; i < STAGES; ++i)
-        if (issued_phase[i] >= 0) {
+        if (used >> i & 1) {
           volatile int32_t dummy = 0;
-          mbar_wait_warp(&full[i], issued_phase[i], &dummy, wd);
+          mbar_wait_warp(&full[i], phases >> i & 1, &dummy, wd);
         }
   } else if (warp == 1) {
     if (leader) {
       const uint32_t idesc = idesc_e4m3(256, 256);
       int s = 0, buf = 0;
-      uint32_t ph = 0, bph = 0;
-      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+      for (int t = pair; t < tiles; t += npairs) {
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_warp(&tempty[buf], bph ^ 1, abort_flag, wd)) break;
-          if (!mbar_wait_warp(&full[s], ph, abort_flag, wd)) break;
+          const bool ok = named_sync_and(kFp8HandoffBarrier, 64, true);
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t a_addr = smem_u32(smem + s * C::STAGE_BYTES);
-            const uint64_t adesc = desc_sw128(a_addr), bdesc = desc_sw128(a_addr + C::TILE_BYTES);
+          if (ok) {
+            if (elect_one()) {
+              const uint32_t a_addr = smem_u32(smem + s * C::STAGE_BYTES);
+              const uint64_t adesc = desc_sw128(a_addr), bdesc = desc_sw128(a_addr + C::TILE_BYTES);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f8_pair(tmem + buf * 256, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0);
-            tc_commit_pair(&empty[s], 3);
-            tc_commit_pair(&tfull[buf], 3);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_f8_pair(tmem + buf * 256, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0);
+              tc_commit_pair(&empty[s], 3);
+              tc_commit_pair(&tfull[buf], 3);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (++s == STAGES) s = 0;
+          buf ^= 1;
+        }
+      }
+      if (elect_one()) tc_commit_pair(drain, 1);
+      __syncwarp();
+      volatile int32_t dummy = 0;
+      mbar_wait_warp(drain, 0, &dummy, wd);
+    }
+  } else if (warp == 2) {
+    // Owns the waits in front of the MMA warp (a stage's bytes, the TMEM buffer's release) and hands
+    // the verdict over through bar.red: an mbarrier wait costs ~110 cycles even when complete, and
+    // two of them between the issues of two blocks left the tensor core idle for a third of the
+    // time. Both warps run exactly the same iterations, also after an abort, so that the named
+    // barrier, which cannot time out, always pairs.
+    if (leader) {
+      int s = 0, buf = 0;
+      uint32_t ph = 0, bph = 0;
+      for (int t = pair; t < tiles; t += npairs)
+        for (int kb = 0; kb < KB; ++kb) {
+          const bool ok = __all_sync(0xffffffffu, *abort_flag == 0) && mbar_poll_warp(&full[s], ph, abort_flag, wd) &&
+                          mbar_poll_warp(&tempty[buf], bph ^ 1, abort_flag, wd);
+          named_sync_and(kFp8HandoffBarrier, 64, ok);
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
@@ -347,11 +382,6 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
           buf ^= 1;
           bph ^= buf == 0;
         }
-      }
-      if (elect_one()) tc_commit_pair(drain, 1);
-      __syncwarp();
-      volatile int32_t dummy = 0;
-      mbar_wait_warp(drain, 0, &dummy, wd);
     }
   }
   }

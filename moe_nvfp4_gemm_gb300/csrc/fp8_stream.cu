@@ -23,15 +23,14 @@ enum { kFp8Dense = 0, kFp8DenseRowScale = 1, kFp8Grouped = 2 };
 // NT: token columns of the accumulator (and rows of the token tile).
 template <int NT>
 struct Fp8StreamCfg {
-  static constexpr int EPI_WARPS = NT <= 64 ? 4 : 8;
-  static constexpr int COLS = NT / (EPI_WARPS / 4);  // token columns per epilogue warp
+  static constexpr int COLS = 32;  // token columns per epilogue warp
+  static constexpr int EPI_WARPS = 4 * (NT / COLS);
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int CTAS = NT <= 64 ? 2 : 1;  // per SM
-  static constexpr int BUFS = NT == 256 ? 2 : 4;
+  static constexpr int CTAS = NT == 32 ? 2 : 1;  // per SM (two of NT = 64 would leave 80 registers: spills)
+  static constexpr int BUFS = 4;
   static constexpr int TMEM_COLS = BUFS * NT;
   static constexpr int STAGE_BYTES = 16384 + NT * 128;
   static constexpr int SCALE_BYTES = EPI_WARPS * 2 * COLS * 4;
-  static constexpr bool REGS = NT == 256;  // register split as in the pair kernel
 };
 
 struct Fp8Item {
@@ -134,9 +133,8 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
   const int first = blockIdx.x, stride = GROUPED ? gridDim.x : n_items;
 
   if (warp >= 4) {
-    if (C::REGS) regs_inc<216>();
     const int q = warp & 3, h = (warp - 4) >> 2;
-    constexpr int COLS = C::COLS, CHUNK = NT >= 128 ? 32 : 16;
+    constexpr int COLS = C::COLS;
     float* cs = scale_buf + (warp - 4) * 2 * COLS;
     int buf = 0, sbuf = 0;
     uint32_t bph = 0;
@@ -182,46 +180,31 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + c0;
         const uint64_t ws2 = f2(ws, ws);
-        uint32_t r[2][CHUNK];
-        auto load = [&](int c, uint32_t* d) {
-          if constexpr (CHUNK == 32)
-            tmem_ld32(taddr + c * CHUNK, d);
-          else
-            tmem_ld16(taddr + c * CHUNK, d);
-        };
-        auto landed = [&](uint32_t* d) {
-          if constexpr (CHUNK == 32)
-            tmem_ld_wait32(d);
-          else
-            tmem_ld_wait16(d);
-        };
-        if (n > 0) {
-          load(0, r[0]);
-          landed(r[0]);
-        }
+        // 16 columns, and 16 more where the warp has them (n is the same for all its lanes)
+        uint32_t r[2][16];
+        const bool wide = n > 16;
+        if (n > 0) tmem_ld16(taddr, r[0]);
+        if (wide) tmem_ld16(taddr + 16, r[1]);
+        tmem_ld_wait16(r[0]);
+        tmem_ld_wait16(r[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
 #pragma unroll
-        for (int c = 0; c < COLS / CHUNK; ++c) {
-          if (c * CHUNK < n) {  // the same for the whole warp
-            uint32_t* cur = r[c & 1];
-            const bool more = c + 1 < COLS / CHUNK && (c + 1) * CHUNK < n;
-            if (more) load(c + 1, r[(c + 1) & 1]);
-            const float4* cv = reinterpret_cast<const float4*>(cs + sbuf * COLS + CHUNK * c);
+        for (int c = 0; c < 2; ++c) {
+          if (c == 0 ? n > 0 : wide) {
+            const float4* cv = reinterpret_cast<const float4*>(cs + sbuf * COLS + 16 * c);
 #pragma unroll
-            for (int j = 0; j < CHUNK / 4; ++j) {
+            for (int j = 0; j < 4; ++j) {
               const float4 v = cv[j];
               uint64_t s0 = f2(v.x, v.y), s1 = f2(v.z, v.w);
               if (MODE == kFp8DenseRowScale) s0 = f2_mul(s0, ws2), s1 = f2_mul(s1, ws2);
-              uint64_t* a = acc + CHUNK / 2 * c + 2 * j;
-              a[0] = f2_fma(f2(__uint_as_float(cur[4 * j]), __uint_as_float(cur[4 * j + 1])), s0, a[0]);
-              a[1] = f2_fma(f2(__uint_as_float(cur[4 * j + 2]), __uint_as_float(cur[4 * j + 3])), s1, a[1]);
+              uint64_t* a = acc + 8 * c + 2 * j;
+              a[0] = f2_fma(f2(__uint_as_float(r[c][4 * j]), __uint_as_float(r[c][4 * j + 1])), s0, a[0]);
+              a[1] = f2_fma(f2(__uint_as_float(r[c][4 * j + 2]), __uint_as_float(r[c][4 * j + 3])), s1, a[1]);
             }
-            if (more) landed(r[(c + 1) & 1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (elect_one()) mbar_arrive(&tempty[buf]);
-        __syncwarp();
         sbuf ^= 1;
         if (++buf == BUFS) {
           buf = 0;
@@ -294,14 +277,12 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
       }
     }
   } else {
-    if (C::REGS) regs_dec<72>();
     if (warp == 0 || warp == 2) {
       // warp 0 requests every stage's weight tile, warp 2 its token rows
       const uint64_t pol = warp == 0 ? policy_evict_first() : policy_evict_last();
       int s = 0, issued = 0;
       uint32_t ph = 0;
-      int issued_phase[MAX_STAGES];
-      for (int j = 0; j < MAX_STAGES; ++j) issued_phase[j] = -1;
+      uint32_t used = 0, phases = 0;  // per stage: requested at all, phase of the last request
       Fp8Item it;
       for (int i = first; fp8_item<NT, MODE>(p, i, n_items, NTW, KB, it) && !*abort_flag; i += stride) {
         const int nbox = (it.rows + 31) >> 5;
@@ -322,7 +303,8 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
               tma_load_2d(st + 16384 + j * 4096, &tmX, &full[s], kb * 128, it.row0 + j * 32, pol);
           }
           __syncwarp();
-          issued_phase[s] = ph;
+          used |= 1u << s;
+          phases = (phases & ~(1u << s)) | ph << s;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
@@ -332,9 +314,9 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
       if (warp == 0) griddep_launch_dependents();
       // this warp's copies in flight land before the CTA leaves
       for (int j = 0; j < STAGES; ++j)
-        if (issued_phase[j] >= 0) {
+        if (used >> j & 1) {
           volatile int32_t dummy = 0;
-          mbar_wait_warp(&full[j], issued_phase[j], &dummy, wd);
+          mbar_wait_warp(&full[j], phases >> j & 1, &dummy, wd);
         }
     } else if (warp == 1) {
       int s = 0, buf = 0;
@@ -418,19 +400,18 @@ static cudaError_t launch_fp8_stream_t(const CUtensorMap& tmW, const CUtensorMap
   return cudaGetLastError();
 }
 
-// Token tiles of `tile_rows` (32, 64, 128, grouped also 256) rows; tmX has 32-row boxes.
+// Token tiles of `tile_rows` (32, 64, 128) rows; tmX has 32-row boxes.
 cudaError_t launch_fp8_stream(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int tile_rows,
                               int sms, cudaStream_t st) {
   const int NTW = static_cast<int>((p.N + 127) / 128);
   if (p.tiles) {
     const int64_t items = static_cast<int64_t>(p.max_tiles) * NTW;
-    const int64_t slots = (tile_rows <= 64 ? 2 : 1) * static_cast<int64_t>(sms);
+    const int64_t slots = (tile_rows == 32 ? 2 : 1) * static_cast<int64_t>(sms);
     const int grid = static_cast<int>(items < slots ? items : slots);
     switch (tile_rows) {
       case 32: return launch_fp8_stream_t<32, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
       case 64: return launch_fp8_stream_t<64, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
-      case 128: return launch_fp8_stream_t<128, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
-      default: return launch_fp8_stream_t<256, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
+      default: return launch_fp8_stream_t<128, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
     }
   }
   const int M = static_cast<int>(p.M), m_own = (M + p.split - 1) / p.split;

@@ -251,6 +251,16 @@ DEVI void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, u
       : "memory");
 }
 
+// Four bytes global -> shared without a register (this thread's cp.async groups).
+DEVI void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+DEVI void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DEVI void cp_async_wait() {  // all but the N youngest groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---- clusters ------------------------------------------------------------------
 
 DEVI uint32_t cluster_ctarank() {
@@ -277,6 +287,11 @@ DEVI uint32_t mapa_shared(uint32_t local_addr, uint32_t rank) {
 // against ~100 for this one, on the critical path of every tile.
 DEVI void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Arrive on an mbarrier of any CTA in the cluster that publishes this thread's earlier writes.
+DEVI void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // 2-D tiled TMA load issued for a CTA pair: lands in this CTA's shared memory and
