@@ -4,8 +4,8 @@
 //
 // Bound by reading the weights: one 128-row x 128-byte TMA tile per block of K, each read once,
 // the tokens from L2. The tensor core sums one block of 128 into one of several TMEM buffers; the
-// epilogue warps add it, times the token scales (staged per warp in shared memory, the weight
-// block's scale multiplied in), to fp32 sums in registers.
+// epilogue warps add it, times the token scales (put into shared memory by a warp of their own, the
+// weight block's scale multiplied in), to fp32 sums in registers.
 //   dense:   grid = (N / 128) x S CTAs in clusters of S along K; the S partial sums meet through
 //            distributed shared memory, each CTA owning some of the tokens.
 //   grouped: a persistent grid walks (token tile, weight tile) items of the device-built list.
@@ -30,7 +30,11 @@ struct Fp8StreamCfg {
   static constexpr int BUFS = 4;
   static constexpr int TMEM_COLS = BUFS * NT;
   static constexpr int STAGE_BYTES = 16384 + NT * 128;
-  static constexpr int SCALE_BYTES = EPI_WARPS * 2 * COLS * 4;
+  // Scales of GROUPS x GROUP blocks of K: per block NT token scales (times the weight block's) and,
+  // with a scale per weight row, 128 of those.
+  static constexpr int GROUP = 8, GROUPS = 4;
+  __host__ __device__ static constexpr int slot_floats(int mode) { return mode == 1 ? NT + 128 : NT; }
+  __host__ __device__ static constexpr int scale_bytes(int mode) { return GROUPS * GROUP * slot_floats(mode) * 4; }
 };
 
 struct Fp8Item {
@@ -68,22 +72,25 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
   constexpr bool GROUPED = MODE == kFp8Grouped;
   constexpr int BUFS = C::BUFS;
   constexpr int MAX_STAGES = 12;
+  constexpr int SCALE_BYTES = C::scale_bytes(MODE), SLOT = C::slot_floats(MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int STAGES = p.stages;
   float* scale_buf = reinterpret_cast<float*>(smem + STAGES * C::STAGE_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES + C::SCALE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES + SCALE_BYTES);
   uint64_t* empty = full + MAX_STAGES;
   uint64_t* tfull = empty + MAX_STAGES;  // [BUFS]
   uint64_t* tempty = tfull + BUFS;       // [BUFS]
   uint64_t* drain = tempty + BUFS;
   uint64_t* red_bar = drain + 1;  // all S partials of this CTA's tokens have landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(red_bar + 1);
+  uint64_t* sfull = red_bar + 1;         // [GROUPS] a group's scales are in shared memory
+  uint64_t* sempty = sfull + C::GROUPS;  // [GROUPS] and have been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + C::GROUPS);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
   // split-K: partial sums leave from the ring ([token][128] fp32; every stage has been consumed
   // by then) and arrive in recv [source rank][own token][128]
   float* part = reinterpret_cast<float*>(smem);
-  float* recv = reinterpret_cast<float*>(smem + STAGES * C::STAGE_BYTES + C::SCALE_BYTES + 512);
+  float* recv = reinterpret_cast<float*>(smem + STAGES * C::STAGE_BYTES + SCALE_BYTES + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t wd = p.watchdog_ns;
@@ -102,6 +109,10 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
     for (int b = 0; b < BUFS; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], C::EPI_WARPS);
+    }
+    for (int g = 0; g < C::GROUPS; ++g) {
+      mbar_init(&sfull[g], 1);
+      mbar_init(&sempty[g], C::EPI_WARPS);
     }
     mbar_init(drain, 1);
     mbar_init(red_bar, 1);
@@ -135,9 +146,8 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
   if (warp >= 4) {
     const int q = warp & 3, h = (warp - 4) >> 2;
     constexpr int COLS = C::COLS;
-    float* cs = scale_buf + (warp - 4) * 2 * COLS;
-    int buf = 0, sbuf = 0;
-    uint32_t bph = 0;
+    int buf = 0, grp = 0;
+    uint32_t bph = 0, gph = 0;
     bool ok = true;
     uint64_t acc[COLS / 2];
     Fp8Item it;
@@ -145,40 +155,23 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
       const int wrow = it.wt * 128 + q * 32 + lane;  // weight row of this lane: output column
       const int c0 = h * COLS;                       // first token column of this warp
       const int n = it.rows - c0;                    // its tokens (may be <= 0)
-      const float* sx = p.sa + it.row0 + c0 + lane;
-      const float* sw = MODE == kFp8DenseRowScale ? p.sb + wrow
-                                                  : p.sb + (static_cast<int64_t>(it.e) * NTW + it.wt) * KB;
-      auto tok_scale = [&](int kb, int j) {
-        return kb < it.kb1 && lane + 32 * j < n ? sx[static_cast<int64_t>(kb) * M + 32 * j] : 0.0f;
-      };
-      auto w_scale = [&](int kb) {
-        if (kb >= it.kb1) return 0.0f;
-        if (MODE == kFp8DenseRowScale) return wrow < N ? sw[static_cast<int64_t>(kb) * N] : 0.0f;
-        return sw[kb];
-      };
 #pragma unroll
       for (int j = 0; j < COLS / 2; ++j) acc[j] = 0;
-      float xa[COLS / 32], xb[COLS / 32], wa = w_scale(it.kb0), wb = w_scale(it.kb0 + 1);
-#pragma unroll
-      for (int j = 0; j < COLS / 32; ++j) xa[j] = tok_scale(it.kb0, j), xb[j] = tok_scale(it.kb0 + 1, j);
+#pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
-        const float ws = wa;
-        if (n > 0) {
-#pragma unroll
-          for (int j = 0; j < COLS / 32; ++j)
-            cs[sbuf * COLS + lane + 32 * j] = MODE == kFp8DenseRowScale ? xa[j] : xa[j] * ws;
+        const int in_group = (kb - it.kb0) & (C::GROUP - 1);
+        if (in_group == 0 && !mbar_wait_warp(&sfull[grp], gph, abort_flag, wd)) {
+          ok = false;
+          break;
         }
-        __syncwarp();
-        wa = wb;
-        wb = w_scale(kb + 2);
-#pragma unroll
-        for (int j = 0; j < COLS / 32; ++j) xa[j] = xb[j], xb[j] = tok_scale(kb + 2, j);
+        const float* sc = scale_buf + (grp * C::GROUP + in_group) * SLOT;
         if (!mbar_wait_warp(&tfull[buf], bph, abort_flag, wd)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + c0;
+        const float ws = MODE == kFp8DenseRowScale ? sc[NT + q * 32 + lane] : 1.0f;
         const uint64_t ws2 = f2(ws, ws);
         // 16 columns, and 16 more where the warp has them (n is the same for all its lanes)
         uint32_t r[2][16];
@@ -193,7 +186,7 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (c == 0 ? n > 0 : wide) {
-            const float4* cv = reinterpret_cast<const float4*>(cs + sbuf * COLS + 16 * c);
+            const float4* cv = reinterpret_cast<const float4*>(sc + c0 + 16 * c);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float4 v = cv[j];
@@ -205,7 +198,14 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
             }
           }
         }
-        sbuf ^= 1;
+        if (in_group == C::GROUP - 1 || kb + 1 == it.kb1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[grp]);
+          if (++grp == C::GROUPS) {
+            grp = 0;
+            gph ^= 1;
+          }
+        }
         if (++buf == BUFS) {
           buf = 0;
           bph ^= 1;
@@ -351,6 +351,64 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
       __syncwarp();
       volatile int32_t dummy = 0;
       mbar_wait_warp(drain, 0, &dummy, wd);
+    } else {
+      // warp 3: the scales, a group of blocks at a time and up to GROUPS groups ahead of the epilogue.
+      // A load issued now queues behind the TMA loads that the SM has in flight; in the epilogue
+      // warps its latency paced every block (M = 33, 8192 x 8192: 24 us, 20 us in two halves of K).
+      constexpr int NX = NT / 32, U = MODE == kFp8DenseRowScale ? 2 : (NT == 128 ? 4 : 8);  // blocks per batch of loads
+      int grp = 0;
+      uint32_t gph = 0;
+      bool ok = true;
+      Fp8Item it;
+      for (int i = first; ok && fp8_item<NT, MODE>(p, i, n_items, NTW, KB, it); i += stride) {
+        // tokens past the tile's and rows past N read a scale inside it; their sums are not stored
+        int tok[NX], wr[4];
+#pragma unroll
+        for (int j = 0; j < NX; ++j) tok[j] = it.row0 + min(lane + 32 * j, it.rows - 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wr[j] = min(it.wt * 128 + lane + 32 * j, N - 1);
+        const float* sw = p.sb + (static_cast<int64_t>(it.e) * NTW + it.wt) * KB;
+        for (int g0 = it.kb0; g0 < it.kb1; g0 += C::GROUP) {
+#pragma unroll 1
+          for (int b0 = 0; b0 < C::GROUP; b0 += U) {
+            float x[U][NX], w[U][MODE == kFp8DenseRowScale ? 4 : 1];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int kb = min(g0 + b0 + u, it.kb1 - 1);
+#pragma unroll
+              for (int j = 0; j < NX; ++j) x[u][j] = (p.sa + static_cast<int64_t>(kb) * M)[tok[j]];
+              if (MODE == kFp8DenseRowScale) {
+#pragma unroll
+                for (int j = 0; j < (MODE == kFp8DenseRowScale ? 4 : 1); ++j)
+                  w[u][j] = (p.sb + static_cast<int64_t>(kb) * N)[wr[j]];
+              } else {
+                w[u][0] = sw[kb];
+              }
+            }
+            if (b0 == 0 && !mbar_wait_warp(&sempty[grp], gph ^ 1, abort_flag, wd)) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              float* d = scale_buf + (grp * C::GROUP + b0 + u) * SLOT + lane;
+#pragma unroll
+              for (int j = 0; j < NX; ++j) d[32 * j] = MODE == kFp8DenseRowScale ? x[u][j] : x[u][j] * w[u][0];
+              if (MODE == kFp8DenseRowScale) {
+#pragma unroll
+                for (int j = 0; j < (MODE == kFp8DenseRowScale ? 4 : 1); ++j) d[NT + 32 * j] = w[u][j];
+              }
+            }
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull[grp]);
+          if (++grp == C::GROUPS) {
+            grp = 0;
+            gph ^= 1;
+          }
+        }
+      }
     }
   }
 
@@ -374,7 +432,7 @@ static cudaError_t launch_fp8_stream_t(const CUtensorMap& tmW, const CUtensorMap
   auto kernel = k_fp8_stream<NT, MODE>;
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kernel));
   if (e != cudaSuccess) return e;
-  const int fixed = 1024 + C::SCALE_BYTES + 512 + recv_bytes;
+  const int fixed = 1024 + C::scale_bytes(MODE) + 512 + recv_bytes;
   int stages = ((C::CTAS == 2 ? 113 * 1024 : 226 * 1024) - fixed) / C::STAGE_BYTES;
   if (stages > 12) stages = 12;
   // the outgoing partials (a multiple of 512 bytes per token) reuse the ring
