@@ -373,7 +373,7 @@ enum { NVFP4_BF16 = 0, NVFP4_F32 = 1 };
  * Load-balance loss over the n routed tokens, with c_e selections of expert e and
  * P_e = (1/n) sum_t p_te:  L = E sum_e (c_e / (n k)) P_e  (0 when n = 0; 1 when balanced).
  *   logits          device [T, E], bf16 or fp32 (logits_type NVFP4_BF16 / NVFP4_F32). Logits of a
- *                   token with valid[t] == 0 are not read; NaN or +inf in a routed token's row
+ *                   token with valid[t] == 0 have no effect; NaN or +inf in a routed token's row
  *                   makes that row's weights, mean_prob and the loss NaN, and nothing else
  *   valid           device u8 [T] (0: padding token) or NULL (all valid)
  *   topk_idx        int32 [T, k] written, largest logit first; -1 in empty slots

@@ -35,6 +35,14 @@ DEVI uint32_t order_key(float v) {
 }
 DEVI float key_value(uint32_t key) { return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu)); }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+constexpr int kCandSlots = 34;  // 32 candidates, read in pairs; 16-byte rows
+
+// 1 / x to within a unit in the last place
+DEVI float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // log2 of exp(v - max)
 DEVI float route_arg(float v, float mx) { return (v - mx) * kLog2E; }
@@ -100,54 +108,69 @@ struct RouteCfg {
   static constexpr int THREADS = 32 * WARPS;
 };
 
-// The k largest of a warp's 32 * VPL keys (lane holds experts lane * VPL + j), in order, ties to
-// the lower expert: lane s < k returns slot s's expert (-1: none above -inf) and key.
+// The k largest of a warp's 32 * VPL logits (lane holds experts lane * VPL + j), in order, ties to
+// the lower expert: lane s < k returns slot s's expert (-1: none above -inf) and logit. `lane_max`
+// is the largest of this lane's.
 //
-// The k-th largest of the 32 lane maxima bounds the k-th largest key from below, so the selected
-// experts are among the few keys (typically k and one or two) that reach it. Those candidates are
+// The k-th largest of the 32 lane maxima bounds the k-th largest logit from below, so the selected
+// experts are among the few (typically k and one or two) that reach it. Those candidates are
 // compacted into `cand` and each counts the candidates that precede it, which is its slot: about
-// 150 instructions for 256 experts and k = 8, against 400 for k rounds of a maximum over all keys.
+// 170 instructions for 256 experts and k = 8, against 400 for k rounds of a maximum over all.
 // With more than 32 candidates (many equal logits) the rounds are run.
 template <int VPL>
-DEVI void warp_top_k(uint32_t (&key)[VPL], int k, uint64_t* cand, int& out_idx, uint32_t& out_key) {
+DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* cand, int& out_idx, float& out_val) {
   const int lane = threadIdx.x & 31;
-  uint32_t lane_max = 0;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) lane_max = max(lane_max, key[j]);
-  uint32_t bound = 0, left = lane_max;
+  uint32_t bound = 0, left = order_key(lane_max);
+#pragma unroll 2
   for (int s = 0; s < k; ++s) {  // equal maxima leave together: the bound is then lower, and still one
     bound = __reduce_max_sync(0xffffffffu, left);
     if (left == bound) left = 0;
   }
   bound = max(bound, kKeyNegInf + 1);
-  int n = 0;
-  const uint32_t below = (1u << lane) - 1u;
+  const float least = key_value(bound);
+  int mine_n = 0;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const bool c = key[j] >= bound;
-    const uint32_t m = __ballot_sync(0xffffffffu, c);
-    const int at = n + __popc(m & below);
-    // the key in the high half, the complement of the expert in the low half: one comparison orders both
-    if (c && at < 32) cand[at] = static_cast<uint64_t>(key[j]) << 32 | static_cast<uint32_t>(~(lane * VPL + j));
-    n += __popc(m);
+  for (int j = 0; j < VPL; ++j) mine_n += v[j] >= least;
+  int at = mine_n;  // inclusive prefix over the lanes
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += u;
   }
+  const int n = __shfl_sync(0xffffffffu, at, 31);
   out_idx = -1;
-  out_key = 0;
-  __syncwarp();
+  out_val = 0.0f;
   if (n <= 32) {
+    at -= mine_n;
+    // the key in the high half, the complement of the expert in the low half: one comparison orders both
+    if (mine_n > 0) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (v[j] >= least) cand[at++] = static_cast<uint64_t>(order_key(v[j])) << 32 | static_cast<uint32_t>(~(lane * VPL + j));
+    }
+    if (lane == 0 && (n & 1)) cand[n] = 0;  // the count below goes in pairs
+    __syncwarp();
     const uint64_t mine = lane < n ? cand[lane] : 0;
     int rank = 0;
-    for (int i = 0; i < n; ++i) rank += cand[i] > mine;
+    for (int i = 0; i < n; i += 2) {
+      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cand + i);
+      rank += c.x > mine;
+      rank += c.y > mine;
+    }
     __syncwarp();
     if (lane < n) cand[rank] = mine;
     __syncwarp();
     if (lane < min(n, k)) {
-      out_key = static_cast<uint32_t>(cand[lane] >> 32);
-      out_idx = static_cast<int>(~static_cast<uint32_t>(cand[lane]));
+      const uint64_t c = cand[lane];
+      out_val = key_value(static_cast<uint32_t>(c >> 32));
+      out_idx = static_cast<int>(~static_cast<uint32_t>(c));
     }
     __syncwarp();
     return;
   }
+  uint32_t key[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) key[j] = order_key(v[j]);
   for (int s = 0; s < k; ++s) {
     uint32_t m = 0;
 #pragma unroll
@@ -155,19 +178,19 @@ DEVI void warp_top_k(uint32_t (&key)[VPL], int k, uint64_t* cand, int& out_idx, 
     const uint32_t best = __reduce_max_sync(0xffffffffu, m);
     if (best <= kKeyNegInf) break;
     const int w = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
-    int at = -1;
+    int pos = -1;
     if (lane == w) {
 #pragma unroll
       for (int j = VPL - 1; j >= 0; --j)
-        if (key[j] == best) at = j;
+        if (key[j] == best) pos = j;
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
-        if (j == at) key[j] = 0;
+        if (j == pos) key[j] = 0;
     }
-    at = __shfl_sync(0xffffffffu, at, w);
+    pos = __shfl_sync(0xffffffffu, pos, w);
     if (lane == s) {
-      out_idx = w * VPL + at;
-      out_key = best;
+      out_idx = w * VPL + pos;
+      out_val = key_value(best);
     }
   }
 }
@@ -188,35 +211,31 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
   int routed = 0;
   for (int64_t t = t0 + warp; t < t1; t += WARPS) {
     float v[VPL];
-    uint32_t key[VPL];
-    uint32_t top = 0;  // largest key of the row
+    float lane_max = 0.0f, mx = __uint_as_float(0xFF800000u);
     if (!a.valid || __ldg(a.valid + t) != 0) {
       load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
-      uint32_t m = 0;
+      lane_max = v[0];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        key[j] = order_key(v[j]);
-        m = max(m, key[j]);
-      }
-      top = __reduce_max_sync(0xffffffffu, m);
+      for (int j = 1; j < VPL; ++j) lane_max = fmaxf(lane_max, v[j]);
+      mx = key_value(__reduce_max_sync(0xffffffffu, order_key(lane_max)));
     }
     int my_idx = -1;
     float my_w = 0.0f;
-    if (top > kKeyNegInf) {
+    if (mx > __uint_as_float(0xFF800000u)) {
+      float my_v;
+      warp_top_k<VPL>(v, lane_max, k, cand + warp * kCandSlots, my_idx, my_v);
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        v[j] = ex2(route_arg(v[j], key_value(top)));
+        v[j] = ex2(route_arg(v[j], mx));
         sum += v[j];
       }
-      const float inv = __frcp_rn(warp_sum(sum));
+      const float inv = rcp(warp_sum(sum));
 #pragma unroll
       for (int j = 0; j < VPL; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
       ++routed;
-      uint32_t my_key;
-      warp_top_k<VPL>(key, k, cand + warp * 32, my_idx, my_key);
-      const float es = my_idx >= 0 ? ex2(route_arg(key_value(my_key), key_value(top))) : 0.0f;
-      my_w = a.renorm ? es / warp_sum(es) : es * inv;
+      const float es = my_idx >= 0 ? ex2(route_arg(my_v, mx)) : 0.0f;
+      my_w = es * (a.renorm ? rcp(warp_sum(es)) : inv);
       if (my_idx >= 0) atomicAdd(&hist[my_idx], 1);
     }
     if (lane < k) {
@@ -323,8 +342,8 @@ DEVI void route_chunk(const RouteArgs& a, int64_t& t0, int64_t& t1) {
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route(const RouteArgs a) {
   extern __shared__ __align__(16) uint64_t sh64[];
-  uint64_t* cand = sh64;  // [WARPS][32]
-  int32_t* hist = reinterpret_cast<int32_t*>(cand + RouteCfg<VPL>::WARPS * 32);  // [E + 1]
+  uint64_t* cand = sh64;  // [WARPS][kCandSlots]
+  int32_t* hist = reinterpret_cast<int32_t*>(cand + RouteCfg<VPL>::WARPS * kCandSlots);  // [E + 1]
   float* psum = reinterpret_cast<float*>(hist + a.E + 1);                          // [WARPS][E]
   griddep_launch_dependents();
   int64_t t0, t1;
@@ -416,8 +435,8 @@ template <int VPL, bool BF16>
 __global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route_one(const RouteArgs a) {
   constexpr int WARPS = RouteCfg<VPL>::WARPS;
   extern __shared__ __align__(16) uint64_t sh64[];
-  uint64_t* cand = sh64;                                      // [WARPS][32]
-  int32_t* hist = reinterpret_cast<int32_t*>(cand + WARPS * 32);  // [E + 1]
+  uint64_t* cand = sh64;                                      // [WARPS][kCandSlots]
+  int32_t* hist = reinterpret_cast<int32_t*>(cand + WARPS * kCandSlots);  // [E + 1]
   int32_t* offs = hist + a.E + 1;                             // [E + 1]
   float* psum = reinterpret_cast<float*>(offs + a.E + 1);     // [WARPS][E], then the means
   route_rows<VPL, BF16>(a, 0, a.T, hist, psum, cand);
@@ -442,17 +461,30 @@ __global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route_one(const 
 // the selected experts when the weights are plain; d l_te = p_te (G_te - sum_i p_ti G_ti).
 // Renormalised weights are a softmax over the selected logits alone: they add
 // w_s (dw_s - sum_r w_r dw_r) at expert idx_s instead. Unrouted tokens get zeros.
+//
+// Bound by memory. With a.vec the rows come by cp.async, kBwdAhead rows ahead of their use (each
+// lane copies and reads back its own bytes, so no lane waits for another): with plain loads the
+// warps' latency left 65,536 x 256 at 39 us.
 constexpr int kBwdThreads = 256;
 constexpr int kBwdWarps = kBwdThreads / 32;
+constexpr int kBwdAhead = 4;
+// Whether a lane's share of a row is whole 16-byte pieces, and a ring of rows fits beside others.
+template <int VPL, bool BF16>
+constexpr bool kBwdRing = VPL <= 8 && VPL * (BF16 ? 2 : 4) % 16 == 0;
+__host__ __device__ constexpr int bwd_slot_bytes(int vpl, bool bf16) {  // logits, then selection, dw, w
+  return 32 * vpl * (bf16 ? 2 : 4) + 3 * 128;
+}
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(kBwdThreads) k_moe_route_bwd(const RouteBwdArgs a) {
-  extern __shared__ float shf[];
+  extern __shared__ __align__(16) float shf[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k;
   float* spot = shf + warp * (32 * VPL);  // this warp's sparse part of the row, zero between rows
 #pragma unroll
   for (int j = 0; j < VPL; ++j) spot[lane * VPL + j] = 0.0f;
   __syncwarp();
+  constexpr int SLOT = bwd_slot_bytes(VPL, BF16), LANE_BYTES = VPL * (BF16 ? 2 : 4);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(shf + kBwdWarps * 32 * VPL) + warp * kBwdAhead * SLOT;
   const float n = static_cast<float>(a.routed_tokens[0]);
   const float scale = (a.d_loss && n > 0.0f) ? __ldg(a.d_loss) * static_cast<float>(E) / (static_cast<float>(k) * n * n) : 0.0f;
   float g[VPL];
@@ -461,15 +493,70 @@ __global__ void __launch_bounds__(kBwdThreads) k_moe_route_bwd(const RouteBwdArg
     const int e = lane * VPL + j;
     g[j] = e < E ? scale * static_cast<float>(__ldg(a.counts + e)) : 0.0f;
   }
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kBwdWarps + warp; t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * kBwdWarps) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kBwdWarps;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kBwdWarps + warp;
+  const bool ringed = kBwdRing<VPL, BF16> && a.vec;
+  auto request = [&](int64_t t, int slot) {
+    if constexpr (kBwdRing<VPL, BF16>) {
+      if (t < a.T) {
+        uint8_t* d = ring + slot * SLOT;
+        const uint8_t* src = static_cast<const uint8_t*>(a.logits) + t * (32 * LANE_BYTES) + lane * LANE_BYTES;
+#pragma unroll
+        for (int i = 0; i < LANE_BYTES; i += 16) cp_async16(d + lane * LANE_BYTES + i, src + i);
+        if (a.d_w && lane < k) {
+          uint8_t* x = d + 32 * LANE_BYTES + lane * 4;
+          cp_async4(x, a.topk_idx + t * k + lane);
+          cp_async4(x + 128, a.d_w + t * k + lane);
+          cp_async4(x + 256, a.topk_w + t * k + lane);
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  if (ringed)
+    for (int i = 0; i < kBwdAhead - 1; ++i) request(first + i * stride, i);
+  int slot = 0;
+  for (int64_t t = first; t < a.T; t += stride) {
     float v[VPL], d[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) d[j] = 0.0f;
-    float mx = __uint_as_float(0xFF800000u);
+    float mx = __uint_as_float(0xFF800000u), slot_dw = 0.0f, slot_w = 0.0f;
+    int slot_idx = -1;
     const bool valid = !a.valid || __ldg(a.valid + t) != 0;
+    if (ringed) {
+      if constexpr (kBwdRing<VPL, BF16>) {
+        request(t + (kBwdAhead - 1) * stride, (slot + kBwdAhead - 1) & (kBwdAhead - 1));
+        cp_async_wait<kBwdAhead - 1>();
+        const uint8_t* r = ring + slot * SLOT;
+#pragma unroll
+        for (int i = 0; i < LANE_BYTES; i += 16) {
+          const uint4 w = *reinterpret_cast<const uint4*>(r + lane * LANE_BYTES + i);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (BF16)
+              v[i / 2 + 2 * j] = bf16lo(u[j]), v[i / 2 + 2 * j + 1] = bf16hi(u[j]);
+            else
+              v[i / 4 + j] = __uint_as_float(u[j]);
+          }
+        }
+        if (a.d_w && lane < k) {
+          const uint8_t* x = r + 32 * LANE_BYTES + lane * 4;
+          slot_idx = *reinterpret_cast<const int32_t*>(x);
+          slot_dw = *reinterpret_cast<const float*>(x + 128);
+          slot_w = *reinterpret_cast<const float*>(x + 256);
+        }
+        slot = (slot + 1) & (kBwdAhead - 1);
+      }
+    } else {
+      if (valid) load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
+      if (a.d_w && lane < k) {
+        slot_idx = __ldg(a.topk_idx + t * k + lane);
+        slot_dw = __ldg(a.d_w + t * k + lane);
+        slot_w = __ldg(a.topk_w + t * k + lane);
+      }
+    }
     if (valid) {
-      load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
 #pragma unroll
       for (int j = 0; j < VPL; ++j) mx = fmaxf(mx, v[j]);
       mx = key_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
@@ -481,18 +568,12 @@ __global__ void __launch_bounds__(kBwdThreads) k_moe_route_bwd(const RouteBwdArg
         v[j] = ex2((v[j] - mx) * kLog2E);
         sum += v[j];
       }
-      const float inv = __frcp_rn(warp_sum(sum));
+      const float inv = rcp(warp_sum(sum));
       int idx = -1;
       if (a.d_w) {
-        float dw = 0.0f, w = 0.0f;
-        if (lane < k) {
-          idx = __ldg(a.topk_idx + t * k + lane);
-          if (idx >= E) idx = -1;
-          if (idx >= 0) {
-            dw = __ldg(a.d_w + t * k + lane);
-            w = __ldg(a.topk_w + t * k + lane);
-          }
-        }
+        if (slot_idx >= 0 && slot_idx < E) idx = slot_idx;
+        float dw = idx >= 0 ? slot_dw : 0.0f;
+        const float w = idx >= 0 ? slot_w : 0.0f;
         if (a.renorm) dw = w * (dw - warp_sum(w * dw));
         if (idx >= 0) spot[idx] = dw;
         __syncwarp();
@@ -600,7 +681,7 @@ cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches) {
   a.vec = route_vec(a.logits, a.E, a.bf16);
   const int E = a.E, warps = route_warps(E), threads = 32 * warps;
   if (a.T <= kRouteOneTokens) {
-    const int smem = warps * 256 + (2 * (E + 1) + warps * E) * 4;
+    const int smem = warps * kCandSlots * 8 + (2 * (E + 1) + warps * E) * 4;
     *launches = 1;
 #define CALL(V, B) k_moe_route_one<V, B><<<1, threads, smem, st>>>(a)
     ROUTE_DISPATCH(CALL)
@@ -608,7 +689,7 @@ cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches) {
     return cudaGetLastError();
   }
   const int blocks = route_blocks(a.T, E);
-  const int smem = warps * 256 + (E + 1 + warps * E) * 4;
+  const int smem = warps * kCandSlots * 8 + (E + 1 + warps * E) * 4;
   *launches = 3;
 #define CALL(V, B) k_moe_route<V, B><<<blocks, threads, smem, st>>>(a)
   ROUTE_DISPATCH(CALL)
@@ -637,8 +718,15 @@ cudaError_t launch_moe_route_bwd(RouteBwdArgs a, int sms, cudaStream_t st) {
   a.vec = route_vec(a.logits, a.E, a.bf16) && route_vec(a.d_logits, a.E, a.bf16);
   const int64_t want = (a.T + kBwdWarps - 1) / kBwdWarps;
   const int grid = static_cast<int>(want < 8 * sms ? want : 8 * sms);
-  const int smem = kBwdWarps * 32 * route_vpl(a.E) * 4;
-#define CALL(V, B) k_moe_route_bwd<V, B><<<grid, kBwdThreads, smem, st>>>(a)
+  const int vpl = route_vpl(a.E);
+  const bool ring = a.vec && vpl <= 8 && vpl * (a.bf16 ? 2 : 4) % 16 == 0;
+  const int smem = kBwdWarps * (32 * vpl * 4 + (ring ? kBwdAhead * bwd_slot_bytes(vpl, a.bf16 != 0) : 0));
+#define CALL(V, B)                                                                              \
+  {                                                                                             \
+    const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(k_moe_route_bwd<V, B>)); \
+    if (e != cudaSuccess) return e;                                                             \
+    k_moe_route_bwd<V, B><<<grid, kBwdThreads, smem, st>>>(a);                                  \
+  }
   ROUTE_DISPATCH(CALL)
 #undef CALL
   return cudaGetLastError();

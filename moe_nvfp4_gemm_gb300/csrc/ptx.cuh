@@ -255,6 +255,10 @@ DEVI void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, u
 DEVI void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// Sixteen bytes, both addresses 16-byte aligned; past L1.
+DEVI void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 DEVI void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 DEVI void cp_async_wait() {  // all but the N youngest groups have landed
