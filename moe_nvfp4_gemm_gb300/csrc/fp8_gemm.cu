@@ -8,10 +8,17 @@
 // c + 1 run while block c is read.
 //
 // One CTA pair (cta_group::2) per 256 x 256 tile of y: per block of K each CTA loads 128 rows of a
-// and of b (32 KB by TMA, 128-byte swizzle) and the pair's MMAs take 512 cycles at the full rate;
-// each CTA's eight epilogue warps (lane quarter x column half) need 4 x (tcgen05.ld of 32 columns +
-// 16 packed fma) per block in that time.
+// and of b (32 KB by TMA, 128-byte swizzle) and the pair's MMAs take 512 cycles at the full rate.
+// What bounds it: a block takes ~860 cycles (4096 x 28672 x 8192: 715 us, 2.69 PFLOP/s; under the power
+// cap 800 us), of which the eight epilogue warps of a CTA need ~660 to read (4 x tcgen05.ld of 32
+// columns) and add (64 packed fma) their 128 columns of a row and ~200 for the block's hand-offs and
+// scales. Without the arithmetic the same loop takes ~580. Tried without gain: 16 epilogue warps of
+// 64 columns, four half-width buffers, 64-column loads, plain instead of packed fma, the scales
+// through a warp of their own. What does cost is any register that spills in the loop: it comes
+// back through the memory system, behind the TMA loads in flight (1.7 times the time).
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "nvfp4_quant.cuh"
@@ -20,7 +27,7 @@
 namespace nvfp4 {
 
 struct Fp8PairCfg {
-  // warps 0-3: producer, MMA issuer, waiter, one idle; warps 4-11: epilogue. 384 x 168 registers at
+  // warps 0-3: producer, MMA issuer, two idle; warps 4-11: epilogue. 384 x 168 registers at
   // launch; the epilogue takes what the first warpgroup gives up: 128 x 72 + 256 x 216 = 384 x 168.
   static constexpr int THREADS = 384;
   static constexpr int CONTROL_REGS = 72, EPILOGUE_REGS = 216;
@@ -29,14 +36,12 @@ struct Fp8PairCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int STAGES = 5;
   static constexpr int OUT_BYTES = 8 * 4096;  // one 32-row x 128-byte store box per epilogue warp
-  // per epilogue warp: DEPTH slots of 32 row scales and 128 column scales (or one block's)
+  // COLSCALE, per epilogue warp: DEPTH slots of 32 row scales and 128 column scales
   static constexpr int DEPTH = 4, SCALES = 160;
   static constexpr int SCALE_BYTES = 8 * DEPTH * SCALES * 4;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 1024 + 256;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
-
-constexpr uint32_t kFp8HandoffBarrier = 1;  // waiter and MMA warp
 
 struct Fp8Tile {
   int m0, m_end;  // rows of a and y: [m0, m_end)
@@ -194,79 +199,123 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
       const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
       const int row0 = tl.m0 + rank * 128 + q * 32, row = row0 + lane;
       const int col0 = tl.n0 + h * 128;
-      // The scales of a block of K reach shared memory by cp.async, DEPTH blocks ahead of their use
-      // (a register held for a later block would make the loop wait for its load one block after
-      // issuing it: L2's latency then paces every block). Rows and columns past the tile's copy a
-      // scale inside it; their sums are not stored.
-      const float* sa = p.sa + min(row, tl.m_end - 1);
-      const float* sb = COLSCALE ? tl.sb : tl.sb + static_cast<int64_t>(min(col0, N - 1) >> 7) * KB;
-      auto fetch_scales = [&](int kb) {
-        const int k = min(kb, KB - 1);
-        float* d = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
-        cp_async4(d + lane, sa + static_cast<int64_t>(k) * M);
-        if (COLSCALE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp_async4(d + 32 + lane + 32 * i, sb + static_cast<int64_t>(k) * N + min(col0 + lane + 32 * i, N - 1));
-        } else if (lane == 0) {
-          cp_async4(d + 32, sb + k);
-        }
-        cp_async_commit();
-      };
-      float acc[128];
-#pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-#pragma unroll
-      for (int kb = 0; kb < C::DEPTH - 1; ++kb) fetch_scales(kb);
-#pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
-        __syncwarp();  // the slot that is filled now has been read by all lanes
-        fetch_scales(kb + C::DEPTH - 1);
-        cp_async_wait<C::DEPTH - 1>();
-        __syncwarp();
-        const float* sc = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
-        const float rs = COLSCALE ? sc[lane] : sc[lane] * sc[32];
-        const uint64_t rs2 = f2(rs, rs);
-        if (!mbar_wait_warp(&tfull[buf], bph, abort_flag, wd)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      // One block's 128 columns of this lane's row from TMEM, 32 or 16 columns at a time with the next
+      // chunk's load under this one's arithmetic `add(first column, values)`; the buffer is released
+      // once its last chunk has landed.
+      auto read_block = [&](auto&& add, auto chunk) {
+        constexpr int CHUNK = decltype(chunk)::value, CHUNKS = 128 / CHUNK;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + h * 128;
-        uint32_t r[2][32];
-        tmem_ld32(taddr, r[0]);
-        tmem_ld_wait32(r[0]);
+        uint32_t r[2][CHUNK];
+        auto load = [&](int c, uint32_t* d) {
+          if constexpr (CHUNK == 32)
+            tmem_ld32(taddr + c * CHUNK, d);
+          else
+            tmem_ld16(taddr + c * CHUNK, d);
+        };
+        auto landed = [&](uint32_t* d) {
+          if constexpr (CHUNK == 32)
+            tmem_ld_wait32(d);
+          else
+            tmem_ld_wait16(d);
+        };
+        load(0, r[0]);
+        landed(r[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t* cur = r[c & 1];
-          if (c < 3) {
-            tmem_ld32(taddr + 32 * (c + 1), r[(c + 1) & 1]);
+        for (int c = 0; c < CHUNKS; ++c) {
+          if (c + 1 < CHUNKS) {
+            load(c + 1, r[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
             if (elect_one()) mbar_arrive_cluster(tempty_leader[buf]);
           }
-          if (COLSCALE) {
-            const float4* cv = reinterpret_cast<const float4*>(sc + 32 + 32 * c);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 v = cv[j];
-              float* a = acc + 32 * c + 4 * j;
-              a[0] = fmaf(__uint_as_float(cur[4 * j]) * v.x, rs, a[0]);
-              a[1] = fmaf(__uint_as_float(cur[4 * j + 1]) * v.y, rs, a[1]);
-              a[2] = fmaf(__uint_as_float(cur[4 * j + 2]) * v.z, rs, a[2]);
-              a[3] = fmaf(__uint_as_float(cur[4 * j + 3]) * v.w, rs, a[3]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(cur[j]), rs, acc[32 * c + j]);
-          }
-          if (c < 3) tmem_ld_wait32(r[(c + 1) & 1]);
+          add(c * CHUNK, r[c & 1]);
+          if (c + 1 < CHUNKS) landed(r[(c + 1) & 1]);
         }
         buf ^= 1;
         bph ^= buf == 0;
+      };
+      // the fp32 sums: one by one, or (one scale a block and row) as pairs for packed arithmetic
+      float acc[COLSCALE ? 128 : 1];
+      uint64_t acc2[COLSCALE ? 1 : 64];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) {
+        if (COLSCALE)
+          acc[COLSCALE ? i : 0] = 0.0f;
+        else
+          acc2[COLSCALE ? 0 : i / 2] = 0;
       }
-      cp_async_wait<0>();
+      if constexpr (COLSCALE) {
+        // The scales of a block of K reach shared memory by cp.async, DEPTH - 1 blocks ahead (in
+        // registers they would not fit). Rows and columns past the tile's copy a scale inside it;
+        // their sums are not stored.
+        const float* sa = p.sa + min(row, tl.m_end - 1);
+        auto fetch_scales = [&](int kb) {
+          const int k = min(kb, KB - 1);
+          float* d = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
+          cp_async4(d + lane, sa + static_cast<int64_t>(k) * M);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async4(d + 32 + lane + 32 * i, tl.sb + static_cast<int64_t>(k) * N + min(col0 + lane + 32 * i, N - 1));
+          cp_async_commit();
+        };
+#pragma unroll
+        for (int kb = 0; kb < C::DEPTH - 1; ++kb) fetch_scales(kb);
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb) {
+          __syncwarp();  // the slot that is filled now has been read by all lanes
+          fetch_scales(kb + C::DEPTH - 1);
+          cp_async_wait<C::DEPTH - 1>();
+          __syncwarp();
+          const float* sc = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
+          const float rs = sc[lane];
+          ok = mbar_wait_warp(&tfull[buf], bph, abort_flag, wd);
+          if (!ok) break;
+          tc_fence_after();
+          read_block(
+              [&](int c0, const uint32_t* v) {
+                const float4* cv = reinterpret_cast<const float4*>(sc + 32 + c0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float4 f = cv[j];
+                  float* a = acc + c0 + 4 * j;
+                  a[0] = fmaf(__uint_as_float(v[4 * j]) * f.x, rs, a[0]);
+                  a[1] = fmaf(__uint_as_float(v[4 * j + 1]) * f.y, rs, a[1]);
+                  a[2] = fmaf(__uint_as_float(v[4 * j + 2]) * f.z, rs, a[2]);
+                  a[3] = fmaf(__uint_as_float(v[4 * j + 3]) * f.w, rs, a[3]);
+                }
+              },
+              std::integral_constant<int, 16>());
+        }
+        cp_async_wait<0>();
+      } else {
+        // this row's and the warp's column block's scale, loaded two blocks ahead of their use
+        const bool row_ok = row < tl.m_end;
+        const float* sa = p.sa + row;
+        const float* sb = tl.sb + static_cast<int64_t>(col0 >> 7) * KB;
+        auto row_scale = [&](int kb) { return row_ok && kb < KB ? sa[static_cast<int64_t>(kb) * M] : 0.0f; };
+        auto block_scale = [&](int kb) { return kb < KB && col0 < N ? sb[kb] : 0.0f; };
+        float ra = row_scale(0), rb = row_scale(1), ca = block_scale(0), cb = block_scale(1);
+        for (int kb = 0; kb < KB; ++kb) {
+          const float rs = ra * ca;
+          ra = rb;
+          rb = row_scale(kb + 2);
+          ca = cb;
+          cb = block_scale(kb + 2);
+          ok = mbar_wait_warp(&tfull[buf], bph, abort_flag, wd);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t rs2 = f2(rs, rs);
+          read_block(
+              [&](int c0, const uint32_t* v) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  acc2[c0 / 2 + j] =
+                      f2_fma(f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), rs2, acc2[c0 / 2 + j]);
+              },
+              std::integral_constant<int, 32>());
+        }
+      }
       if (!ok) break;
       // results to y; a grouped tile that ends inside the box's rows must not touch the next expert's
       const bool by_tma = aligned_rows && (!GROUPED || row0 + 32 <= tl.m_end);
@@ -278,14 +327,14 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
             uint32_t w[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
+              // fp32: column 32 b + j; bf16: columns 64 b + 2 j and the next
+              const int i = F32 ? 32 * b + j : 64 * b + 2 * j;
               float lo, hi;
-              if (F32) {
-                lo = hi = acc[32 * b + j];
-                w[j] = __float_as_uint(lo);
-              } else {
-                lo = acc[64 * b + 2 * j], hi = acc[64 * b + 2 * j + 1];
-                w[j] = pack_bf16x2(lo, hi);
-              }
+              if constexpr (COLSCALE)
+                lo = acc[i], hi = acc[F32 ? i : i + 1];
+              else
+                f2_split(acc2[i / 2], lo, hi);
+              w[j] = F32 ? __float_as_uint(!COLSCALE && (i & 1) ? hi : lo) : pack_bf16x2(lo, hi);
             }
             fp8_store_box<F32>(p, box, w, &tmY, by_tma, row0, tl.m_end, c0, N);
           }
@@ -295,52 +344,54 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
     if (lane == 0) bulk_wait_group0();  // this warp's stores are complete before the CTA exits
     __syncwarp();
   } else {
-  regs_dec<C::CONTROL_REGS>();
-  if (warp == 0) {
-    const uint64_t pol = policy_evict_last();
-    int s = 0;
-    uint32_t ph = 0;
-    uint32_t used = 0, phases = 0;  // per stage: requested at all, phase of the last request
-    int issued = 0;
-    for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
-      const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag, wd)) break;
-        // test hook: the first CTA withholds its expect-tx arrival and loads
-        const bool withheld = blockIdx.x == 0 && ++issued == p.drop_stage;
-        if (!withheld && elect_one()) {
-          uint8_t* st = smem + s * C::STAGE_BYTES;
-          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
-          tma_load_2d_pair(st, &tmA, bar, kb * 128, tl.m0 + rank * 128, pol);
-          tma_load_2d_pair(st + C::TILE_BYTES, &tmB, bar, kb * 128, tl.b_row + rank * 128, pol);
-        }
-        __syncwarp();
-        used |= 1u << s;
-        phases = (phases & ~(1u << s)) | ph << s;
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1;
+    regs_dec<C::CONTROL_REGS>();
+    if (warp == 0) {
+      const uint64_t pol = policy_evict_last();
+      int s = 0;
+      uint32_t ph = 0;
+      uint32_t used = 0, phases = 0;  // per stage: requested at all, phase of the last request
+      int issued = 0;
+      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+        const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag, wd)) break;
+          // test hook: the first CTA withholds its expect-tx arrival and loads
+          const bool withheld = blockIdx.x == 0 && ++issued == p.drop_stage;
+          if (!withheld && elect_one()) {
+            uint8_t* st = smem + s * C::STAGE_BYTES;
+            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+            tma_load_2d_pair(st, &tmA, bar, kb * 128, tl.m0 + rank * 128, pol);
+            tma_load_2d_pair(st + C::TILE_BYTES, &tmB, bar, kb * 128, tl.b_row + rank * 128, pol);
+          }
+          __syncwarp();
+          used |= 1u << s;
+          phases = (phases & ~(1u << s)) | ph << s;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
-    }
-    griddep_launch_dependents();
-    // The even CTA's full barriers count both CTAs' bytes: let them all land.
-    if (leader)
-      for (int i = 0; i < STAGES; ++i)
-        if (used >> i & 1) {
-          volatile int32_t dummy = 0;
-          mbar_wait_warp(&full[i], phases >> i & 1, &dummy, wd);
-        }
-  } else if (warp == 1) {
-    if (leader) {
-      const uint32_t idesc = idesc_e4m3(256, 256);
-      int s = 0, buf = 0;
-      for (int t = pair; t < tiles; t += npairs) {
-        for (int kb = 0; kb < KB; ++kb) {
-          const bool ok = named_sync_and(kFp8HandoffBarrier, 64, true);
-          tc_fence_after();
-          if (ok) {
+      griddep_launch_dependents();
+      // The even CTA's full barriers count both CTAs' bytes: let them all land.
+      if (leader)
+        for (int i = 0; i < STAGES; ++i)
+          if (used >> i & 1) {
+            volatile int32_t dummy = 0;
+            mbar_wait_warp(&full[i], phases >> i & 1, &dummy, wd);
+          }
+    } else if (warp == 1) {
+      if (leader) {
+        const uint32_t idesc = idesc_e4m3(256, 256);
+        int s = 0, buf = 0;
+        uint32_t ph = 0, bph = 0;
+        for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+          for (int kb = 0; kb < KB; ++kb) {
+            // the operands first: they normally wait, so that the issue follows the buffer's release
+            if (!mbar_wait_warp(&full[s], ph, abort_flag, wd)) break;
+            if (!mbar_wait_warp(&tempty[buf], bph ^ 1, abort_flag, wd)) break;
+            tc_fence_after();
             if (elect_one()) {
               const uint32_t a_addr = smem_u32(smem + s * C::STAGE_BYTES);
               const uint64_t adesc = desc_sw128(a_addr), bdesc = desc_sw128(a_addr + C::TILE_BYTES);
@@ -351,39 +402,20 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
               tc_commit_pair(&tfull[buf], 3);
             }
             __syncwarp();
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1;
+            }
+            buf ^= 1;
+            bph ^= buf == 0;
           }
-          if (++s == STAGES) s = 0;
-          buf ^= 1;
         }
+        if (elect_one()) tc_commit_pair(drain, 1);
+        __syncwarp();
+        volatile int32_t dummy = 0;
+        mbar_wait_warp(drain, 0, &dummy, wd);
       }
-      if (elect_one()) tc_commit_pair(drain, 1);
-      __syncwarp();
-      volatile int32_t dummy = 0;
-      mbar_wait_warp(drain, 0, &dummy, wd);
     }
-  } else if (warp == 2) {
-    // Owns the waits in front of the MMA warp (a stage's bytes, the TMEM buffer's release) and hands
-    // the verdict over through bar.red: an mbarrier wait costs ~110 cycles even when complete, and
-    // two of them between the issues of two blocks left the tensor core idle for a third of the
-    // time. Both warps run exactly the same iterations, also after an abort, so that the named
-    // barrier, which cannot time out, always pairs.
-    if (leader) {
-      int s = 0, buf = 0;
-      uint32_t ph = 0, bph = 0;
-      for (int t = pair; t < tiles; t += npairs)
-        for (int kb = 0; kb < KB; ++kb) {
-          const bool ok = __all_sync(0xffffffffu, *abort_flag == 0) && mbar_poll_warp(&full[s], ph, abort_flag, wd) &&
-                          mbar_poll_warp(&tempty[buf], bph ^ 1, abort_flag, wd);
-          named_sync_and(kFp8HandoffBarrier, 64, ok);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1;
-          }
-          buf ^= 1;
-          bph ^= buf == 0;
-        }
-    }
-  }
   }
 
   tc_fence_before();

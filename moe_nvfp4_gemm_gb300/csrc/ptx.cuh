@@ -86,18 +86,6 @@ DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uin
   }
 }
 
-// Warp-collective wait for hand-offs that normally complete within a microsecond: a short uniform
-// loop (one try_wait and one vote when the phase is already complete), the clock not read before
-// 128 failed polls, since its read alone costs the warp several hundred cycles.
-DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns);
-DEVI bool mbar_poll_warp(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns) {
-  const uint32_t a = smem_u32(bar);
-#pragma unroll 1
-  for (int i = 0; i < 128; ++i)
-    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
-}
-
 // Warp-collective wait: every lane polls, the result is the same in all lanes.
 DEVI bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int32_t* abort, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
@@ -291,11 +279,6 @@ DEVI uint32_t mapa_shared(uint32_t local_addr, uint32_t rank) {
 // against ~100 for this one, on the critical path of every tile.
 DEVI void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// Arrive on an mbarrier of any CTA in the cluster that publishes this thread's earlier writes.
-DEVI void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // 2-D tiled TMA load issued for a CTA pair: lands in this CTA's shared memory and

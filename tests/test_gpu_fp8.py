@@ -253,6 +253,60 @@ def test_grouped(counts, N, K):
     assert (y[int(off[-1]):] == 7.0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(2600, 5200, 384), (1100, 9000, 144)])
+@pytest.mark.parametrize("b_rows", [128, 1])
+def test_gemm_more_tiles_than_ctas(M, N, K, b_rows):
+    a, sa = m.nvfp4_fp8_quantize(acts(M, K, 1))
+    b, sb = m.nvfp4_fp8_quantize(acts(N, K, 2, 0.02), b_rows)
+    check(m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K, b_block_rows=b_rows), decode(a, sa, 1), decode(b, sb, b_rows))
+
+
+@pytest.mark.parametrize("mean", [6, 30, 60, 130, 600])
+def test_grouped_more_items_than_ctas(mean):
+    """Every kernel form of the grouped product (by rows per expert) with several items per CTA."""
+    E, N, K = 24, 1160, 528
+    g = np.random.default_rng(mean)
+    counts = [int(v) for v in g.poisson(mean, E)]
+    counts[3] = 0
+    counts[7] = 2 * mean + 33  # more rows than a tile
+    off, rows, a, sa, b, sb = grouped_case(counts, N, K, mean, tail=2)
+    y = m.nvfp4_fp8_grouped_gemm(a, sa, b, sb, off.to(dev()), E, rows, N, K)
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if counts[e]:
+            check(y[r], decode(a[r], sa[:, r].contiguous(), 1), decode(b[e], sb[e], 128))
+
+
+def test_withheld_stage_is_reported_and_the_next_call_is_right():
+    """The pipeline waits are bounded: a stage that never arrives ends in a status, not a hang."""
+    cases = [(7, 520, 1024, 0), (7, 520, 1024, 1), (300, 520, 1024, 0)]  # streaming, split along K; tiles
+    try:
+        for M, N, K, split in cases:
+            a, sa = m.nvfp4_fp8_quantize(acts(M, K, 1))
+            b, sb = m.nvfp4_fp8_quantize(acts(N, K, 2, 0.02), 128)
+            m.nvfp4_tune(m.NVFP4_TUNE_STREAM_SPLIT, split)
+            m.nvfp4_tune(m.NVFP4_TUNE_WATCHDOG_US, 20000)
+            m.nvfp4_tune(m.NVFP4_TUNE_TEST_WITHHOLD_STAGE, 2)
+            st = torch.zeros(1, dtype=torch.int32, device=dev())
+            m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K, dev_status=st)
+            torch.cuda.synchronize()
+            assert st.item() == -7
+            m.nvfp4_tune(m.NVFP4_TUNE_TEST_WITHHOLD_STAGE, 0)
+            st.zero_()
+            y = m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K, dev_status=st)
+            assert st.item() == 0
+            check(y, decode(a, sa, 1), decode(b, sb, 128))
+        off, rows, a, sa, b, sb = grouped_case([5, 9, 200], 260, 512, 3)
+        m.nvfp4_tune(m.NVFP4_TUNE_TEST_WITHHOLD_STAGE, 1)
+        st = torch.zeros(1, dtype=torch.int32, device=dev())
+        m.nvfp4_fp8_grouped_gemm(a, sa, b, sb, off.to(dev()), 3, rows, 260, 512, dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() == -7
+    finally:
+        for key in (m.NVFP4_TUNE_STREAM_SPLIT, m.NVFP4_TUNE_WATCHDOG_US, m.NVFP4_TUNE_TEST_WITHHOLD_STAGE):
+            m.nvfp4_tune(key, 0)
+
+
 @pytest.mark.parametrize("bad", [[0, 5, 3, 8], [1, 2, 3, 8], [0, 2, 4, 9], [0, -1, 4, 8]])
 def test_grouped_bad_offsets_are_reported(bad):
     off, rows, a, sa, b, sb = grouped_case([2, 3, 3], 128, 256, 5)
