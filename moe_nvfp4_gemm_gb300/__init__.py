@@ -11,7 +11,6 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import NamedTuple
 
 import torch
 
@@ -463,17 +462,72 @@ NVFP4_MOE_MAX_TOPK = 32
 _FLOAT_TYPES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32}
 
 
-class MoeRouting(NamedTuple):
-    """What nvfp4_moe_route returns (T tokens, k slots each, E experts)."""
-    topk_idx: torch.Tensor        # int32 [T, k]: selected experts, -1 in empty slots
-    topk_w: torch.Tensor          # fp32 [T, k]: their weights
-    slot_row: torch.Tensor        # int32 [T, k]: routed row of each slot, -1 in empty slots
-    counts: torch.Tensor          # int32 [E]: rows per expert
-    expert_offsets: torch.Tensor  # int32 [E + 1]: as the grouped GEMMs read them
-    row_token: torch.Tensor       # int32 [T * k]: token of each routed row, -1 past the last
-    mean_prob: torch.Tensor       # fp32 [E]: mean probability over the routed tokens
-    balance_loss: torch.Tensor    # fp32 [1]
-    routed_tokens: torch.Tensor   # int32 [1]
+class MoeRouting:
+    """What nvfp4_moe_route returns (T tokens, k slots each, E experts): tensors that share one
+    allocation, as attributes made when they are first asked for (a call's host time is mostly
+    that of making tensors).
+
+    topk_idx        int32 [T, k]: selected experts, -1 in empty slots
+    topk_w          fp32 [T, k]: their weights
+    slot_row        int32 [T, k]: routed row of each slot, -1 in empty slots
+    row_token       int32 [T * k]: token of each routed row, -1 past the last
+    counts          int32 [E]: rows per expert
+    expert_offsets  int32 [E + 1]: as the grouped GEMMs read them
+    mean_prob       fp32 [E]: mean probability over the routed tokens
+    balance_loss    fp32 [1]
+    routed_tokens   int32 [1]
+    """
+    _fields = ("topk_idx", "topk_w", "slot_row", "counts", "expert_offsets", "row_token", "mean_prob", "balance_loss",
+               "routed_tokens")
+
+    def __init__(self, T, E, k, device, workspace_words):
+        n = T * max(k, 0)
+        self.T, self.E, self.k = T, E, k
+        self._all = None
+        # field: first word in the allocation
+        self._at = {"topk_idx": 0, "topk_w": n, "slot_row": 2 * n, "row_token": 3 * n, "counts": 4 * n,
+                    "expert_offsets": 4 * n + E, "mean_prob": 4 * n + 2 * E + 1, "balance_loss": 4 * n + 3 * E + 1,
+                    "routed_tokens": 4 * n + 3 * E + 2}
+        words = (4 * n + 3 * E + 6) // 4 * 4
+        self._buf = torch.empty(words + workspace_words, dtype=torch.int32, device=device)
+        self._base = self._buf.data_ptr()
+        self._workspace = self._base + 4 * words
+
+    def _address(self, field):
+        return self._base + 4 * self._at[field]
+
+    def _make(self, name):
+        buf = self._buf.view(torch.float32) if name in ("topk_w", "mean_prob", "balance_loss") else self._buf
+        if name in ("topk_idx", "topk_w", "slot_row"):
+            return buf.as_strided((self.T, self.k), (self.k, 1), self._at[name])
+        n = {"row_token": self.T * self.k, "counts": self.E, "expert_offsets": self.E + 1, "mean_prob": self.E}.get(name, 1)
+        return buf.as_strided((n,), (1,), self._at[name])
+
+    def __getattr__(self, name):  # only for what is not there yet
+        if name not in MoeRouting._fields:
+            raise AttributeError(name)
+        t = self.__dict__[name] = self._make(name)
+        return t
+
+    def _asdict(self):
+        if self._all is None:
+            T, E, k, at, b = self.T, self.E, self.k, self._at, self._buf.as_strided
+            f = self._buf.view(torch.float32).as_strided
+            per, row, one, n = (T, k), (k, 1), (1,), T * k
+            made = {"topk_idx": b(per, row, 0), "topk_w": f(per, row, n), "slot_row": b(per, row, 2 * n),
+                    "counts": b((E,), one, at["counts"]), "expert_offsets": b((E + 1,), one, at["expert_offsets"]),
+                    "row_token": b((n,), one, 3 * n), "mean_prob": f((E,), one, at["mean_prob"]),
+                    "balance_loss": f(one, one, at["balance_loss"]), "routed_tokens": b(one, one, at["routed_tokens"])}
+            have = self.__dict__
+            for field in made:  # those handed out before stay
+                if field in have:
+                    made[field] = have[field]
+            have.update(made)
+            self._all = made
+        return dict(self._all)
+
+    def __iter__(self):
+        return iter(self._asdict().values())
 
 
 def _route_inputs(logits, valid):
@@ -495,30 +549,16 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
     """Softmax router: top-k experts and weights of each token, per-expert counts and offsets, the
     expert-sorted row lists that the grouped GEMMs read, and the load-balance loss."""
     T, E = _route_inputs(logits, valid)
-    n = T * max(k, 0)
     ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
-    # one allocation: the outputs as consecutive 4-byte words, then the workspace
-    at_w, at_slot, at_row = n, 2 * n, 3 * n
-    at_counts = 4 * n
-    at_off = at_counts + E
-    at_mean = at_off + E + 1
-    at_loss = at_mean + E
-    at_routed = at_loss + 1
-    at_ws = (at_routed + 1 + 3) // 4 * 4
-    buf = torch.empty(at_ws + (ws_bytes // 4 if workspace is None else 0), dtype=torch.int32, device=logits.device)
-    p = buf.data_ptr()
-    ws = p + 4 * at_ws if workspace is None else workspace.data_ptr()
+    r = MoeRouting(T, E, k, logits.device, ws_bytes // 4 if workspace is None else 0)
+    at = r._address
     _check("nvfp4_moe_route",
            lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
-                                 p, p + 4 * at_w, p + 4 * at_slot, p + 4 * at_counts, p + 4 * at_off, p + 4 * at_row,
-                                 p + 4 * at_mean, p + 4 * at_loss, p + 4 * at_routed, ws,
+                                 at("topk_idx"), at("topk_w"), at("slot_row"), at("counts"), at("expert_offsets"),
+                                 at("row_token"), at("mean_prob"), at("balance_loss"), at("routed_tokens"),
+                                 r._workspace if workspace is None else workspace.data_ptr(),
                                  ws_bytes if workspace is None else workspace.numel(), _stream(stream)))
-    real = buf.view(torch.float32)
-    per, row = (T, k), (k, 1)
-    return MoeRouting(buf.as_strided(per, row, 0), real.as_strided(per, row, at_w), buf.as_strided(per, row, at_slot),
-                      buf.as_strided((E,), (1,), at_counts), buf.as_strided((E + 1,), (1,), at_off),
-                      buf.as_strided((n,), (1,), at_row), real.as_strided((E,), (1,), at_mean),
-                      real.as_strided((1,), (1,), at_loss), buf.as_strided((1,), (1,), at_routed))
+    return r
 
 
 def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None, d_loss=None,
@@ -526,22 +566,22 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
     """Gradient of nvfp4_moe_route's logits (arguments as in that call) from the gradients of the
     weights topk_w (d_w, fp32 [T, k]) and of the balance loss (d_loss, fp32 [1])."""
     T, E = _route_inputs(logits, valid)
-    k = routing.topk_idx.shape[1]
-    for t, dt, shape, n in ((routing.topk_idx, torch.int32, (T, k), "topk_idx"),
-                            (routing.topk_w, torch.float32, (T, k), "topk_w"),
-                            (routing.counts, torch.int32, (E,), "counts"),
-                            (routing.routed_tokens, torch.int32, (1,), "routed_tokens"),
-                            (d_w, torch.float32, (T, k), "d_w"), (d_loss, torch.float32, (1,), "d_loss")):
+    k = routing.k
+    if (routing.T, routing.E) != (T, E):
+        raise TypeError(f"routing is of {routing.T} tokens and {routing.E} experts, logits of {T} and {E}")
+    for t, shape, n in ((d_w, (T, k), "d_w"), (d_loss, (1,), "d_loss")):
         if t is not None:
-            _cuda(t, dt, n)
+            _cuda(t, torch.float32, n)
             if tuple(t.shape) != shape:
                 raise TypeError(f"{n} must have shape {shape}")
     d_logits = torch.empty_like(logits) if d_logits is None else _cuda(d_logits, logits.dtype, "d_logits")
+    _holds(d_logits, T * E, "d_logits")
+    at = routing._address
     _check("nvfp4_moe_route_backward",
-           lib().nvfp4_moe_route_backward(_ptr(logits), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
-                                          int(renormalize), _ptr(routing.topk_idx), _ptr(routing.topk_w),
-                                          _ptr(routing.counts), _ptr(routing.routed_tokens), _ptr(d_w), _ptr(d_loss),
-                                          _ptr(d_logits), _stream(stream)))
+           lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
+                                          int(renormalize), at("topk_idx"), at("topk_w"), at("counts"),
+                                          at("routed_tokens"), _ptr(d_w), _ptr(d_loss), d_logits.data_ptr(),
+                                          _stream(stream)))
     return d_logits
 
 
