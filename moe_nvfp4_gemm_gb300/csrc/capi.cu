@@ -1014,7 +1014,7 @@ static int check_fp8_shape(int64_t M, int64_t N, int64_t K) {
 }
 
 // Launches the pair kernel on `tiles` 256 x 256 tiles (grouped: at most that many).
-static int run_fp8_pair(const uint8_t* a, const uint8_t* b, int64_t b_rows_total, const Fp8GemmArgs& p, int64_t tiles,
+static int run_fp8_pair(const uint8_t* a, const uint8_t* b, int64_t b_rows_total, Fp8GemmArgs p, int64_t tiles,
                         int sms, cudaStream_t st) {
   CUtensorMap tmA, tmB, tmY;
   int rc;
@@ -1023,9 +1023,20 @@ static int run_fp8_pair(const uint8_t* a, const uint8_t* b, int64_t b_rows_total
   tmY = tmA;  // unused when y's rows are not 16-byte aligned
   if (p.N % (p.f32 ? 4 : 8) == 0 && (rc = encode_out(&tmY, p.y, p.M, p.N, p.f32 != 0))) return rc;
   int64_t pairs = (g_tune.dense_grid ? g_tune.dense_grid : sms) / 2;
-  if (pairs > tiles) pairs = tiles;
+  // K in parts for few tiles of many blocks: the exchange of the parts costs 4-6 us. Two where the
+  // pairs have a place (256 x 8192 x 8192, 32 tiles: 32 -> 23.5 us; 256 x 4096 x 6144: 25 -> 18; at 17
+  // blocks nothing), four for up to 8 tiles (300 x 777 x 4096: 18.8 -> 15.0 -> 13.1; with 16 tiles the
+  // clusters of eight CTAs do not fit at once: 18 -> 29).
+  const int64_t kb = (p.K + 127) / 128;
+  p.split = 1;
+  if (!p.tiles) {
+    if (kb >= 24 && tiles * 2 <= pairs) p.split = tiles <= 8 ? 4 : 2;
+    if (g_tune.stream_split) p.split = g_tune.stream_split >= 4 ? 4 : (g_tune.stream_split >= 2 ? 2 : 1);
+    if (p.split > kb) p.split = 1;
+  }
+  if (pairs > tiles || p.split > 1) pairs = tiles;
   if (pairs < 1) pairs = 1;
-  return from_cuda(launch_fp8_gemm_pair(tmA, tmB, tmY, p, static_cast<int>(2 * pairs), st));
+  return from_cuda(launch_fp8_gemm_pair(tmA, tmB, tmY, p, static_cast<int>(2 * pairs * p.split), st));
 }
 
 int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int32_t b_block_rows,
@@ -1056,10 +1067,12 @@ int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const fl
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int max_m = g_tune.stream_max_m == 0 ? 128 : g_tune.stream_max_m;
+  // Up to 64 rows the streaming kernel (64 x 4096 x 6144: 12.6 us, tiles 18.4; 64 x 8192 x 8192: both 23),
+  // above it tiles (128 x 28672 x 8192: 68 us; streaming with 128 token columns took 94).
+  const int max_m = g_tune.stream_max_m == 0 || g_tune.stream_max_m > 64 ? 64 : g_tune.stream_max_m;
   if (M <= max_m) {
     const int64_t ntw = (N + 127) / 128, kb = (K + 127) / 128;
-    const int tile_rows = M <= 32 ? 32 : (M <= 64 ? 64 : 128);
+    const int tile_rows = M <= 32 ? 32 : 64;
     // As many CTAs along K as fill the resident slots (two per SM up to 32 tokens, else one), with
     // at least four blocks each: K = 2064 in 4 parts 6.2 us, in 7 parts 9.5 us.
     int64_t split = (tile_rows == 32 ? 2 : 1) * int64_t(d.sms) / ntw;
@@ -1125,11 +1138,17 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   p.b_rows = 128;
   p.tiles = tiles;
   p.n_tiles = n_tiles;
-  // Token tiles: experts with few rows each go to the streaming kernel, in tiles that most
-  // experts fit in once (an expert with more rows streams its weights once per tile).
+  // Token tiles by the mean rows of an expert. The streaming kernel, whose time grows with every
+  // further tile of an expert (its weights are read again), in tiles of 32 rows up to a mean of 16
+  // and 64 up to 56; then 256-row tiles. Measured, us, for 256 experts of 6144 x 2048:
+  //   mean rows     8     16     24     32     48     64     96    128
+  //   32 rows     488    503    578    685    880   1053
+  //   64 rows     486    483    501    516    595    743   1025
+  //   256 rows    653    675    681    691    690    696    712    745
+  // and for 64 of 4096 x 2048, two tiles of 32 an SM ahead of one of 64: 16: 86 / 90, 48: 106 / 108 / 131.
   const int64_t mean = (M_total + E - 1) / E;
-  const bool tile_kernel = mean > 72;
-  const int tile_rows = tile_kernel ? 256 : (mean <= 20 ? 32 : (mean <= 48 ? 64 : 128));
+  const bool tile_kernel = mean > 56;
+  const int tile_rows = tile_kernel ? 256 : (mean <= 16 ? 32 : 64);
   p.max_tiles = static_cast<int>(fp8_max_tiles(E, M_total, tile_rows));
   p.status = dev_status;
   p.watchdog_ns = watchdog_ns();

@@ -129,7 +129,11 @@ DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, const uint32_t (&w)[
 
 // COLSCALE: one scale per row of b (a column of y), staged per warp in shared memory and applied
 // before the row scale; otherwise one per 128 rows of b, which a warp's 128 columns share.
-template <bool COLSCALE, bool GROUPED, bool F32>
+//
+// SPLIT > 1: K in SPLIT parts, for products of few tiles. The SPLIT pairs of a cluster sum one tile's
+// parts, then each CTA gets a SPLIT-th of its rows' columns from all of them through distributed
+// shared memory, adds them in the order of K and stores them (one tile per cluster).
+template <bool COLSCALE, bool GROUPED, bool F32, int SPLIT>
 __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
     k_fp8_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Fp8GemmArgs p) {
@@ -149,7 +153,9 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t wd = p.watchdog_ns;
-  const uint32_t rank = cluster_ctarank();
+  // pair `part` of the cluster: its even CTA, which issues the MMAs, has cluster rank `lead`
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
+  const int part = static_cast<int>(crank >> 1);
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -183,14 +189,16 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
   const int mt = (M + 255) / 256;
   const int KB = static_cast<int>((p.K + 127) / 128);
   const int tiles = GROUPED ? p.n_tiles[0] * nt : mt * nt;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int pair = blockIdx.x / (2 * SPLIT), npairs = gridDim.x / (2 * SPLIT);
+  // this pair's blocks of K
+  const int kb_begin = SPLIT > 1 ? KB * part / SPLIT : 0, kb_end = SPLIT > 1 ? KB * (part + 1) / SPLIT : KB;
 
   if (warp >= 4) {
     regs_inc<C::EPILOGUE_REGS>();
     const int q = warp & 3, h = (warp - 4) >> 2;
     uint8_t* box = out_buf + (warp - 4) * 4096;
     float* cs = scale_buf + (warp - 4) * C::DEPTH * C::SCALES;
-    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), lead), mapa_shared(smem_u32(&tempty[1]), lead)};
     const bool aligned_rows = N % (F32 ? 4 : 8) == 0;
     int buf = 0;
     uint32_t bph = 0;
@@ -260,9 +268,9 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
           cp_async_commit();
         };
 #pragma unroll
-        for (int kb = 0; kb < C::DEPTH - 1; ++kb) fetch_scales(kb);
+        for (int i = 0; i < C::DEPTH - 1; ++i) fetch_scales(kb_begin + i);
 #pragma unroll 1
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           __syncwarp();  // the slot that is filled now has been read by all lanes
           fetch_scales(kb + C::DEPTH - 1);
           cp_async_wait<C::DEPTH - 1>();
@@ -295,8 +303,8 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
         const float* sb = tl.sb + static_cast<int64_t>(col0 >> 7) * KB;
         auto row_scale = [&](int kb) { return row_ok && kb < KB ? sa[static_cast<int64_t>(kb) * M] : 0.0f; };
         auto block_scale = [&](int kb) { return kb < KB && col0 < N ? sb[kb] : 0.0f; };
-        float ra = row_scale(0), rb = row_scale(1), ca = block_scale(0), cb = block_scale(1);
-        for (int kb = 0; kb < KB; ++kb) {
+        float ra = row_scale(kb_begin), rb = row_scale(kb_begin + 1), ca = block_scale(kb_begin), cb = block_scale(kb_begin + 1);
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           const float rs = ra * ca;
           ra = rb;
           rb = row_scale(kb + 2);
@@ -315,6 +323,73 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
               },
               std::integral_constant<int, 32>());
         }
+      }
+      if constexpr (SPLIT > 1) {
+        // Every CTA's ring is free once all its roles are here: it takes the parts of the columns that
+        // this CTA stores, [part][warp][4 columns][row, 16 bytes; padded so that a row's columns lie in
+        // different banks]. Also after an abort (then garbage, not stored), so that the cluster's
+        // barriers pair.
+        constexpr int OWN = 128 / SPLIT;  // columns of each warp's 128 that a CTA stores
+        constexpr int GROUP = 32 * 4 + 4, WARP_FLOATS = OWN / 4 * GROUP;
+        static_assert(SPLIT * 8 * WARP_FLOATS * 4 <= STAGES * C::STAGE_BYTES, "exchange area");
+        float* recv = reinterpret_cast<float*>(smem);
+        __syncwarp();
+        cluster_sync();
+        auto value = [&](int i) {
+          if constexpr (COLSCALE) {
+            return acc[i];
+          } else {
+            float lo, hi;
+            f2_split(acc2[i / 2], lo, hi);
+            return (i & 1) ? hi : lo;
+          }
+        };
+#pragma unroll
+        for (int o = 0; o < SPLIT; ++o) {
+          const uint32_t dst = mapa_shared(smem_u32(recv + (part * 8 + warp - 4) * WARP_FLOATS + lane * 4), 2 * o + rank);
+#pragma unroll
+          for (int c = 0; c < OWN; c += 4)
+            st_shared_cluster_v4(dst + c * GROUP, value(o * OWN + c), value(o * OWN + c + 1), value(o * OWN + c + 2),
+                                 value(o * OWN + c + 3));
+        }
+        __syncwarp();
+        cluster_sync();
+        if (ok && !*abort_flag) {
+          // a row at a time (two of 32 columns), lanes along the columns, the parts added in the order of K
+          constexpr int PER = F32 ? 1 : 2, LANES = OWN / PER < 32 ? OWN / PER : 32;  // columns a lane, lanes a row
+          const int c_first = col0 + part * OWN;
+          const bool paired = N % 2 == 0;
+#pragma unroll 4
+          for (int r = lane / LANES; r < 32; r += 32 / LANES) {
+            if (row0 + r >= tl.m_end) continue;
+            const int64_t at = static_cast<int64_t>(row0 + r) * N + c_first;
+#pragma unroll
+            for (int c0 = 0; c0 < OWN; c0 += LANES * PER) {
+              const int c = c0 + (lane % LANES) * PER;
+              const float* src = recv + (warp - 4) * WARP_FLOATS + (c >> 2) * GROUP + r * 4 + (c & 3);
+              float v[PER];
+#pragma unroll
+              for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+#pragma unroll
+              for (int s = 0; s < SPLIT; ++s)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) v[j] += src[s * 8 * WARP_FLOATS + j];
+              if constexpr (F32) {
+                if (c_first + c < N) static_cast<float*>(p.y)[at + c] = v[0];
+              } else {
+                const uint32_t w = pack_bf16x2(v[0], v[1]);
+                uint16_t* y = static_cast<uint16_t*>(p.y) + at + c;
+                if (paired) {
+                  if (c_first + c < N) *reinterpret_cast<uint32_t*>(y) = w;
+                } else {
+                  if (c_first + c < N) y[0] = static_cast<uint16_t>(w & 0xFFFFu);
+                  if (c_first + c + 1 < N) y[1] = static_cast<uint16_t>(w >> 16);
+                }
+              }
+            }
+          }
+        }
+        break;
       }
       if (!ok) break;
       // results to y; a grouped tile that ends inside the box's rows must not touch the next expert's
@@ -353,13 +428,13 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
       int issued = 0;
       for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
         const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag, wd)) break;
           // test hook: the first CTA withholds its expect-tx arrival and loads
           const bool withheld = blockIdx.x == 0 && ++issued == p.drop_stage;
           if (!withheld && elect_one()) {
             uint8_t* st = smem + s * C::STAGE_BYTES;
-            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+            const uint32_t bar = mapa_shared(smem_u32(&full[s]), lead);
             if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
             tma_load_2d_pair(st, &tmA, bar, kb * 128, tl.m0 + rank * 128, pol);
             tma_load_2d_pair(st + C::TILE_BYTES, &tmB, bar, kb * 128, tl.b_row + rank * 128, pol);
@@ -387,7 +462,7 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
         int s = 0, buf = 0;
         uint32_t ph = 0, bph = 0;
         for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
-          for (int kb = 0; kb < KB; ++kb) {
+          for (int kb = kb_begin; kb < kb_end; ++kb) {
             // the operands first: they normally wait, so that the issue follows the buffer's release
             if (!mbar_wait_warp(&full[s], ph, abort_flag, wd)) break;
             if (!mbar_wait_warp(&tempty[buf], bph ^ 1, abort_flag, wd)) break;
@@ -398,8 +473,8 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 tc_mma_f8_pair(tmem + buf * 256, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0);
-              tc_commit_pair(&empty[s], 3);
-              tc_commit_pair(&tfull[buf], 3);
+              tc_commit_pair(&empty[s], 3u << lead);
+              tc_commit_pair(&tfull[buf], 3u << lead);
             }
             __syncwarp();
             if (++s == STAGES) {
@@ -410,11 +485,16 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
             bph ^= buf == 0;
           }
         }
-        if (elect_one()) tc_commit_pair(drain, 1);
+        if (elect_one()) tc_commit_pair(drain, 1u << lead);
         __syncwarp();
         volatile int32_t dummy = 0;
         mbar_wait_warp(drain, 0, &dummy, wd);
       }
+    }
+    if constexpr (SPLIT > 1) {  // the epilogue warps' two barriers around the exchange of the parts
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
     }
   }
 
@@ -495,15 +575,21 @@ cudaError_t launch_fp8_tiles(const int32_t* offsets, int E, int M, int tile_rows
   return cudaLaunchKernelEx(&cfg, k_fp8_tiles, offsets, E, M, tile_rows, tiles, n_tiles, status);
 }
 
+template <bool COLSCALE, bool F32>
+static auto pick_fp8_pair(int split) -> void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Fp8GemmArgs) {
+  return split == 4 ? k_fp8_gemm_pair<COLSCALE, false, F32, 4>
+                    : (split == 2 ? k_fp8_gemm_pair<COLSCALE, false, F32, 2> : k_fp8_gemm_pair<COLSCALE, false, F32, 1>);
+}
+
 cudaError_t launch_fp8_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmY,
                                  const Fp8GemmArgs& p, int grid, cudaStream_t st) {
   void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Fp8GemmArgs);
   if (p.tiles)
-    kernel = k_fp8_gemm_pair<false, true, false>;
+    kernel = k_fp8_gemm_pair<false, true, false, 1>;
   else if (p.b_rows == 1)
-    kernel = p.f32 ? k_fp8_gemm_pair<true, false, true> : k_fp8_gemm_pair<true, false, false>;
+    kernel = p.f32 ? pick_fp8_pair<true, true>(p.split) : pick_fp8_pair<true, false>(p.split);
   else
-    kernel = p.f32 ? k_fp8_gemm_pair<false, false, true> : k_fp8_gemm_pair<false, false, false>;
+    kernel = p.f32 ? pick_fp8_pair<false, true>(p.split) : pick_fp8_pair<false, false>(p.split);
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kernel));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -513,7 +599,7 @@ cudaError_t launch_fp8_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = p.tiles ? 2 : 2 * p.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;

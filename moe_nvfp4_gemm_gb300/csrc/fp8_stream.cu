@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, Fp8StreamCfg<NT>::C
       // warp 3: the scales, a group of blocks at a time and up to GROUPS groups ahead of the epilogue.
       // A load issued now queues behind the TMA loads that the SM has in flight; in the epilogue
       // warps its latency paced every block (M = 33, 8192 x 8192: 24 us, 20 us in two halves of K).
-      constexpr int NX = NT / 32, U = MODE == kFp8DenseRowScale ? 2 : (NT == 128 ? 4 : 8);  // blocks per batch of loads
+      constexpr int NX = NT / 32, U = MODE == kFp8DenseRowScale ? 2 : 8;  // blocks per batch of loads
       int grp = 0;
       uint32_t gph = 0;
       bool ok = true;
@@ -458,7 +458,7 @@ static cudaError_t launch_fp8_stream_t(const CUtensorMap& tmW, const CUtensorMap
   return cudaGetLastError();
 }
 
-// Token tiles of `tile_rows` (32, 64, 128) rows; tmX has 32-row boxes.
+// Token tiles of `tile_rows` (32 or 64) rows; tmX has 32-row boxes.
 cudaError_t launch_fp8_stream(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int tile_rows,
                               int sms, cudaStream_t st) {
   const int NTW = static_cast<int>((p.N + 127) / 128);
@@ -466,23 +466,18 @@ cudaError_t launch_fp8_stream(const CUtensorMap& tmW, const CUtensorMap& tmX, co
     const int64_t items = static_cast<int64_t>(p.max_tiles) * NTW;
     const int64_t slots = (tile_rows == 32 ? 2 : 1) * static_cast<int64_t>(sms);
     const int grid = static_cast<int>(items < slots ? items : slots);
-    switch (tile_rows) {
-      case 32: return launch_fp8_stream_t<32, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
-      case 64: return launch_fp8_stream_t<64, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
-      default: return launch_fp8_stream_t<128, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
-    }
+    if (tile_rows == 32) return launch_fp8_stream_t<32, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
+    return launch_fp8_stream_t<64, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
   }
   const int M = static_cast<int>(p.M), m_own = (M + p.split - 1) / p.split;
   const int recv = p.split > 1 ? p.split * m_own * 512 : 0;
   const int grid = NTW * p.split;
   if (p.b_rows == 1) {
     if (tile_rows == 32) return launch_fp8_stream_t<32, kFp8DenseRowScale>(tmW, tmX, p, grid, recv, st);
-    if (tile_rows == 64) return launch_fp8_stream_t<64, kFp8DenseRowScale>(tmW, tmX, p, grid, recv, st);
-    return launch_fp8_stream_t<128, kFp8DenseRowScale>(tmW, tmX, p, grid, recv, st);
+    return launch_fp8_stream_t<64, kFp8DenseRowScale>(tmW, tmX, p, grid, recv, st);
   }
   if (tile_rows == 32) return launch_fp8_stream_t<32, kFp8Dense>(tmW, tmX, p, grid, recv, st);
-  if (tile_rows == 64) return launch_fp8_stream_t<64, kFp8Dense>(tmW, tmX, p, grid, recv, st);
-  return launch_fp8_stream_t<128, kFp8Dense>(tmW, tmX, p, grid, recv, st);
+  return launch_fp8_stream_t<64, kFp8Dense>(tmW, tmX, p, grid, recv, st);
 }
 
 }  // namespace nvfp4

@@ -272,6 +272,12 @@ DEVI uint32_t mapa_shared(uint32_t local_addr, uint32_t rank) {
   return r;
 }
 
+// Sixteen bytes into any CTA's shared memory of the cluster.
+DEVI void st_shared_cluster_v4(uint32_t cluster_addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+
 // Relaxed arrive on an mbarrier of any CTA in the cluster. Used only to hand a
 // drained TMEM accumulator back to the MMA issuer: the tcgen05.ld reads are already
 // complete (tcgen05.wait::ld) when the arrive executes, so no memory needs to be
