@@ -153,7 +153,7 @@ def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     # the current stream's handle without the Stream object (3 us of a small call's host time)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(fn, rc):
@@ -462,6 +462,21 @@ NVFP4_MOE_MAX_TOPK = 32
 _FLOAT_TYPES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32}
 
 
+_FP8_TYPES = (torch.float8_e4m3fn, torch.uint8)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+
+
+def _operand(t, types, n, name):
+    """t's address; t must be a contiguous CUDA tensor of one of `types` with at least n elements."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in types and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, types))}")
+    if t.numel() < n:
+        raise TypeError(f"{name} holds {t.numel()} elements, needs {n}")
+    return t.data_ptr()
+
+
 class MoeRouting:
     """What nvfp4_moe_route returns (T tokens, k slots each, E experts): tensors that share one
     allocation, as attributes made when they are first asked for (a call's host time is mostly
@@ -500,7 +515,8 @@ class MoeRouting:
         buf = self._buf.view(torch.float32) if name in ("topk_w", "mean_prob", "balance_loss") else self._buf
         if name in ("topk_idx", "topk_w", "slot_row"):
             return buf.as_strided((self.T, self.k), (self.k, 1), self._at[name])
-        n = {"row_token": self.T * self.k, "counts": self.E, "expert_offsets": self.E + 1, "mean_prob": self.E}.get(name, 1)
+        n = {"row_token": self.T * self.k, "counts": self.E, "expert_offsets": self.E + 1,
+             "mean_prob": self.E}.get(name, 1)
         return buf.as_strided((n,), (1,), self._at[name])
 
     def __getattr__(self, name):  # only for what is not there yet
@@ -556,7 +572,7 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
            lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
                                  at("topk_idx"), at("topk_w"), at("slot_row"), at("counts"), at("expert_offsets"),
                                  at("row_token"), at("mean_prob"), at("balance_loss"), at("routed_tokens"),
-                                 r._workspace if workspace is None else workspace.data_ptr(),
+                                 r._workspace if workspace is None else _operand(workspace, _U8, 0, "workspace"),
                                  ws_bytes if workspace is None else workspace.numel(), _stream(stream)))
     return r
 
@@ -574,27 +590,14 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
             _cuda(t, torch.float32, n)
             if tuple(t.shape) != shape:
                 raise TypeError(f"{n} must have shape {shape}")
-    d_logits = torch.empty_like(logits) if d_logits is None else _cuda(d_logits, logits.dtype, "d_logits")
-    _holds(d_logits, T * E, "d_logits")
+    d_logits = torch.empty_like(logits) if d_logits is None else d_logits
     at = routing._address
     _check("nvfp4_moe_route_backward",
            lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
                                           int(renormalize), at("topk_idx"), at("topk_w"), at("counts"),
-                                          at("routed_tokens"), _ptr(d_w), _ptr(d_loss), d_logits.data_ptr(),
-                                          _stream(stream)))
+                                          at("routed_tokens"), _ptr(d_w), _ptr(d_loss),
+                                          _operand(d_logits, (logits.dtype,), T * E, "d_logits"), _stream(stream)))
     return d_logits
-
-
-def _fp8(t, name):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in (torch.float8_e4m3fn, torch.uint8)
-            and t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous CUDA tensor of torch.float8_e4m3fn (or uint8 codes)")
-    return t
-
-
-def _holds(t, n, name):
-    if t.numel() < n:
-        raise TypeError(f"{name} holds {t.numel()} elements, needs {n}")
 
 
 def _blocks(n):
@@ -632,21 +635,17 @@ def nvfp4_fp8_gemm(a, sa, b, sb, M: int, N: int, K: int, b_block_rows: int = 128
                    dev_status=None, stream=None):
     """y = a b^T [M, N] in bf16 or fp32 from E4M3 codes a [M, K], b [N, K] and their block scales
     (see nvfp4_fp8_quantize; b_block_rows: rows of b that share a scale, 128 or 1)."""
-    _fp8(a, "a")
-    _fp8(b, "b")
-    _cuda(sa, torch.float32, "sa")
-    _cuda(sb, torch.float32, "sb")
-    if out_dtype not in _FLOAT_TYPES:
+    y_type = _FLOAT_TYPES.get(out_dtype)
+    if y_type is None:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-    _holds(a, M * K, "a")
-    _holds(b, N * K, "b")
-    _holds(sa, _blocks(K) * M, "sa")
-    _holds(sb, _blocks(K) * (N if b_block_rows == 1 else _blocks(N)), "sb")
-    y = torch.empty((M, N), dtype=out_dtype, device=a.device) if y is None else _cuda(y, out_dtype, "y")
-    _holds(y, M * N, "y")
+    kb = _blocks(K)
+    pa = _operand(a, _FP8_TYPES, M * K, "a")
+    y = torch.empty((M, N), dtype=out_dtype, device=a.device) if y is None else y
     _check("nvfp4_fp8_gemm",
-           lib().nvfp4_fp8_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), b_block_rows, _ptr(y), _FLOAT_TYPES[out_dtype],
-                                M, N, K, _ptr(dev_status), _stream(stream)))
+           lib().nvfp4_fp8_gemm(pa, _operand(sa, _F32, kb * M, "sa"), _operand(b, _FP8_TYPES, N * K, "b"),
+                                _operand(sb, _F32, kb * (N if b_block_rows == 1 else _blocks(N)), "sb"), b_block_rows,
+                                _operand(y, (out_dtype,), M * N, "y"), y_type, M, N, K, _ptr(dev_status),
+                                _stream(stream)))
     return y
 
 
@@ -658,25 +657,20 @@ def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N
                            workspace=None, dev_status=None, stream=None):
     """Per-expert y[rows of e] = a[rows of e] b_e^T (bf16 [M_total, N]) from E4M3 codes a [M_total, K],
     b [E, N, K] and their block scales; rows sorted by expert, rows past expert_offsets[E] untouched."""
-    _fp8(a, "a")
-    _fp8(b, "b")
-    _cuda(sa, torch.float32, "sa")
-    _cuda(sb, torch.float32, "sb")
-    _cuda(expert_offsets, torch.int32, "expert_offsets")
-    _holds(a, M_total * K, "a")
-    _holds(b, E * N * K, "b")
-    _holds(sa, _blocks(K) * M_total, "sa")
-    _holds(sb, E * _blocks(N) * _blocks(K), "sb")
-    _holds(expert_offsets, E + 1, "expert_offsets")
-    y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else _cuda(y, torch.bfloat16, "y")
-    _holds(y, M_total * N, "y")
+    kb = _blocks(K)
+    pa = _operand(a, _FP8_TYPES, M_total * K, "a")
+    y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else y
     if workspace is None:
         workspace = torch.empty(max(1, nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K)), dtype=torch.uint8,
                                 device=a.device)
     _check("nvfp4_fp8_grouped_gemm",
-           lib().nvfp4_fp8_grouped_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(expert_offsets), E, M_total, N, K,
-                                        _ptr(y), _ptr(workspace), workspace.numel(), _ptr(dev_status),
-                                        _stream(stream)))
+           lib().nvfp4_fp8_grouped_gemm(pa, _operand(sa, _F32, kb * M_total, "sa"),
+                                        _operand(b, _FP8_TYPES, E * N * K, "b"),
+                                        _operand(sb, _F32, E * _blocks(N) * kb, "sb"),
+                                        _operand(expert_offsets, _I32, E + 1, "expert_offsets"), E, M_total, N, K,
+                                        _operand(y, (torch.bfloat16,), M_total * N, "y"),
+                                        _operand(workspace, _U8, 0, "workspace"), workspace.numel(),
+                                        _ptr(dev_status), _stream(stream)))
     return y
 
 
