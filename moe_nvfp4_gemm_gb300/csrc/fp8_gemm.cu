@@ -18,8 +18,6 @@
 // back through the memory system, behind the TMA loads in flight (1.7 times the time).
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "kernels.h"
 #include "nvfp4_quant.cuh"
 #include "ptx.cuh"
@@ -36,12 +34,25 @@ struct Fp8PairCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int STAGES = 5;
   static constexpr int OUT_BYTES = 8 * 4096;  // one 32-row x 128-byte store box per epilogue warp
-  // COLSCALE, per epilogue warp: DEPTH slots of 32 row scales and 128 column scales
-  static constexpr int DEPTH = 4, SCALES = 160;
-  static constexpr int SCALE_BYTES = 8 * DEPTH * SCALES * 4;
+  // COLSCALE: slots of 256 column and 128 row scales. When block c is written the MMA of block c - 3 is
+  // known to be done, so the buffer of block c - 5 was released and all warps are past block c - 6.
+  static constexpr int SLOTS = 8, SCALES = 384;
+  static constexpr int SCALE_BYTES = SLOTS * SCALES * 4;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 1024 + 256;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
+
+// Loads that stay at their place: hoisted, a block's scales would not fit the registers.
+DEVI uint64_t ld_shared_b64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
+DEVI float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 
 struct Fp8Tile {
   int m0, m_end;  // rows of a and y: [m0, m_end)
@@ -78,18 +89,13 @@ DEVI Fp8Tile fp8_tile(const Fp8GemmArgs& p, int t, int mt, int nt, int kbs) {
 // A warp's 32 rows x 128 bytes of results to y, through its 4 KB box (16-byte chunk c of row r at
 // chunk c ^ (r % 8)): by a TMA store (whole boxes), or with plain stores where y's rows are
 // not 16-byte aligned (a row at a time) or a grouped tile ends inside the box (four rows at a time).
-template <bool F32>
-DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, const uint32_t (&w)[32], const CUtensorMap* tmY, bool by_tma,
-                        int row0, int m_end, int col0, int N) {
+template <bool F32, typename Fill>
+DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, Fill&& fill, const CUtensorMap* tmY, bool by_tma, int row0,
+                        int m_end, int col0, int N) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) bulk_wait_group_read0();  // the previous box has left the buffer
   __syncwarp();
-  const uint32_t row_addr = smem_u32(buf) + lane * 128;
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
-                 "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
-                 : "memory");
+  fill(smem_u32(buf));
   if (by_tma) {
     fence_proxy_async_shared();
     __syncwarp();
@@ -127,8 +133,12 @@ DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, const uint32_t (&w)[
   }
 }
 
-// COLSCALE: one scale per row of b (a column of y), staged per warp in shared memory and applied
-// before the row scale; otherwise one per 128 rows of b, which a warp's 128 columns share.
+// COLSCALE: one scale per row of b (a column of y), applied before the row scale; otherwise one per 128
+// rows of b, which a warp's 128 columns share. A broadcast read of shared memory returns 16 bytes a lane
+// all the same, so with a lane to a row the columns' scales cost 1,024 cycles a block and CTA; with the
+// 16 x 256-bit TMEM loads a lane has four rows of a column pair, and a quarter of that is left. A warp of
+// its own brings the scales (through cp.async of each epilogue warp 187 us for 4096 x 6144 x 4112 with
+// fp32 results, now 140: a block takes ~1,360 cycles, half of them the 128 packed operations).
 //
 // SPLIT > 1: K in SPLIT parts, for products of few tiles. The SPLIT pairs of a cluster sum one tile's
 // parts, then each CTA gets a SPLIT-th of its rows' columns from all of them through distributed
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], 1);
+      mbar_init(&tfull[b], COLSCALE ? 2 : 1);  // the MMA's commit; the warp of the scales
       mbar_init(&tempty[b], 16);  // one elected lane per epilogue warp, both CTAs
     }
     mbar_init(drain, 1);
@@ -197,107 +207,78 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
     regs_inc<C::EPILOGUE_REGS>();
     const int q = warp & 3, h = (warp - 4) >> 2;
     uint8_t* box = out_buf + (warp - 4) * 4096;
-    float* cs = scale_buf + (warp - 4) * C::DEPTH * C::SCALES;
     const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), lead), mapa_shared(smem_u32(&tempty[1]), lead)};
     const bool aligned_rows = N % (F32 ? 4 : 8) == 0;
     int buf = 0;
-    uint32_t bph = 0;
+    uint32_t bph = 0, block = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += npairs) {
-      const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
-      const int row0 = tl.m0 + rank * 128 + q * 32, row = row0 + lane;
-      const int col0 = tl.n0 + h * 128;
-      // One block's 128 columns of this lane's row from TMEM, 32 or 16 columns at a time with the next
-      // chunk's load under this one's arithmetic `add(first column, values)`; the buffer is released
-      // once its last chunk has landed.
-      auto read_block = [&](auto&& add, auto chunk) {
-        constexpr int CHUNK = decltype(chunk)::value, CHUNKS = 128 / CHUNK;
+      // (with COLSCALE the tile is not needed before its results are stored)
+      Fp8Tile tl = {};
+      if (!COLSCALE) tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+      // One block's 128 columns of the warp's rows from TMEM, 32 columns at a time (`load`) with the next
+      // chunk's load under this one's arithmetic `add(chunk, values)`; the buffer is released once its
+      // last chunk has landed.
+      auto read_block = [&](auto&& load, auto&& add) {
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + h * 128;
-        uint32_t r[2][CHUNK];
-        auto load = [&](int c, uint32_t* d) {
-          if constexpr (CHUNK == 32)
-            tmem_ld32(taddr + c * CHUNK, d);
-          else
-            tmem_ld16(taddr + c * CHUNK, d);
-        };
-        auto landed = [&](uint32_t* d) {
-          if constexpr (CHUNK == 32)
-            tmem_ld_wait32(d);
-          else
-            tmem_ld_wait16(d);
-        };
-        load(0, r[0]);
-        landed(r[0]);
+        uint32_t r[2][32];
+        load(taddr, r[0]);
+        tmem_ld_wait32(r[0]);
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          if (c + 1 < CHUNKS) {
-            load(c + 1, r[(c + 1) & 1]);
+        for (int c = 0; c < 4; ++c) {
+          if (c + 1 < 4) {
+            load(taddr + (c + 1) * 32, r[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
-            if (elect_one()) mbar_arrive_cluster(tempty_leader[buf]);
+            // one address or two: whichever leaves all registers of that form unspilled
+            if (elect_one()) mbar_arrive_cluster(COLSCALE ? tempty_leader[0] + 8 * buf : tempty_leader[buf]);
           }
-          add(c * CHUNK, r[c & 1]);
-          if (c + 1 < CHUNKS) landed(r[(c + 1) & 1]);
+          add(c, r[c & 1]);
+          if (c + 1 < 4) tmem_ld_wait32(r[(c + 1) & 1]);
         }
         buf ^= 1;
         bph ^= buf == 0;
       };
-      // the fp32 sums: one by one, or (one scale a block and row) as pairs for packed arithmetic
-      float acc[COLSCALE ? 128 : 1];
-      uint64_t acc2[COLSCALE ? 1 : 64];
+      // The fp32 sums, as pairs of neighbouring columns for packed arithmetic: a lane has one row's 128
+      // columns, or with COLSCALE (16 c + 8 i + 2 g + j) rows 16 i + 8 j + lane / 4, columns
+      // 32 c + 8 g + 2 (lane % 4) and the next: a column's scale then comes from shared memory for four rows
+      // at once.
+      uint64_t acc2[64];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) {
-        if (COLSCALE)
-          acc[COLSCALE ? i : 0] = 0.0f;
-        else
-          acc2[COLSCALE ? 0 : i / 2] = 0;
-      }
+      for (int i = 0; i < 64; ++i) acc2[i] = 0;
       if constexpr (COLSCALE) {
-        // The scales of a block of K reach shared memory by cp.async, DEPTH - 1 blocks ahead (in
-        // registers they would not fit). Rows and columns past the tile's copy a scale inside it;
-        // their sums are not stored.
-        const float* sa = p.sa + min(row, tl.m_end - 1);
-        auto fetch_scales = [&](int kb) {
-          const int k = min(kb, KB - 1);
-          float* d = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
-          cp_async4(d + lane, sa + static_cast<int64_t>(k) * M);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp_async4(d + 32 + lane + 32 * i, tl.sb + static_cast<int64_t>(k) * N + min(col0 + lane + 32 * i, N - 1));
-          cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < C::DEPTH - 1; ++i) fetch_scales(kb_begin + i);
 #pragma unroll 1
-        for (int kb = kb_begin; kb < kb_end; ++kb) {
-          __syncwarp();  // the slot that is filled now has been read by all lanes
-          fetch_scales(kb + C::DEPTH - 1);
-          cp_async_wait<C::DEPTH - 1>();
-          __syncwarp();
-          const float* sc = cs + (kb & (C::DEPTH - 1)) * C::SCALES;
-          const float rs = sc[lane];
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++block) {
           ok = mbar_wait_warp(&tfull[buf], bph, abort_flag, wd);
           if (!ok) break;
           tc_fence_after();
-          read_block(
-              [&](int c0, const uint32_t* v) {
-                const float4* cv = reinterpret_cast<const float4*>(sc + 32 + c0);
+          uint32_t sc = smem_u32(scale_buf) + (block & (C::SLOTS - 1)) * (C::SCALES * 4);
+          float rs[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float4 f = cv[j];
-                  float* a = acc + c0 + 4 * j;
-                  a[0] = fmaf(__uint_as_float(v[4 * j]) * f.x, rs, a[0]);
-                  a[1] = fmaf(__uint_as_float(v[4 * j + 1]) * f.y, rs, a[1]);
-                  a[2] = fmaf(__uint_as_float(v[4 * j + 2]) * f.z, rs, a[2]);
-                  a[3] = fmaf(__uint_as_float(v[4 * j + 3]) * f.w, rs, a[3]);
-                }
+          for (int i = 0; i < 4; ++i) rs[i] = ld_shared_f32(sc + (256 + q * 32 + 8 * i + (lane >> 2)) * 4);
+          sc += (h * 128 + 2 * (lane & 3)) * 4;
+          read_block(
+              [&](uint32_t at, uint32_t* d) {
+                tmem_ld_frag32(at, d);
+                tmem_ld_frag32(at + (16u << 16), d + 16);
               },
-              std::integral_constant<int, 16>());
+              [&](int c, const uint32_t* v) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  const uint64_t cs = ld_shared_b64(sc + (c * 32 + g * 8) * 4);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint32_t* x = v + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
+                    uint64_t& a = acc2[16 * c + 8 * (i >> 1) + 2 * g + (i & 1)];
+                    a = f2_fma(f2_mul(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), cs), f2(rs[i], rs[i]), a);
+                  }
+                }
+              });
         }
-        cp_async_wait<0>();
       } else {
         // this row's and the warp's column block's scale, loaded two blocks ahead of their use
+        const int row = tl.m0 + rank * 128 + q * 32 + lane, col0 = tl.n0 + h * 128;
         const bool row_ok = row < tl.m_end;
         const float* sa = p.sa + row;
         const float* sb = tl.sb + static_cast<int64_t>(col0 >> 7) * KB;
@@ -314,16 +295,18 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const uint64_t rs2 = f2(rs, rs);
-          read_block(
-              [&](int c0, const uint32_t* v) {
+          read_block([&](uint32_t at, uint32_t* d) { tmem_ld32(at, d); },
+                     [&](int c, const uint32_t* v) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  acc2[c0 / 2 + j] =
-                      f2_fma(f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), rs2, acc2[c0 / 2 + j]);
-              },
-              std::integral_constant<int, 32>());
+                       for (int j = 0; j < 16; ++j) {
+                         uint64_t& a = acc2[16 * c + j];
+                         a = f2_fma(f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), rs2, a);
+                       }
+                     });
         }
       }
+      if (COLSCALE) tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+      const int row0 = tl.m0 + rank * 128 + q * 32, col0 = tl.n0 + h * 128;
       if constexpr (SPLIT > 1) {
         // Every CTA's ring is free once all its roles are here: it takes the parts of the columns that
         // this CTA stores, [part][warp][4 columns][row, 16 bytes; padded so that a row's columns lie in
@@ -335,22 +318,26 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
         float* recv = reinterpret_cast<float*>(smem);
         __syncwarp();
         cluster_sync();
-        auto value = [&](int i) {
-          if constexpr (COLSCALE) {
-            return acc[i];
-          } else {
-            float lo, hi;
-            f2_split(acc2[i / 2], lo, hi);
-            return (i & 1) ? hi : lo;
-          }
-        };
 #pragma unroll
         for (int o = 0; o < SPLIT; ++o) {
-          const uint32_t dst = mapa_shared(smem_u32(recv + (part * 8 + warp - 4) * WARP_FLOATS + lane * 4), 2 * o + rank);
+          const uint32_t dst = mapa_shared(smem_u32(recv + (part * 8 + warp - 4) * WARP_FLOATS), 2 * o + rank);
 #pragma unroll
-          for (int c = 0; c < OWN; c += 4)
-            st_shared_cluster_v4(dst + c * GROUP, value(o * OWN + c), value(o * OWN + c + 1), value(o * OWN + c + 2),
-                                 value(o * OWN + c + 3));
+          for (int c = 0; c < OWN; c += COLSCALE ? 8 : 4) {
+            float v[4];
+            if constexpr (COLSCALE) {
+              const int column = o * OWN + c;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f2_split(acc2[16 * (column / 32) + 8 * (i >> 1) + 2 * (column % 32 / 8) + (i & 1)], v[0], v[1]);
+                const int at = (c / 4 + (lane >> 1 & 1)) * GROUP + (8 * i + (lane >> 2)) * 4 + 2 * (lane & 1);
+                st_shared_cluster_v2(dst + at * 4, v[0], v[1]);
+              }
+            } else {
+              f2_split(acc2[(o * OWN + c) / 2], v[0], v[1]);
+              f2_split(acc2[(o * OWN + c) / 2 + 1], v[2], v[3]);
+              st_shared_cluster_v4(dst + (c / 4 * GROUP + lane * 4) * 4, v[0], v[1], v[2], v[3]);
+            }
+          }
         }
         __syncwarp();
         cluster_sync();
@@ -399,19 +386,42 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
         for (int b = 0; b < (F32 ? 4 : 2); ++b) {
           const int c0 = col0 + b * (F32 ? 32 : 64);
           if (c0 < N) {
-            uint32_t w[32];
+            // 16-byte piece c of row r at c ^ (r % 8)
+            auto fill = [&](uint32_t to) {
+              if constexpr (COLSCALE) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              // fp32: column 32 b + j; bf16: columns 64 b + 2 j and the next
-              const int i = F32 ? 32 * b + j : 64 * b + 2 * j;
-              float lo, hi;
-              if constexpr (COLSCALE)
-                lo = acc[i], hi = acc[F32 ? i : i + 1];
-              else
-                f2_split(acc2[i / 2], lo, hi);
-              w[j] = F32 ? __float_as_uint(!COLSCALE && (i & 1) ? hi : lo) : pack_bf16x2(lo, hi);
-            }
-            fp8_store_box<F32>(p, box, w, &tmY, by_tma, row0, tl.m_end, c0, N);
+                for (int g = 0; g < (F32 ? 4 : 8); ++g)  // eight columns
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int column = b * (F32 ? 32 : 64) + 8 * g, r = 8 * i + (lane >> 2);
+                    float lo, hi;
+                    f2_split(acc2[16 * (column / 32) + 8 * (i >> 1) + 2 * (column % 32 / 8) + (i & 1)], lo, hi);
+                    if (F32)
+                      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
+                                       to + r * 128 + (((2 * g + (lane >> 1 & 1)) ^ (r & 7)) << 4) + (lane & 1) * 8),
+                                   "f"(lo), "f"(hi)
+                                   : "memory");
+                    else
+                      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 128 + ((g ^ (r & 7)) << 4) + (lane & 3) * 4),
+                                   "r"(pack_bf16x2(lo, hi))
+                                   : "memory");
+                  }
+              } else {
+                uint32_t w[32];  // fp32: column 32 b + j; bf16: columns 64 b + 2 j and the next
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  float lo, hi;
+                  f2_split(acc2[F32 ? 16 * b + j / 2 : 32 * b + j], lo, hi);
+                  w[j] = F32 ? __float_as_uint((j & 1) ? hi : lo) : pack_bf16x2(lo, hi);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                               "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                               : "memory");
+              }
+            };
+            fp8_store_box<F32>(p, box, fill, &tmY, by_tma, row0, tl.m_end, c0, N);
           }
         }
       }
@@ -489,6 +499,54 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
         __syncwarp();
         volatile int32_t dummy = 0;
         mbar_wait_warp(drain, 0, &dummy, wd);
+      }
+    } else if (COLSCALE && warp == 2) {
+      // The scales: loaded AHEAD blocks before they are written to shared memory, written one block
+      // before they are announced, on the barrier that the block's MMA completes.
+      constexpr int AHEAD = 3;
+      int t = pair, kb = kb_begin;
+      float v[AHEAD][12];
+      bool have[AHEAD];
+      auto request = [&](int i) {
+        have[i] = t < tiles;
+        if (!have[i]) return;
+        const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+        const int col = tl.n0 + lane, row = tl.m0 + rank * 128 + lane;
+        const float* sb = tl.sb + static_cast<int64_t>(kb) * N + col;
+        const float* sa = p.sa + static_cast<int64_t>(kb) * M + row;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = col + 32 * j < N ? sb[32 * j] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][8 + j] = row + 32 * j < tl.m_end ? sa[32 * j] : 0.0f;
+        if (++kb == kb_end) {
+          kb = kb_begin;
+          t += npairs;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) request(i);
+      uint32_t block = 0;
+      bool go = true, written = false;
+      while (go) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          if (!go) break;
+          if (written) {  // announce block - 1, after the block two before it is complete
+            const uint32_t b = block - 1;
+            if (b >= 2) go = mbar_wait_warp(&tfull[b & 1], (b >> 1 & 1) ^ 1, abort_flag, wd);
+            __syncwarp();
+            if (go && lane == 0) mbar_arrive(&tfull[b & 1]);
+          }
+          written = have[i];
+          go = go && written;
+          if (written) {
+            float* d = scale_buf + (block & (C::SLOTS - 1)) * C::SCALES + lane;
+#pragma unroll
+            for (int j = 0; j < 12; ++j) d[32 * j] = v[i][j];
+          }
+          ++block;
+          request(i);
+        }
       }
     }
     if constexpr (SPLIT > 1) {  // the epilogue warps' two barriers around the exchange of the parts

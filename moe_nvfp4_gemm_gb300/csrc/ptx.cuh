@@ -278,6 +278,10 @@ DEVI void st_shared_cluster_v4(uint32_t cluster_addr, float a, float b, float c,
                : "memory");
 }
 
+DEVI void st_shared_cluster_v2(uint32_t cluster_addr, float a, float b) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr), "f"(a), "f"(b) : "memory");
+}
+
 // Relaxed arrive on an mbarrier of any CTA in the cluster. Used only to hand a
 // drained TMEM accumulator back to the MMA issuer: the tcgen05.ld reads are already
 // complete (tcgen05.wait::ld) when the arrive executes, so no memory needs to be
@@ -411,6 +415,16 @@ DEVI void tmem_ld32(uint32_t taddr, uint32_t* r) {
 DEVI void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 16 lanes x 32 consecutive 32-bit columns: r[4 g + 2 i + j] is lane (threadIdx % 32) / 4 + 8 i, column
+// 8 g + 2 (threadIdx % 4) + j.
+DEVI void tmem_ld_frag32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
