@@ -138,7 +138,7 @@ DEVI void fp8_store_box(const Fp8GemmArgs& p, uint8_t* buf, Fill&& fill, const C
 // all the same, so with a lane to a row the columns' scales cost 1,024 cycles a block and CTA; with the
 // 16 x 256-bit TMEM loads a lane has four rows of a column pair, and a quarter of that is left. A warp of
 // its own brings the scales (through cp.async of each epilogue warp 187 us for 4096 x 6144 x 4112 with
-// fp32 results, now 140: a block takes ~1,360 cycles, half of them the 128 packed operations).
+// fp32 results, now 136: a block takes ~1,320 cycles, half of them the 128 packed operations).
 //
 // SPLIT > 1: K in SPLIT parts, for products of few tiles. The SPLIT pairs of a cluster sum one tile's
 // parts, then each CTA gets a SPLIT-th of its rows' columns from all of them through distributed
@@ -507,10 +507,11 @@ __global__ void __launch_bounds__(Fp8PairCfg::THREADS, 1)
       int t = pair, kb = kb_begin;
       float v[AHEAD][12];
       bool have[AHEAD];
+      Fp8Tile tl = {};
       auto request = [&](int i) {
         have[i] = t < tiles;
         if (!have[i]) return;
-        const Fp8Tile tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
+        if (kb == kb_begin) tl = fp8_tile<GROUPED>(p, t, mt, nt, KB);
         const int col = tl.n0 + lane, row = tl.m0 + rank * 128 + lane;
         const float* sb = tl.sb + static_cast<int64_t>(kb) * N + col;
         const float* sa = p.sa + static_cast<int64_t>(kb) * M + row;
