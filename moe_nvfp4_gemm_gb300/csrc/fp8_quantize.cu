@@ -7,6 +7,8 @@
 // applies it to fp32 sums (no rounding of the scale is needed).
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "nvfp4_quant.cuh"
 #include "ptx.cuh"
@@ -101,14 +103,23 @@ __global__ void __launch_bounds__(kFp8QuantThreads, TRANSPOSED ? 4 : 5) k_fp8_qu
   const int64_t col = k0 + tx * 8;
   const bool col_ok = col < a.K;  // K is a multiple of 16: a group of 8 columns is whole
   uint4 v[8];
+  const int64_t r0 = m0 + ty * 8;
+  if (a.row_token) {
+    int32_t src[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = m0 + ty * 8 + i;
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < a.M && col_ok) {
-      int64_t src = r;
-      if (a.row_token) src = __ldg(a.row_token + r);
-      if (src >= 0 && src < a.M_x) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + src * a.K + col));
+    for (int i = 0; i < 8; ++i) src[i] = r0 + i < a.M ? __ldg(a.row_token + r0 + i) : -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (col_ok && src[i] >= 0 && src[i] < a.M_x) v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + src[i] * a.K + col));
+    }
+  } else {
+    const uint16_t* x = a.x + r0 * a.K + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (col_ok && r0 + i < a.M) v[i] = __ldg(reinterpret_cast<const uint4*>(x));
+      x += a.K;
     }
   }
   uint32_t rm[8], cm[4];
@@ -173,19 +184,28 @@ __global__ void __launch_bounds__(kFp8QuantThreads, TRANSPOSED ? 4 : 5) k_fp8_qu
   uint2 codes[8];
   if (a.q || SQUARE) {
     const Reciprocal ry = fp8_reciprocal(rs);
-    const bool fast = __all_sync(0xffffffffu, fp8_fast(rs));
+    uint8_t* q = a.q ? a.q + r0 * a.K + col : nullptr;
+    const int rows = a.q && col_ok ? static_cast<int>(min(int64_t(8), a.M - r0)) : 0;
+    auto code_rows = [&](auto fast) {
+      constexpr bool FAST = decltype(fast)::value;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      auto of_row = [&](float x) {
-        const float f = SQUARE ? x : __shfl_sync(0xffffffffu, x, (lane & 16) + 2 * i);
-        return make_float2(f, f);
-      };
-      const float2 s = of_row(rs), hi = of_row(ry.hi), lo = of_row(ry.lo);
-      const float2 ss[4] = {s, s, s, s}, hh[4] = {hi, hi, hi, hi}, ll[4] = {lo, lo, lo, lo};
-      codes[i] = fast ? e4m3_codes8<true>(v[i], ss, hh, ll) : e4m3_codes8<false>(v[i], ss, hh, ll);
-      const int64_t r = m0 + ty * 8 + i;
-      if (a.q && r < a.M && col_ok) *reinterpret_cast<uint2*>(a.q + r * a.K + col) = codes[i];
-    }
+      for (int i = 0; i < 8; ++i) {
+        auto of_row = [&](float x) {
+          const float f = SQUARE ? x : __shfl_sync(0xffffffffu, x, (lane & 16) + 2 * i);
+          return make_float2(f, f);
+        };
+        const float2 s = FAST ? make_float2(0.0f, 0.0f) : of_row(rs);
+        const float2 hi = FAST ? of_row(ry.hi) : s, lo = FAST ? of_row(ry.lo) : s;
+        const float2 ss[4] = {s, s, s, s}, hh[4] = {hi, hi, hi, hi}, ll[4] = {lo, lo, lo, lo};
+        codes[i] = e4m3_codes8<FAST>(v[i], ss, hh, ll);
+        if (i < rows) *reinterpret_cast<uint2*>(q) = codes[i];
+        q += a.K;
+      }
+    };
+    if (__all_sync(0xffffffffu, fp8_fast(rs)))
+      code_rows(std::true_type());
+    else
+      code_rows(std::false_type());
   }
   if (TRANSPOSED) {
     if (!SQUARE) {
@@ -202,9 +222,13 @@ __global__ void __launch_bounds__(kFp8QuantThreads, TRANSPOSED ? 4 : 5) k_fp8_qu
         fast = fast && fp8_fast(s4.x) && fp8_fast(s4.y) && fp8_fast(s4.z) && fp8_fast(s4.w);
       }
       fast = __all_sync(0xffffffffu, fast);
+      if (fast) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        codes[i] = fast ? e4m3_codes8<true>(v[i], cs, hi, lo) : e4m3_codes8<false>(v[i], cs, hi, lo);
+        for (int i = 0; i < 8; ++i) codes[i] = e4m3_codes8<true>(v[i], cs, hi, lo);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) codes[i] = e4m3_codes8<false>(v[i], cs, hi, lo);
+      }
     }
     // 8 x 8 byte transpose: column tx*8 + j gets rows ty*8 .. +7 as one 8-byte unit, unit ty
     // stored at ty ^ tx so that a warp's 32 units of one j cover all banks
