@@ -457,10 +457,11 @@ __global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route_one(const 
 
 // ---- gradient of the logits ------------------------------------------------------------------
 //
-// G_te = dL E c_e / (k n^2) from the balance loss (its counts carry no gradient), plus dw_ts at
-// the selected experts when the weights are plain; d l_te = p_te (G_te - sum_i p_ti G_ti).
-// Renormalised weights are a softmax over the selected logits alone: they add
-// w_s (dw_s - sum_r w_r dw_r) at expert idx_s instead. Unrouted tokens get zeros.
+// G_te = dL E c_e / (k n^2) from the balance loss (its counts carry no gradient): d l_te gets
+// p_te (G_te - sum_i p_ti G_ti). The weights' gradients dw_ts add at the selected experts
+// w_s dw_s and, when the weights are plain probabilities, -p_te sum_s w_s dw_s everywhere (it joins
+// the sum above); renormalised weights are a softmax over the selected logits alone, which add
+// w_s (dw_s - sum_r w_r dw_r) there. Unrouted tokens get zeros.
 //
 // Bound by memory. With a.vec the rows come by cp.async, kBwdAhead rows ahead of their use (each
 // lane copies and reads back its own bytes, so no lane waits for another): with plain loads the
@@ -475,7 +476,7 @@ __host__ __device__ constexpr int bwd_slot_bytes(int vpl, bool bf16) {  // logit
   return 32 * vpl * (bf16 ? 2 : 4) + 3 * 128;
 }
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kBwdThreads) k_moe_route_bwd(const RouteBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, VPL <= 8 ? 4 : 1) k_moe_route_bwd(const RouteBwdArgs a) {
   extern __shared__ __align__(16) float shf[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, k = a.k;
@@ -570,28 +571,25 @@ __global__ void __launch_bounds__(kBwdThreads) k_moe_route_bwd(const RouteBwdArg
       }
       const float inv = rcp(warp_sum(sum));
       int idx = -1;
+      float dot = 0.0f;
       if (a.d_w) {
         if (slot_idx >= 0 && slot_idx < E) idx = slot_idx;
-        float dw = idx >= 0 ? slot_dw : 0.0f;
-        const float w = idx >= 0 ? slot_w : 0.0f;
-        if (a.renorm) dw = w * (dw - warp_sum(w * dw));
-        if (idx >= 0) spot[idx] = dw;
+        float add = idx >= 0 ? slot_w * slot_dw : 0.0f;
+        if (a.renorm)
+          add -= (idx >= 0 ? slot_w : 0.0f) * warp_sum(add);
+        else
+          dot = add;
+        if (idx >= 0) spot[idx] = add;
         __syncwarp();
       }
-      float dot = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
         v[j] *= inv;
-        d[j] = spot[lane * VPL + j];
-        const float G = a.renorm ? g[j] : g[j] + d[j];
-        dot += v[j] * G;
+        dot = fmaf(v[j], g[j], dot);
       }
       dot = warp_sum(dot);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const float G = a.renorm ? g[j] : g[j] + d[j];
-        d[j] = v[j] * (G - dot) + (a.renorm ? d[j] : 0.0f);
-      }
+      for (int j = 0; j < VPL; ++j) d[j] = fmaf(v[j], g[j] - dot, spot[lane * VPL + j]);
       __syncwarp();
       if (idx >= 0) spot[idx] = 0.0f;
       __syncwarp();
