@@ -128,29 +128,30 @@ DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* can
   }
   bound = max(bound, kKeyNegInf + 1);
   const float least = key_value(bound);
-  int mine_n = 0;
+  int n = 0;
+  uint32_t at[VPL];  // where this lane's logit j goes
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) mine_n += v[j] >= least;
-  int at = mine_n;  // inclusive prefix over the lanes
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += u;
+  for (int j = 0; j < VPL; ++j) {
+    const uint32_t in = __ballot_sync(0xffffffffu, v[j] >= least);
+    at[j] = n + __popc(in & ((1u << lane) - 1u));
+    n += __popc(in);
   }
-  const int n = __shfl_sync(0xffffffffu, at, 31);
   out_idx = -1;
   out_val = 0.0f;
   if (n <= 32) {
-    at -= mine_n;
-    // the key in the high half, the complement of the expert in the low half: one comparison orders both
-    if (mine_n > 0) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (v[j] >= least) cand[at++] = static_cast<uint64_t>(order_key(v[j])) << 32 | static_cast<uint32_t>(~(lane * VPL + j));
-    }
-    if (lane == 0 && (n & 1)) cand[n] = 0;  // the count below goes in pairs
+    for (int j = 0; j < VPL; ++j)
+      if (v[j] >= least) cand[at[j]] = static_cast<uint64_t>(__float_as_uint(v[j])) << 32 | static_cast<uint32_t>(lane * VPL + j);
     __syncwarp();
-    const uint64_t mine = lane < n ? cand[lane] : 0;
+    // the key in the high half, the complement of the expert in the low half: one comparison orders both
+    uint64_t mine = 0;
+    if (lane < n) {
+      const uint64_t c = cand[lane];
+      mine = static_cast<uint64_t>(order_key(__uint_as_float(static_cast<uint32_t>(c >> 32)))) << 32 |
+             static_cast<uint32_t>(~static_cast<uint32_t>(c));
+    }
+    if (lane <= n) cand[lane] = mine;  // and a 0 behind the last: the count below goes in pairs
+    __syncwarp();
     int rank = 0;
     for (int i = 0; i < n; i += 2) {
       const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cand + i);
