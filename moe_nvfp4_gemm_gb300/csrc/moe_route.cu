@@ -108,17 +108,18 @@ struct RouteCfg {
   static constexpr int THREADS = 32 * WARPS;
 };
 
-// The k largest of a warp's 32 * VPL logits (lane holds experts lane * VPL + j), in order, ties to
-// the lower expert: lane s < k returns slot s's expert (-1: none above -inf) and logit. `lane_max`
-// is the largest of this lane's.
+// The k largest of a warp's 32 * VPL logits (lane holds experts lane * VPL + j), ties to the lower
+// expert: a lane gets a slot and, where that is below k, its expert (-1: none above -inf is left for
+// it) and logit; every slot below k is some lane's. `lane_max` is the largest of this lane's logits.
 //
 // The k-th largest of the 32 lane maxima bounds the k-th largest logit from below, so the selected
 // experts are among the few (typically k and one or two) that reach it. Those candidates are
-// compacted into `cand` and each counts the candidates that precede it, which is its slot: about
-// 170 instructions for 256 experts and k = 8, against 400 for k rounds of a maximum over all.
-// With more than 32 candidates (many equal logits) the rounds are run.
+// compacted into `cand`, a lane takes one each and counts the ones that precede it, which is its
+// slot: less than half the instructions of k rounds of a maximum over all. With more than 32
+// candidates (many equal logits) the rounds are run.
 template <int VPL>
-DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* cand, int& out_idx, float& out_val) {
+DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* cand, int& out_idx, float& out_val,
+                     int& out_slot) {
   const int lane = threadIdx.x & 31;
   uint32_t bound = 0, left = order_key(lane_max);
 #pragma unroll 2
@@ -138,6 +139,7 @@ DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* can
   }
   out_idx = -1;
   out_val = 0.0f;
+  out_slot = lane;
   if (n <= 32) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
@@ -158,13 +160,12 @@ DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* can
       rank += c.x > mine;
       rank += c.y > mine;
     }
-    __syncwarp();
-    if (lane < n) cand[rank] = mine;
-    __syncwarp();
-    if (lane < min(n, k)) {
-      const uint64_t c = cand[lane];
-      out_val = key_value(static_cast<uint32_t>(c >> 32));
-      out_idx = static_cast<int>(~static_cast<uint32_t>(c));
+    if (lane < n) {
+      out_slot = rank;
+      if (rank < k) {
+        out_val = key_value(static_cast<uint32_t>(mine >> 32));
+        out_idx = static_cast<int>(~static_cast<uint32_t>(mine));
+      }
     }
     __syncwarp();
     return;
@@ -220,11 +221,11 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
       for (int j = 1; j < VPL; ++j) lane_max = fmaxf(lane_max, v[j]);
       mx = key_value(__reduce_max_sync(0xffffffffu, order_key(lane_max)));
     }
-    int my_idx = -1;
+    int my_idx = -1, my_slot = lane;
     float my_w = 0.0f;
     if (mx > __uint_as_float(0xFF800000u)) {
       float my_v;
-      warp_top_k<VPL>(v, lane_max, k, cand + warp * kCandSlots, my_idx, my_v);
+      warp_top_k<VPL>(v, lane_max, k, cand + warp * kCandSlots, my_idx, my_v, my_slot);
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
@@ -239,9 +240,9 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
       my_w = es * (a.renorm ? rcp(warp_sum(es)) : inv);
       if (my_idx >= 0) atomicAdd(&hist[my_idx], 1);
     }
-    if (lane < k) {
-      a.topk_idx[t * k + lane] = my_idx;
-      a.topk_w[t * k + lane] = my_w;
+    if (my_slot < k) {
+      a.topk_idx[t * k + my_slot] = my_idx;
+      a.topk_w[t * k + my_slot] = my_w;
     }
   }
   if (lane == 0) atomicAdd(&hist[E], routed);
