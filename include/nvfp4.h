@@ -400,7 +400,7 @@ int nvfp4_moe_route(const void* logits, int32_t logits_type, const uint8_t* vali
 /*
  * Gradient of nvfp4_moe_route's logits from the gradients of the weights and of the balance
  * loss. The selection and the counts carry no gradient. With
- * G_te = dL E c_e / (k n^2), plus dw_ts at the selected experts (plain weights):
+ * G_te = dL E c_e / (k n^2), plus dw_ts at the selected experts (plain weights, p there = w_ts):
  *   dl_te = p_te (G_te - sum_i p_ti G_ti);
  * renormalised weights add w_ts (dw_ts - sum_r w_tr dw_tr) at the selected experts instead.
  *   logits, valid, T, E, k, renormalize   as in the forward call
@@ -525,6 +525,10 @@ int nvfp4_encode_e4m3(const float* v, int64_t n, uint8_t* out, void* stream);
  *                              of each GEMM kernel withhold the loads of the k-th pipeline stage
  *                              it would request, so that stage never arrives and the waits run
  *                              into the watchdog (the result is then unspecified). 0: off.
+ * The FP8 GEMMs follow DENSE_GRID (their tile kernels), STREAM_MAX_M (up to 64 rows there; not the
+ * grouped one), STREAM_SPLIT (the dense ones: cluster size along K of the streaming kernel, and
+ * 1, 2 or 4 parts of K of the tile kernel), STREAM_L2_PREFETCH (blocks of 128 K elements),
+ * WATCHDOG_US and TEST_WITHHOLD_STAGE.
  * Returns NVFP4_OK or NVFP4_ERR_INVALID_ARG.
  */
 enum {

@@ -340,7 +340,11 @@ DEVI void route_chunk(const RouteArgs& a, int64_t& t0, int64_t& t1) {
   t1 = min(a.T, t0 + per);
 }
 
-// Stage 1: every CTA routes its tokens; counts and sums of p per CTA to the workspace.
+// Stage 1: every CTA routes its tokens; counts and sums of p per CTA to the workspace. 65,536 tokens x 256
+// fp32, top-8: 36 us of the call's 47 (stages 2 and 3: 8.5 and 13 alone, cold, and partly under one
+// another's launches). Bound by instruction issue (~410 a row, 68 % of the slots), not by its 67 MB
+// (10 us): a warp is half idle only in the selection's exchanges, and requesting the next row ahead
+// gained nothing.
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route(const RouteArgs a) {
   extern __shared__ __align__(16) uint64_t sh64[];
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kScanWarps * 32) k_moe_scan(const RouteArgs a,
   if (blockIdx.x == 0 && threadIdx.x == 0) a.routed_tokens[0] = n;
 }
 
-// Stage 3: every CTA places its tokens' rows.
+// Stage 3: every CTA places its tokens' rows. Bound by the latency of its few dependent steps.
 __global__ void __launch_bounds__(kPlaceThreads) k_moe_place(const RouteArgs a) {
   extern __shared__ int32_t sh[];
   int32_t* offs = sh;                // [E + 1]
@@ -465,9 +469,10 @@ __global__ void __launch_bounds__(RouteCfg<VPL>::THREADS) k_moe_route_one(const 
 // the sum above); renormalised weights are a softmax over the selected logits alone, which add
 // w_s (dw_s - sum_r w_r dw_r) there. Unrouted tokens get zeros.
 //
-// Bound by memory. With a.vec the rows come by cp.async, kBwdAhead rows ahead of their use (each
-// lane copies and reads back its own bytes, so no lane waits for another): with plain loads the
-// warps' latency left 65,536 x 256 at 39 us.
+// Bound by memory and its latency: 65,536 x 256 fp32 in 29 us (its 140 MB: 21 us). With a.vec the rows
+// come by cp.async, kBwdAhead rows ahead of their use (each lane copies and reads back its own bytes,
+// so no lane waits for another); with plain loads 39 us. Four CTAs on an SM (64 registers) take 1 us
+// less than three.
 constexpr int kBwdThreads = 256;
 constexpr int kBwdWarps = kBwdThreads / 32;
 constexpr int kBwdAhead = 4;
@@ -666,9 +671,13 @@ static bool route_vec(const void* p, int E, int bf16) {
     default: call(32, true); break;                               \
   }
 
-// Tokens up to which one CTA does all the stages in one launch: two tokens a warp (32 tokens of 256
-// experts: see the figures at the launcher).
-constexpr int kRouteOneTokens = 32;
+// Tokens up to which one CTA does all the stages in one launch. One CTA / three kernels, us:
+//   tokens          16          32          48          64          96
+//   8 experts    4.1 /  9.7  5.0 /  9.7  5.9 /  9.7  6.8 /  9.6  8.5 /  9.5
+//   64           4.6 / 10.2  6.1 / 10.1  7.0 /  9.6  8.1 /  9.7 10.8 /  9.9
+//   256          5.8 / 11.1  7.5 / 10.8  9.0 / 10.9 10.5 / 10.8 13.9 / 11.2
+//   1024        18.4 / 20.4 23.8 / 19.9
+static int route_one_tokens(int E) { return route_vpl(E) <= 8 ? 64 : 16; }
 
 static int route_warps(int E) { return route_vpl(E) <= 8 ? 16 : 8; }
 
@@ -680,7 +689,7 @@ int route_blocks(int64_t T, int E) {
 cudaError_t launch_moe_route(RouteArgs a, cudaStream_t st, int* launches) {
   a.vec = route_vec(a.logits, a.E, a.bf16);
   const int E = a.E, warps = route_warps(E), threads = 32 * warps;
-  if (a.T <= kRouteOneTokens) {
+  if (a.T <= route_one_tokens(E)) {
     const int smem = warps * kCandSlots * 8 + (2 * (E + 1) + warps * E) * 4;
     *launches = 1;
 #define CALL(V, B) k_moe_route_one<V, B><<<1, threads, smem, st>>>(a)
