@@ -9,13 +9,14 @@
 //
 // One CTA pair (cta_group::2) per 256 x 256 tile of y: per block of K each CTA loads 128 rows of a
 // and of b (32 KB by TMA, 128-byte swizzle) and the pair's MMAs take 512 cycles at the full rate.
-// What bounds it: a block takes ~860 cycles (4096 x 28672 x 8192: 715 us, 2.69 PFLOP/s; under the power
-// cap 800 us), of which the eight epilogue warps of a CTA need ~660 to read (4 x tcgen05.ld of 32
-// columns) and add (64 packed fma) their 128 columns of a row and ~200 for the block's hand-offs and
-// scales. Without the arithmetic the same loop takes ~580. Tried without gain: 16 epilogue warps of
-// 64 columns, four half-width buffers, 64-column loads, plain instead of packed fma, the scales
-// through a warp of their own. What does cost is any register that spills in the loop: it comes
-// back through the memory system, behind the TMA loads in flight (1.7 times the time).
+// What bounds it: a block takes ~860 cycles (4096 x 28672 x 8192: 712 us, 2.70 PFLOP/s; under the power
+// cap 800 us), half of the chain MMA - commit - TMEM loads and arithmetic - release, as there are two
+// buffers. The eight epilogue warps of a CTA need ~530 of it to read (4 x tcgen05.ld of 32 columns)
+// and add (64 packed fma) their 128 columns of a row; a ready barrier costs ~110; without the arithmetic
+// the same loop takes ~580. Tried without gain: 16 epilogue warps of 64 columns, four half-width
+// buffers, 64-column loads, plain instead of packed fma, the row scales through a warp of their own,
+// plain stores instead of TMA (765 us). What does cost is any register that spills in the loop: it
+// comes back through the memory system, behind the TMA loads in flight (1.7 times the time).
 #include <stdint.h>
 
 #include "kernels.h"
