@@ -1092,7 +1092,7 @@ int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const fl
   return rc;
 }
 
-// Tiles of at most kFp8TileRows rows of one expert each.
+// Tiles of at most tile_rows rows of one expert each.
 static int64_t fp8_max_tiles(int32_t E, int64_t M_total, int64_t tile_rows) {
   return (M_total + tile_rows - 1) / tile_rows + E;
 }
@@ -1138,17 +1138,21 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   p.b_rows = 128;
   p.tiles = tiles;
   p.n_tiles = n_tiles;
-  // Token tiles by the mean rows of an expert. The streaming kernel, whose time grows with every
-  // further tile of an expert (its weights are read again), in tiles of 32 rows up to a mean of 16
-  // and 64 up to 56; then 256-row tiles. Measured, us, for 256 experts of 6144 x 2048:
-  //   mean rows     8     16     24     32     48     64     96    128
-  //   32 rows     488    503    578    685    880   1053
-  //   64 rows     486    483    501    516    595    743   1025
-  //   256 rows    653    675    681    691    690    696    712    745
-  // and for 64 of 4096 x 2048, two tiles of 32 an SM ahead of one of 64: 16: 86 / 90, 48: 106 / 108 / 131.
+  // By the mean rows of an expert, us for experts of N x K (256 of 6144 x 2048, 256 of 4096 x 6144, 64 of
+  // 4096 x 2048, 8 of 6144 x 4096), token tiles of 128 rows on the MMA's N / of 256 on its M:
+  //   mean rows     32           64           112          128          144          160
+  //             498 /  690   518 /  693   654 /  724   721 /  739   800 /  779   890 /  801
+  //             987 / 1364  1019 / 1341  1267 / 1403  1337 / 1492  1548 / 1501  1729 / 1495
+  //              84 /  133    91 /  135   117 /  136   123 /  142   136 /  140   150 /  142
+  //              41 /   55    43 /   57    52 /   59    59 /   61    59 /   61    61 /   61
+  // The streaming kernel (tiles of 32 rows, two CTAs an SM) where all its items are resident at once:
+  // 32 experts of 777 x 1040 (224 items) with 16 rows 11.4 / 13.2, with 32 15.2 / 15.2; with more items
+  // it gains nothing (8 of 6144 x 4096, 384 items, 8 rows: 41.5 / 40.8; 256 of 4096 x 6144, 16 rows:
+  // 991 / 966).
   const int64_t mean = (M_total + E - 1) / E;
-  const bool tile_kernel = mean > 56;
-  const int tile_rows = tile_kernel ? 256 : (mean <= 16 ? 32 : 64);
+  const int64_t items = (M_total < E ? M_total : E) * ((N + 127) / 128);
+  const bool streamed = mean <= 24 && items <= 2 * d.sms;
+  const int tile_rows = streamed ? 32 : (mean <= 136 ? 128 : 256);
   p.max_tiles = static_cast<int>(fp8_max_tiles(E, M_total, tile_rows));
   p.status = dev_status;
   p.watchdog_ns = watchdog_ns();
@@ -1156,13 +1160,22 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   rc = from_cuda(launch_fp8_tiles(expert_offsets, E, static_cast<int>(M_total), tile_rows, tiles, n_tiles, dev_status, st));
   g_last_launches = 1;
   if (rc) return rc;
-  if (tile_kernel) {
-    rc = run_fp8_pair(a, b, static_cast<int64_t>(E) * N, p, p.max_tiles * ((N + 255) / 256), d.sms, st);
+  const int64_t n_weights = static_cast<int64_t>(E) * N;
+  if (tile_rows == 256) {
+    rc = run_fp8_pair(a, b, n_weights, p, p.max_tiles * ((N + 255) / 256), d.sms, st);
   } else {
     CUtensorMap tmW, tmX;
-    if ((rc = encode_2d(&tmW, b, static_cast<uint64_t>(E) * N, K, 128))) return rc;
+    if ((rc = encode_2d(&tmW, b, n_weights, K, 128))) return rc;
     if ((rc = encode_2d(&tmX, a, M_total, K, 32))) return rc;
-    rc = from_cuda(launch_fp8_stream(tmW, tmX, p, tile_rows, d.sms, st));
+    if (streamed) {
+      rc = from_cuda(launch_fp8_stream(tmW, tmX, p, tile_rows, d.sms, st));
+    } else {
+      const int64_t most = p.max_tiles * ((N + 255) / 256);
+      int64_t pairs = (g_tune.dense_grid ? g_tune.dense_grid : d.sms) / 2;
+      if (pairs > most) pairs = most;
+      if (pairs < 1) pairs = 1;
+      rc = from_cuda(launch_fp8_grouped_pair(tmW, tmX, p, static_cast<int>(2 * pairs), st));
+    }
   }
   g_last_launches = 2;
   return rc;

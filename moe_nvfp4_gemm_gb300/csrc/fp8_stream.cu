@@ -1,5 +1,5 @@
-// FP8 block-scaled GEMM for few rows per weight: decode-size dense layers and the grouped (MoE)
-// product. Same sums as fp8_gemm.cu, with the operands exchanged: 128 weight rows on the MMA's
+// FP8 block-scaled GEMM for few rows per weight: decode-size dense layers and small grouped (MoE)
+// products. Same sums as fp8_gemm.cu, with the operands exchanged: 128 weight rows on the MMA's
 // 128-lane side, the tokens (padded to 16) on its N side, so that no token is padded to a tile.
 //
 // Bound by reading the weights: one 128-row x 128-byte TMA tile per block of K, each read once,
@@ -8,7 +8,8 @@
 // weight block's scale multiplied in), to fp32 sums in registers.
 //   dense:   grid = (N / 128) x S CTAs in clusters of S along K; the S partial sums meet through
 //            distributed shared memory, each CTA owning some of the tokens.
-//   grouped: a persistent grid walks (token tile, weight tile) items of the device-built list.
+//   grouped: a persistent grid walks (token tile, weight tile) items of the device-built list; for
+//            problems whose items are all resident at once (fp8_grouped.cu has the larger ones).
 // Data that the previous kernel may have written is read with plain loads (see fp8_gemm.cu).
 #include <stdint.h>
 
@@ -458,16 +459,14 @@ static cudaError_t launch_fp8_stream_t(const CUtensorMap& tmW, const CUtensorMap
   return cudaGetLastError();
 }
 
-// Token tiles of `tile_rows` (32 or 64) rows; tmX has 32-row boxes.
+// Token tiles of `tile_rows` rows (32 or 64; grouped: 32); tmX has 32-row boxes.
 cudaError_t launch_fp8_stream(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int tile_rows,
                               int sms, cudaStream_t st) {
   const int NTW = static_cast<int>((p.N + 127) / 128);
   if (p.tiles) {
-    const int64_t items = static_cast<int64_t>(p.max_tiles) * NTW;
-    const int64_t slots = (tile_rows == 32 ? 2 : 1) * static_cast<int64_t>(sms);
+    const int64_t items = static_cast<int64_t>(p.max_tiles) * NTW, slots = 2 * static_cast<int64_t>(sms);
     const int grid = static_cast<int>(items < slots ? items : slots);
-    if (tile_rows == 32) return launch_fp8_stream_t<32, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
-    return launch_fp8_stream_t<64, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
+    return launch_fp8_stream_t<32, kFp8Grouped>(tmW, tmX, p, grid, 0, st);
   }
   const int M = static_cast<int>(p.M), m_own = (M + p.split - 1) / p.split;
   const int recv = p.split > 1 ? p.split * m_own * 512 : 0;

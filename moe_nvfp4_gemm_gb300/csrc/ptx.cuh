@@ -430,6 +430,14 @@ DEVI void tmem_ld_frag32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
+// Four 8 x 8 matrices of 16-bit values, held as by tmem_ld_frag32 (two neighbouring columns in a
+// register), to shared memory transposed: lane 8 j + t gives the address of matrix j's column t.
+DEVI void st_matrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
 // Waits for this thread's tcgen05.ld results; the registers pass through the statement, so that
 // no use of them can be moved in front of it.
 DEVI void tmem_ld_wait16(uint32_t* r) {

@@ -253,6 +253,37 @@ def test_grouped(counts, N, K):
     assert (y[int(off[-1]):] == 7.0).all()
 
 
+@pytest.mark.parametrize("K", [16, 256, 272, 1024, 1152, 2192])
+@pytest.mark.parametrize("N", [8, 131, 520])
+def test_grouped_tokens_on_the_narrow_side(N, K):
+    """Experts around the edges of a token tile (32, 64, 128 rows), odd and even numbers of blocks of K."""
+    counts = [1, 33, 0, 64, 65, 127, 128, 129]
+    off, rows, a, sa, b, sb = grouped_case(counts, N, K, N + K, tail=5)
+    st = torch.zeros(1, dtype=torch.int32, device=dev())
+    y = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device=dev())
+    m.nvfp4_fp8_grouped_gemm(a, sa, b, sb, off.to(dev()), len(counts), rows, N, K, y=y, dev_status=st)
+    again = m.nvfp4_fp8_grouped_gemm(a, sa, b, sb, off.to(dev()), len(counts), rows, N, K)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert torch.equal(again[:int(off[-1])], y[:int(off[-1])])
+    for e in range(len(counts)):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if counts[e]:
+            check(y[r], decode(a[r], sa[:, r].contiguous(), 1), decode(b[e], sb[e], 128))
+    assert (y[int(off[-1]):] == 7.0).all()
+
+
+def test_grouped_many_experts_of_few_rows():
+    E, N, K = 80, 1160, 400
+    counts = [int(v) for v in np.random.default_rng(5).poisson(3, E)]
+    off, rows, a, sa, b, sb = grouped_case(counts, N, K, 6, tail=2)
+    y = m.nvfp4_fp8_grouped_gemm(a, sa, b, sb, off.to(dev()), E, rows, N, K)
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if counts[e]:
+            check(y[r], decode(a[r], sa[:, r].contiguous(), 1), decode(b[e], sb[e], 128))
+
+
 @pytest.mark.parametrize("M,N,K", [(2600, 5200, 384), (1100, 9000, 144)])
 @pytest.mark.parametrize("b_rows", [128, 1])
 def test_gemm_more_tiles_than_ctas(M, N, K, b_rows):
