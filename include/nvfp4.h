@@ -525,9 +525,9 @@ int nvfp4_encode_e4m3(const float* v, int64_t n, uint8_t* out, void* stream);
  *                              of each GEMM kernel withhold the loads of the k-th pipeline stage
  *                              it would request, so that stage never arrives and the waits run
  *                              into the watchdog (the result is then unspecified). 0: off.
- * The FP8 GEMMs follow DENSE_GRID (their tile kernels), STREAM_MAX_M (up to 64 rows there; not the
- * grouped one), STREAM_SPLIT (the dense ones: cluster size along K of the streaming kernel, and
- * 1, 2 or 4 parts of K of the tile kernel), STREAM_L2_PREFETCH (blocks of 128 K elements),
+ * The FP8 GEMMs follow DENSE_GRID (their tile kernels), STREAM_MAX_M (the dense one: streaming up to
+ * that many rows, at most 64, and 256 x 256 tiles above), STREAM_SPLIT (the dense one: cluster size along
+ * K of the streaming kernel, or 1, 2 or 4 parts of K of the tile kernel), STREAM_L2_PREFETCH (blocks of 128 K elements),
  * WATCHDOG_US and TEST_WITHHOLD_STAGE.
  * Returns NVFP4_OK or NVFP4_ERR_INVALID_ARG.
  */

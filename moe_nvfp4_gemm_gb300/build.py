@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libnvfp4.so")
 SOURCES = ["capi.cu", "quantize.cu", "gemm_dense.cu", "gemm_stream.cu", "sparse.cu", "moe_route.cu",
-           "fp8_quantize.cu", "fp8_gemm.cu", "fp8_grouped.cu", "fp8_stream.cu"]
+           "fp8_quantize.cu", "fp8_gemm.cu", "fp8_narrow.cu", "fp8_stream.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1039,6 +1039,20 @@ static int run_fp8_pair(const uint8_t* a, const uint8_t* b, int64_t b_rows_total
   return from_cuda(launch_fp8_gemm_pair(tmA, tmB, tmY, p, static_cast<int>(2 * pairs * p.split), st));
 }
 
+// Launches the kernel with the tokens on the narrow side on `tiles` tiles of 256 weight rows and up to 128
+// tokens (grouped: at most that many).
+static int run_fp8_narrow(const uint8_t* a, const uint8_t* b, int64_t b_rows_total, const Fp8GemmArgs& p, int64_t tiles,
+                          int sms, cudaStream_t st) {
+  CUtensorMap tmW, tmX;
+  int rc;
+  if ((rc = encode_2d(&tmW, b, b_rows_total, p.K, 128))) return rc;
+  if ((rc = encode_2d(&tmX, a, p.M, p.K, 32))) return rc;
+  int64_t pairs = (g_tune.dense_grid ? g_tune.dense_grid : sms) / 2;
+  if (pairs > tiles) pairs = tiles;
+  if (pairs < 1) pairs = 1;
+  return from_cuda(launch_fp8_narrow(tmW, tmX, p, static_cast<int>(2 * pairs), st));
+}
+
 int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int32_t b_block_rows,
                    void* y, int32_t y_type, int64_t M, int64_t N, int64_t K, int32_t* dev_status, void* stream) {
   g_last_launches = 0;
@@ -1070,7 +1084,19 @@ int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const fl
   // Up to 64 rows the streaming kernel (64 x 4096 x 6144: 12.6 us, tiles 18.4; 64 x 8192 x 8192: both 23),
   // above it tiles (128 x 28672 x 8192: 68 us; streaming with 128 token columns took 94).
   const int max_m = g_tune.stream_max_m == 0 || g_tune.stream_max_m > 64 ? 64 : g_tune.stream_max_m;
-  if (M <= max_m) {
+  // Tokens on the MMA's narrow side, in tiles of 128: from 33 rows to 128 where the weight has more than
+  // half a round of 256-row tiles, and while all tiles are resident at once if K is too short to be
+  // split. Measured, us, this / otherwise, 48 | 128 | 256 rows:
+  //   28672 x 8192   45 / 57 | 51 / 68 | 69 / 71      8192 x 8192   21 / 21 | 25 / 23 | 26 / 23 (split)
+  //   12288 x 4096   14 / 18 | 16 / 19 | 27 / 19      4096 x 6144   17 / 11 | 20 / 18 | 20 / 19 (split)
+  //   16384 x 2048   10 / 12 | 11 / 13 | 17 / 13      5003 x 2064  9.5 / 9.3 | 11.4 / 13.3 | 11.8 / 13.5
+  // Up to 32 rows streaming has two CTAs an SM (28672 x 8192 37 / 46, 16384 x 2048 12 / 10).
+  const int64_t nt = (N + 255) / 256, narrow_tiles = nt * ((M + 127) / 128), all_pairs = d.sms / 2;
+  const bool narrow = M > 32 && b_block_rows == 128 && !p.f32 && !g_tune.stream_max_m && !g_tune.stream_split &&
+                      ((M <= 128 && nt * 2 > all_pairs) || ((K + 127) / 128 < 24 && narrow_tiles <= all_pairs));
+  if (narrow) {
+    rc = run_fp8_narrow(a, b, N, p, narrow_tiles, d.sms, st);
+  } else if (M <= max_m) {
     const int64_t ntw = (N + 127) / 128, kb = (K + 127) / 128;
     const int tile_rows = M <= 32 ? 32 : 64;
     // As many CTAs along K as fill the resident slots (two per SM up to 32 tokens, else one), with
@@ -1160,22 +1186,16 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   rc = from_cuda(launch_fp8_tiles(expert_offsets, E, static_cast<int>(M_total), tile_rows, tiles, n_tiles, dev_status, st));
   g_last_launches = 1;
   if (rc) return rc;
-  const int64_t n_weights = static_cast<int64_t>(E) * N;
-  if (tile_rows == 256) {
-    rc = run_fp8_pair(a, b, n_weights, p, p.max_tiles * ((N + 255) / 256), d.sms, st);
-  } else {
+  const int64_t n_weights = static_cast<int64_t>(E) * N, tiles_256 = p.max_tiles * ((N + 255) / 256);
+  if (streamed) {
     CUtensorMap tmW, tmX;
     if ((rc = encode_2d(&tmW, b, n_weights, K, 128))) return rc;
     if ((rc = encode_2d(&tmX, a, M_total, K, 32))) return rc;
-    if (streamed) {
-      rc = from_cuda(launch_fp8_stream(tmW, tmX, p, tile_rows, d.sms, st));
-    } else {
-      const int64_t most = p.max_tiles * ((N + 255) / 256);
-      int64_t pairs = (g_tune.dense_grid ? g_tune.dense_grid : d.sms) / 2;
-      if (pairs > most) pairs = most;
-      if (pairs < 1) pairs = 1;
-      rc = from_cuda(launch_fp8_grouped_pair(tmW, tmX, p, static_cast<int>(2 * pairs), st));
-    }
+    rc = from_cuda(launch_fp8_stream(tmW, tmX, p, tile_rows, d.sms, st));
+  } else if (tile_rows == 128) {
+    rc = run_fp8_narrow(a, b, n_weights, p, tiles_256, d.sms, st);
+  } else {
+    rc = run_fp8_pair(a, b, n_weights, p, tiles_256, d.sms, st);
   }
   g_last_launches = 2;
   return rc;

@@ -1,8 +1,8 @@
-// FP8 block-scaled grouped GEMM for experts of up to a few hundred rows: for each expert e and its rows
-// m (sorted by expert), y[m, n] = sum_c sa[c, m] sb_e(c, n / 128) sum_{k in block c} a[m, k] b_e[n, k],
-// a, b E4M3.
+// FP8 block-scaled GEMM with the tokens on the MMA's narrow side, for experts of up to a few hundred
+// rows (rows sorted by expert) and dense layers of up to 128: with the weight of row m's expert (or
+// the one weight), y[m, n] = sum_c sa[c, m] sb(c, n / 128) sum_{k in block c} a[m, k] b[n, k], a, b E4M3.
 //
-// A CTA pair (cta_group::2) takes 256 rows of an expert's weights as the MMA's M and up to 128 of its
+// A CTA pair (cta_group::2) takes 256 rows of a weight as the MMA's M and up to 128 of its
 // tokens as N, 64 or 128: with the tokens on M a tile of 256 would be mostly empty. As in the tile
 // kernel (fp8_gemm.cu) the tensor core sums one block of 128 of K from zero into a TMEM buffer, and
 // the epilogue warps add it, times its scales, to fp32 registers; as in the streaming kernel the
@@ -12,7 +12,8 @@
 // first, under the arithmetic of the one before.
 //
 // What bounds it: up to ~100 rows an expert the weights' bytes (256 experts of 6144 x 2048, 64 rows: 514 us,
-// 0.99 of the measured copy rate; 256-row tiles 696, streaming 742). With more, ~720 cycles for a
+// 0.99 of the measured copy rate; 256-row tiles 696, streaming 742; dense 28672 x 8192, 128 rows: 51 us,
+// 256-row tiles 68). With more, ~720 cycles for a
 // block of 128 tokens, and second tiles (128 rows on average: 714 us; its bytes 544). The loop must be free
 // of conditions around the TMEM loads: guarding the last ones by `if` made the compiler keep the
 // registers' old values too, and a block took 1,300 cycles instead of 720.
@@ -26,7 +27,7 @@
 
 namespace nvfp4 {
 
-struct Fp8GroupCfg {
+struct Fp8NarrowCfg {
   // warps 0-3: producer, MMA issuer, scales, idle; warps 4-11: epilogue. 384 x 168 registers at launch.
   static constexpr int THREADS = 384;
   static constexpr int CONTROL_REGS = 104, EPILOGUE_REGS = 200;
@@ -49,16 +50,27 @@ struct Fp8GroupCfg {
 // may be the previous kernel's, which this one overlaps (programmatic dependent launch).
 struct Fp8Walk {
   const int4* list;
-  int t, step, tiles, nt;
+  int t, step, tiles, nt, mt;
+  int M;
   int expert, m0, rows, n0;
   int4 ahead;
-  DEVI void start(const Fp8GemmArgs& p, int first, int step_, int tiles_, int nt_) {
+  DEVI void look(int at) {
+    if (list) {
+      ahead = list[at / nt];
+    } else {  // one weight: token tiles of M rows
+      const int r = at % mt * 128;
+      ahead = make_int4(0, r, min(128, M - r), 0);
+    }
+  }
+  DEVI void start(const Fp8GemmArgs& p, int first, int step_) {
     list = p.tiles;
+    M = static_cast<int>(p.M);
+    nt = (static_cast<int>(p.N) + 255) / 256;
+    mt = (M + 127) / 128;
     t = first - step_;
     step = step_;
-    tiles = tiles_;
-    nt = nt_;
-    if (first < tiles) ahead = list[first / nt];
+    tiles = nt * (list ? p.n_tiles[0] : mt);
+    if (first < tiles) look(first);
     next();
   }
   DEVI bool valid() const { return t < tiles; }
@@ -68,16 +80,16 @@ struct Fp8Walk {
     expert = ahead.x;
     m0 = ahead.y;
     rows = ahead.z;
-    n0 = (t % nt) * 256;
-    if (t + step < tiles) ahead = list[(t + step) / nt];
+    n0 = (list ? t % nt : t / mt) * 256;
+    if (t + step < tiles) look(t + step);
   }
   DEVI int columns() const { return (rows + 63) & ~63; }  // the MMA's N
 };
 
-__global__ void __launch_bounds__(Fp8GroupCfg::THREADS, 1)
-    k_fp8_grouped_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+__global__ void __launch_bounds__(Fp8NarrowCfg::THREADS, 1)
+    k_fp8_narrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ Fp8GemmArgs p) {
-  using C = Fp8GroupCfg;
+  using C = Fp8NarrowCfg;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -128,13 +140,13 @@ __global__ void __launch_bounds__(Fp8GroupCfg::THREADS, 1)
   griddep_wait();  // set-up overlaps the previous kernel; every memory access waits for it
 
   const int M = static_cast<int>(p.M), N = static_cast<int>(p.N);
-  const int nt = (N + 255) / 256, nb = (N + 127) / 128;
+  const int nb = (N + 127) / 128;
   const int KB = static_cast<int>((p.K + 127) / 128);
   Fp8Walk w;
 
   if (warp >= 4) {
     regs_inc<C::EPILOGUE_REGS>();
-    w.start(p, blockIdx.x / 2, gridDim.x / 2, p.n_tiles[0] * nt, nt);
+    w.start(p, blockIdx.x / 2, gridDim.x / 2);
     const int q = warp & 3, h = (warp - 4) >> 2;
     uint8_t* box = out_buf + (warp - 4) * 4096;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(Fp8GroupCfg::THREADS, 1)
     }
   } else {
     regs_dec<C::CONTROL_REGS>();
-    if (warp < 3) w.start(p, blockIdx.x / 2, gridDim.x / 2, p.n_tiles[0] * nt, nt);
+    if (warp < 3) w.start(p, blockIdx.x / 2, gridDim.x / 2);
     if (warp == 0) {
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
       int s = 0;
@@ -404,14 +416,14 @@ __global__ void __launch_bounds__(Fp8GroupCfg::THREADS, 1)
   if (threadIdx.x == 0 && *abort_flag) report_status(p.status, kStatusTimeout);
 }
 
-cudaError_t launch_fp8_grouped_pair(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int grid,
+cudaError_t launch_fp8_narrow(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int grid,
                                     cudaStream_t st) {
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(k_fp8_grouped_pair));
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(k_fp8_narrow));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Fp8GroupCfg::THREADS);
-  cfg.dynamicSmemBytes = Fp8GroupCfg::SMEM_BYTES;
+  cfg.blockDim = dim3(Fp8NarrowCfg::THREADS);
+  cfg.dynamicSmemBytes = Fp8NarrowCfg::SMEM_BYTES;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -422,7 +434,7 @@ cudaError_t launch_fp8_grouped_pair(const CUtensorMap& tmW, const CUtensorMap& t
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, k_fp8_grouped_pair, tmW, tmX, p);
+  e = cudaLaunchKernelEx(&cfg, k_fp8_narrow, tmW, tmX, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -9,7 +9,7 @@
 //   dense:   grid = (N / 128) x S CTAs in clusters of S along K; the S partial sums meet through
 //            distributed shared memory, each CTA owning some of the tokens.
 //   grouped: a persistent grid walks (token tile, weight tile) items of the device-built list; for
-//            problems whose items are all resident at once (fp8_grouped.cu has the larger ones).
+//            problems whose items are all resident at once (fp8_narrow.cu has the larger ones).
 // Data that the previous kernel may have written is read with plain loads (see fp8_gemm.cu).
 #include <stdint.h>
 

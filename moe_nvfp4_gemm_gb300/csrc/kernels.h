@@ -201,8 +201,9 @@ cudaError_t launch_fp8_tiles(const int32_t* offsets, int E, int M, int tile_rows
 // grid: an even number of CTAs (two per 256 x 256 tile in flight)
 cudaError_t launch_fp8_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmY,
                                  const Fp8GemmArgs& p, int grid, cudaStream_t st);
-// grid: an even number of CTAs (two per tile of 256 weight rows and up to 128 tokens in flight)
-cudaError_t launch_fp8_grouped_pair(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int grid,
+// grid: an even number of CTAs (two per tile of 256 weight rows and up to 128 tokens in flight);
+// dense without p.tiles. tmW has 128-row boxes, tmX 32.
+cudaError_t launch_fp8_narrow(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int grid,
                                     cudaStream_t st);
 
 int stream_smem_bytes(int stages, int x_rows, int recv_bytes, bool sparse = false);

@@ -167,6 +167,25 @@ def test_gemm(M, N, K, b_rows, out):
     assert (guard[M * N:] == 7.0).all()  # nothing past the output
 
 
+@pytest.mark.parametrize("M,N,K", [(33, 10000, 144), (64, 9984, 2064), (65, 257, 400), (100, 12000, 1040), (128, 8, 16),
+                                   (129, 1000, 272), (300, 2500, 528), (77, 9995, 3088)])
+def test_gemm_tokens_on_the_narrow_side(M, N, K):
+    """Dense sizes that take token tiles of up to 128 rows, and the same product in 256 x 256 tiles."""
+    a, sa = m.nvfp4_fp8_quantize(acts(M, K, M + K))
+    b, sb = m.nvfp4_fp8_quantize(acts(N, K, N, 0.02), 128)
+    A, B = decode(a, sa, 1), decode(b, sb, 128)
+    st = torch.zeros(1, dtype=torch.int32, device=dev())
+    y = m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K, dev_status=st)
+    check(y, A, B)
+    assert torch.equal(y, m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K))
+    try:
+        m.nvfp4_tune(m.NVFP4_TUNE_STREAM_MAX_M, -1)
+        check(m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K, dev_status=st), A, B)
+    finally:
+        m.nvfp4_tune(m.NVFP4_TUNE_STREAM_MAX_M, 0)
+    assert st.item() == 0
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 31, 48, 100, 128, 160, 300])
 def test_gemm_repeats_and_scales_apply_per_block(M):
     """Block scales that differ by powers of two between neighbours, ones codes: the result is a closed form."""
