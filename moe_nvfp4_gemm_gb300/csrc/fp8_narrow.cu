@@ -16,7 +16,8 @@
 // 256-row tiles 68). With more, ~720 cycles for a
 // block of 128 tokens, and second tiles (128 rows on average: 714 us; its bytes 544). The loop must be free
 // of conditions around the TMEM loads: guarding the last ones by `if` made the compiler keep the
-// registers' old values too, and a block took 1,300 cycles instead of 720.
+// registers' old values too, and a block took 1,300 cycles instead of 720. Both chunks of a block by one
+// load, with registers for two blocks, was slower (128 rows 773 us).
 #include <stdint.h>
 
 #include <type_traits>
