@@ -1081,19 +1081,33 @@ int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const fl
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Up to 64 rows the streaming kernel (64 x 4096 x 6144: 12.6 us, tiles 18.4; 64 x 8192 x 8192: both 23),
-  // above it tiles (128 x 28672 x 8192: 68 us; streaming with 128 token columns took 94).
+  // Otherwise up to 64 rows the streaming kernel (64 x 4096 x 6144: 12.6 us, tiles 18.4; 64 x 8192 x 8192: both
+  // 23), above it tiles.
   const int max_m = g_tune.stream_max_m == 0 || g_tune.stream_max_m > 64 ? 64 : g_tune.stream_max_m;
   // Tokens on the MMA's narrow side, in tiles of 128: from 33 rows to 128 where the weight has more than
-  // half a round of 256-row tiles, and while all tiles are resident at once if K is too short to be
-  // split. Measured, us, this / otherwise, 48 | 128 | 256 rows:
-  //   28672 x 8192   45 / 57 | 51 / 68 | 69 / 71      8192 x 8192   21 / 21 | 25 / 23 | 26 / 23 (split)
-  //   12288 x 4096   14 / 18 | 16 / 19 | 27 / 19      4096 x 6144   17 / 11 | 20 / 18 | 20 / 19 (split)
-  //   16384 x 2048   10 / 12 | 11 / 13 | 17 / 13      5003 x 2064  9.5 / 9.3 | 11.4 / 13.3 | 11.8 / 13.5
-  // Up to 32 rows streaming has two CTAs an SM (28672 x 8192 37 / 46, 16384 x 2048 12 / 10).
-  const int64_t nt = (N + 255) / 256, narrow_tiles = nt * ((M + 127) / 128), all_pairs = d.sms / 2;
-  const bool narrow = M > 32 && b_block_rows == 128 && !p.f32 && !g_tune.stream_max_m && !g_tune.stream_split &&
-                      ((M <= 128 && nt * 2 > all_pairs) || ((K + 127) / 128 < 24 && narrow_tiles <= all_pairs));
+  // half a round of 256-row tiles, and while all tiles are resident at once if K is too short for parts
+  // of it to gain. Measured, us, this / otherwise:
+  //   rows               40          64          128         256         1024
+  //   28672 x 8192    45 / 57     44 / 60     51 / 68     69 / 71
+  //   14336 x 2816  10.7 / 14.1 10.8 / 14.8 12.6 / 14.9
+  //   8192 x 2816    9.6 / 11.4  9.5 / 13.2 11.8 / 13.8 12.8 / 14.0
+  //   2048 x 2816    9.3 / 7.3   9.2 / 8.3  11.7 / 13.4 11.6 / 13.5 12.6 / 13.9
+  //   4096 x 2048    7.7 / 7.6   7.8 / 8.7   9.4 / 11.2  9.4 / 11.2
+  //   2048 x 1040    5.8 / 7.8   5.8 / 9.4   6.9 / 7.9   7.0 / 8.2   7.9 / 8.3
+  //   1536 x 512     4.1 / 5.3   4.3 / 5.6   5.1 / 5.7   5.2 / 5.8   5.7 / 5.9
+  //   8192 x 8192    21 / 21     21 / 23     25 / 23     26 / 23  (K in parts; 4096 x 6144, 128 rows: 20 / 18)
+  //   16384 x 2048   10 / 12     10 / 12     11 / 13     17 / 13  (more than a round)
+  // Up to 32 rows streaming has two CTAs an SM and splits K further; shorter K cannot be split:
+  //   rows                1           8          16          32
+  //   2048 x 2048    7.6 / 5.1   7.5 / 5.1   7.7 / 5.5   7.6 / 6.6
+  //   2048 x 1040    5.6 / 5.2   5.8 / 5.8   5.7 / 6.6   5.9 / 8.2
+  //   8192 x 1040    6.1 / 6.1   6.1 / 6.6   6.2 / 7.5   6.2 / 9.0
+  //   8192 x 512     4.3 / 4.9   4.4 / 4.9   4.5 / 5.0   4.7 / 5.1
+  const int64_t blocks = (K + 127) / 128, nt = (N + 255) / 256, narrow_tiles = nt * ((M + 127) / 128);
+  const int64_t all_pairs = d.sms / 2;
+  const bool short_k = blocks <= 16 || (blocks < 24 && (M > 64 || nt >= 20));
+  const bool narrow = (M > 32 || (M > 8 && blocks <= 12)) && b_block_rows == 128 && !p.f32 && !g_tune.stream_max_m && !g_tune.stream_split &&
+                      ((M > 32 && M <= 128 && nt * 2 > all_pairs) || (short_k && narrow_tiles <= all_pairs));
   if (narrow) {
     rc = run_fp8_narrow(a, b, N, p, narrow_tiles, d.sms, st);
   } else if (M <= max_m) {

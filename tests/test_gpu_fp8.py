@@ -186,6 +186,13 @@ def test_gemm_tokens_on_the_narrow_side(M, N, K):
     assert st.item() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(9, 260, 1536), (16, 384, 2064), (20, 8200, 1680), (32, 1000, 4112), (32, 9000, 400)])
+def test_gemm_few_rows(M, N, K):
+    a, sa = m.nvfp4_fp8_quantize(acts(M, K, M + K))
+    b, sb = m.nvfp4_fp8_quantize(acts(N, K, N, 0.02), 128)
+    check(m.nvfp4_fp8_gemm(a, sa, b, sb, M, N, K), decode(a, sa, 1), decode(b, sb, 128))
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 31, 48, 100, 128, 160, 300])
 def test_gemm_repeats_and_scales_apply_per_block(M):
     """Block scales that differ by powers of two between neighbours, ones codes: the result is a closed form."""
