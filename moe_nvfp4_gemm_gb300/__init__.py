@@ -495,29 +495,33 @@ class MoeRouting:
     _fields = ("topk_idx", "topk_w", "slot_row", "counts", "expert_offsets", "row_token", "mean_prob", "balance_loss",
                "routed_tokens")
 
+    # field: words from the start in units of (T k, E, 1), elements in the same units, fp32
+    _layout = {"topk_idx": (0, 0, 0, None, False), "topk_w": (1, 0, 0, None, True), "slot_row": (2, 0, 0, None, False),
+               "row_token": (3, 0, 0, (1, 0, 0), False), "counts": (4, 0, 0, (0, 1, 0), False),
+               "expert_offsets": (4, 1, 0, (0, 1, 1), False), "mean_prob": (4, 2, 1, (0, 1, 0), True),
+               "balance_loss": (4, 3, 1, (0, 0, 1), True), "routed_tokens": (4, 3, 2, (0, 0, 1), False)}
+
     def __init__(self, T, E, k, device, workspace_words):
-        n = T * max(k, 0)
+        n = T * k if k > 0 else 0
         self.T, self.E, self.k = T, E, k
-        self._all = None
-        # field: first word in the allocation
-        self._at = {"topk_idx": 0, "topk_w": n, "slot_row": 2 * n, "row_token": 3 * n, "counts": 4 * n,
-                    "expert_offsets": 4 * n + E, "mean_prob": 4 * n + 2 * E + 1, "balance_loss": 4 * n + 3 * E + 1,
-                    "routed_tokens": 4 * n + 3 * E + 2}
+        self._all = self._float = None
         words = (4 * n + 3 * E + 6) // 4 * 4
         self._buf = torch.empty(words + workspace_words, dtype=torch.int32, device=device)
-        self._base = self._buf.data_ptr()
+        self._base = self._buf.data_ptr()  # topk_idx; counts at _counts, in bytes
+        self._counts = self._base + 16 * n
         self._workspace = self._base + 4 * words
 
-    def _address(self, field):
-        return self._base + 4 * self._at[field]
-
     def _make(self, name):
-        buf = self._buf.view(torch.float32) if name in ("topk_w", "mean_prob", "balance_loss") else self._buf
-        if name in ("topk_idx", "topk_w", "slot_row"):
-            return buf.as_strided((self.T, self.k), (self.k, 1), self._at[name])
-        n = {"row_token": self.T * self.k, "counts": self.E, "expert_offsets": self.E + 1,
-             "mean_prob": self.E}.get(name, 1)
-        return buf.as_strided((n,), (1,), self._at[name])
+        a, b, c, size, fp32 = MoeRouting._layout[name]
+        T, E, k, buf = self.T, self.E, self.k, self._buf
+        if fp32:
+            buf = self._float
+            if buf is None:
+                buf = self._float = self._buf.view(torch.float32)
+        at = a * T * k + b * E + c
+        if size is None:
+            return buf.as_strided((T, k), (k, 1), at)
+        return buf.as_strided((size[0] * T * k + size[1] * E + size[2],), (1,), at)
 
     def __getattr__(self, name):  # only for what is not there yet
         if name not in MoeRouting._fields:
@@ -527,13 +531,15 @@ class MoeRouting:
 
     def _asdict(self):
         if self._all is None:
-            T, E, k, at, b = self.T, self.E, self.k, self._at, self._buf.as_strided
-            f = self._buf.view(torch.float32).as_strided
+            T, E, k, b = self.T, self.E, self.k, self._buf.as_strided
+            if self._float is None:
+                self._float = self._buf.view(torch.float32)
+            f = self._float.as_strided
             per, row, one, n = (T, k), (k, 1), (1,), T * k
             made = {"topk_idx": b(per, row, 0), "topk_w": f(per, row, n), "slot_row": b(per, row, 2 * n),
-                    "counts": b((E,), one, at["counts"]), "expert_offsets": b((E + 1,), one, at["expert_offsets"]),
-                    "row_token": b((n,), one, 3 * n), "mean_prob": f((E,), one, at["mean_prob"]),
-                    "balance_loss": f(one, one, at["balance_loss"]), "routed_tokens": b(one, one, at["routed_tokens"])}
+                    "counts": b((E,), one, 4 * n), "expert_offsets": b((E + 1,), one, 4 * n + E),
+                    "row_token": b((n,), one, 3 * n), "mean_prob": f((E,), one, 4 * n + 2 * E + 1),
+                    "balance_loss": f(one, one, 4 * n + 3 * E + 1), "routed_tokens": b(one, one, 4 * n + 3 * E + 2)}
             have = self.__dict__
             for field in made:  # those handed out before stay
                 if field in have:
@@ -567,11 +573,12 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
     T, E = _route_inputs(logits, valid)
     ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
     r = MoeRouting(T, E, k, logits.device, ws_bytes // 4 if workspace is None else 0)
-    at = r._address
+    base, counts = r._base, r._counts  # four arrays of T k words, then counts and what follows
+    n = (counts - base) // 4
     _check("nvfp4_moe_route",
            lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
-                                 at("topk_idx"), at("topk_w"), at("slot_row"), at("counts"), at("expert_offsets"),
-                                 at("row_token"), at("mean_prob"), at("balance_loss"), at("routed_tokens"),
+                                 base, base + n, base + 2 * n, counts, counts + 4 * E, base + 3 * n,
+                                 counts + 8 * E + 4, counts + 12 * E + 4, counts + 12 * E + 8,
                                  r._workspace if workspace is None else _operand(workspace, _U8, 0, "workspace"),
                                  ws_bytes if workspace is None else workspace.numel(), _stream(stream)))
     return r
@@ -591,11 +598,11 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
             if tuple(t.shape) != shape:
                 raise TypeError(f"{n} must have shape {shape}")
     d_logits = torch.empty_like(logits) if d_logits is None else d_logits
-    at = routing._address
+    base, counts = routing._base, routing._counts
     _check("nvfp4_moe_route_backward",
            lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
-                                          int(renormalize), at("topk_idx"), at("topk_w"), at("counts"),
-                                          at("routed_tokens"), _ptr(d_w), _ptr(d_loss),
+                                          int(renormalize), base, base + (counts - base) // 4, counts,
+                                          counts + 12 * E + 8, _ptr(d_w), _ptr(d_loss),
                                           _operand(d_logits, (logits.dtype,), T * E, "d_logits"), _stream(stream)))
     return d_logits
 
