@@ -417,13 +417,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     const int q = warp & 3, h = (warp - 2) >> 2;
-    griddep_wait();  // reads the global scales, writes y
-    const float alpha = __ldg(p.ga) * __ldg(p.gb);
+    griddep_wait();  // reads the global scales (plain loads stay behind the wait; __ldg need not), writes y
+    const float alpha = *p.ga * *p.gb;
     uint8_t* buf = out_buf + (warp - 2) * 4096;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     float g_q = 1.0f, g_q_inv = 1.0f;
     if (QOUT) {
-      g_q = __ldg(p.g_out);
+      g_q = *p.g_out;
       g_q_inv = __frcp_rn(g_q);
     }
     uint32_t acc_ph = 0;

@@ -61,12 +61,16 @@ struct Item {
   int kb0, kb1;
 };
 
+// What the previous kernel in the stream may have written (tile list and count, row_token, global
+// scales) is read with plain loads: under programmatic dependent launch this kernel is already
+// running while that one writes, so the data is not read-only for its life, as the non-coherent path
+// (__ldg) requires; the compiler may move such a load above griddep_wait, a plain one stays behind it.
 template <bool GROUPED>
 DEVI bool get_item(const StreamArgs& p, int i, int n_items, int NT, int KB, Item& it) {
   if (i >= n_items) return false;
   if (GROUPED) {
     const int tile = i / NT;
-    const int4 t = __ldg(p.tiles + tile);
+    const int4 t = p.tiles[tile];
     it.wt = i % NT;
     it.e = t.x;
     it.row0 = t.y;
@@ -105,13 +109,13 @@ DEVI bool next_item(const StreamArgs& p, int i, int stride, int n_items, int NT,
   it.slab = desc.w;
   it.kb0 = 0;
   it.kb1 = KB;
-  if (i + stride < n_items) desc = __ldg(p.tiles + (i + stride) / NT);
+  if (i + stride < n_items) desc = p.tiles[(i + stride) / NT];
   return true;
 }
 
 template <bool GROUPED>
 DEVI int4 first_desc(const StreamArgs& p, int first, int n_items, int NT) {
-  return (GROUPED && first < n_items) ? __ldg(p.tiles + first / NT) : make_int4(0, 0, 0, 0);
+  return (GROUPED && first < n_items) ? p.tiles[first / NT] : make_int4(0, 0, 0, 0);
 }
 
 // Warp roles: 0 weight producer (each stage's weight tile and scales), 1 MMA issuer, 2-5
@@ -322,7 +326,7 @@ DEVI void stream_body(const CUtensorMap& tmW, const CUtensorMap& tmX, const Stre
   if (GROUPED && p.pdl) griddep_wait();
   int n_items, first, stride;
   if (GROUPED) {
-    n_items = __ldg(p.n_tiles) * NT;
+    n_items = p.n_tiles[0] * NT;
     first = cta;
     stride = gridDim.x;
   } else {
@@ -393,10 +397,9 @@ DEVI void stream_body(const CUtensorMap& tmW, const CUtensorMap& tmX, const Stre
       for (int j = 0; j < 16; ++j) issued_phase[j] = -1;
       Item it;
       auto load_tokens = [&](const Item& x) {
-        return make_int4(__ldg(p.row_token + x.row0 + min(lane, x.rows - 1)),
-                         __ldg(p.row_token + x.row0 + min(lane + 32, x.rows - 1)),
-                         __ldg(p.row_token + x.row0 + min(lane + 64, x.rows - 1)),
-                         __ldg(p.row_token + x.row0 + min(lane + 96, x.rows - 1)));
+        const int32_t* tok = p.row_token + x.row0;
+        return make_int4(tok[min(lane, x.rows - 1)], tok[min(lane + 32, x.rows - 1)], tok[min(lane + 64, x.rows - 1)],
+                         tok[min(lane + 96, x.rows - 1)]);
       };
       int4 tok_regs = make_int4(0, 0, 0, 0);
       bool tok_ready = false;
@@ -544,10 +547,10 @@ DEVI void stream_body(const CUtensorMap& tmW, const CUtensorMap& tmX, const Stre
     }
     if (!GROUPED && p.pdl) griddep_wait();  // the global scales may come from the previous kernel
     const int q = warp & 3;
-    const float ga = __ldg(p.ga);
-    const float gq = (VARIANT & 8) ? __ldg(p.g_out) : 1.0f;  // NVFP4 output: the caller's global scale
+    const float ga = *p.ga;
+    const float gq = (VARIANT & 8) ? *p.g_out : 1.0f;  // NVFP4 output: the caller's global scale
     const float gq_inv = __frcp_rn(gq);
-    const float gb0 = GROUPED ? 0.0f : __ldg(p.gb);  // dense: read while the mainloop runs
+    const float gb0 = GROUPED ? 0.0f : *p.gb;  // dense: read while the mainloop runs
     dense_alpha = ga * gb0;
     int buf = 0;
     uint32_t acc_ph[2] = {0, 0};
@@ -556,7 +559,7 @@ DEVI void stream_body(const CUtensorMap& tmW, const CUtensorMap& tmX, const Stre
     for (int i = first; next_item<GROUPED>(p, i, stride, n_items, NT, KB, desc, it); i += stride) {
       if (!mbar_wait_warp(&tfull[buf], acc_ph[buf], abort_flag, wd)) break;
       tc_fence_after();
-      const float alpha = ga * (GROUPED ? __ldg(p.gb + it.e) : gb0);
+      const float alpha = ga * (GROUPED ? p.gb[it.e] : gb0);
       const int wrow = it.wt * 128 + q * 32 + lane;  // output column
       const int n_mma = ((it.rows + 15) >> 4) * 16;
       const bool has_k = it.kb1 > it.kb0;

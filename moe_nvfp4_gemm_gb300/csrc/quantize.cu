@@ -18,6 +18,10 @@
 
 namespace nvfp4 {
 
+// The kernels here that start under programmatic dependent launch read their inputs with plain loads
+// through plain pointers: the previous kernel may still be writing those inputs when they start, and a
+// load that is declared read-only (__ldg, const __restrict__) may be moved above griddep_wait.
+
 // ---- amax ------------------------------------------------------------------------
 
 constexpr int kAmaxUnroll = 4;  // 16-byte loads in flight per thread
@@ -27,8 +31,7 @@ constexpr int kAmaxUnroll = 4;  // 16-byte loads in flight per thread
 // step); maxima are taken on bf16 pairs with their sign bits cleared, which is exact.
 // (A grid-stride sweep with one load in flight per thread took 14.5 us on the prefill
 // activations from HBM; this one 11.8 us.)
-__global__ void __launch_bounds__(256) k_amax_partial(const uint16_t* __restrict__ x, int64_t n,
-                                                      float* __restrict__ partial) {
+__global__ void __launch_bounds__(256) k_amax_partial(const uint16_t* x, int64_t n, float* partial) {
   // Launched with programmatic stream serialization: the CTAs may start while the previous
   // kernel in the stream finishes, and wait for it here before reading x.
   griddep_wait();
@@ -44,7 +47,7 @@ __global__ void __launch_bounds__(256) k_amax_partial(const uint16_t* __restrict
   for (; i + (kAmaxUnroll - 1) * bd < b1; i += kAmaxUnroll * bd) {
     uint4 v[kAmaxUnroll];
 #pragma unroll
-    for (int u = 0; u < kAmaxUnroll; ++u) v[u] = __ldg(xv + i + u * bd);
+    for (int u = 0; u < kAmaxUnroll; ++u) v[u] = xv[i + u * bd];
 #pragma unroll
     for (int u = 0; u < kAmaxUnroll; ++u) {
       const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -53,7 +56,7 @@ __global__ void __launch_bounds__(256) k_amax_partial(const uint16_t* __restrict
     }
   }
   for (; i < b1; i += bd) {
-    const uint4 v = __ldg(xv + i);
+    const uint4 v = xv[i];
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[j] & 0x7FFF7FFFu));
@@ -76,8 +79,8 @@ __global__ void __launch_bounds__(256) k_amax_partial(const uint16_t* __restrict
 }
 
 // Reduces the partial maxima; writes amax and the decode-direction global scale.
-__global__ void __launch_bounds__(256) k_amax_final(const float* __restrict__ partial, int np,
-                                                    float* amax_out, float* g_out) {
+__global__ void __launch_bounds__(256) k_amax_final(const float* partial, int np, float* amax_out,
+                                                    float* g_out) {
   griddep_wait();  // launched programmatically behind k_amax_partial: its partials are complete
   // the next kernel in the stream may launch now (one CTA here holds no resources it needs);
   // a kernel that waits for this one's completion still sees amax and g
@@ -114,9 +117,8 @@ constexpr int kQuantRows = kQuantThreads / 4;
 // loads' and the arithmetic's latency than larger CTAs or more blocks per thread
 // (measured on the prefill activations, 4096 x 8192: 20.2-20.5 us against 22.9 us for
 // 128-row CTAs with four blocks per thread and the scale tile staged in shared memory).
-__global__ void __launch_bounds__(kQuantThreads, 6) k_quantize(const uint16_t* __restrict__ x, int64_t M, int64_t K,
-                                                               const float* __restrict__ gptr,
-                                                               uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
+__global__ void __launch_bounds__(kQuantThreads, 6) k_quantize(const uint16_t* x, int64_t M, int64_t K,
+                                                               const float* gptr, uint8_t* q, uint8_t* sf) {
   // Launched with programmatic stream serialization (set-up overlap only): wait for the
   // previous kernel in the stream before any memory access.
   griddep_wait();
@@ -125,15 +127,15 @@ __global__ void __launch_bounds__(kQuantThreads, 6) k_quantize(const uint16_t* _
   const int64_t row = static_cast<int64_t>(blockIdx.y) * 128 + (blockIdx.x & 1) * kQuantRows + r_local;
   const int64_t kc4 = K / 64;
   const int64_t col4_0 = static_cast<int64_t>(blockIdx.x >> 1) * kQuantTiles;
-  const float g = __ldg(gptr);
+  const float g = *gptr;
   const float g_inv = __frcp_rn(g);
   uint4 v[kQuantTiles][2];
 #pragma unroll
   for (int t = 0; t < kQuantTiles; ++t) {
     if (row < M && col4_0 + t < kc4) {
       const uint4* src = reinterpret_cast<const uint4*>(x + row * K + ((col4_0 + t) * 4 + c_local) * 16);
-      v[t][0] = __ldg(src);
-      v[t][1] = __ldg(src + 1);
+      v[t][0] = src[0];
+      v[t][1] = src[1];
     }
   }
 #pragma unroll
