@@ -5,6 +5,8 @@ their data pointers and the current CUDA stream to the function of the same
 name in libnvfp4.so, and raises on a non-zero status. All arithmetic runs in
 the library's kernels; there is no fallback of any kind. Output tensors and
 workspaces are allocated here with torch (the library itself never allocates).
+Every call takes `stream`: the torch.cuda.Stream to run on, the current one by default; what the call
+allocates belongs to that stream, and the caller orders it against other streams as any torch work.
 """
 from __future__ import annotations
 
@@ -149,11 +151,26 @@ def _ptr(t):  # an int: every entry point's argtypes convert it to the pointer
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream=None):
-    if stream is not None:
-        return stream.cuda_stream
+def _stream():
     # the current stream's handle without the Stream object (3 us of a small call's host time)
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on_stream(stream, fn, args):
+    """The call fn(**args) with `stream` as the current stream, so that what it allocates (outputs, workspaces)
+    is that stream's: torch's allocator then neither hands the call a block that another stream still reads nor
+    passes a dropped workspace on while the kernels use it. The outputs are recorded for the caller's current
+    stream too, where they are usually read next (after waiting)."""
+    args["stream"] = None
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = fn(**args)
+    if stream != here:
+        for t in out if isinstance(out, tuple) else (out,):
+            t = t._buf if isinstance(t, MoeRouting) else t
+            if t is not None:
+                t.record_stream(here)
+    return out
 
 
 def _check(fn, rc):
@@ -193,6 +210,8 @@ def nvfp4_status_string(status: int) -> str:
 
 def nvfp4_amax(x: torch.Tensor, amax_out=None, g_out=None, workspace=None, stream=None):
     """Returns (amax, g) as 1-element fp32 CUDA tensors; g = amax / 2688 (1 if amax == 0)."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_amax, locals())
     _cuda(x, torch.bfloat16, "x")
     dev = x.device
     amax_out = torch.empty(1, dtype=torch.float32, device=dev) if amax_out is None else amax_out
@@ -201,12 +220,14 @@ def nvfp4_amax(x: torch.Tensor, amax_out=None, g_out=None, workspace=None, strea
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check("nvfp4_amax", lib().nvfp4_amax(_ptr(x), x.numel(), _ptr(amax_out), _ptr(g_out),
-                                          _ptr(workspace), workspace.numel(), _stream(stream)))
+                                          _ptr(workspace), workspace.numel(), _stream()))
     return amax_out, g_out
 
 
 def nvfp4_quantize(x: torch.Tensor, global_scale: torch.Tensor, q_out=None, sf_out=None, stream=None):
     """bf16 [M, K] -> (q u8 [M, K/2], sf u8 [nvfp4_scale_bytes(M, K)])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_quantize, locals())
     _cuda(x, torch.bfloat16, "x")
     _cuda(global_scale, torch.float32, "global_scale")
     M, K = x.shape
@@ -214,13 +235,15 @@ def nvfp4_quantize(x: torch.Tensor, global_scale: torch.Tensor, q_out=None, sf_o
     sf_out = (torch.empty(nvfp4_scale_bytes(M, K), dtype=torch.uint8, device=x.device)
               if sf_out is None else sf_out)
     _check("nvfp4_quantize", lib().nvfp4_quantize(_ptr(x), M, K, _ptr(global_scale), _ptr(q_out),
-                                                  _ptr(sf_out), _stream(stream)))
+                                                  _ptr(sf_out), _stream()))
     return q_out, sf_out
 
 
 def nvfp4_gemm(a, sfa, ga, b, sfb, gb, M: int, N: int, K: int, y=None, dev_status=None,
                stream=None):
     """y = x @ W^T in bf16 [M, N] from packed NVFP4 operands (see include/nvfp4.h)."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_gemm, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b, "b"), (sfb, "sfb")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -230,7 +253,7 @@ def nvfp4_gemm(a, sfa, ga, b, sfb, gb, M: int, N: int, K: int, y=None, dev_statu
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=a.device) if ws_bytes else None
     _check("nvfp4_gemm", lib().nvfp4_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                           _ptr(y), M, N, K, _ptr(ws), ws_bytes, _ptr(dev_status),
-                                          _stream(stream)))
+                                          _stream()))
     return y
 
 
@@ -242,6 +265,8 @@ def nvfp4_gemm_quantize_out(a, sfa, ga, b, sfb, gb, g_out, M: int, N: int, K: in
                             dev_status=None, stream=None):
     """y = x . W^T as nvfp4_gemm, emitted as NVFP4 with global scale g_out: returns
     (codes uint8 [M, N/2], tiled scales uint8 [nvfp4_scale_bytes(M, N)])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_gemm_quantize_out, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b, "b"), (sfb, "sfb")):
         _cuda(t, torch.uint8, n)
     for t, n in ((ga, "ga"), (gb, "gb"), (g_out, "g_out")):
@@ -252,13 +277,15 @@ def nvfp4_gemm_quantize_out(a, sfa, ga, b, sfb, gb, g_out, M: int, N: int, K: in
         sf_out = torch.empty(nvfp4_scale_bytes(M, N), dtype=torch.uint8, device=a.device)
     _check("nvfp4_gemm_quantize_out",
            lib().nvfp4_gemm_quantize_out(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb), _ptr(g_out),
-                                         _ptr(q_out), _ptr(sf_out), M, N, K, _ptr(dev_status), _stream(stream)))
+                                         _ptr(q_out), _ptr(sf_out), M, N, K, _ptr(dev_status), _stream()))
     return q_out, sf_out
 
 
 def nvfp4_grouped_gemm(a, sfa, ga, b, sfb, gb, expert_offsets, E: int, M_total: int, N: int,
                        K: int, y=None, workspace=None, dev_status=None, stream=None):
     """Per-expert y[rows of e] = x[rows of e] @ W_e^T, rows sorted by expert (bf16 [M_total, N])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grouped_gemm, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b, "b"), (sfb, "sfb")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -272,7 +299,7 @@ def nvfp4_grouped_gemm(a, sfa, ga, b, sfb, gb, expert_offsets, E: int, M_total: 
            lib().nvfp4_grouped_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                     _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
                                     _ptr(workspace), workspace.numel(), _ptr(dev_status),
-                                    _stream(stream)))
+                                    _stream()))
     return y
 
 
@@ -282,6 +309,8 @@ def nvfp4_grouped_gemm_gather(a_tok, sfa_tok, ga, b, sfb, gb, expert_offsets, ro
     the T-row activations a_tok: bf16 [M_total, N] in routed-row order. The default
     workspace has room for the rows to be copied out ahead of the GEMM; one of
     nvfp4_grouped_gemm_workspace_bytes bytes makes the GEMM's load stage gather them."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grouped_gemm_gather, locals())
     for t, n in ((a_tok, "a_tok"), (sfa_tok, "sfa_tok"), (b, "b"), (sfb, "sfb")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -295,7 +324,7 @@ def nvfp4_grouped_gemm_gather(a_tok, sfa_tok, ga, b, sfb, gb, expert_offsets, ro
     _check("nvfp4_grouped_gemm_gather",
            lib().nvfp4_grouped_gemm_gather(_ptr(a_tok), _ptr(sfa_tok), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                            _ptr(expert_offsets), _ptr(row_token), E, T, M_total, N, K, _ptr(y),
-                                           _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)))
+                                           _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream()))
     return y
 
 
@@ -307,6 +336,8 @@ def nvfp4_grouped_gemm_swiglu(a, sfa, ga, b_gu, sfb_gu, gb, expert_offsets, E: i
                               K: int, y=None, workspace=None, dev_status=None, stream=None):
     """Gate/up projection with fused SwiGLU: b_gu interleaves gate and up rows (row 2c gate c,
     2c + 1 up c); returns y[m, c] = silu(gate) * up as bf16 [M_total, N_gu // 2]."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grouped_gemm_swiglu, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b_gu, "b_gu"), (sfb_gu, "sfb_gu")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -320,7 +351,7 @@ def nvfp4_grouped_gemm_swiglu(a, sfa, ga, b_gu, sfb_gu, gb, expert_offsets, E: i
            lib().nvfp4_grouped_gemm_swiglu(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_gu), _ptr(sfb_gu), _ptr(gb),
                                            _ptr(expert_offsets), E, M_total, N_gu, K, _ptr(y),
                                            _ptr(workspace), workspace.numel(), _ptr(dev_status),
-                                           _stream(stream)))
+                                           _stream()))
     return y
 
 
@@ -334,6 +365,8 @@ def nvfp4_grouped_gemm_noalloc(a, sfa, ga, b, sfb, gb, expert_offsets, E: int, M
     For callers that cannot allocate device memory where they run the MoE layer (runtimes
     with a fixed memory budget and no allocator). Only `y` is allocated here when not given.
     """
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grouped_gemm_noalloc, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b, "b"), (sfb, "sfb")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -343,7 +376,7 @@ def nvfp4_grouped_gemm_noalloc(a, sfa, ga, b, sfb, gb, expert_offsets, E: int, M
     _check("nvfp4_grouped_gemm_noalloc",
            lib().nvfp4_grouped_gemm_noalloc(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                             _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
-                                            _ptr(dev_status), _stream(stream)))
+                                            _ptr(dev_status), _stream()))
     return y
 
 
@@ -358,18 +391,22 @@ def nvfp4_scale_bytes_b32(rows: int, K: int) -> int:
 def nvfp4_prune_pairs(w: torch.Tensor, c_out=None, meta_out=None, stream=None):
     """Pair-wise 2:4 pruning + compression of a bf16 weight [N, K]: returns (c bf16 [N, K/2],
     tiled metadata uint8 [nvfp4_sparse_meta_bytes(N, K)])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_prune_pairs, locals())
     _cuda(w, torch.bfloat16, "w")
     N, K = w.shape
     c_out = torch.empty((N, K // 2), dtype=torch.bfloat16, device=w.device) if c_out is None else c_out
     meta_out = (torch.empty(nvfp4_sparse_meta_bytes(N, K), dtype=torch.uint8, device=w.device)
                 if meta_out is None else meta_out)
     _check("nvfp4_prune_pairs", lib().nvfp4_prune_pairs(_ptr(w), N, K, _ptr(c_out), _ptr(meta_out),
-                                                        _stream(stream)))
+                                                        _stream()))
     return c_out, meta_out
 
 
 def nvfp4_quantize_b32(x: torch.Tensor, global_scale: torch.Tensor, q_out=None, sf_out=None, stream=None):
     """bf16 [M, K] -> NVFP4 with 32-element blocks: (q u8 [M, K/2], sf u8 [nvfp4_scale_bytes_b32(M, K)])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_quantize_b32, locals())
     _cuda(x, torch.bfloat16, "x")
     _cuda(global_scale, torch.float32, "global_scale")
     M, K = x.shape
@@ -377,7 +414,7 @@ def nvfp4_quantize_b32(x: torch.Tensor, global_scale: torch.Tensor, q_out=None, 
     sf_out = (torch.empty(nvfp4_scale_bytes_b32(M, K), dtype=torch.uint8, device=x.device)
               if sf_out is None else sf_out)
     _check("nvfp4_quantize_b32", lib().nvfp4_quantize_b32(_ptr(x), M, K, _ptr(global_scale), _ptr(q_out),
-                                                          _ptr(sf_out), _stream(stream)))
+                                                          _ptr(sf_out), _stream()))
     return q_out, sf_out
 
 
@@ -386,6 +423,8 @@ def nvfp4_grouped_gemm_swiglu_quantize_out(a, sfa, ga, b_gu, sfb_gu, gb, expert_
                                            dev_status=None, stream=None):
     """Gate/up projection with SwiGLU emitting NVFP4 with the global scale g_out: returns
     (codes u8 [M_total, N_gu // 4], tiled scales u8 [nvfp4_scale_bytes(M_total, N_gu // 2)])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grouped_gemm_swiglu_quantize_out, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b_gu, "b_gu"), (sfb_gu, "sfb_gu")):
         _cuda(t, torch.uint8, n)
     for t, n in ((ga, "ga"), (gb, "gb"), (g_out, "g_out")):
@@ -401,13 +440,15 @@ def nvfp4_grouped_gemm_swiglu_quantize_out(a, sfa, ga, b_gu, sfb_gu, gb, expert_
            lib().nvfp4_grouped_gemm_swiglu_quantize_out(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_gu), _ptr(sfb_gu),
                                                         _ptr(gb), _ptr(expert_offsets), E, M_total, N_gu, K,
                                                         _ptr(g_out), _ptr(q_out), _ptr(sf_out), _ptr(workspace),
-                                                        workspace.numel(), _ptr(dev_status), _stream(stream)))
+                                                        workspace.numel(), _ptr(dev_status), _stream()))
     return q_out, sf_out
 
 
 def nvfp4_gemm_batched(problems, M: int, dev_status=None, stream=None):
     """Several decode-M GEMMs in one launch. problems: sequence of (a, sfa, ga, b, sfb, gb, y)
     tuples of CUDA tensors (y bf16 [M, N], preallocated); N and K come from b and a."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_gemm_batched, locals())
     arr = (GemmProblem * max(1, len(problems)))()
     for i, (a, sfa, ga, b, sfb, gb, y) in enumerate(problems):
         for t, n in ((a, "a"), (sfa, "sfa"), (b, "b"), (sfb, "sfb")):
@@ -418,13 +459,15 @@ def nvfp4_gemm_batched(problems, M: int, dev_status=None, stream=None):
         arr[i] = GemmProblem(a.data_ptr(), sfa.data_ptr(), ga.data_ptr(), b.data_ptr(), sfb.data_ptr(),
                              gb.data_ptr(), y.data_ptr(), b.shape[0], 2 * b.shape[1])
     _check("nvfp4_gemm_batched", lib().nvfp4_gemm_batched(ctypes.cast(arr, ctypes.c_void_p), len(problems), M,
-                                                          _ptr(dev_status), _stream(stream)))
+                                                          _ptr(dev_status), _stream()))
 
 
 def nvfp4_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, M: int, N: int, K: int, y=None, dev_status=None,
                       stream=None):
     """y = x @ W^T, W pair-wise 2:4 sparse (compressed codes b_c [N, K/4], scales sfb_c, tiled meta),
     x in 32-element blocks; bf16 [M, N]."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_sparse_gemm, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b_c, "b_c"), (sfb_c, "sfb_c"), (meta, "meta")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -432,13 +475,15 @@ def nvfp4_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, M: int, N: int, K: int, 
     y = torch.empty((M, N), dtype=torch.bfloat16, device=a.device) if y is None else y
     _check("nvfp4_sparse_gemm", lib().nvfp4_sparse_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_c), _ptr(sfb_c),
                                                         _ptr(meta), _ptr(gb), _ptr(y), M, N, K, _ptr(dev_status),
-                                                        _stream(stream)))
+                                                        _stream()))
     return y
 
 
 def nvfp4_grouped_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, expert_offsets, E: int, M_total: int, N: int,
                               K: int, y=None, workspace=None, dev_status=None, stream=None):
     """Grouped form of nvfp4_sparse_gemm over pair-wise 2:4 sparse experts; bf16 [M_total, N]."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grouped_sparse_gemm, locals())
     for t, n in ((a, "a"), (sfa, "sfa"), (b_c, "b_c"), (sfb_c, "sfb_c"), (meta, "meta")):
         _cuda(t, torch.uint8, n)
     _cuda(ga, torch.float32, "ga")
@@ -451,7 +496,7 @@ def nvfp4_grouped_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, expert_offsets, 
     _check("nvfp4_grouped_sparse_gemm",
            lib().nvfp4_grouped_sparse_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_c), _ptr(sfb_c), _ptr(meta),
                                            _ptr(gb), _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
-                                           _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)))
+                                           _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream()))
     return y
 
 
@@ -570,6 +615,8 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
                     stream=None) -> MoeRouting:
     """Softmax router: top-k experts and weights of each token, per-expert counts and offsets, the
     expert-sorted row lists that the grouped GEMMs read, and the load-balance loss."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_moe_route, locals())
     T, E = _route_inputs(logits, valid)
     ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
     r = MoeRouting(T, E, k, logits.device, ws_bytes // 4 if workspace is None else 0)
@@ -580,7 +627,7 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
                                  base, base + n, base + 2 * n, counts, counts + 4 * E, base + 3 * n,
                                  counts + 8 * E + 4, counts + 12 * E + 4, counts + 12 * E + 8,
                                  r._workspace if workspace is None else _operand(workspace, _U8, 0, "workspace"),
-                                 ws_bytes if workspace is None else workspace.numel(), _stream(stream)))
+                                 ws_bytes if workspace is None else workspace.numel(), _stream()))
     return r
 
 
@@ -588,6 +635,8 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
                              renormalize: bool = False, valid=None, d_logits=None, stream=None) -> torch.Tensor:
     """Gradient of nvfp4_moe_route's logits (arguments as in that call) from the gradients of the
     weights topk_w (d_w, fp32 [T, k]) and of the balance loss (d_loss, fp32 [1])."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_moe_route_backward, locals())
     T, E = _route_inputs(logits, valid)
     k = routing.k
     if (routing.T, routing.E) != (T, E):
@@ -603,7 +652,7 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
            lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
                                           int(renormalize), base, base + (counts - base) // 4, counts,
                                           counts + 12 * E + 8, _ptr(d_w), _ptr(d_loss),
-                                          _operand(d_logits, (logits.dtype,), T * E, "d_logits"), _stream(stream)))
+                                          _operand(d_logits, (logits.dtype,), T * E, "d_logits"), _stream()))
     return d_logits
 
 
@@ -616,6 +665,8 @@ def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, row_token=None, tra
     (scales [K/128, M]) or, with block_rows=128, per 128 x 128 block (scales [M/128, K/128]; sizes
     rounded up). row_token (int32): quantise the rows x[row_token]. transposed: also return the
     codes [K, M rounded up to 16] and scales of the transpose, blocks along M."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_fp8_quantize, locals())
     _cuda(x, torch.bfloat16, "x")
     if x.dim() != 2:
         raise TypeError("x must be [M, K]")
@@ -634,7 +685,7 @@ def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, row_token=None, tra
         st = torch.empty((_blocks(K), _blocks(M)) if square else (_blocks(M), K), dtype=torch.float32, device=dev)
     _check("nvfp4_fp8_quantize",
            lib().nvfp4_fp8_quantize(_ptr(x), M_x, K, block_rows, _ptr(row_token), M, _ptr(q), _ptr(s), _ptr(qt),
-                                    _ptr(st), _stream(stream)))
+                                    _ptr(st), _stream()))
     return (q, s, qt, st) if transposed else (q, s)
 
 
@@ -642,6 +693,8 @@ def nvfp4_fp8_gemm(a, sa, b, sb, M: int, N: int, K: int, b_block_rows: int = 128
                    dev_status=None, stream=None):
     """y = a b^T [M, N] in bf16 or fp32 from E4M3 codes a [M, K], b [N, K] and their block scales
     (see nvfp4_fp8_quantize; b_block_rows: rows of b that share a scale, 128 or 1)."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_fp8_gemm, locals())
     y_type = _FLOAT_TYPES.get(out_dtype)
     if y_type is None:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
@@ -652,7 +705,7 @@ def nvfp4_fp8_gemm(a, sa, b, sb, M: int, N: int, K: int, b_block_rows: int = 128
            lib().nvfp4_fp8_gemm(pa, _operand(sa, _F32, kb * M, "sa"), _operand(b, _FP8_TYPES, N * K, "b"),
                                 _operand(sb, _F32, kb * (N if b_block_rows == 1 else _blocks(N)), "sb"), b_block_rows,
                                 _operand(y, (out_dtype,), M * N, "y"), y_type, M, N, K, _ptr(dev_status),
-                                _stream(stream)))
+                                _stream()))
     return y
 
 
@@ -664,6 +717,8 @@ def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N
                            workspace=None, dev_status=None, stream=None):
     """Per-expert y[rows of e] = a[rows of e] b_e^T (bf16 [M_total, N]) from E4M3 codes a [M_total, K],
     b [E, N, K] and their block scales; rows sorted by expert, rows past expert_offsets[E] untouched."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_fp8_grouped_gemm, locals())
     kb = _blocks(K)
     pa = _operand(a, _FP8_TYPES, M_total * K, "a")
     y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else y
@@ -677,19 +732,23 @@ def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N
                                         _operand(expert_offsets, _I32, E + 1, "expert_offsets"), E, M_total, N, K,
                                         _operand(y, (torch.bfloat16,), M_total * N, "y"),
                                         _operand(workspace, _U8, 0, "workspace"), workspace.numel(),
-                                        _ptr(dev_status), _stream(stream)))
+                                        _ptr(dev_status), _stream()))
     return y
 
 
 def nvfp4_encode_e2m1(v: torch.Tensor, stream=None) -> torch.Tensor:
+    if stream is not None:
+        return _on_stream(stream, nvfp4_encode_e2m1, locals())
     _cuda(v, torch.float32, "v")
     out = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
-    _check("nvfp4_encode_e2m1", lib().nvfp4_encode_e2m1(_ptr(v), v.numel(), _ptr(out), _stream(stream)))
+    _check("nvfp4_encode_e2m1", lib().nvfp4_encode_e2m1(_ptr(v), v.numel(), _ptr(out), _stream()))
     return out
 
 
 def nvfp4_encode_e4m3(v: torch.Tensor, stream=None) -> torch.Tensor:
+    if stream is not None:
+        return _on_stream(stream, nvfp4_encode_e4m3, locals())
     _cuda(v, torch.float32, "v")
     out = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
-    _check("nvfp4_encode_e4m3", lib().nvfp4_encode_e4m3(_ptr(v), v.numel(), _ptr(out), _stream(stream)))
+    _check("nvfp4_encode_e4m3", lib().nvfp4_encode_e4m3(_ptr(v), v.numel(), _ptr(out), _stream()))
     return out
