@@ -11,6 +11,7 @@ allocates belongs to that stream, and the caller orders it against other streams
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -148,7 +149,16 @@ def lib():
 
 
 def _ptr(t):  # an int: every entry point's argtypes convert it to the pointer
-    return None if t is None else t.data_ptr()
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise TypeError("operands must be CUDA tensors")
+    return t.data_ptr()
+
+
+def _status(t):
+    """dev_status's address: None, or where the kernels write a status."""
+    return None if t is None else _operand(t, _I32, (1,), "dev_status")
 
 
 def _stream():
@@ -252,7 +262,7 @@ def nvfp4_gemm(a, sfa, ga, b, sfb, gb, M: int, N: int, K: int, y=None, dev_statu
     ws_bytes = int(lib().nvfp4_gemm_workspace_bytes(M, N, K))
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=a.device) if ws_bytes else None
     _check("nvfp4_gemm", lib().nvfp4_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
-                                          _ptr(y), M, N, K, _ptr(ws), ws_bytes, _ptr(dev_status),
+                                          _ptr(y), M, N, K, _ptr(ws), ws_bytes, _status(dev_status),
                                           _stream()))
     return y
 
@@ -277,7 +287,7 @@ def nvfp4_gemm_quantize_out(a, sfa, ga, b, sfb, gb, g_out, M: int, N: int, K: in
         sf_out = torch.empty(nvfp4_scale_bytes(M, N), dtype=torch.uint8, device=a.device)
     _check("nvfp4_gemm_quantize_out",
            lib().nvfp4_gemm_quantize_out(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb), _ptr(g_out),
-                                         _ptr(q_out), _ptr(sf_out), M, N, K, _ptr(dev_status), _stream()))
+                                         _ptr(q_out), _ptr(sf_out), M, N, K, _status(dev_status), _stream()))
     return q_out, sf_out
 
 
@@ -298,7 +308,7 @@ def nvfp4_grouped_gemm(a, sfa, ga, b, sfb, gb, expert_offsets, E: int, M_total: 
     _check("nvfp4_grouped_gemm",
            lib().nvfp4_grouped_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                     _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
-                                    _ptr(workspace), workspace.numel(), _ptr(dev_status),
+                                    _ptr(workspace), workspace.numel(), _status(dev_status),
                                     _stream()))
     return y
 
@@ -324,7 +334,7 @@ def nvfp4_grouped_gemm_gather(a_tok, sfa_tok, ga, b, sfb, gb, expert_offsets, ro
     _check("nvfp4_grouped_gemm_gather",
            lib().nvfp4_grouped_gemm_gather(_ptr(a_tok), _ptr(sfa_tok), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                            _ptr(expert_offsets), _ptr(row_token), E, T, M_total, N, K, _ptr(y),
-                                           _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream()))
+                                           _ptr(workspace), workspace.numel(), _status(dev_status), _stream()))
     return y
 
 
@@ -350,7 +360,7 @@ def nvfp4_grouped_gemm_swiglu(a, sfa, ga, b_gu, sfb_gu, gb, expert_offsets, E: i
     _check("nvfp4_grouped_gemm_swiglu",
            lib().nvfp4_grouped_gemm_swiglu(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_gu), _ptr(sfb_gu), _ptr(gb),
                                            _ptr(expert_offsets), E, M_total, N_gu, K, _ptr(y),
-                                           _ptr(workspace), workspace.numel(), _ptr(dev_status),
+                                           _ptr(workspace), workspace.numel(), _status(dev_status),
                                            _stream()))
     return y
 
@@ -376,7 +386,7 @@ def nvfp4_grouped_gemm_noalloc(a, sfa, ga, b, sfb, gb, expert_offsets, E: int, M
     _check("nvfp4_grouped_gemm_noalloc",
            lib().nvfp4_grouped_gemm_noalloc(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b), _ptr(sfb), _ptr(gb),
                                             _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
-                                            _ptr(dev_status), _stream()))
+                                            _status(dev_status), _stream()))
     return y
 
 
@@ -440,7 +450,7 @@ def nvfp4_grouped_gemm_swiglu_quantize_out(a, sfa, ga, b_gu, sfb_gu, gb, expert_
            lib().nvfp4_grouped_gemm_swiglu_quantize_out(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_gu), _ptr(sfb_gu),
                                                         _ptr(gb), _ptr(expert_offsets), E, M_total, N_gu, K,
                                                         _ptr(g_out), _ptr(q_out), _ptr(sf_out), _ptr(workspace),
-                                                        workspace.numel(), _ptr(dev_status), _stream()))
+                                                        workspace.numel(), _status(dev_status), _stream()))
     return q_out, sf_out
 
 
@@ -459,7 +469,7 @@ def nvfp4_gemm_batched(problems, M: int, dev_status=None, stream=None):
         arr[i] = GemmProblem(a.data_ptr(), sfa.data_ptr(), ga.data_ptr(), b.data_ptr(), sfb.data_ptr(),
                              gb.data_ptr(), y.data_ptr(), b.shape[0], 2 * b.shape[1])
     _check("nvfp4_gemm_batched", lib().nvfp4_gemm_batched(ctypes.cast(arr, ctypes.c_void_p), len(problems), M,
-                                                          _ptr(dev_status), _stream()))
+                                                          _status(dev_status), _stream()))
 
 
 def nvfp4_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, M: int, N: int, K: int, y=None, dev_status=None,
@@ -474,7 +484,7 @@ def nvfp4_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, M: int, N: int, K: int, 
     _cuda(gb, torch.float32, "gb")
     y = torch.empty((M, N), dtype=torch.bfloat16, device=a.device) if y is None else y
     _check("nvfp4_sparse_gemm", lib().nvfp4_sparse_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_c), _ptr(sfb_c),
-                                                        _ptr(meta), _ptr(gb), _ptr(y), M, N, K, _ptr(dev_status),
+                                                        _ptr(meta), _ptr(gb), _ptr(y), M, N, K, _status(dev_status),
                                                         _stream()))
     return y
 
@@ -496,7 +506,7 @@ def nvfp4_grouped_sparse_gemm(a, sfa, ga, b_c, sfb_c, meta, gb, expert_offsets, 
     _check("nvfp4_grouped_sparse_gemm",
            lib().nvfp4_grouped_sparse_gemm(_ptr(a), _ptr(sfa), _ptr(ga), _ptr(b_c), _ptr(sfb_c), _ptr(meta),
                                            _ptr(gb), _ptr(expert_offsets), E, M_total, N, K, _ptr(y),
-                                           _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream()))
+                                           _ptr(workspace), workspace.numel(), _status(dev_status), _stream()))
     return y
 
 
@@ -511,14 +521,19 @@ _FP8_TYPES = (torch.float8_e4m3fn, torch.uint8)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
+_BF16 = (torch.bfloat16,)
 
 
-def _operand(t, types, n, name):
-    """t's address; t must be a contiguous CUDA tensor of one of `types` with at least n elements."""
+def _operand(t, types, shape, name):
+    """t's address; t must be a contiguous CUDA tensor of one of `types` whose memory starts with a tensor of
+    `shape`: of that shape, a flat buffer, or with the same dimensions but for the first (more rows, or
+    leading dimensions merged or split), and at least as many elements."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in types and t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, types))}")
-    if t.numel() < n:
-        raise TypeError(f"{name} holds {t.numel()} elements, needs {n}")
+    if t.shape != shape:
+        inner = min(t.dim(), len(shape)) - 1
+        if (inner > 0 and t.shape[-inner:] != shape[-inner:]) or t.numel() < math.prod(shape):
+            raise TypeError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
     return t.data_ptr()
 
 
@@ -626,7 +641,7 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
            lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
                                  base, base + n, base + 2 * n, counts, counts + 4 * E, base + 3 * n,
                                  counts + 8 * E + 4, counts + 12 * E + 4, counts + 12 * E + 8,
-                                 r._workspace if workspace is None else _operand(workspace, _U8, 0, "workspace"),
+                                 r._workspace if workspace is None else _operand(workspace, _U8, (0,), "workspace"),
                                  ws_bytes if workspace is None else workspace.numel(), _stream()))
     return r
 
@@ -652,7 +667,7 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
            lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
                                           int(renormalize), base, base + (counts - base) // 4, counts,
                                           counts + 12 * E + 8, _ptr(d_w), _ptr(d_loss),
-                                          _operand(d_logits, (logits.dtype,), T * E, "d_logits"), _stream()))
+                                          _operand(d_logits, (logits.dtype,), (T, E), "d_logits"), _stream()))
     return d_logits
 
 
@@ -699,13 +714,17 @@ def nvfp4_fp8_gemm(a, sa, b, sb, M: int, N: int, K: int, b_block_rows: int = 128
     if y_type is None:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     kb = _blocks(K)
-    pa = _operand(a, _FP8_TYPES, M * K, "a")
-    y = torch.empty((M, N), dtype=out_dtype, device=a.device) if y is None else y
-    _check("nvfp4_fp8_gemm",
-           lib().nvfp4_fp8_gemm(pa, _operand(sa, _F32, kb * M, "sa"), _operand(b, _FP8_TYPES, N * K, "b"),
-                                _operand(sb, _F32, kb * (N if b_block_rows == 1 else _blocks(N)), "sb"), b_block_rows,
-                                _operand(y, (out_dtype,), M * N, "y"), y_type, M, N, K, _ptr(dev_status),
-                                _stream()))
+    try:
+        pa = _operand(a, _FP8_TYPES, (M, K), "a")
+        y = torch.empty((M, N), dtype=out_dtype, device=a.device) if y is None else y
+        args = (pa, _operand(sa, _F32, (kb, M), "sa"), _operand(b, _FP8_TYPES, (N, K), "b"),
+                _operand(sb, _F32, (kb, N) if b_block_rows == 1 else (_blocks(N), kb), "sb"), b_block_rows,
+                _operand(y, (out_dtype,), (M, N), "y"))
+    except TypeError:  # sizes that the library refuses are its error
+        _check("nvfp4_fp8_gemm", lib().nvfp4_fp8_gemm(None, None, None, None, b_block_rows, None, y_type, min(M, 0), N, K,
+                                                      None, None))
+        raise
+    _check("nvfp4_fp8_gemm", lib().nvfp4_fp8_gemm(*args, y_type, M, N, K, _status(dev_status), _stream()))
     return y
 
 
@@ -720,19 +739,22 @@ def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N
     if stream is not None:
         return _on_stream(stream, nvfp4_fp8_grouped_gemm, locals())
     kb = _blocks(K)
-    pa = _operand(a, _FP8_TYPES, M_total * K, "a")
-    y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else y
+    try:
+        pa = _operand(a, _FP8_TYPES, (M_total, K), "a")
+        y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else y
+        args = (pa, _operand(sa, _F32, (kb, M_total), "sa"), _operand(b, _FP8_TYPES, (E, N, K), "b"),
+                _operand(sb, _F32, (E, _blocks(N), kb), "sb"), _operand(expert_offsets, _I32, (E + 1,), "expert_offsets"),
+                E, M_total, N, K, _operand(y, _BF16, (M_total, N), "y"))
+    except TypeError:  # sizes that the library refuses are its error
+        _check("nvfp4_fp8_grouped_gemm",
+               lib().nvfp4_fp8_grouped_gemm(None, None, None, None, None, E, min(M_total, 0), N, K, None, None, 0, None, None))
+        raise
     if workspace is None:
         workspace = torch.empty(max(1, nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K)), dtype=torch.uint8,
                                 device=a.device)
     _check("nvfp4_fp8_grouped_gemm",
-           lib().nvfp4_fp8_grouped_gemm(pa, _operand(sa, _F32, kb * M_total, "sa"),
-                                        _operand(b, _FP8_TYPES, E * N * K, "b"),
-                                        _operand(sb, _F32, E * _blocks(N) * kb, "sb"),
-                                        _operand(expert_offsets, _I32, E + 1, "expert_offsets"), E, M_total, N, K,
-                                        _operand(y, (torch.bfloat16,), M_total * N, "y"),
-                                        _operand(workspace, _U8, 0, "workspace"), workspace.numel(),
-                                        _ptr(dev_status), _stream()))
+           lib().nvfp4_fp8_grouped_gemm(*args, _operand(workspace, _U8, (0,), "workspace"), workspace.numel(),
+                                        _status(dev_status), _stream()))
     return y
 
 
