@@ -366,7 +366,7 @@ enum { NVFP4_BF16 = 0, NVFP4_F32 = 1 };
 /*
  * MoE router: the step in front of the grouped GEMMs ("The Moment of Recalibration",
  * magik.net, Input Knowledge: 256 experts, top-8 routing). For token t with logits l_te, routed
- * when valid[t] != 0 and some l_te is above -inf:
+ * when valid[t] != 0 and some l_te is above -inf or NaN:
  *   p_te = exp(l_te) / sum_e exp(l_te); the k largest l_te are selected, ties to the lower
  *   expert; an expert whose logit is -inf is never selected (its slot: index -1, weight 0);
  *   weights p at the selected experts, with `renormalize` divided by their sum.
@@ -374,7 +374,9 @@ enum { NVFP4_BF16 = 0, NVFP4_F32 = 1 };
  * P_e = (1/n) sum_t p_te:  L = E sum_e (c_e / (n k)) P_e  (0 when n = 0; 1 when balanced).
  *   logits          device [T, E], bf16 or fp32 (logits_type NVFP4_BF16 / NVFP4_F32). Logits of a
  *                   token with valid[t] == 0 have no effect; NaN or +inf in a routed token's row
- *                   makes that row's weights, mean_prob and the loss NaN, and nothing else
+ *                   makes that row's k weights (those of empty slots too), mean_prob, the loss and in
+ *                   the backward call that row's gradient NaN, and no other row's weights or
+ *                   gradient; +inf is selected as the largest, a NaN is never selected
  *   valid           device u8 [T] (0: padding token) or NULL (all valid)
  *   topk_idx        int32 [T, k] written, largest logit first; -1 in empty slots
  *   topk_w          fp32 [T, k] written

@@ -7,6 +7,9 @@
 //   w_ts = p at the selected experts, optionally divided by their sum.
 // With n routed tokens, c_e selections of expert e and P_e = (1/n) sum_t p_te:
 //   balance loss L = E sum_e (c_e / (n k)) P_e.
+// A NaN is never selected and no maximum, but a valid token with one is routed like any other (also when it has
+// nothing else above -inf): its p, its weights, the means, the loss and the gradient of its row are NaN, so
+// that a router that has diverged shows.
 // A routed row's place is offsets[e] + the number of earlier (token, slot) pairs that chose e,
 // in (token, slot) order, so the order does not depend on how the work was split. Counts are
 // integers and every floating sum runs in a fixed order: results repeat bit for bit.
@@ -28,7 +31,7 @@ DEVI float ex2(float x) {
   return y;
 }
 
-// Order-preserving map of fp32 onto uint32; 0 is below every float's key.
+// Order-preserving map of fp32 (no NaN) onto uint32; 0 is below every float's key.
 DEVI uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);  // -0 and +0 tie
   return u ^ ((u & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
@@ -46,6 +49,16 @@ DEVI float rcp(float x) {
 
 // log2 of exp(v - max)
 DEVI float route_arg(float v, float mx) { return (v - mx) * kLog2E; }
+
+// Whether a valid token is routed: some logit above -inf (mx, the largest but for NaN, is), or NaN.
+template <int VPL>
+DEVI bool row_routed(const float (&v)[VPL], float mx) {
+  if (mx > __uint_as_float(0xFF800000u)) return true;
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) nan = nan || v[j] != v[j];
+  return __any_sync(0xffffffffu, nan);
+}
 
 DEVI float warp_sum(float v) {
 #pragma unroll
@@ -110,7 +123,8 @@ struct RouteCfg {
 
 // The k largest of a warp's 32 * VPL logits (lane holds experts lane * VPL + j), ties to the lower
 // expert: a lane gets a slot and, where that is below k, its expert (-1: none above -inf is left for
-// it) and logit; every slot below k is some lane's. `lane_max` is the largest of this lane's logits.
+// it) and logit; every slot below k is some lane's. `lane_max` is the largest of this lane's logits that are
+// not NaN (-inf without one).
 //
 // The k-th largest of the 32 lane maxima bounds the k-th largest logit from below, so the selected
 // experts are among the few (typically k and one or two) that reach it. Those candidates are
@@ -172,13 +186,13 @@ DEVI void warp_top_k(const float (&v)[VPL], float lane_max, int k, uint64_t* can
   }
   uint32_t key[VPL];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) key[j] = order_key(v[j]);
+  for (int j = 0; j < VPL; ++j) key[j] = v[j] >= least ? order_key(v[j]) : 0u;
   for (int s = 0; s < k; ++s) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
     const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-    if (best <= kKeyNegInf) break;
+    if (best == 0u) break;
     const int w = __ffs(__ballot_sync(0xffffffffu, m == best)) - 1;
     int pos = -1;
     if (lane == w) {
@@ -213,17 +227,18 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
   int routed = 0;
   for (int64_t t = t0 + warp; t < t1; t += WARPS) {
     float v[VPL];
-    float lane_max = 0.0f, mx = __uint_as_float(0xFF800000u);
+    float lane_max = __uint_as_float(0xFF800000u), mx = lane_max;
+    bool on = false;
     if (!a.valid || __ldg(a.valid + t) != 0) {
       load_row<VPL, BF16>(a.logits, t, E, a.vec, lane, v);
-      lane_max = v[0];
 #pragma unroll
-      for (int j = 1; j < VPL; ++j) lane_max = fmaxf(lane_max, v[j]);
+      for (int j = 0; j < VPL; ++j) lane_max = fmaxf(lane_max, v[j]);
       mx = key_value(__reduce_max_sync(0xffffffffu, order_key(lane_max)));
+      on = row_routed<VPL>(v, mx);
     }
     int my_idx = -1, my_slot = lane;
     float my_w = 0.0f;
-    if (mx > __uint_as_float(0xFF800000u)) {
+    if (on) {
       float my_v;
       warp_top_k<VPL>(v, lane_max, k, cand + warp * kCandSlots, my_idx, my_v, my_slot);
       float sum = 0.0f;
@@ -237,7 +252,8 @@ DEVI void route_rows(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* hist, 
       for (int j = 0; j < VPL; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
       ++routed;
       const float es = my_idx >= 0 ? ex2(route_arg(my_v, mx)) : 0.0f;
-      my_w = es * (a.renorm ? rcp(warp_sum(es)) : inv);
+      // inv is at most 1, or NaN: then the renormalised weights are, whichever expert's logit it came from
+      my_w = es * (a.renorm ? rcp(fmaf(inv, 0.0f, warp_sum(es))) : inv);
       if (my_idx >= 0) atomicAdd(&hist[my_idx], 1);
     }
     if (my_slot < k) {
@@ -531,6 +547,7 @@ __global__ void __launch_bounds__(kBwdThreads, VPL <= 8 ? 4 : 1) k_moe_route_bwd
     float mx = __uint_as_float(0xFF800000u), slot_dw = 0.0f, slot_w = 0.0f;
     int slot_idx = -1;
     const bool valid = !a.valid || __ldg(a.valid + t) != 0;
+    bool on = false;
     if (ringed) {
       if constexpr (kBwdRing<VPL, BF16>) {
         request(t + (kBwdAhead - 1) * stride, (slot + kBwdAhead - 1) & (kBwdAhead - 1));
@@ -568,8 +585,9 @@ __global__ void __launch_bounds__(kBwdThreads, VPL <= 8 ? 4 : 1) k_moe_route_bwd
 #pragma unroll
       for (int j = 0; j < VPL; ++j) mx = fmaxf(mx, v[j]);
       mx = key_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
+      on = row_routed<VPL>(v, mx);
     }
-    if (mx > __uint_as_float(0xFF800000u)) {
+    if (on) {
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
