@@ -71,11 +71,11 @@ def forward_nvfp4_gate_up(x, logits, w_gu, k):
 
 
 def router_step(logits, r, out, dy, coef, valid=None):
-    """d logits of sum(dy * y) + coef * balance loss, y the weighted sum of the expert outputs."""
+    """d logits of sum(dy * y) + coef * balance loss, y the weighted sum of the expert outputs. (The routing knows
+    what it was made with; `valid`, where given, has to be that of the forward call.)"""
     picked = torch.where((r.slot_row >= 0)[..., None], out[r.slot_row.clamp(min=0).long()].float(), 0.0)
     d_w = torch.einsum("th,tkh->tk", dy.float(), picked).contiguous()
-    return m.nvfp4_moe_route_backward(logits, r, d_w=d_w, d_loss=torch.full((1,), coef, device="cuda"), renormalize=True,
-                                      valid=valid)
+    return m.nvfp4_moe_route_backward(logits, r, d_w=d_w, d_loss=torch.full((1,), coef, device="cuda"), valid=valid)
 
 
 def linear_step(x, w, dy):

@@ -551,6 +551,8 @@ class MoeRouting:
     mean_prob       fp32 [E]: mean probability over the routed tokens
     balance_loss    fp32 [1]
     routed_tokens   int32 [1]
+
+    It also keeps what the call was given and its gradient depends on: renormalize and valid.
     """
     _fields = ("topk_idx", "topk_w", "slot_row", "counts", "expert_offsets", "row_token", "mean_prob", "balance_loss",
                "routed_tokens")
@@ -561,9 +563,9 @@ class MoeRouting:
                "expert_offsets": (4, 1, 0, (0, 1, 1), False), "mean_prob": (4, 2, 1, (0, 1, 0), True),
                "balance_loss": (4, 3, 1, (0, 0, 1), True), "routed_tokens": (4, 3, 2, (0, 0, 1), False)}
 
-    def __init__(self, T, E, k, device, workspace_words):
+    def __init__(self, T, E, k, renormalize, valid, device, workspace_words):
         n = T * k if k > 0 else 0
-        self.T, self.E, self.k = T, E, k
+        self.T, self.E, self.k, self.renormalize, self.valid = T, E, k, renormalize, valid
         self._all = self._float = None
         words = (4 * n + 3 * E + 6) // 4 * 4
         self._buf = torch.empty(words + workspace_words, dtype=torch.int32, device=device)
@@ -634,7 +636,8 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
         return _on_stream(stream, nvfp4_moe_route, locals())
     T, E = _route_inputs(logits, valid)
     ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
-    r = MoeRouting(T, E, k, logits.device, ws_bytes // 4 if workspace is None else 0)
+    renormalize = bool(renormalize)
+    r = MoeRouting(T, E, k, renormalize, valid, logits.device, ws_bytes // 4 if workspace is None else 0)
     base, counts = r._base, r._counts  # four arrays of T k words, then counts and what follows
     n = (counts - base) // 4
     _check("nvfp4_moe_route",
@@ -647,15 +650,22 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
 
 
 def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None, d_loss=None,
-                             renormalize: bool = False, valid=None, d_logits=None, stream=None) -> torch.Tensor:
-    """Gradient of nvfp4_moe_route's logits (arguments as in that call) from the gradients of the
-    weights topk_w (d_w, fp32 [T, k]) and of the balance loss (d_loss, fp32 [1])."""
+                             renormalize=None, valid=None, d_logits=None, stream=None) -> torch.Tensor:
+    """Gradient of nvfp4_moe_route's logits from the gradients of the weights topk_w (d_w, fp32 [T, k])
+    and of the balance loss (d_loss, fp32 [1]). renormalize and valid are those of the routing; given
+    here, they have to agree with it."""
     if stream is not None:
         return _on_stream(stream, nvfp4_moe_route_backward, locals())
     T, E = _route_inputs(logits, valid)
     k = routing.k
     if (routing.T, routing.E) != (T, E):
         raise TypeError(f"routing is of {routing.T} tokens and {routing.E} experts, logits of {T} and {E}")
+    if renormalize is not None and bool(renormalize) != routing.renormalize:
+        raise TypeError(f"the routing was made with renormalize={routing.renormalize}")
+    if valid is None:
+        valid = routing.valid
+    elif routing.valid is None:
+        raise TypeError("the routing was made without valid")
     for t, shape, n in ((d_w, (T, k), "d_w"), (d_loss, (1,), "d_loss")):
         if t is not None:
             _cuda(t, torch.float32, n)
@@ -665,7 +675,7 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
     base, counts = routing._base, routing._counts
     _check("nvfp4_moe_route_backward",
            lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
-                                          int(renormalize), base, base + (counts - base) // 4, counts,
+                                          int(routing.renormalize), base, base + (counts - base) // 4, counts,
                                           counts + 12 * E + 8, _ptr(d_w), _ptr(d_loss),
                                           _operand(d_logits, (logits.dtype,), (T, E), "d_logits"), _stream()))
     return d_logits
