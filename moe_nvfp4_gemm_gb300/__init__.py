@@ -11,6 +11,7 @@ allocates belongs to that stream, and the caller orders it against other streams
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -537,6 +538,28 @@ def _operand(t, types, shape, name):
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=128)
+def _routing_layout(T, E, k):
+    """The one description of a MoeRouting's buffer: the fields as {name: (first word, shape, strides, fp32)} in
+    the order in which they lie there, which is MoeRouting._fields and the order of nvfp4_moe_route's arguments;
+    the byte offsets of all of them and of the workspace behind them (16-byte aligned); the words up to it."""
+    n = max(T * k, 0)  # (a negative k is the library's to refuse)
+    per = ((T, k), (k, 1), n)
+
+    def row(size):
+        return (size,), (1,), size
+
+    fields, at = {}, 0
+    for name, (size, strides, words), fp32 in (
+            ("topk_idx", per, False), ("topk_w", per, True), ("slot_row", per, False), ("counts", row(E), False),
+            ("expert_offsets", row(E + 1), False), ("row_token", row(n), False), ("mean_prob", row(E), True),
+            ("balance_loss", row(1), True), ("routed_tokens", row(1), False)):
+        fields[name] = (at, size, strides, fp32)
+        at += words
+    words = (at + 3) // 4 * 4
+    return fields, tuple(4 * f[0] for f in fields.values()) + (4 * words,), words
+
+
 class MoeRouting:
     """What nvfp4_moe_route returns (T tokens, k slots each, E experts): tensors that share one
     allocation, as attributes made when they are first asked for (a call's host time is mostly
@@ -557,75 +580,65 @@ class MoeRouting:
     _fields = ("topk_idx", "topk_w", "slot_row", "counts", "expert_offsets", "row_token", "mean_prob", "balance_loss",
                "routed_tokens")
 
-    # field: words from the start in units of (T k, E, 1), elements in the same units, fp32
-    _layout = {"topk_idx": (0, 0, 0, None, False), "topk_w": (1, 0, 0, None, True), "slot_row": (2, 0, 0, None, False),
-               "row_token": (3, 0, 0, (1, 0, 0), False), "counts": (4, 0, 0, (0, 1, 0), False),
-               "expert_offsets": (4, 1, 0, (0, 1, 1), False), "mean_prob": (4, 2, 1, (0, 1, 0), True),
-               "balance_loss": (4, 3, 1, (0, 0, 1), True), "routed_tokens": (4, 3, 2, (0, 0, 1), False)}
-
     def __init__(self, T, E, k, renormalize, valid, device, workspace_words):
-        n = T * k if k > 0 else 0
         self.T, self.E, self.k, self.renormalize, self.valid = T, E, k, renormalize, valid
         self._all = self._float = None
-        words = (4 * n + 3 * E + 6) // 4 * 4
-        self._buf = torch.empty(words + workspace_words, dtype=torch.int32, device=device)
-        self._base = self._buf.data_ptr()  # topk_idx; counts at _counts, in bytes
-        self._counts = self._base + 16 * n
-        self._workspace = self._base + 4 * words
+        self._layout = layout = _routing_layout(T, E, k)
+        self._buf = torch.empty(layout[2] + workspace_words, dtype=torch.int32, device=device)
 
-    def _make(self, name):
-        a, b, c, size, fp32 = MoeRouting._layout[name]
-        T, E, k, buf = self.T, self.E, self.k, self._buf
-        if fp32:
-            buf = self._float
-            if buf is None:
-                buf = self._float = self._buf.view(torch.float32)
-        at = a * T * k + b * E + c
-        if size is None:
-            return buf.as_strided((T, k), (k, 1), at)
-        return buf.as_strided((size[0] * T * k + size[1] * E + size[2],), (1,), at)
+    def __getstate__(self):  # for copies: the views are made anew
+        return {f: self.__dict__[f] for f in ("T", "E", "k", "renormalize", "valid", "_layout", "_buf")} | {
+            "_all": None, "_float": None}
+
+    def _addresses(self):
+        """Of the fields, in their order, and of the workspace behind them."""
+        base = self._buf.data_ptr()
+        return [base + at for at in self._layout[1]]
+
+    def _floats(self):
+        if self._float is None:
+            self._float = self._buf.view(torch.float32)
+        return self._float
 
     def __getattr__(self, name):  # only for what is not there yet
         if name not in MoeRouting._fields:
             raise AttributeError(name)
-        t = self.__dict__[name] = self._make(name)
+        at, size, strides, fp32 = self._layout[0][name]
+        t = self.__dict__[name] = (self._floats() if fp32 else self._buf).as_strided(size, strides, at)
         return t
 
     def _asdict(self):
-        if self._all is None:
-            T, E, k, b = self.T, self.E, self.k, self._buf.as_strided
-            if self._float is None:
-                self._float = self._buf.view(torch.float32)
-            f = self._float.as_strided
-            per, row, one, n = (T, k), (k, 1), (1,), T * k
-            made = {"topk_idx": b(per, row, 0), "topk_w": f(per, row, n), "slot_row": b(per, row, 2 * n),
-                    "counts": b((E,), one, 4 * n), "expert_offsets": b((E + 1,), one, 4 * n + E),
-                    "row_token": b((n,), one, 3 * n), "mean_prob": f((E,), one, 4 * n + 2 * E + 1),
-                    "balance_loss": f(one, one, 4 * n + 3 * E + 1), "routed_tokens": b(one, one, 4 * n + 3 * E + 2)}
-            have = self.__dict__
-            for field in made:  # those handed out before stay
-                if field in have:
-                    made[field] = have[field]
-            have.update(made)
-            self._all = made
-        return dict(self._all)
+        made = self._all
+        if made is None:
+            views, floats, have = self._buf.as_strided, self._floats().as_strided, self.__dict__
+            made = self._all = {}
+            for name, (at, size, strides, fp32) in self._layout[0].items():
+                t = have.get(name)  # those handed out before stay
+                if t is None:
+                    t = have[name] = floats(size, strides, at) if fp32 else views(size, strides, at)
+                made[name] = t
+        return dict(made)
 
     def __iter__(self):
         return iter(self._asdict().values())
 
 
 def _route_inputs(logits, valid):
+    """T and E of the logits, and the address of valid."""
     if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype in _FLOAT_TYPES
             and logits.is_contiguous() and logits.dim() == 2):
         raise TypeError("logits must be a contiguous CUDA tensor [T, E] of torch.bfloat16 or torch.float32")
     if valid is not None and not (isinstance(valid, torch.Tensor) and valid.is_cuda and valid.is_contiguous()
                                   and valid.dtype in (torch.bool, torch.uint8) and valid.numel() == logits.shape[0]):
         raise TypeError("valid must be a contiguous CUDA tensor [T] of torch.bool or torch.uint8")
-    return logits.shape
+    return *logits.shape, None if valid is None else valid.data_ptr()
 
 
 def nvfp4_moe_route_workspace_bytes(T: int, E: int) -> int:
     return int(lib().nvfp4_moe_route_workspace_bytes(T, E))
+
+
+_route_workspace_bytes = functools.lru_cache(maxsize=128)(nvfp4_moe_route_workspace_bytes)
 
 
 def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, valid=None, workspace=None,
@@ -634,18 +647,16 @@ def nvfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = False, val
     expert-sorted row lists that the grouped GEMMs read, and the load-balance loss."""
     if stream is not None:
         return _on_stream(stream, nvfp4_moe_route, locals())
-    T, E = _route_inputs(logits, valid)
-    ws_bytes = nvfp4_moe_route_workspace_bytes(T, E)
+    T, E, on = _route_inputs(logits, valid)
+    ws_bytes = _route_workspace_bytes(T, E)
     renormalize = bool(renormalize)
     r = MoeRouting(T, E, k, renormalize, valid, logits.device, ws_bytes // 4 if workspace is None else 0)
-    base, counts = r._base, r._counts  # four arrays of T k words, then counts and what follows
-    n = (counts - base) // 4
+    *fields, ws = r._addresses()
+    if workspace is not None:
+        ws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
     _check("nvfp4_moe_route",
-           lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k, int(renormalize),
-                                 base, base + n, base + 2 * n, counts, counts + 4 * E, base + 3 * n,
-                                 counts + 8 * E + 4, counts + 12 * E + 4, counts + 12 * E + 8,
-                                 r._workspace if workspace is None else _operand(workspace, _U8, (0,), "workspace"),
-                                 ws_bytes if workspace is None else workspace.numel(), _stream()))
+           lib().nvfp4_moe_route(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], on, T, E, k, renormalize, *fields,
+                                 ws, ws_bytes, _stream()))
     return r
 
 
@@ -656,28 +667,27 @@ def nvfp4_moe_route_backward(logits: torch.Tensor, routing: MoeRouting, d_w=None
     here, they have to agree with it."""
     if stream is not None:
         return _on_stream(stream, nvfp4_moe_route_backward, locals())
-    T, E = _route_inputs(logits, valid)
+    if valid is None:
+        valid = routing.valid
+    elif routing.valid is None:
+        raise TypeError("the routing was made without valid")
+    T, E, on = _route_inputs(logits, valid)
     k = routing.k
     if (routing.T, routing.E) != (T, E):
         raise TypeError(f"routing is of {routing.T} tokens and {routing.E} experts, logits of {T} and {E}")
     if renormalize is not None and bool(renormalize) != routing.renormalize:
         raise TypeError(f"the routing was made with renormalize={routing.renormalize}")
-    if valid is None:
-        valid = routing.valid
-    elif routing.valid is None:
-        raise TypeError("the routing was made without valid")
     for t, shape, n in ((d_w, (T, k), "d_w"), (d_loss, (1,), "d_loss")):
         if t is not None:
             _cuda(t, torch.float32, n)
             if tuple(t.shape) != shape:
                 raise TypeError(f"{n} must have shape {shape}")
     d_logits = torch.empty_like(logits) if d_logits is None else d_logits
-    base, counts = routing._base, routing._counts
+    topk_idx, topk_w, _, counts, _, _, _, _, routed_tokens, _ = routing._addresses()
     _check("nvfp4_moe_route_backward",
-           lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], _ptr(valid), T, E, k,
-                                          int(routing.renormalize), base, base + (counts - base) // 4, counts,
-                                          counts + 12 * E + 8, _ptr(d_w), _ptr(d_loss),
-                                          _operand(d_logits, (logits.dtype,), (T, E), "d_logits"), _stream()))
+           lib().nvfp4_moe_route_backward(logits.data_ptr(), _FLOAT_TYPES[logits.dtype], on, T, E, k,
+                                          routing.renormalize, topk_idx, topk_w, counts, routed_tokens, _ptr(d_w),
+                                          _ptr(d_loss), _operand(d_logits, (logits.dtype,), (T, E), "d_logits"), _stream()))
     return d_logits
 
 
@@ -696,21 +706,21 @@ def nvfp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, row_token=None, tra
     if x.dim() != 2:
         raise TypeError("x must be [M, K]")
     M_x, K = x.shape
-    M = M_x
+    M, rows, transpose = M_x, None, (None, None)
     if row_token is not None:
         _cuda(row_token, torch.int32, "row_token")
-        M = row_token.numel()
+        M, rows = row_token.numel(), row_token.data_ptr()
     dev = x.device
     square = block_rows == 128
     q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     s = torch.empty((_blocks(M), _blocks(K)) if square else (_blocks(K), M), dtype=torch.float32, device=dev)
-    qt = st = None
     if transposed:
         qt = torch.empty((K, (M + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=dev)
         st = torch.empty((_blocks(K), _blocks(M)) if square else (_blocks(M), K), dtype=torch.float32, device=dev)
+        transpose = qt.data_ptr(), st.data_ptr()
     _check("nvfp4_fp8_quantize",
-           lib().nvfp4_fp8_quantize(_ptr(x), M_x, K, block_rows, _ptr(row_token), M, _ptr(q), _ptr(s), _ptr(qt),
-                                    _ptr(st), _stream()))
+           lib().nvfp4_fp8_quantize(x.data_ptr(), M_x, K, block_rows, rows, M, q.data_ptr(), s.data_ptr(), *transpose,
+                                    _stream()))
     return (q, s, qt, st) if transposed else (q, s)
 
 
@@ -726,20 +736,26 @@ def nvfp4_fp8_gemm(a, sa, b, sb, M: int, N: int, K: int, b_block_rows: int = 128
     kb = _blocks(K)
     try:
         pa = _operand(a, _FP8_TYPES, (M, K), "a")
-        y = torch.empty((M, N), dtype=out_dtype, device=a.device) if y is None else y
         args = (pa, _operand(sa, _F32, (kb, M), "sa"), _operand(b, _FP8_TYPES, (N, K), "b"),
-                _operand(sb, _F32, (kb, N) if b_block_rows == 1 else (_blocks(N), kb), "sb"), b_block_rows,
-                _operand(y, (out_dtype,), (M, N), "y"))
+                _operand(sb, _F32, (kb, N) if b_block_rows == 1 else (_blocks(N), kb), "sb"), b_block_rows)
+        if y is None:
+            y = torch.empty((M, N), dtype=out_dtype, device=a.device)
+            py = y.data_ptr()
+        else:
+            py = _operand(y, (out_dtype,), (M, N), "y")
     except TypeError:  # sizes that the library refuses are its error
         _check("nvfp4_fp8_gemm", lib().nvfp4_fp8_gemm(None, None, None, None, b_block_rows, None, y_type, min(M, 0), N, K,
                                                       None, None))
         raise
-    _check("nvfp4_fp8_gemm", lib().nvfp4_fp8_gemm(*args, y_type, M, N, K, _status(dev_status), _stream()))
+    _check("nvfp4_fp8_gemm", lib().nvfp4_fp8_gemm(*args, py, y_type, M, N, K, _status(dev_status), _stream()))
     return y
 
 
 def nvfp4_fp8_grouped_gemm_workspace_bytes(E: int, M_total: int, N: int, K: int) -> int:
     return int(lib().nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K))
+
+
+_fp8_grouped_workspace_bytes = functools.lru_cache(maxsize=128)(nvfp4_fp8_grouped_gemm_workspace_bytes)
 
 
 def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N: int, K: int, y=None,
@@ -751,20 +767,26 @@ def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N
     kb = _blocks(K)
     try:
         pa = _operand(a, _FP8_TYPES, (M_total, K), "a")
-        y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device) if y is None else y
         args = (pa, _operand(sa, _F32, (kb, M_total), "sa"), _operand(b, _FP8_TYPES, (E, N, K), "b"),
                 _operand(sb, _F32, (E, _blocks(N), kb), "sb"), _operand(expert_offsets, _I32, (E + 1,), "expert_offsets"),
-                E, M_total, N, K, _operand(y, _BF16, (M_total, N), "y"))
+                E, M_total, N, K)
+        if y is None:
+            y = torch.empty((M_total, N), dtype=torch.bfloat16, device=a.device)
+            py = y.data_ptr()
+        else:
+            py = _operand(y, _BF16, (M_total, N), "y")
     except TypeError:  # sizes that the library refuses are its error
         _check("nvfp4_fp8_grouped_gemm",
                lib().nvfp4_fp8_grouped_gemm(None, None, None, None, None, E, min(M_total, 0), N, K, None, None, 0, None, None))
         raise
     if workspace is None:
-        workspace = torch.empty(max(1, nvfp4_fp8_grouped_gemm_workspace_bytes(E, M_total, N, K)), dtype=torch.uint8,
-                                device=a.device)
+        ws_bytes = max(1, _fp8_grouped_workspace_bytes(E, M_total, N, K))
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=a.device)
+        pws = workspace.data_ptr()
+    else:
+        pws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
     _check("nvfp4_fp8_grouped_gemm",
-           lib().nvfp4_fp8_grouped_gemm(*args, _operand(workspace, _U8, (0,), "workspace"), workspace.numel(),
-                                        _status(dev_status), _stream()))
+           lib().nvfp4_fp8_grouped_gemm(*args, py, pws, ws_bytes, _status(dev_status), _stream()))
     return y
 
 
