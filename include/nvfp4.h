@@ -422,7 +422,8 @@ int nvfp4_moe_route_backward(const void* logits, int32_t logits_type, const uint
  * every step one IEEE fp32 operation. Two forms of blocks:
  *   block_rows 1     1 x 128 along the row (activations, gradients); scales [ceil(K/128)][rows]
  *   block_rows 128   128 x 128 (weights); scales [ceil(rows/128)][ceil(K/128)], row-major
- * Last blocks may be partial. K % 16 == 0.
+ * Last blocks may be partial. K % 16 == 0. A NaN does not count in amax and gets a NaN code (a block of
+ * NaN and zeros alone: scale 1); an infinity makes its block's scale infinite, all its values NaN.
  *   x          device bf16 [M_x, K], 16-byte aligned (q, qt and st too)
  *   row_token  NULL (then M == M_x), or device int32 [M]: row r is quantised from
  *              x[row_token[r]] (the router's row lists: gathers and quantises in one pass); an

@@ -3,6 +3,8 @@
 // and the same for the transpose (the operands of the products' gradients).
 //
 //   s = amax_block / 448 (1 for a block of zeros);  code = E4M3_rn_sat(x / s).
+// A NaN does not count in amax and has a NaN code, so that it reaches the products through its own value
+// alone; a block of nothing but NaN and zeros has scale 1. An infinity makes its block's scale infinite.
 // Both divisions are IEEE round-to-nearest; the block scale is held in fp32 because the product
 // applies it to fp32 sums (no rounding of the scale is needed).
 #include <stdint.h>
@@ -76,7 +78,8 @@ DEVI void transpose4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_
   c[3] = __byte_perm(t2, t3, 0x7632);
 }
 
-DEVI float fp8_block_scale(float amax) { return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f); }
+// amax: the block's maximum but for NaN, NaN where it holds nothing else
+DEVI float fp8_block_scale(float amax) { return amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f; }
 
 // Scales for which the two-part reciprocal holds: hi, lo, the products that matter (quotients from
 // 2^-11 on) and lo's remainder all stay clear of underflow; smaller quotients have code 0 anyway.
