@@ -445,6 +445,11 @@ int nvfp4_fp8_quantize(const uint16_t* x, int64_t M_x, int64_t K, int32_t block_
  *   b, sb   codes [N, K], scales by b_block_rows (128: weights; 1: a second activation, for dW)
  *   y       [M, N] row-major, bf16 or fp32 (y_type NVFP4_BF16 / NVFP4_F32), 16-byte aligned
  * K % 16 == 0; any M >= 0, N >= 1. dev_status as for nvfp4_gemm.
+ * Scales: a block's sum (at most 128 * 448^2 < 2^24.7) meets sa sb, formed first in fp32, or with
+ * b_block_rows 1 sb and then sa. |y - y_ref| <= 1e-5 sum_k |a_k b_k| (plus the rounding of a bf16 y)
+ * holds where both sa sb and sb times the block's sum are normal fp32 numbers (2^-126 to 2^128) or 0.
+ * Below that range a block adds an error of up to 2^-125 max(1, sa): results around the smallest
+ * normal numbers lose places. Above it results are infinite or NaN.
  */
 int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int32_t b_block_rows,
                    void* y, int32_t y_type, int64_t M, int64_t N, int64_t K, int32_t* dev_status, void* stream);
