@@ -1097,6 +1097,12 @@ int nvfp4_fp8_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const fl
   //   1536 x 512     4.1 / 5.3   4.3 / 5.6   5.1 / 5.7   5.2 / 5.8   5.7 / 5.9
   //   8192 x 8192    21 / 21     21 / 23     25 / 23     26 / 23  (K in parts; 4096 x 6144, 128 rows: 20 / 18)
   //   16384 x 2048   10 / 12     10 / 12     11 / 13     17 / 13  (more than a round)
+  // Of 17 to 23 blocks up to 64 rows, by the 256-row tiles of the weight, K = 2560 (20 blocks):
+  //   rows               33          48          64
+  //   16 tiles       8.7 / 7.6   8.6 / 8.1   8.6 / 9.0
+  //   18             8.7 / 7.9   8.6 / 8.4   8.5 / 9.3
+  //   20             8.7 / 8.5   8.5 / 9.1   8.6 / 10.1
+  //   32             8.7 / 10.3  8.7 / 11.2  8.8 / 12.6  (K = 2176, 20 tiles: 7.9 / 8.1, 7.8 / 8.8, 7.9 / 9.6)
   // Up to 32 rows streaming has two CTAs an SM and splits K further; shorter K cannot be split:
   //   rows                1           8          16          32
   //   2048 x 2048    7.6 / 5.1   7.5 / 5.1   7.7 / 5.5   7.6 / 6.6

@@ -1,6 +1,8 @@
 // FP8 block-scaled GEMM with the tokens on the MMA's narrow side, for experts of up to a few hundred
-// rows (rows sorted by expert) and dense layers of up to 128: with the weight of row m's expert (or
-// the one weight), y[m, n] = sum_c sa[c, m] sb(c, n / 128) sum_{k in block c} a[m, k] b[n, k], a, b E4M3.
+// rows (rows sorted by expert) and for dense layers: of 33 to 128 rows where the weight is wide, and of
+// any number of rows from 9 on whose tiles are all resident at once where K is short (the rule with its
+// measurements: capi.cu). With the weight of row m's expert (or the one weight),
+// y[m, n] = sum_c sa[c, m] sb(c, n / 128) sum_{k in block c} a[m, k] b[n, k], a, b E4M3.
 //
 // A CTA pair (cta_group::2) takes 256 rows of a weight as the MMA's M and up to 128 of its
 // tokens as N, 64 or 128: with the tokens on M a tile of 256 would be mostly empty. As in the tile
