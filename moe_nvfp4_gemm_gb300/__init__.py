@@ -575,7 +575,8 @@ class MoeRouting:
     balance_loss    fp32 [1]
     routed_tokens   int32 [1]
 
-    It also keeps what the call was given and its gradient depends on: renormalize and valid.
+    It also keeps what the call was given and its gradient depends on: renormalize and valid (the tensor
+    itself, which has to hold the same at the backward call).
     """
     _fields = ("topk_idx", "topk_w", "slot_row", "counts", "expert_offsets", "row_token", "mean_prob", "balance_loss",
                "routed_tokens")
