@@ -525,16 +525,24 @@ _U8 = (torch.uint8,)
 _BF16 = (torch.bfloat16,)
 
 
+def _fits(have, shape):
+    """Whether a contiguous tensor of sizes `have` holds one of `shape` at its start: as many elements, and, unless
+    it is a flat buffer, rows of the same length. Dimensions may be merged or split ([tokens, heads, size] for
+    [tokens, K]) and there may be more rows."""
+    if math.prod(have) < math.prod(shape):
+        return False
+    runs = [1] + [math.prod(have[-i:]) for i in range(1, len(have) + 1)]  # elements of the inner slices
+    inner = min(len(have), len(shape))
+    return all(math.prod(shape[-i:]) in runs for i in range(1, inner))
+
+
 def _operand(t, types, shape, name):
     """t's address; t must be a contiguous CUDA tensor of one of `types` whose memory starts with a tensor of
-    `shape`: of that shape, a flat buffer, or with the same dimensions but for the first (more rows, or
-    leading dimensions merged or split), and at least as many elements."""
+    `shape` (see _fits)."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in types and t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, types))}")
-    if t.shape != shape:
-        inner = min(t.dim(), len(shape)) - 1
-        if (inner > 0 and t.shape[-inner:] != shape[-inner:]) or t.numel() < math.prod(shape):
-            raise TypeError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    if t.shape != shape and not _fits(t.shape, shape):
+        raise TypeError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
     return t.data_ptr()
 
 
