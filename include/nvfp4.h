@@ -359,9 +359,9 @@ int nvfp4_gemm_batched(const nvfp4_gemm_problem* problems, int32_t count, int64_
                        void* stream);
 
 /*
- * Element types of operands that may be bf16 or fp32.
+ * Element types of operands that may have several.
  */
-enum { NVFP4_BF16 = 0, NVFP4_F32 = 1 };
+enum { NVFP4_BF16 = 0, NVFP4_F32 = 1, NVFP4_F16 = 2 };
 
 /*
  * MoE router: the step in front of the grouped GEMMs ("The Moment of Recalibration",
@@ -469,6 +469,45 @@ size_t nvfp4_fp8_grouped_gemm_workspace_bytes(int32_t E, int64_t M_total, int64_
 int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
                            const int32_t* expert_offsets, int32_t E, int64_t M_total, int64_t N, int64_t K,
                            uint16_t* y, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Gated feed-forward block on 16-bit tensors: both projections, the activation and the product
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) u
+ * in one kernel, summed in fp32; act(g) = g sigma(p(g)) of the fp32 sums, p = g (NVFP4_SILU) or
+ * 2 sqrt(2/pi) (g + 0.044715 g^3) (NVFP4_GELU_TANH: gelu in its tanh form). h is rounded once.
+ *   x          device [M, K], bf16 or fp16 (type NVFP4_BF16 / NVFP4_F16), rows ldx elements apart
+ *   w_gate, w_up  device [I, K], of the same type, rows ld_gate and ld_up apart (the halves of one
+ *              [2 I, K] tensor, for instance)
+ *   h          [M, I] written, rows ldh apart
+ *   gate, up   [M, I] contiguous, written: g and u rounded to the type, for the backward call; or both NULL
+ *   workspace  nvfp4_gated_ffn_workspace_bytes(M, I, K) bytes, 16-byte aligned (NULL where that is 0)
+ * I, K and the row strides are multiples of 8, pointers 16-byte aligned, I and K at most 2^24. A NaN or an
+ * infinity stays in its token's row. dev_status as for nvfp4_gemm.
+ */
+enum { NVFP4_SILU = 0, NVFP4_GELU_TANH = 1 };
+size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K);
+int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
+                    int64_t ld_up, int32_t type, int32_t activation, uint16_t* h, int64_t ldh, uint16_t* gate, uint16_t* up,
+                    int64_t M, int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                    void* stream);
+
+/*
+ * Its gradients, from the forward call's gate and up and the gradient dh of h:
+ *   dg = dh u act'(g),  du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+ * dg and du are rounded to the type (the tensor cores read them), the sums are fp32, the results are
+ * rounded once.
+ *   gate, up   device [M, I] contiguous;  dh [M, I], rows lddh apart
+ *   dx         [M, K] contiguous, written, or NULL: not wanted (w_gate and w_up may then be NULL)
+ *   dw_gate, dw_up  [I, K] contiguous, written, or NULL each (x may be NULL when both are). M == 0 writes zeros.
+ *   workspace  nvfp4_gated_ffn_backward_workspace_bytes(M, I, K) bytes, 256-byte aligned
+ * The weights' gradients sum over all M rows: a NaN in a row of x, gate, up or dh reaches all that it
+ * meets, so padding rows must hold finite values (and dh zeros).
+ */
+size_t nvfp4_gated_ffn_backward_workspace_bytes(int64_t M, int64_t I, int64_t K);
+int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
+                             int64_t ld_up, const uint16_t* gate, const uint16_t* up, const uint16_t* dh, int64_t lddh,
+                             int32_t type, int32_t activation, uint16_t* dx, uint16_t* dw_gate, uint16_t* dw_up, int64_t M,
+                             int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
  * Elementwise device encoders used by the quantiser, for exhaustive checks:

@@ -53,7 +53,9 @@ EXPORTS = ["nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_amax_workspace_byt
            "nvfp4_sparse_gemm", "nvfp4_grouped_sparse_gemm", "nvfp4_gemm_batched",
            "nvfp4_grouped_gemm_swiglu_quantize_out",
            "nvfp4_moe_route_workspace_bytes", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_fp8_quantize",
-           "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm_workspace_bytes", "nvfp4_fp8_grouped_gemm"]
+           "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm_workspace_bytes", "nvfp4_fp8_grouped_gemm",
+           "nvfp4_gated_ffn_workspace_bytes", "nvfp4_gated_ffn", "nvfp4_gated_ffn_backward_workspace_bytes",
+           "nvfp4_gated_ffn_backward"]
 
 
 class NVFP4Error(RuntimeError):
@@ -144,6 +146,14 @@ def lib():
             L.nvfp4_fp8_grouped_gemm_workspace_bytes.argtypes = [_i32, _i64, _i64, _i64]
             L.nvfp4_fp8_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _sz, _vp,
                                                  _vp]
+            L.nvfp4_gated_ffn_workspace_bytes.restype = _sz
+            L.nvfp4_gated_ffn_workspace_bytes.argtypes = [_i64, _i64, _i64]
+            L.nvfp4_gated_ffn.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i64,
+                                          _i64, _vp, _sz, _vp, _vp]
+            L.nvfp4_gated_ffn_backward_workspace_bytes.restype = _sz
+            L.nvfp4_gated_ffn_backward_workspace_bytes.argtypes = [_i64, _i64, _i64]
+            L.nvfp4_gated_ffn_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _vp,
+                                                   _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp, _vp]
             L.nvfp4_last_launch_count.restype = ctypes.c_int
             _lib = L
     return _lib
@@ -797,6 +807,112 @@ def nvfp4_fp8_grouped_gemm(a, sa, b, sb, expert_offsets, E: int, M_total: int, N
     _check("nvfp4_fp8_grouped_gemm",
            lib().nvfp4_fp8_grouped_gemm(*args, py, pws, ws_bytes, _status(dev_status), _stream()))
     return y
+
+
+NVFP4_F16 = 2
+NVFP4_SILU = 0
+NVFP4_GELU_TANH = 1
+_HALF_TYPES = {torch.bfloat16: NVFP4_BF16, torch.float16: NVFP4_F16}
+_ACTIVATIONS = {"silu": NVFP4_SILU, "gelu_tanh": NVFP4_GELU_TANH}
+
+
+def nvfp4_gated_ffn_workspace_bytes(M: int, I: int, K: int) -> int:
+    return int(lib().nvfp4_gated_ffn_workspace_bytes(M, I, K))
+
+
+def nvfp4_gated_ffn_backward_workspace_bytes(M: int, I: int, K: int) -> int:
+    return int(lib().nvfp4_gated_ffn_backward_workspace_bytes(M, I, K))
+
+
+_ffn_workspace_bytes = functools.lru_cache(maxsize=128)(nvfp4_gated_ffn_workspace_bytes)
+_ffn_backward_workspace_bytes = functools.lru_cache(maxsize=128)(nvfp4_gated_ffn_backward_workspace_bytes)
+
+
+def _rows(t, dtype, shape, name):
+    """Address and row stride of a matrix of `shape` on the current device, whose rows may lie apart."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype):
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.shape != shape:
+        raise TypeError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise TypeError(f"{name} is on {t.device}, not on the current device")
+    ld, step = t.stride()
+    if shape[0] <= 1 or 0 in shape:  # no second row: the stride says nothing
+        ld = shape[1]
+    if step != 1 and shape[1] != 1 or ld < shape[1]:
+        raise TypeError(f"{name} must have contiguous rows, one behind the other")
+    return t.data_ptr(), ld
+
+
+def _ffn_inputs(x, w_gate, w_up, activation):
+    """M, I, K, the codes of the type and of the activation."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _HALF_TYPES and x.dim() == 2):
+        raise TypeError("x must be a CUDA tensor [M, K] of torch.bfloat16 or torch.float16")
+    if not (isinstance(w_gate, torch.Tensor) and w_gate.dim() == 2):
+        raise TypeError("w_gate must be a CUDA tensor [I, K]")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    return x.shape[0], w_gate.shape[0], x.shape[1], _HALF_TYPES[x.dtype], act
+
+
+def nvfp4_gated_ffn(x, w_gate, w_up, activation="silu", save=False, h=None, workspace=None, dev_status=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T), bf16 or fp16: x [M, K], w_gate and w_up [I, K], h [M, I]; activation
+    "silu" or "gelu_tanh". With save, returns (h, gate, up), what nvfp4_gated_ffn_backward needs. The rows of
+    x, the weights and h may lie apart (views of wider tensors); their strides, I and K are multiples of 8."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_gated_ffn, locals())
+    M, I, K, kind, act = _ffn_inputs(x, w_gate, w_up, activation)
+    dtype, dev = x.dtype, x.device
+    args = _rows(x, dtype, (M, K), "x") + _rows(w_gate, dtype, (I, K), "w_gate") + _rows(w_up, dtype, (I, K), "w_up")
+    h = torch.empty((M, I), dtype=dtype, device=dev) if h is None else h
+    ph, ldh = _rows(h, dtype, (M, I), "h")
+    gate = up = pg = pu = None
+    if save:
+        gate, up = torch.empty((M, I), dtype=dtype, device=dev), torch.empty((M, I), dtype=dtype, device=dev)
+        pg, pu = gate.data_ptr(), up.data_ptr()
+    ws_bytes, pws = _ffn_workspace_bytes(M, I, K), None
+    if workspace is not None:
+        pws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        pws = workspace.data_ptr()
+    _check("nvfp4_gated_ffn", lib().nvfp4_gated_ffn(*args, kind, act, ph, ldh, pg, pu, M, I, K, pws, ws_bytes,
+                                                    _status(dev_status), _stream()))
+    return (h, gate, up) if save else h
+
+
+def nvfp4_gated_ffn_backward(x, w_gate, w_up, gate, up, dh, activation="silu", need=(True, True, True), dx=None,
+                             dw_gate=None, dw_up=None, workspace=None, dev_status=None, stream=None):
+    """(dx, dw_gate, dw_up) of nvfp4_gated_ffn from its gate and up and the gradient dh [M, I] of h, in the operands'
+    type; `need` says which are wanted (None for the others). The gradients are contiguous."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_gated_ffn_backward, locals())
+    M, I, K, kind, act = _ffn_inputs(x, w_gate, w_up, activation)
+    dtype, dev = x.dtype, x.device
+    args = _rows(x, dtype, (M, K), "x") + _rows(w_gate, dtype, (I, K), "w_gate") + _rows(w_up, dtype, (I, K), "w_up")
+    for t, n in ((gate, "gate"), (up, "up")):
+        if _rows(t, dtype, (M, I), n)[1] != I:
+            raise TypeError(f"{n} must be contiguous")
+        args += (t.data_ptr(),)
+    args += _rows(dh, dtype, (M, I), "dh")
+    outs, ptrs = [], []
+    for t, wanted, shape, n in zip((dx, dw_gate, dw_up), need, ((M, K), (I, K), (I, K)), ("dx", "dw_gate", "dw_up")):
+        if wanted and t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif wanted and _rows(t, dtype, shape, n)[1] != K:
+            raise TypeError(f"{n} must be contiguous")
+        outs.append(t if wanted else None)
+        ptrs.append(t.data_ptr() if wanted else None)
+    if workspace is None:
+        ws_bytes = _ffn_backward_workspace_bytes(M, I, K)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        pws = workspace.data_ptr()
+    else:
+        pws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
+    _check("nvfp4_gated_ffn_backward",
+           lib().nvfp4_gated_ffn_backward(*args, kind, act, *ptrs, M, I, K, pws, ws_bytes, _status(dev_status), _stream()))
+    return tuple(outs)
 
 
 def nvfp4_encode_e2m1(v: torch.Tensor, stream=None) -> torch.Tensor:

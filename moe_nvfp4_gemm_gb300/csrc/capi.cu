@@ -136,6 +136,21 @@ int encode_out(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols, bool f3
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
+// 16-bit operand [rows, cols], rows `ld` elements apart, in boxes of 64 columns (128 bytes, 128-byte swizzle) x
+// box_rows rows; loads read zeros outside the tensor, stores write nothing there.
+int encode_16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return NVFP4_ERR_CUDA;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
 // Programmatic-dependent-launch mode of the streaming kernels: 0 off, 1 weights requested
 // before the dependency wait, 2 set-up overlap only (the default).
 int stream_pdl_mode() { return g_tune.pdl == 0 ? 2 : (g_tune.pdl < 0 ? 0 : g_tune.pdl); }
@@ -169,6 +184,8 @@ int pow2_at_least(int v) {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxFp8Dim = int64_t(1) << 30;
+constexpr int64_t kMaxFfnWidth = int64_t(1) << 24;
+constexpr int64_t kPairs = 76;  // CTA pairs of a GB300; workspace sizes follow it
 constexpr int64_t kFp8MinTileRows = 32;  // smallest token tile of the grouped FP8 kernels
 
 }  // namespace
@@ -1219,6 +1236,189 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
   }
   g_last_launches = 2;
   return rc;
+}
+
+// ---- 16-bit gated feed-forward block -------------------------------------------------------------
+
+// Sizes and row strides that TMA can address: multiples of 16 bytes.
+static int check_ffn_shape(int64_t M, int64_t I, int64_t K, int32_t type, int32_t activation) {
+  if (M < 0 || I <= 0 || K <= 0 || (type != NVFP4_BF16 && type != NVFP4_F16) ||
+      (activation != NVFP4_SILU && activation != NVFP4_GELU_TANH))
+    return NVFP4_ERR_INVALID_ARG;
+  // 2^24: tiles are counted, and columns past the last addressed, in 32 bits
+  if (I % 8 != 0 || K % 8 != 0 || M > kMaxFp8Dim || I > kMaxFfnWidth || K > kMaxFfnWidth) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t mt = (M + 255) / 256, it = (I + 127) / 128, kt = (K + 255) / 256;
+  if (mt * it > kMaxFp8Dim || mt * kt > kMaxFp8Dim || it * kt > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return NVFP4_OK;
+}
+
+static int check_ld(int64_t ld, int64_t cols) {
+  if (ld < cols) return NVFP4_ERR_INVALID_ARG;
+  return ld % 8 != 0 || ld >= int64_t(1) << 38 ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
+}
+
+// Parts of a product's contraction: as many as give every CTA pair an item, of at least eight blocks of 64.
+static int ffn_split(int64_t items, int64_t kblocks) {
+  int64_t split = items < kPairs ? kPairs / items : 1;
+  if (split > kblocks / 8) split = kblocks / 8;
+  return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
+}
+
+// Sizes of one tile product, and the workspace bytes of its parts.
+static size_t ffn_plan(FfnTileArgs& p, int64_t M, int64_t N, int64_t tile_cols, int64_t kblocks, int weights) {
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.mt = static_cast<int>((M + 255) / 256);
+  p.nt = static_cast<int>((N + tile_cols - 1) / tile_cols);
+  p.kblocks = static_cast<int>(kblocks);
+  p.weights = weights;
+  p.split = ffn_split(static_cast<int64_t>(p.mt) * p.nt * weights, kblocks);
+  return p.split == 1 ? 0 : static_cast<size_t>(weights) * p.split * p.mt * p.nt * 256 * 256 * 4;
+}
+
+static int run_ffn_tile(FfnTileMaps& maps, FfnTileArgs& p, int mode, int sms, cudaStream_t st) {
+  if (p.split > 1) {
+    const uint64_t rows = static_cast<uint64_t>(p.weights) * p.split * p.mt * 256;
+    int rc = encode_out(&maps.part, p.ws, rows, static_cast<uint64_t>(p.nt) * 256, true);
+    if (rc) return rc;
+  } else {
+    maps.part = maps.y[0];  // not used
+  }
+  p.raster = g_tune.dense_raster;
+  p.watchdog_ns = watchdog_ns();
+  p.drop_stage = g_tune.withhold_stage;
+  g_last_launches += p.split > 1 ? 2 : 1;
+  return from_cuda(launch_ffn_tile(maps, p, mode, sms, st));
+}
+
+size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K) {
+  if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0) return 0;
+  FfnTileArgs p = {};
+  return ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
+}
+
+int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
+                    int64_t ld_up, int32_t type, int32_t activation, uint16_t* h, int64_t ldh, uint16_t* gate, uint16_t* up,
+                    int64_t M, int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                    void* stream) {
+  g_last_launches = 0;
+  int rc = check_ffn_shape(M, I, K, type, activation);
+  if (rc) return rc;
+  if ((rc = check_ld(ldx, K)) || (rc = check_ld(ld_gate, K)) || (rc = check_ld(ld_up, K)) || (rc = check_ld(ldh, I))) return rc;
+  if (M == 0) return NVFP4_OK;
+  if (!x || !w_gate || !w_up || !h || (gate == nullptr) != (up == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || !aligned16(gate) || !aligned16(up) ||
+      !aligned16(workspace))
+    return NVFP4_ERR_ALIGNMENT;
+  FfnTileArgs p = {};
+  const size_t need = ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  DevInfo d;
+  rc = device_info(d);
+  if (rc) return rc;
+  FfnTileMaps maps;
+  if ((rc = encode_16(&maps.a[0], x, M, K, ldx, 128))) return rc;
+  maps.a[1] = maps.a[0];
+  if ((rc = encode_16(&maps.b[0], w_gate, I, K, ld_gate, 128))) return rc;
+  if ((rc = encode_16(&maps.b[1], w_up, I, K, ld_up, 128))) return rc;
+  if ((rc = encode_16(&maps.y[0], h, M, I, ldh, 32))) return rc;
+  maps.y[1] = maps.y[2] = maps.y[0];
+  if (gate && ((rc = encode_16(&maps.y[1], gate, M, I, I, 32)) || (rc = encode_16(&maps.y[2], up, M, I, I, 32)))) return rc;
+  p.act = activation;
+  p.save = gate != nullptr;
+  p.half = type == NVFP4_F16;
+  p.status = dev_status;
+  p.ws = static_cast<float*>(workspace);
+  p.y[0] = h;
+  p.y[1] = gate;
+  p.y[2] = up;
+  p.ldy = ldh;
+  return run_ffn_tile(maps, p, kFfnForward, d.sms, static_cast<cudaStream_t>(stream));
+}
+
+// The workspace: dg and du, [M, I] each, then the parts of the product that runs (one after the other).
+static size_t ffn_backward_plan(FfnTileArgs& input, FfnTileArgs& weight, int64_t M, int64_t I, int64_t K, int weights,
+                                size_t& parts_at) {
+  parts_at = (static_cast<size_t>(M) * I * 4 + 255) / 256 * 256;
+  const size_t a = ffn_plan(input, M, K, 256, 2 * ((I + 63) / 64), 1);
+  const size_t b = weights ? ffn_plan(weight, I, K, 256, (M + 63) / 64, weights) : 0;
+  return parts_at + (a > b ? a : b);
+}
+
+size_t nvfp4_gated_ffn_backward_workspace_bytes(int64_t M, int64_t I, int64_t K) {
+  if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0) return 0;
+  FfnTileArgs a = {}, b = {};
+  size_t at;
+  const size_t two = ffn_backward_plan(a, b, M, I, K, 2, at), one = ffn_backward_plan(a, b, M, I, K, 1, at);
+  return two > one ? two : one;
+}
+
+int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
+                             int64_t ld_up, const uint16_t* gate, const uint16_t* up, const uint16_t* dh, int64_t lddh,
+                             int32_t type, int32_t activation, uint16_t* dx, uint16_t* dw_gate, uint16_t* dw_up, int64_t M,
+                             int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  g_last_launches = 0;
+  int rc = check_ffn_shape(M, I, K, type, activation);
+  if (rc) return rc;
+  if ((rc = check_ld(ldx, K)) || (rc = check_ld(ld_gate, K)) || (rc = check_ld(ld_up, K)) || (rc = check_ld(lddh, I))) return rc;
+  const int weights = (dw_gate != nullptr) + (dw_up != nullptr);
+  if (M > 0 && ((dx && (!w_gate || !w_up)) || (weights && !x) || !gate || !up || !dh)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(gate) || !aligned16(up) || !aligned16(dh) ||
+      !aligned16(dx) || !aligned16(dw_gate) || !aligned16(dw_up) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return NVFP4_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DevInfo d;
+  if (M == 0) {  // no tokens: the weights' gradients are sums over none
+    for (uint16_t* dw : {dw_gate, dw_up})
+      if (dw) {
+        if ((rc = device_info(d))) return rc;
+        if ((rc = from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(I) * K * 2, st)))) return rc;
+      }
+    return NVFP4_OK;
+  }
+  if (!dx && !weights) return NVFP4_OK;
+  FfnTileArgs pi = {}, pw = {};
+  size_t parts_at;
+  const size_t need = ffn_backward_plan(pi, pw, M, I, K, weights, parts_at);
+  if (!workspace || workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
+  rc = device_info(d);
+  if (rc) return rc;
+  uint16_t* dg = static_cast<uint16_t*>(workspace);
+  uint16_t* du = dg + static_cast<size_t>(M) * I;
+  FfnGradArgs ga = {gate, up, dh, dg, du, M, lddh, static_cast<int>(I), activation, type == NVFP4_F16};
+  if ((rc = from_cuda(launch_ffn_grad(ga, d.sms, st)))) return rc;
+  g_last_launches = 1;
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + parts_at);
+  for (FfnTileArgs* p : {&pi, &pw}) {
+    p->half = type == NVFP4_F16;
+    p->status = dev_status;
+    p->ws = parts;
+  }
+  FfnTileMaps maps;
+  if (dx) {
+    if ((rc = encode_16(&maps.a[0], dg, M, I, I, 128)) || (rc = encode_16(&maps.a[1], du, M, I, I, 128)) ||
+        (rc = encode_16(&maps.b[0], w_gate, I, K, ld_gate, 64)) || (rc = encode_16(&maps.b[1], w_up, I, K, ld_up, 64)) ||
+        (rc = encode_16(&maps.y[0], dx, M, K, K, 32)))
+      return rc;
+    maps.y[1] = maps.y[2] = maps.y[0];
+    pi.y[0] = dx;
+    if ((rc = run_ffn_tile(maps, pi, kFfnInput, d.sms, st))) return rc;
+  }
+  if (weights) {
+    const int gate_first = dw_gate ? 0 : 1;  // what stands first
+    for (int i = 0; i < 2; ++i) {
+      const bool is_up = i == 1 || gate_first == 1;
+      uint16_t* dw = is_up ? dw_up : dw_gate;
+      if (!dw) dw = dw_gate;
+      if ((rc = encode_16(&maps.a[i], is_up ? du : dg, M, I, I, 64)) || (rc = encode_16(&maps.y[i], dw, I, K, K, 32))) return rc;
+      pw.y[i] = dw;
+    }
+    if ((rc = encode_16(&maps.b[0], x, M, K, ldx, 64))) return rc;
+    maps.b[1] = maps.b[0];
+    maps.y[2] = maps.y[0];
+    if ((rc = run_ffn_tile(maps, pw, kFfnWeight, d.sms, st))) return rc;
+  }
+  return NVFP4_OK;
 }
 
 }  // extern "C"

@@ -206,6 +206,41 @@ cudaError_t launch_fp8_gemm_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
 cudaError_t launch_fp8_narrow(const CUtensorMap& tmW, const CUtensorMap& tmX, const Fp8GemmArgs& p, int grid,
                                     cudaStream_t st);
 
+// ---- 16-bit gated feed-forward block ------------------------------------------------------
+enum { kFfnForward = 0, kFfnInput = 1, kFfnWeight = 2 };
+struct FfnTileMaps {
+  CUtensorMap a[2], b[2];  // gate and up where the operand has both
+  CUtensorMap y[3];        // forward: h, gate, up; input: dx; weight: dw_gate, dw_up
+  CUtensorMap part;        // the parts' sums, fp32
+};
+struct FfnTileArgs {
+  int M, N;       // rows and columns of a result
+  int mt, nt;     // 256 x 256 tiles of sums (forward: 128 columns of h each)
+  int kblocks;    // blocks of 64 of the contraction
+  int split;      // parts of the contraction
+  int weights;    // weight gradients: results wanted, the first `weights` of y
+  int raster;     // tile order, see tile_coords
+  int act, save;  // forward: activation; also write gate and up
+  int half;       // fp16 instead of bf16
+  int drop_stage;  // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
+  int32_t* status;
+  uint64_t watchdog_ns;  // limit of every pipeline wait
+  float* ws;      // split > 1: fp32 [weights][split][mt * 256][nt * 256]
+  void* y[3];     // and the results, written by k_ffn_join
+  int64_t ldy;    // forward: row stride of h
+};
+cudaError_t launch_ffn_tile(const FfnTileMaps& maps, const FfnTileArgs& p, int mode, int sms, cudaStream_t st);
+struct FfnGradArgs {
+  const uint16_t* gate;  // [M, I]
+  const uint16_t* up;    // [M, I]
+  const uint16_t* dh;    // rows lddh apart
+  uint16_t* dg;          // [M, I]
+  uint16_t* du;          // [M, I]
+  int64_t M, lddh;
+  int I, act, half;
+};
+cudaError_t launch_ffn_grad(const FfnGradArgs& p, int sms, cudaStream_t st);
+
 int stream_smem_bytes(int stages, int x_rows, int recv_bytes, bool sparse = false);
 // shared memory after the ring for one tile's token indices (and with qout the epilogue's
 // NVFP4 transpose tiles, 1 KB per epilogue warp)

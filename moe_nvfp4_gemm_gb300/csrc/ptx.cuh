@@ -398,6 +398,24 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// D(tmem) (+)= A(smem) * B(smem)^T, both operands bf16 or both fp16, K = 16 per instruction.
+DEVI void tc_mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::f16: fp32 accumulator, shape M x N x 16; a_mn, b_mn: the operand's tile
+// lies along its rows (MN-major) instead of along K.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool a_mn = false, bool b_mn = false) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // 32 lanes x 32 consecutive 32-bit columns.
 DEVI void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -505,6 +523,18 @@ DEVI uint64_t desc_sw128(uint32_t saddr) {
   d |= static_cast<uint64_t>(1024 >> 4) << 32;           // stride byte offset: next 8-row group
   d |= static_cast<uint64_t>(1) << 46;                   // descriptor version
   d |= static_cast<uint64_t>(2) << 61;                   // 128-byte swizzle
+  return d;
+}
+
+// The same for an MN-major 16-bit tile: boxes of 64 of MN (128 bytes, 128-byte swizzle) x the K rows, `chunk` bytes
+// from one 64 of MN to the next; eight K rows (1,024 bytes) to the next eight. K offsets of 16: 2,048 bytes.
+DEVI uint64_t desc_sw128_mn(uint32_t saddr, uint32_t chunk) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+  d |= static_cast<uint64_t>(chunk >> 4) << 16;  // leading byte offset: next 64 of MN
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;   // stride byte offset: next 8 of K
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
 
