@@ -55,7 +55,8 @@ EXPORTS = ["nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_amax_workspace_byt
            "nvfp4_moe_route_workspace_bytes", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_fp8_quantize",
            "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm_workspace_bytes", "nvfp4_fp8_grouped_gemm",
            "nvfp4_gated_ffn_workspace_bytes", "nvfp4_gated_ffn", "nvfp4_gated_ffn_backward_workspace_bytes",
-           "nvfp4_gated_ffn_backward"]
+           "nvfp4_gated_ffn_backward", "nvfp4_int8_quantize", "nvfp4_int8_gemm_workspace_bytes",
+           "nvfp4_int8_gemm", "nvfp4_grad_clip_workspace_bytes", "nvfp4_grad_clip"]
 
 
 class NVFP4Error(RuntimeError):
@@ -154,6 +155,13 @@ def lib():
             L.nvfp4_gated_ffn_backward_workspace_bytes.argtypes = [_i64, _i64, _i64]
             L.nvfp4_gated_ffn_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _vp,
                                                    _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp, _vp]
+            L.nvfp4_int8_quantize.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _vp, _vp]
+            L.nvfp4_int8_gemm_workspace_bytes.restype = _sz
+            L.nvfp4_int8_gemm_workspace_bytes.argtypes = [_i64, _i64, _i64]
+            L.nvfp4_int8_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _sz, _vp, _vp]
+            L.nvfp4_grad_clip_workspace_bytes.restype = _sz
+            L.nvfp4_grad_clip_workspace_bytes.argtypes = [_i32]
+            L.nvfp4_grad_clip.argtypes = [_vp, _vp, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _sz, _vp]
             L.nvfp4_last_launch_count.restype = ctypes.c_int
             _lib = L
     return _lib
@@ -913,6 +921,106 @@ def nvfp4_gated_ffn_backward(x, w_gate, w_up, gate, up, dh, activation="silu", n
     _check("nvfp4_gated_ffn_backward",
            lib().nvfp4_gated_ffn_backward(*args, kind, act, *ptrs, M, I, K, pws, ws_bytes, _status(dev_status), _stream()))
     return tuple(outs)
+
+
+def nvfp4_int8_quantize(x: torch.Tensor, stream=None):
+    """bf16 or fp16 [M, K] -> (codes int8 [M, K], scales fp32 [M]): the largest magnitude of a row becomes 127. The
+    rows of x may lie apart. Weights [N, K] are quantised for each output channel by the same call."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_int8_quantize, locals())
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _HALF_TYPES and x.dim() == 2):
+        raise TypeError("x must be a CUDA tensor [M, K] of torch.bfloat16 or torch.float16")
+    M, K = x.shape
+    px, ldx = _rows(x, x.dtype, (M, K), "x")
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    s = torch.empty(M, dtype=torch.float32, device=x.device)
+    _check("nvfp4_int8_quantize",
+           lib().nvfp4_int8_quantize(px, ldx, _HALF_TYPES[x.dtype], M, K, q.data_ptr(), s.data_ptr(), _stream()))
+    return q, s
+
+
+_I8 = (torch.int8,)
+_OUT_TYPES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32, torch.float16: NVFP4_F16}
+
+
+def nvfp4_int8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().nvfp4_int8_gemm_workspace_bytes(M, N, K))
+
+
+_int8_workspace_bytes = functools.lru_cache(maxsize=128)(nvfp4_int8_gemm_workspace_bytes)
+
+
+def nvfp4_int8_gemm(a, sa, b, sb, M: int, N: int, K: int, out_dtype=torch.bfloat16, y=None, workspace=None, dev_status=None,
+                    stream=None):
+    """y = sa[m] sb[n] (a b^T) [M, N] in bf16, fp16 or fp32 from int8 codes a [M, K], b [N, K] and their row scales
+    (see nvfp4_int8_quantize); the integer sums are exact."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_int8_gemm, locals())
+    y_type = _OUT_TYPES.get(out_dtype)
+    if y_type is None:
+        raise TypeError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
+    try:
+        pa = _operand(a, _I8, (M, K), "a")
+        args = (pa, _operand(sa, _F32, (M,), "sa"), _operand(b, _I8, (N, K), "b"), _operand(sb, _F32, (N,), "sb"))
+        if y is None:
+            y = torch.empty((M, N), dtype=out_dtype, device=a.device)
+            py = y.data_ptr()
+        else:
+            py = _operand(y, (out_dtype,), (M, N), "y")
+    except TypeError:  # sizes that the library refuses are its error
+        _check("nvfp4_int8_gemm", lib().nvfp4_int8_gemm(None, None, None, None, None, y_type, min(M, 0), N, K, None, 0, None, None))
+        raise
+    ws_bytes, pws = _int8_workspace_bytes(M, N, K), None
+    if workspace is not None:
+        pws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=a.device)
+        pws = workspace.data_ptr()
+    _check("nvfp4_int8_gemm",
+           lib().nvfp4_int8_gemm(*args, py, y_type, M, N, K, pws, ws_bytes, _status(dev_status), _stream()))
+    return y
+
+
+_GRAD_TYPES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32, torch.float16: NVFP4_F16}
+
+
+def nvfp4_grad_clip_workspace_bytes(count: int) -> int:
+    return int(lib().nvfp4_grad_clip_workspace_bytes(count))
+
+
+def nvfp4_grad_clip(grads, max_norm=math.inf, out=None, norm=None, workspace=None, stream=None) -> torch.Tensor:
+    """The norm over all values of `grads` (contiguous CUDA tensors, bf16, fp16 or fp32, mixed as they come), fp32 [1];
+    the gradients are multiplied by min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out` of the same
+    types and shapes. Without max_norm only the norm is computed. No two results may share memory."""
+    if stream is not None:
+        return _on_stream(stream, nvfp4_grad_clip, locals())
+    grads = list(grads)
+    n, here = len(grads), torch._C._cuda_getDevice()
+    types, sizes = [], []
+    for t in grads:
+        kind = _GRAD_TYPES.get(t.dtype)
+        if kind is None or not t.is_cuda or not t.is_contiguous() or t.get_device() != here:
+            raise TypeError("grads must be contiguous tensors of torch.bfloat16, float16 or float32 on the current CUDA device")
+        types.append(kind)
+        sizes.append(t.numel())
+    to = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise TypeError(f"out has {len(out)} tensors, grads {n}")
+        for t, o in zip(grads, out):
+            if not (o.is_cuda and o.dtype == t.dtype and o.shape == t.shape and o.is_contiguous() and o.get_device() == here):
+                raise TypeError("out must hold tensors like grads")
+        to = (_vp * n)(*[o.data_ptr() for o in out])
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device="cuda")
+    if workspace is None:
+        workspace = torch.empty(nvfp4_grad_clip_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    _check("nvfp4_grad_clip",
+           lib().nvfp4_grad_clip((_vp * n)(*[t.data_ptr() for t in grads]), to, (_i64 * n)(*sizes), (_i32 * n)(*types), n,
+                                 max_norm, _operand(norm, _F32, (1,), "norm"),
+                                 _operand(workspace, _U8, (0,), "workspace"), workspace.numel(), _stream()))
+    return norm
 
 
 def nvfp4_encode_e2m1(v: torch.Tensor, stream=None) -> torch.Tensor:

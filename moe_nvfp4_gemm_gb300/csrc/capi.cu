@@ -2,9 +2,12 @@
 // launches. Declarations and the contract of every entry point: include/nvfp4.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
+#include <new>
 
 #include "nvfp4.h"
 #include "kernels.h"
@@ -1417,6 +1420,186 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
     maps.b[1] = maps.b[0];
     maps.y[2] = maps.y[0];
     if ((rc = run_ffn_tile(maps, pw, kFfnWeight, d.sms, st))) return rc;
+  }
+  return NVFP4_OK;
+}
+
+// ---- 8-bit integers with a scale for each row ------------------------------------------------------
+
+int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M, int64_t K, int8_t* q, float* s, void* stream) {
+  g_last_launches = 0;
+  if (M < 0 || K < 0 || (type != NVFP4_BF16 && type != NVFP4_F16)) return NVFP4_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M > kMaxFp8Dim || K > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  int rc = check_ld(ldx, K);
+  if (rc) return rc;
+  if (M == 0 || K == 0) return NVFP4_OK;
+  if (!x || !q || !s) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(s)) return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  if ((rc = device_info(d))) return rc;
+  Int8QuantArgs a = {x, M, K, ldx, reinterpret_cast<uint8_t*>(q), s, type == NVFP4_F16};
+  g_last_launches = 1;
+  return from_cuda(launch_int8_quantize(a, d.sms, static_cast<cudaStream_t>(stream)));
+}
+
+// Tokens of a tile: two sizes of tiles on the CTAs' own conversion, then 256 from the workspace.
+static int int8_tile_tokens(int64_t M) { return M <= 64 ? 64 : (M <= 128 ? 128 : 256); }
+
+static int check_int8_shape(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N <= 0 || K <= 0) return NVFP4_ERR_INVALID_ARG;
+  // 131,071 products of at most 2^14 fit 32 bits
+  if (K % 16 != 0 || K > 131056 || M > kMaxFp8Dim || N > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return ((M + 255) / 256) * ((N + 255) / 256) > kMaxFp8Dim ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
+}
+
+size_t nvfp4_int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_int8_shape(M, N, K) || int8_tile_tokens(M) != 256) return 0;
+  return static_cast<size_t>(M) * K * 2;
+}
+
+int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* y, int32_t y_type, int64_t M,
+                    int64_t N, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  g_last_launches = 0;
+  int rc = check_int8_shape(M, N, K);
+  if (rc) return rc;
+  if (y_type != NVFP4_BF16 && y_type != NVFP4_F32 && y_type != NVFP4_F16) return NVFP4_ERR_INVALID_ARG;
+  if (M == 0) return NVFP4_OK;
+  if (!a || !sa || !b || !sb || !y) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(y) || !aligned4(sa) || !aligned4(sb) || !aligned16(workspace))
+    return NVFP4_ERR_ALIGNMENT;
+  const size_t need = nvfp4_int8_gemm_workspace_bytes(M, N, K);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  DevInfo d;
+  if ((rc = device_info(d))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int tokens = int8_tile_tokens(M);
+  const uint8_t* a8 = reinterpret_cast<const uint8_t*>(a);
+  Int8GemmArgs p = {};
+  p.sa = sa;
+  p.sb = sb;
+  p.y = y;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.mt = static_cast<int>((M + tokens - 1) / tokens);
+  p.nt = static_cast<int>((N + 255) / 256);
+  p.out = y_type;
+  p.status = dev_status;
+  p.watchdog_ns = watchdog_ns();
+  p.drop_stage = g_tune.withhold_stage;
+  const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt, kb = (K + 127) / 128;
+  p.split = 1;
+  while (p.split < 4 && tiles * p.split * 2 <= d.sms / 2 && kb >= p.split * 8) p.split *= 2;
+  CUtensorMap tmW, tmX;
+  if ((rc = encode_2d(&tmW, reinterpret_cast<const uint8_t*>(b), N, K, 128))) return rc;
+  if (tokens == 256) {
+    if ((rc = from_cuda(launch_int8_widen(a8, workspace, M * K, d.sms, st)))) return rc;
+    ++g_last_launches;
+    if ((rc = encode_16(&tmX, workspace, M, K, K, 128))) return rc;
+  } else if ((rc = encode_2d(&tmX, a8, M, K, tokens / 2))) {
+    return rc;
+  }
+  ++g_last_launches;
+  return from_cuda(launch_int8_gemm(tmW, tmX, p, tokens, d.sms, st));
+}
+
+// ---- gradient norm and clipping -----------------------------------------------------------------
+
+size_t nvfp4_grad_clip_workspace_bytes(int32_t count) {
+  if (count < 0) return 0;
+  const size_t groups = (static_cast<size_t>(count) + kClipGroup - 1) / kClipGroup;
+  return (groups ? groups : 1) * kClipBlocks * sizeof(double);
+}
+
+// Whether two different gradients, or one's result and another gradient, share memory.
+static int clip_overlaps(const ClipArgs& a, int32_t count, bool& found) {
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  found = false;
+  const size_t n = static_cast<size_t>(count) * 2;
+  Span few[128];
+  Span* spans = n <= 128 ? few : new (std::nothrow) Span[n];
+  if (!spans) return NVFP4_ERR_CUDA;
+  size_t used = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    ClipEntry e;
+    if (!clip_list_entry(a, i, e)) continue;
+    const uintptr_t bytes = static_cast<uintptr_t>(e.numel) * (e.type == kClipF32 ? 4 : 2);
+    const uintptr_t src = reinterpret_cast<uintptr_t>(e.src), dst = reinterpret_cast<uintptr_t>(e.dst);
+    spans[used++] = {dst, dst + bytes, true};
+    if (src != dst) spans[used++] = {src, src + bytes, false};
+  }
+  std::sort(spans, spans + used, [](const Span& x, const Span& y) { return x.begin < y.begin; });
+  // the ends reached so far, of what is written and of all
+  uintptr_t written = 0, any = 0;
+  for (size_t i = 0; i < used && !found; ++i) {
+    found = spans[i].begin < (spans[i].written ? any : written);
+    any = spans[i].end > any ? spans[i].end : any;
+    if (spans[i].written && spans[i].end > written) written = spans[i].end;
+  }
+  if (spans != few) delete[] spans;
+  return NVFP4_OK;
+}
+
+int nvfp4_grad_clip(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* types, int32_t count,
+                    float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  if (count < 0 || !(max_norm >= 0.0f) || !norm || (count > 0 && (!grads || !numel || !types))) return NVFP4_ERR_INVALID_ARG;
+  if (count > 1 << 24) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned4(norm) || !aligned16(workspace)) return NVFP4_ERR_ALIGNMENT;
+  for (int32_t i = 0; i < count; ++i) {
+    if (numel[i] < 0 || (types[i] != NVFP4_BF16 && types[i] != NVFP4_F32 && types[i] != NVFP4_F16)) return NVFP4_ERR_INVALID_ARG;
+    if (numel[i] > int64_t(1) << 40) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (numel[i] == 0) continue;
+    if (!grads[i] || (out && !out[i])) return NVFP4_ERR_INVALID_ARG;
+    const uintptr_t mask = types[i] == NVFP4_F32 ? 3 : 1;
+    if ((reinterpret_cast<uintptr_t>(grads[i]) | (out ? reinterpret_cast<uintptr_t>(out[i]) : 0)) & mask) return NVFP4_ERR_ALIGNMENT;
+  }
+  if (!workspace || workspace_bytes < nvfp4_grad_clip_workspace_bytes(count)) return NVFP4_ERR_WORKSPACE;
+  ClipArgs a = {grads, out, numel, types, static_cast<double*>(workspace), norm, 0, max_norm, 0};
+  // in place without a limit only the norm is wanted
+  a.scale = out != nullptr || max_norm < HUGE_VALF;
+  int rc;
+  if (a.scale) {
+    bool found;
+    if ((rc = clip_overlaps(a, count, found))) return rc;
+    if (found) return NVFP4_ERR_INVALID_ARG;
+  }
+  DevInfo d;
+  if ((rc = device_info(d))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto group = [&](int32_t first, int slot0, ClipGroup& g) {
+    g.first = first;
+    g.end = count - first < kClipGroup ? count : first + kClipGroup;
+    g.slot0 = slot0;
+    int64_t chunks = 0;
+    for (int32_t i = g.first; i < g.end; ++i) chunks += (numel[i] + kClipChunk - 1) / kClipChunk;
+    if (chunks > kMaxDim) return false;
+    g.grid = static_cast<int>(chunks < kClipBlocks ? chunks : kClipBlocks);
+    return true;
+  };
+  ClipGroup g;
+  for (int32_t i = 0; i < count; i += kClipGroup) {
+    if (!group(i, a.slots, g)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    a.slots += g.grid;
+  }
+  for (int pass = 0; pass < 2; ++pass) {
+    int slot0 = 0;
+    bool first = true;  // in the second pass the first group's launch writes the norm, whatever it holds
+    for (int32_t i = 0; i < count || (pass == 1 && first); i += kClipGroup) {
+      group(i, slot0, g);
+      slot0 += g.grid;
+      const bool wanted = pass == 0 ? g.grid > 0 : (first || (a.scale && g.grid > 0));
+      if (wanted) {
+        g.slot0 = pass == 1 ? !first : g.slot0;
+        if ((rc = from_cuda(launch_clip_group(a, g, pass == 1, st)))) return rc;
+        ++g_last_launches;
+      }
+      first = false;
+      if (pass == 1 && !a.scale) break;
+    }
   }
   return NVFP4_OK;
 }

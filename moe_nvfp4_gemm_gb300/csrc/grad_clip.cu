@@ -1,0 +1,288 @@
+// Norm over a list of gradients and clipping to a largest norm:
+//   norm = sqrt(sum over all values of g^2),  f = min(1, max_norm / (norm + 1e-6)),  out = g f.
+//
+// Bound by memory: the gradients are read for the norm and, since every value needs the whole norm, once
+// more for the scaling, and written once. The list travels in the kernels' parameters (no copy to the
+// device, so that a captured graph carries it); it is cut into chunks of 16,384 values, which a fixed grid
+// walks in strides, so that the order of the sums, and with it every bit of the result, depends on the sizes
+// alone. The second kernel walks the chunks backwards: the last ones read are still in L2.
+//
+// Squares: a thread adds those of a chunk (up to 64) in fp32 and joins chunks in fp64. Where that fp32 sum is
+// infinite (|g| > 2^63) or so small that squares fell below fp32's range, the thread's values are added
+// again in fp64: the norm is right for every finite input (and infinite or NaN for the others).
+#include <stdint.h>
+
+#include "ffn.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = kClipChunk;
+
+template <int N>
+struct ClipTable {
+  ClipEntry e[N];
+  int count;      // entries
+  int chunks;     // chunks of all of them
+  int slot0;      // first kernel: its first partial sum; second: 0 in the launch that writes the norm
+  int slots;      // partial sums of all launches
+  double* partial;
+  float* norm;
+  float max_norm;
+  int scale;      // second kernel: scale, or the norm alone
+};
+
+// Entry that chunk c belongs to: the last one whose first chunk is <= c.
+template <int N>
+DEVI int clip_entry(const ClipTable<N>& t, int c) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.e[mid].first <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+DEVI float clip_value(const void* p, int64_t i, int type) {
+  if (type == kClipF32) return static_cast<const float*>(p)[i];
+  const uint32_t w = static_cast<const uint16_t*>(p)[i];
+  return type == kClipF16 ? unpack16<true>(w, 0) : unpack16<false>(w, 0);
+}
+
+// The values [i0, i1) of a chunk as: single values up to the first 16-byte boundary, 16-byte groups, single
+// values behind the last. Returns the groups' first value and count.
+DEVI void clip_ranges(const void* p, int64_t i0, int64_t i1, int size, int64_t& v0, int& groups) {
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) + i0 * size) & 15u);
+  const int64_t head = off ? (16 - off) / size : 0;
+  v0 = i0 + head < i1 ? i0 + head : i1;
+  groups = static_cast<int>((i1 - v0) * size / 16);
+}
+
+DEVI double block_sum(double v, double* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double total = 0.0;
+  for (int w = 0; w < kThreads / 32; ++w) total += sh[w];
+  return total;
+}
+
+template <int TYPE>
+DEVI void add_squares(uint4 v, float& s0, float& s1, uint32_t& any) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    any |= w[j];
+    if (TYPE == kClipF32) {
+      const float a = __uint_as_float(w[j]);
+      (j & 1 ? s1 : s0) = fmaf(a, a, j & 1 ? s1 : s0);
+    } else {
+      const float a = unpack16<TYPE == kClipF16>(w[j], 0), b = unpack16<TYPE == kClipF16>(w[j], 1);
+      s0 = fmaf(a, a, s0);
+      s1 = fmaf(b, b, s1);
+    }
+  }
+}
+
+template <int TYPE>
+DEVI double chunk_squares(const void* p, int64_t i0, int64_t i1) {
+  constexpr int SIZE = TYPE == kClipF32 ? 4 : 2, PER = 16 / SIZE;
+  int64_t v0;
+  int groups;
+  clip_ranges(p, i0, i1, SIZE, v0, groups);
+  const int64_t tail = v0 + static_cast<int64_t>(groups) * PER;
+  float s0 = 0.0f, s1 = 0.0f;
+  uint32_t any = 0;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + v0 * SIZE);
+  constexpr int DEEP = 8;
+  int g = threadIdx.x;
+  for (; g + (DEEP - 1) * kThreads < groups; g += DEEP * kThreads) {
+    uint4 v[DEEP];
+#pragma unroll
+    for (int j = 0; j < DEEP; ++j) v[j] = src[g + j * kThreads];
+#pragma unroll
+    for (int j = 0; j < DEEP; ++j) add_squares<TYPE>(v[j], s0, s1, any);
+  }
+  for (; g < groups; g += kThreads) add_squares<TYPE>(src[g], s0, s1, any);
+  const int64_t single = i0 + threadIdx.x;  // at most 7 values in front and 7 behind: a thread each
+  const int64_t behind = tail + threadIdx.x;
+  const bool has_single = single < v0, has_behind = behind < i1;
+  if (has_single) {
+    const float a = clip_value(p, single, TYPE);
+    s0 = fmaf(a, a, s0);
+    any |= __float_as_uint(a);
+  }
+  if (has_behind) {
+    const float a = clip_value(p, behind, TYPE);
+    s1 = fmaf(a, a, s1);
+    any |= __float_as_uint(a);
+  }
+  const float s = s0 + s1;
+  if ((s >= 0x1p-90f && s <= 0x1p127f) || (any & (TYPE == kClipF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return s;
+  double d = 0.0;
+  for (int q = threadIdx.x; q < groups; q += kThreads)
+    for (int j = 0; j < PER; ++j) {
+      const double a = clip_value(p, v0 + static_cast<int64_t>(q) * PER + j, TYPE);
+      d += a * a;
+    }
+  if (has_single) {
+    const double a = clip_value(p, single, TYPE);
+    d += a * a;
+  }
+  if (has_behind) {
+    const double a = clip_value(p, behind, TYPE);
+    d += a * a;
+  }
+  return d;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ ClipTable<N> t) {
+  __shared__ double sh[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  double sum = 0.0;
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const ClipEntry& e = t.e[clip_entry(t, c)];
+    const int64_t i0 = static_cast<int64_t>(c - e.first) * kChunk;
+    const int64_t i1 = i0 + kChunk < e.numel ? i0 + kChunk : e.numel;
+    if (e.type == kClipF32)
+      sum += chunk_squares<kClipF32>(e.src, i0, i1);
+    else if (e.type == kClipF16)
+      sum += chunk_squares<kClipF16>(e.src, i0, i1);
+    else
+      sum += chunk_squares<kClipBf16>(e.src, i0, i1);
+  }
+  sum = block_sum(sum, sh);
+  if (threadIdx.x == 0) t.partial[t.slot0 + blockIdx.x] = sum;
+}
+
+template <int TYPE>
+DEVI uint4 scaled(uint4 v, float f) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = TYPE == kClipF32 ? __float_as_uint(__uint_as_float(w[j]) * f)
+                            : pack16<TYPE == kClipF16>(unpack16<TYPE == kClipF16>(w[j], 0) * f,
+                                                       unpack16<TYPE == kClipF16>(w[j], 1) * f);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int TYPE>
+DEVI void scale_single(const void* p, void* out, int64_t i, float f) {
+  const float v = clip_value(p, i, TYPE) * f;
+  if (TYPE == kClipF32)
+    static_cast<float*>(out)[i] = v;
+  else
+    static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack16<TYPE == kClipF16>(v, 0.0f) & 0xFFFFu);
+}
+
+template <int TYPE>
+DEVI void scale_chunk(const void* p, void* out, int64_t i0, int64_t i1, float f) {
+  constexpr int SIZE = TYPE == kClipF32 ? 4 : 2, PER = 16 / SIZE;
+  if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15u) != 0) {
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) scale_single<TYPE>(p, out, i, f);
+    return;
+  }
+  int64_t v0;
+  int groups;
+  clip_ranges(p, i0, i1, SIZE, v0, groups);
+  const int64_t tail = v0 + static_cast<int64_t>(groups) * PER;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + v0 * SIZE);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + v0 * SIZE);
+  constexpr int DEEP = 8;
+  int g = threadIdx.x;
+  for (; g + (DEEP - 1) * kThreads < groups; g += DEEP * kThreads) {
+    uint4 v[DEEP];
+#pragma unroll
+    for (int j = 0; j < DEEP; ++j) v[j] = src[g + j * kThreads];
+#pragma unroll
+    for (int j = 0; j < DEEP; ++j) dst[g + j * kThreads] = scaled<TYPE>(v[j], f);
+  }
+  for (; g < groups; g += kThreads) dst[g] = scaled<TYPE>(src[g], f);
+  if (i0 + threadIdx.x < v0) scale_single<TYPE>(p, out, i0 + threadIdx.x, f);
+  if (tail + threadIdx.x < i1) scale_single<TYPE>(p, out, tail + threadIdx.x, f);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipTable<N> t) {
+  __shared__ double sh[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < t.slots; i += kThreads) sum += t.partial[i];
+  const float norm = static_cast<float>(sqrt(block_sum(sum, sh)));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && t.slot0 == 0) *t.norm = norm;
+  if (!t.scale) return;
+  const float q = t.max_norm / (norm + 1e-6f);
+  const float f = q > 1.0f ? 1.0f : q;  // NaN stays
+  for (int c = t.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+    const ClipEntry& e = t.e[clip_entry(t, c)];
+    if (f == 1.0f && e.src == e.dst) continue;  // nothing changes
+    const int64_t i0 = static_cast<int64_t>(c - e.first) * kChunk;
+    const int64_t i1 = i0 + kChunk < e.numel ? i0 + kChunk : e.numel;
+    if (e.type == kClipF32)
+      scale_chunk<kClipF32>(e.src, e.dst, i0, i1, f);
+    else if (e.type == kClipF16)
+      scale_chunk<kClipF16>(e.src, e.dst, i0, i1, f);
+    else
+      scale_chunk<kClipBf16>(e.src, e.dst, i0, i1, f);
+  }
+}
+
+template <typename Kernel, typename Table>
+cudaError_t launch_clip(Kernel kernel, int grid, cudaStream_t st, const Table& t) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, t);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// One kernel of the pair for the entries [first, first + count) of the list.
+template <int N>
+cudaError_t run_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaStream_t st) {
+  static_assert(sizeof(ClipTable<N>) <= 32764, "kernel parameters");
+  ClipTable<N> t;
+  t.count = 0;
+  t.chunks = 0;
+  for (int i = g.first; i < g.end; ++i) {
+    ClipEntry e;
+    if (!clip_list_entry(a, i, e)) continue;
+    e.first = t.chunks;
+    t.chunks += static_cast<int>((e.numel + kChunk - 1) / kChunk);
+    t.e[t.count++] = e;
+  }
+  t.slot0 = g.slot0;
+  t.slots = a.slots;
+  t.partial = a.partial;
+  t.norm = a.norm;
+  t.max_norm = a.max_norm;
+  t.scale = a.scale;
+  if (second) return launch_clip(k_clip_scale<N>, a.scale && g.grid > 0 ? g.grid : 1, st, t);
+  return launch_clip(k_clip_norm<N>, g.grid, st, t);
+}
+
+}  // namespace
+
+cudaError_t launch_clip_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaStream_t st) {
+  const int n = g.end - g.first;  // short lists in a short table: the parameters are copied with every launch
+  if (n <= 64) return run_group<64>(a, g, second, st);
+  return run_group<kClipGroup>(a, g, second, st);
+}
+
+}  // namespace nvfp4

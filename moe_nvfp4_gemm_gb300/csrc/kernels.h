@@ -241,6 +241,73 @@ struct FfnGradArgs {
 };
 cudaError_t launch_ffn_grad(const FfnGradArgs& p, int sms, cudaStream_t st);
 
+// ---- 8-bit integers with a scale for each row ----------------------------------------------
+struct Int8QuantArgs {
+  const uint16_t* x;  // rows ldx apart
+  int64_t M, K, ldx;
+  uint8_t* q;         // [M, K]
+  float* s;           // [M]
+  int half;           // fp16 instead of bf16
+};
+enum { kInt8OutBf16 = 0, kInt8OutF32 = 1, kInt8OutF16 = 2 };
+struct Int8GemmArgs {
+  const float* sa;  // [M]
+  const float* sb;  // [N]
+  void* y;          // [M, N]
+  int64_t M, N, K;
+  int mt, nt;       // tiles: tokens, 256 channels
+  int split;        // pairs of a cluster, along K
+  int out;
+  int drop_stage;   // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
+  int32_t* status;
+  uint64_t watchdog_ns;  // limit of every pipeline wait
+};
+// tile_tokens 64 or 128: tmX over the codes [M, K], boxes of 128 x tile_tokens / 2; 256: over their fp16 values,
+// boxes of 64 x 128. tmW: boxes of 128 x 128.
+cudaError_t launch_int8_gemm(const CUtensorMap& tmW, const CUtensorMap& tmX, const Int8GemmArgs& p, int tile_tokens, int sms,
+                             cudaStream_t st);
+// n codes (a multiple of 16) to fp16
+cudaError_t launch_int8_widen(const uint8_t* a, void* out, int64_t n, int sms, cudaStream_t st);
+cudaError_t launch_int8_quantize(const Int8QuantArgs& p, int sms, cudaStream_t st);
+
+// ---- gradient norm and clipping -----------------------------------------------------------
+constexpr int kClipChunk = 16384;  // values that a block takes at a time
+constexpr int kClipGroup = 960;    // gradients a launch takes (its parameters hold the list)
+constexpr int kClipBlocks = 608;   // blocks of a launch at most: four on each SM
+enum { kClipBf16 = 0, kClipF32 = 1, kClipF16 = 2 };
+struct ClipEntry {
+  const void* src;
+  void* dst;
+  int64_t numel;
+  int first;  // its first chunk
+  int type;
+};
+struct ClipArgs {
+  const void* const* src;  // host arrays
+  void* const* dst;        // null: in place
+  const int64_t* numel;
+  const int32_t* types;
+  double* partial;         // a sum of squares for each block of the first kernels
+  float* norm;
+  int slots;               // of them
+  float max_norm;
+  int scale;               // also write the scaled gradients
+};
+struct ClipGroup {
+  int first, end;  // gradients of this launch
+  int slot0, grid;
+};
+// Entry i of the list; false where it has no values.
+inline bool clip_list_entry(const ClipArgs& a, int i, ClipEntry& e) {
+  e.src = a.src[i];
+  e.dst = a.dst ? a.dst[i] : const_cast<void*>(a.src[i]);
+  e.numel = a.numel[i];
+  e.type = a.types[i];
+  return e.numel > 0;
+}
+// `second`: the kernel that joins the sums and scales
+cudaError_t launch_clip_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaStream_t st);
+
 int stream_smem_bytes(int stages, int x_rows, int recv_bytes, bool sparse = false);
 // shared memory after the ring for one tile's token indices (and with qout the epilogue's
 // NVFP4 transpose tiles, 1 KB per epilogue warp)
