@@ -1294,8 +1294,11 @@ static int run_ffn_tile(FfnTileMaps& maps, FfnTileArgs& p, int mode, int sms, cu
   return from_cuda(launch_ffn_tile(maps, p, mode, sms, st));
 }
 
+// Few tokens: the weight-streaming kernel.
+static bool ffn_streams(int64_t M) { return M <= 64; }
+
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K) {
-  if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0) return 0;
+  if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0 || ffn_streams(M)) return 0;
   FfnTileArgs p = {};
   return ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
 }
@@ -1313,10 +1316,31 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
   if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || !aligned16(gate) || !aligned16(up) ||
       !aligned16(workspace))
     return NVFP4_ERR_ALIGNMENT;
+  DevInfo d;
+  if (ffn_streams(M)) {
+    if ((rc = device_info(d))) return rc;
+    FfnStreamArgs s = {h, gate, up, ldh, static_cast<int>(M), static_cast<int>(I), static_cast<int>((K + 63) / 64)};
+    // as many CTAs along K as fill the resident slots, with at least four blocks each
+    const int64_t tiles = (I + 63) / 64;
+    int64_t split = 2 * int64_t(d.sms) / tiles;
+    if (split > s.kblocks / 4) split = s.kblocks / 4;
+    s.split = static_cast<int>(split < 1 ? 1 : (split > 8 ? 8 : split));
+    s.act = activation;
+    s.half = type == NVFP4_F16;
+    s.l2_prefetch = stream_l2_prefetch(tiles * s.split, d.sms, 16384);
+    s.drop_stage = g_tune.withhold_stage;
+    s.status = dev_status;
+    s.watchdog_ns = watchdog_ns();
+    FfnStreamMaps maps;
+    if ((rc = encode_16(&maps.w[0], w_gate, I, K, ld_gate, 64)) || (rc = encode_16(&maps.w[1], w_up, I, K, ld_up, 64)) ||
+        (rc = encode_16(&maps.x, x, M, K, ldx, 32)))
+      return rc;
+    g_last_launches = 1;
+    return from_cuda(launch_ffn_stream(maps, s, static_cast<cudaStream_t>(stream)));
+  }
   FfnTileArgs p = {};
   const size_t need = ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
-  DevInfo d;
   rc = device_info(d);
   if (rc) return rc;
   FfnTileMaps maps;
@@ -1488,8 +1512,10 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
   const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt, kb = (K + 127) / 128;
-  p.split = 1;
-  while (p.split < 4 && tiles * p.split * 2 <= d.sms / 2 && kb >= p.split * 8) p.split *= 2;
+  // parts of K: as many as have a place, of at least four blocks of 128
+  int64_t split = d.sms / 2 / tiles;
+  if (split > kb / 4) split = kb / 4;
+  p.split = static_cast<int>(split < 1 ? 1 : (split > 4 ? 4 : split));
   CUtensorMap tmW, tmX;
   if ((rc = encode_2d(&tmW, reinterpret_cast<const uint8_t*>(b), N, K, 128))) return rc;
   if (tokens == 256) {

@@ -31,11 +31,16 @@ namespace {
 template <int NT>
 struct Int8Cfg {
   // warps 0-3: weights' producer, MMA issuer, two for the tokens (converters; with NT = 256 one loads them);
-  // warps 4-7: the weights' converters; warps 8-15: epilogue. 512 x 128 registers at launch.
+  // then one or two warpgroups that convert weights, two or one of epilogue warps. 512 x 128 registers at launch.
   static constexpr int THREADS = 512;
   static constexpr bool WIDE = NT == 256;  // tokens come as fp16
-  static constexpr int CONTROL_REGS = WIDE ? 72 : 112, EPILOGUE_REGS = WIDE ? 184 : 144;
-  static_assert(256 * CONTROL_REGS + 256 * EPILOGUE_REGS <= 512 * 128, "register shares");
+  // converting groups take blocks in turn. Few tokens: bound by the weights' bytes, which one group (a block of 16 KB
+  // in about 500 cycles) just keeps up with. With 256 tokens a block's MMAs take 1,024 cycles.
+  static constexpr int CONV_GROUPS = WIDE ? 1 : 2;
+  static constexpr int EPI_WARP = 4 + 4 * CONV_GROUPS;  // first epilogue warp
+  static constexpr int EPI_WARPS = 16 - EPI_WARP;
+  static constexpr int CONTROL_REGS = WIDE ? 72 : 96, EPILOGUE_REGS = WIDE ? 184 : 200;
+  static_assert(32 * EPI_WARP * CONTROL_REGS + 32 * EPI_WARPS * EPILOGUE_REGS <= 512 * 128, "register shares");
   static constexpr int XROWS = NT / 2;                  // token rows of a CTA
   static constexpr int W_BYTES = 128 * 128;             // 128 channels x 128 of K
   static constexpr int RAW_BYTES = W_BYTES + (WIDE ? 0 : XROWS * 128);
@@ -44,12 +49,14 @@ struct Int8Cfg {
   static constexpr int X_BYTES = XROWS * 256;           // two boxes of XROWS x 64 of K, fp16
   static constexpr int BUFS = WIDE ? 1 : 2;             // TMEM buffers of sums
   static constexpr int CHUNK = 8;                       // blocks of 128 between two readings of the sums
-  static constexpr int COLS = NT / 2;                   // tokens of an epilogue warp
-  static constexpr int OUT_BYTES = 8 * 4096;            // a box for each epilogue warp
+  static constexpr int COLS = NT * 4 / EPI_WARPS;       // tokens of an epilogue warp
+  static constexpr int OUT_BYTES = EPI_WARPS * 4096;            // a box for each epilogue warp
   static constexpr int SMEM_BYTES = RAW * RAW_BYTES + OPS * X_BYTES + OUT_BYTES + 1024 + 512;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  // the exchange of split sums, [part][own token][132] words, in the place of the operand rings
-  static constexpr int EXCHANGE_BYTES = NT * 132 * 4;
+  // The exchange of split sums, [part][own token][132] words, in the place of the operand rings. Tokens are owned in
+  // groups of eight.
+  __host__ __device__ static constexpr int own(int split) { return (NT / 8 + split - 1) / split * 8; }
+  static constexpr int EXCHANGE_BYTES = (4 * own(4) > 3 * own(3) ? 4 * own(4) : 3 * own(3)) * 132 * 4;
   static_assert(EXCHANGE_BYTES <= RAW * RAW_BYTES + OPS * X_BYTES, "exchange area");
 };
 
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
     }
     for (int b = 0; b < BUFS; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 16);  // one elected lane per epilogue warp, both CTAs
+      mbar_init(&tempty[b], 2 * C::EPI_WARPS);  // one elected lane per epilogue warp, both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -144,15 +151,26 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
   const int tiles = p.mt * p.nt;
   const int first = blockIdx.x / (2 * split), step = gridDim.x / (2 * split);
 
-  if (warp >= 8) {
+  if (warp >= C::EPI_WARP) {
     regs_inc<C::EPILOGUE_REGS>();
-    const int q = warp & 3, h = (warp - 8) >> 2;
-    uint8_t* box = out_buf + (warp - 8) * 4096;
+    const int q = warp & 3, h = (warp - C::EPI_WARP) >> 2;
+    uint8_t* box = out_buf + (warp - C::EPI_WARP) * 4096;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), lead);
     int buf = 0;
     uint32_t bph = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
+      const Int8Tile tl = int8_tile(p, t, NT);
+      const int own = C::own(split);  // split: tokens that this CTA stores
+      const int row0 = tl.m0 + (split > 1 ? part * own : h * C::COLS);
+      const int col0 = tl.n0 + static_cast<int>(rank) * 128 + q * 32;
+      // A lane holds the scales of tokens 32 c + lane of those that its warp stores, and of channel `lane` of the
+      // warp's 32: requested here, so that no load waits behind the sums.
+      constexpr int SA = NT / 32 < 4 ? NT / 32 : 4;
+      float sa[SA];
+#pragma unroll
+      for (int c = 0; c < SA; ++c) sa[c] = row0 + 32 * c + lane < M ? p.sa[row0 + 32 * c + lane] : 0.0f;
+      const float sb_lane = col0 + lane < N ? p.sb[col0 + lane] : 0.0f;
       // acc[32 c + 16 i + 4 g + 2 j + u]: channel 16 i + 8 j + lane / 4 of the warp's 32, token
       // 32 c + 8 g + 2 (lane % 4) + u of its COLS
       int acc[C::COLS];
@@ -183,11 +201,9 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
           bph ^= 1;
         }
       }
-      const Int8Tile tl = int8_tile(p, t, NT);
       if (split > 1) {
         // All roles of all the cluster's CTAs are done with the rings; also after an abort (then garbage, not
-        // stored), so that the cluster's barriers pair. CTA `part` of its half stores tokens [part, part + 1) NT / split.
-        const int own = NT / split;
+        // stored), so that the cluster's barriers pair. CTA `part` of its half stores tokens [part, part + 1) own.
         uint32_t* recv = reinterpret_cast<uint32_t*>(smem);
         __syncwarp();
         cluster_sync();
@@ -207,45 +223,46 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
         __syncwarp();
         cluster_sync();
         if (ok && !*abort_flag) {
-          const int ch = static_cast<int>(threadIdx.x) & 127;
-          const int n = tl.n0 + static_cast<int>(rank) * 128 + ch;
-          const float sb = n < N ? p.sb[n] : 0.0f;
-          for (int i = (static_cast<int>(threadIdx.x) - 256) >> 7; i < own; i += 2) {
-            const int m = tl.m0 + part * own + i;
-            if (m >= M) break;
-            uint32_t v = 0;
-            for (int s = 0; s < split; ++s) v += recv[(s * own + i) * 132 + ch];
-            const float f = static_cast<float>(static_cast<int>(v)) * p.sa[m] * sb;
-            const int64_t to = static_cast<int64_t>(m) * N + n;
-            if (n < N) {
-              if (OUT == kInt8OutF32)
-                static_cast<float*>(p.y)[to] = f;
-              else
-                static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack16<OUT == kInt8OutF16>(f, 0.0f) & 0xFFFFu);
+          // a lane: one channel; a warp: every other token where two have the same channels
+          const int n = col0 + lane;
+          constexpr int STEP = C::EPI_WARPS / 4;
+          const int rows = min(min(own, NT - part * own), M - row0);
+          const uint32_t* src = recv + q * 32 + lane;
+#pragma unroll
+          for (int c = 0; c < SA; ++c)
+#pragma unroll 4
+            for (int j = h; j < 32; j += STEP) {
+              const float sa_j = __shfl_sync(0xffffffffu, sa[c], j);
+              const int i = 32 * c + j;
+              if (i >= rows) break;
+              uint32_t v = 0;
+              for (int s = 0; s < split; ++s) v += src[(s * own + i) * 132];
+              const float f = static_cast<float>(static_cast<int>(v)) * sa_j * sb_lane;
+              const int64_t to = static_cast<int64_t>(row0 + i) * N + n;
+              if (n < N) {
+                if (OUT == kInt8OutF32)
+                  static_cast<float*>(p.y)[to] = f;
+                else
+                  static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack16<OUT == kInt8OutF16>(f, 0.0f) & 0xFFFFu);
+              }
             }
-          }
         }
         break;
       }
       if (!ok) break;
-      const int col0 = tl.n0 + static_cast<int>(rank) * 128 + q * 32;
       if (col0 < N) {
         float sb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = col0 + 8 * i + (lane >> 2);
-          sb[i] = n < N ? p.sb[n] : 0.0f;
-        }
+        for (int i = 0; i < 4; ++i) sb[i] = __shfl_sync(0xffffffffu, sb_lane, 8 * i + (lane >> 2));
         // 32 tokens x 32 channels at a time through the warp's box
 #pragma unroll
         for (int c = 0; c < C::COLS / 32; ++c) {
-          const int row0 = tl.m0 + h * C::COLS + 32 * c;
-          const int rows = min(32, M - row0);
+          const int rows = min(32, M - row0 - 32 * c);
           if (rows <= 0) continue;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int m = row0 + 8 * g + 2 * (lane & 3);
-            const float sa0 = m < M ? p.sa[m] : 0.0f, sa1 = m + 1 < M ? p.sa[m + 1] : 0.0f;
+            const float sa0 = __shfl_sync(0xffffffffu, sa[c], 8 * g + 2 * (lane & 3));
+            const float sa1 = __shfl_sync(0xffffffffu, sa[c], 8 * g + 2 * (lane & 3) + 1);
             float v[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -271,7 +288,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
             }
           }
           __syncwarp();
-          const int64_t at = static_cast<int64_t>(row0) * N + col0;
+          const int64_t at = static_cast<int64_t>(row0 + 32 * c) * N + col0;
           if (OUT == kInt8OutF32) {
             float* y = static_cast<float*>(p.y) + at;
             if (N % 4 == 0) {  // 16 bytes a lane, four tokens at a time
@@ -408,17 +425,19 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
       // converters: a lane takes a channel's 128 bytes (warps 4-7), or with the other token warp the
       // tokens', a row or half a row each
       const bool weights = warp >= 4;
-      const int q = warp & 3;
+      const int q = warp & 3, group = (warp - 4) >> 2;
       const uint32_t ofull_leader = mapa_shared(smem_u32(ofull), lead);
       int r = 0, s = 0;
-      uint32_t rph = 0, ph = 0;
+      uint32_t rph = 0, ph = 0, block = 0;
       for (int t = first; t < tiles && !*abort_flag; t += step) {
-        for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (!mbar_wait_warp(&rfull[r], rph, abort_flag, wd)) break;
-          if (!mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd)) break;
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++block) {
+          const bool turn = !weights || C::CONV_GROUPS == 1 || static_cast<int>(block & 1) == group;
+          if (turn && !mbar_wait_warp(&rfull[r], rph, abort_flag, wd)) break;
+          if (turn && !mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd)) break;
           tc_fence_after();
           const uint32_t raw = smem_u32(smem + r * C::RAW_BYTES);
-          if (weights) {
+          if (!turn) {
+          } else if (weights) {
             const int row = q * 32 + lane;
             const uint32_t src = raw + row * 128;
             const uint32_t dst = tmem + (static_cast<uint32_t>(q * 32) << 16) + 256 + s * 64;
@@ -461,7 +480,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
             fence_proxy_async_shared();
           }
           __syncwarp();
-          if (lane == 0) {
+          if (turn && lane == 0) {
             mbar_arrive(&rempty[r]);
             mbar_arrive_operands(ofull_leader + 8 * s);
           }
