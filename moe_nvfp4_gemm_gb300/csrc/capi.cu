@@ -1521,7 +1521,7 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
   if (tokens == 256) {
     if ((rc = from_cuda(launch_int8_widen(a8, workspace, M * K, d.sms, st)))) return rc;
     ++g_last_launches;
-    if ((rc = encode_16(&tmX, workspace, M, K, K, 128))) return rc;
+    if ((rc = encode_16(&tmX, workspace, M, K, K, 64))) return rc;
   } else if ((rc = encode_2d(&tmX, a8, M, K, tokens / 2))) {
     return rc;
   }

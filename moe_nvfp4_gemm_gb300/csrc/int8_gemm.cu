@@ -9,15 +9,16 @@
 // to the SM: a TMA ring brings blocks of 128 of K, and a warpgroup turns each channel's 128 bytes into
 // fp16 in registers (byte order 0x64uu is 1024 + u; u = b + 128; minus 1152) and stores them to TMEM, from
 // where the MMA takes its A operand: the fp16 weights never pass through shared memory, whose bandwidth
-// they would fill (four blocks of 64 columns). Tokens: up to 128 are converted by two warps into
-// the swizzled shared-memory tile that the MMA reads; tiles of 256 come as fp16 from the workspace, converted
-// once by k_int8_widen.
+// they would fill. Tokens: up to 128 are converted by the same warps into the swizzled shared-memory tile that the
+// MMA reads; tiles of 256 come as fp16 from the workspace, converted once by k_int8_widen.
 //
 // Few tiles: the pairs of a cluster (p.split of them) sum a tile's parts of K, exchange the integer sums through
 // distributed shared memory and store a share of the tokens each.
 #include <stdint.h>
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "ffn.cuh"
 #include "kernels.h"
@@ -30,34 +31,40 @@ namespace {
 
 template <int NT>
 struct Int8Cfg {
-  // warps 0-3: weights' producer, MMA issuer, two for the tokens (converters; with NT = 256 one loads them);
-  // then one or two warpgroups that convert weights, two or one of epilogue warps. 512 x 128 registers at launch.
+  // warps 0-3: producer of the 8-bit operands, MMA issuer, WIDE: the tokens' producer, idle; then one or two
+  // warpgroups that convert, two or one of epilogue warps. 512 x 128 registers at launch.
   static constexpr int THREADS = 512;
   static constexpr bool WIDE = NT == 256;  // tokens come as fp16
-  // converting groups take blocks in turn. Few tokens: bound by the weights' bytes, which one group (a block of 16 KB
-  // in about 500 cycles) just keeps up with. With 256 tokens a block's MMAs take 1,024 cycles.
+  // Converting groups take blocks in turn. Few tokens: bound by the weights' bytes, a block of 16 KB in about 700
+  // cycles; a group needs about 600 for the weights and up to 300 for the tokens. With 256 tokens a block's MMAs
+  // take 1,024 cycles and one group is enough.
   static constexpr int CONV_GROUPS = WIDE ? 1 : 2;
   static constexpr int EPI_WARP = 4 + 4 * CONV_GROUPS;  // first epilogue warp
   static constexpr int EPI_WARPS = 16 - EPI_WARP;
-  static constexpr int CONTROL_REGS = WIDE ? 72 : 96, EPILOGUE_REGS = WIDE ? 184 : 200;
+  static constexpr int CONTROL_REGS = WIDE ? 80 : 96, EPILOGUE_REGS = WIDE ? 176 : 200;
   static_assert(32 * EPI_WARP * CONTROL_REGS + 32 * EPI_WARPS * EPILOGUE_REGS <= 512 * 128, "register shares");
   static constexpr int XROWS = NT / 2;                  // token rows of a CTA
   static constexpr int W_BYTES = 128 * 128;             // 128 channels x 128 of K
   static constexpr int RAW_BYTES = W_BYTES + (WIDE ? 0 : XROWS * 128);
   static constexpr int RAW = WIDE ? 4 : (NT == 128 ? 5 : 7);  // stages of 8-bit operands
-  static constexpr int OPS = 4;                         // operand buffers: TMEM columns 256 + 64 i, X tile i
+  // TMEM: the sums, then A in OPS operand blocks of OP_K. Up to 128 tokens: two buffers of NT columns, a chunk each.
+  // 256: three slots of 128 columns; chunks take slots 0, 1 and 1, 2 in turn, the first half of the tokens in the
+  // lower one, so that a chunk's first blocks can be summed into the free slot while slot 1 is still read.
+  static constexpr int HALVES = WIDE ? 2 : 1, HALF = NT / HALVES, BUFS = WIDE ? 3 : 2;
+  static constexpr int OPS = WIDE ? 2 : 4, OP_K = 128, PER = 128 / OP_K;  // PER operand blocks to a block of 128
+  static constexpr int APART = WIDE ? 2 : 0;  // a chunk's first blocks, summed half by half
+  static constexpr int A_COL = BUFS * HALF;
+  static_assert(A_COL + OP_K / 2 * OPS <= 512 && APART * PER <= OPS, "TMEM columns");
+  static constexpr int XS = 4;                          // tokens' fp16 tiles of 128 of K
   static constexpr int X_BYTES = XROWS * 256;           // two boxes of XROWS x 64 of K, fp16
-  static constexpr int BUFS = WIDE ? 1 : 2;             // TMEM buffers of sums
   static constexpr int CHUNK = 8;                       // blocks of 128 between two readings of the sums
   static constexpr int COLS = NT * 4 / EPI_WARPS;       // tokens of an epilogue warp
-  static constexpr int OUT_BYTES = EPI_WARPS * 4096;            // a box for each epilogue warp
-  static constexpr int SMEM_BYTES = RAW * RAW_BYTES + OPS * X_BYTES + OUT_BYTES + 1024 + 512;
+  static constexpr int OUT_BYTES = EPI_WARPS * 4096;    // a box for each epilogue warp
+  static constexpr int SMEM_BYTES = RAW * RAW_BYTES + XS * X_BYTES + OUT_BYTES + 1024 + 512;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  // The exchange of split sums, [part][own token][132] words, in the place of the operand rings. Tokens are owned in
-  // groups of eight.
+  // Split sums: tokens that a CTA stores, in groups of eight; the area of a CTA's sums.
   __host__ __device__ static constexpr int own(int split) { return (NT / 8 + split - 1) / split * 8; }
-  static constexpr int EXCHANGE_BYTES = (4 * own(4) > 3 * own(3) ? 4 * own(4) : 3 * own(3)) * 132 * 4;
-  static_assert(EXCHANGE_BYTES <= RAW * RAW_BYTES + OPS * X_BYTES, "exchange area");
+  static_assert(NT * 132 * 4 <= RAW * RAW_BYTES + XS * X_BYTES, "exchange area");
 };
 
 struct Int8Tile {
@@ -91,17 +98,18 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
                 const __grid_constant__ Int8GemmArgs p) {
   using C = Int8Cfg<NT>;
   constexpr bool WIDE = C::WIDE;
-  constexpr int RAW = C::RAW, OPS = C::OPS, BUFS = C::BUFS;
+  constexpr int RAW = C::RAW, OPS = C::OPS, BUFS = C::BUFS, XS = C::XS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* x_buf = smem + RAW * C::RAW_BYTES;
-  uint8_t* out_buf = x_buf + OPS * C::X_BYTES;
+  uint8_t* out_buf = x_buf + XS * C::X_BYTES;
   uint64_t* rfull = reinterpret_cast<uint64_t*>(out_buf + C::OUT_BYTES);  // [RAW] 8-bit operands have landed
   uint64_t* rempty = rfull + RAW;                                         // [RAW] and have been read
-  uint64_t* ofull = rempty + RAW;   // [OPS] fp16 operands are in place (leader)
+  uint64_t* ofull = rempty + RAW;   // [OPS] converted operands are in place (leader)
   uint64_t* oempty = ofull + OPS;   // [OPS] and have been used
-  uint64_t* xfull = oempty + OPS;   // [OPS] WIDE: the tokens' tile has landed (leader)
-  uint64_t* tfull = xfull + OPS;    // [BUFS] a chunk's sums are complete
+  uint64_t* xfull = oempty + OPS;   // [XS] WIDE: the tokens' tile has landed (leader)
+  uint64_t* xempty = xfull + XS;    // [XS] and has been used
+  uint64_t* tfull = xempty + XS;    // [BUFS] a chunk's sums are complete
   uint64_t* tempty = tfull + BUFS;  // [BUFS] and have been read (leader)
   uint64_t* drain = tempty + BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -116,12 +124,15 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < RAW; ++s) {
       mbar_init(&rfull[s], 1);
-      mbar_init(&rempty[s], WIDE ? 4 : 6);  // the warps that read it
+      mbar_init(&rempty[s], 4);  // the converting group's warps
     }
     for (int s = 0; s < OPS; ++s) {
-      mbar_init(&ofull[s], WIDE ? 8 : 12);  // the converting warps of both CTAs
+      mbar_init(&ofull[s], 8);  // the converting groups' warps of both CTAs
       mbar_init(&oempty[s], 1);
+    }
+    for (int s = 0; s < XS; ++s) {
       mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], 1);
     }
     for (int b = 0; b < BUFS; ++b) {
       mbar_init(&tfull[b], 1);
@@ -156,94 +167,155 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
     const int q = warp & 3, h = (warp - C::EPI_WARP) >> 2;
     uint8_t* box = out_buf + (warp - C::EPI_WARP) * 4096;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), lead);
-    int buf = 0;
-    uint32_t bph = 0;
+    uint32_t chunk = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const Int8Tile tl = int8_tile(p, t, NT);
       const int own = C::own(split);  // split: tokens that this CTA stores
-      const int row0 = tl.m0 + (split > 1 ? part * own : h * C::COLS);
+      // first token: of the CTA's own after the exchange; of 32 tokens c of this warp
+      const int own0 = tl.m0 + part * own;
+      auto row_of = [&](int c) {
+        return tl.m0 + (WIDE ? (c >> 1) * 128 + h * 64 + (c & 1) * 32 : c * 32);
+      };
       const int col0 = tl.n0 + static_cast<int>(rank) * 128 + q * 32;
       // A lane holds the scales of tokens 32 c + lane of those that its warp stores, and of channel `lane` of the
       // warp's 32: requested here, so that no load waits behind the sums.
       constexpr int SA = NT / 32 < 4 ? NT / 32 : 4;
       float sa[SA];
 #pragma unroll
-      for (int c = 0; c < SA; ++c) sa[c] = row0 + 32 * c + lane < M ? p.sa[row0 + 32 * c + lane] : 0.0f;
+      for (int c = 0; c < SA; ++c) {
+        const int m = (split > 1 ? own0 + 32 * c : row_of(c)) + lane;
+        sa[c] = m < M ? p.sa[m] : 0.0f;
+      }
       const float sb_lane = col0 + lane < N ? p.sb[col0 + lane] : 0.0f;
+      float sb4[4] = {};  // split: of four of the CTA's 128
+      if (split > 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int n = tl.n0 + static_cast<int>(rank) * 128 + 4 * lane + k;
+          if (n < N) sb4[k] = p.sb[n];
+        }
+      }
       // acc[32 c + 16 i + 4 g + 2 j + u]: channel 16 i + 8 j + lane / 4 of the warp's 32, token
-      // 32 c + 8 g + 2 (lane % 4) + u of its COLS
+      // row_of(c) + 8 g + 2 (lane % 4) + u
       int acc[C::COLS];
 #pragma unroll
       for (int i = 0; i < C::COLS; ++i) acc[i] = 0;
+      constexpr int PARTS = C::COLS / 32 / C::HALVES;  // of 32 tokens in a buffer
 #pragma unroll 1
-      for (int kb = kb_begin; kb < kb_end; kb += C::CHUNK) {
-        ok = mbar_wait_warp(&tfull[buf], bph, abort_flag, wd);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + h * C::COLS;
+      for (int kb = kb_begin; kb < kb_end && ok; kb += C::CHUNK, ++chunk) {
+        // WIDE: slot 1 first, which the next chunk waits for: this one's second half, then (odd chunks) its first
+        auto read = [&](auto half_, int slot, uint32_t phase) {
+          constexpr int half = decltype(half_)::value;
+          if (!ok) return;
+          ok = mbar_wait_warp(&tfull[slot], phase, abort_flag, wd);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + slot * C::HALF + h * (32 * PARTS);
 #pragma unroll
-        for (int c = 0; c < C::COLS / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld_frag32(at + c * 32, r);
-          tmem_ld_frag32(at + c * 32 + (16u << 16), r + 16);
-          tmem_ld_wait32(r);
-          if (c + 1 == C::COLS / 32) {
-            tc_fence_before();
-            __syncwarp();
-            if (elect_one()) mbar_arrive_cluster(tempty_leader + 8 * buf);
+          for (int c = 0; c < PARTS; ++c) {
+            uint32_t r[32];
+            tmem_ld_frag32(at + c * 32, r);
+            tmem_ld_frag32(at + c * 32 + (16u << 16), r + 16);
+            tmem_ld_wait32(r);
+            if (c + 1 == PARTS) {
+              tc_fence_before();
+              __syncwarp();
+              if (elect_one()) mbar_arrive_cluster(tempty_leader + 8 * slot);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[32 * (half * PARTS + c) + j] += __float2int_rn(__uint_as_float(r[j]));
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[32 * c + j] += __float2int_rn(__uint_as_float(r[j]));
-        }
-        if (++buf == BUFS) {
-          buf = 0;
-          bph ^= 1;
+        };
+        constexpr std::integral_constant<int, 0> lower;
+        if constexpr (WIDE) {
+          constexpr std::integral_constant<int, 1> upper;
+          if ((chunk & 1) == 0) {
+            read(upper, 1, chunk & 1);
+            read(lower, 0, chunk >> 1 & 1);
+          } else {
+            read(lower, 1, chunk & 1);
+            read(upper, 2, chunk >> 1 & 1);
+          }
+        } else {
+          read(lower, chunk & 1, chunk >> 1 & 1);
         }
       }
       if (split > 1) {
-        // All roles of all the cluster's CTAs are done with the rings; also after an abort (then garbage, not
-        // stored), so that the cluster's barriers pair. CTA `part` of its half stores tokens [part, part + 1) own.
-        uint32_t* recv = reinterpret_cast<uint32_t*>(smem);
+        // Every CTA's sums go to its own shared memory, [token][132] in the place of the operand rings (its roles are
+        // done with them: the last tfull followed all MMAs, and those all loads), and each CTA then reads the parts of
+        // the tokens that it stores, [part, part + 1) own, from the others, a row of 128 channels at once. Also after an
+        // abort (then garbage, not stored), so that the cluster's barriers pair.
+        const uint32_t sums = smem_u32(smem);
         __syncwarp();
         cluster_sync();
 #pragma unroll
         for (int c = 0; c < C::COLS / 32; ++c)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int tok = h * C::COLS + 32 * c + 8 * g + 2 * (lane & 3);  // a group of 8 has one owner
-            const int o = tok / own;
-            const uint32_t dst = mapa_shared(smem_u32(recv + (part * own + tok - o * own) * 132 + q * 32 + (lane >> 2)), 2 * o + rank);
+            const int tok8 = row_of(c) - tl.m0 + 8 * g;
+            if (tl.m0 + tok8 >= M) continue;
+            const uint32_t at = sums + ((tok8 + 2 * (lane & 3)) * 132 + q * 32 + (lane >> 2)) * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int u = 0; u < 2; ++u)
-                st_shared_cluster_b32(dst + (u * 132 + 8 * i) * 4, acc[32 * c + 16 * (i >> 1) + 4 * g + 2 * (i & 1) + u]);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (u * 132 + 8 * i) * 4),
+                             "r"(acc[32 * c + 16 * (i >> 1) + 4 * g + 2 * (i & 1) + u])
+                             : "memory");
           }
         __syncwarp();
         cluster_sync();
         if (ok && !*abort_flag) {
-          // a lane: one channel; a warp: every other token where two have the same channels
-          const int n = col0 + lane;
-          constexpr int STEP = C::EPI_WARPS / 4;
-          const int rows = min(min(own, NT - part * own), M - row0);
-          const uint32_t* src = recv + q * 32 + lane;
+          // a lane: four channels; a warp: every EPI_WARPS-th token, four at a time with all their parts in flight
+          const int n = tl.n0 + static_cast<int>(rank) * 128 + 4 * lane;
+          const int rows = min(min(own, NT - part * own), M - own0);
+          uint32_t from[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) from[s] = mapa_shared(sums + (part * own * 132 + 4 * lane) * 4, 2 * min(s, split - 1) + rank);
+          const bool whole = N % 4 == 0 && n < N;  // 16 or 8 bytes at once
 #pragma unroll
           for (int c = 0; c < SA; ++c)
-#pragma unroll 4
-            for (int j = h; j < 32; j += STEP) {
-              const float sa_j = __shfl_sync(0xffffffffu, sa[c], j);
-              const int i = 32 * c + j;
-              if (i >= rows) break;
-              uint32_t v = 0;
-              for (int s = 0; s < split; ++s) v += src[(s * own + i) * 132];
-              const float f = static_cast<float>(static_cast<int>(v)) * sa_j * sb_lane;
-              const int64_t to = static_cast<int64_t>(row0 + i) * N + n;
-              if (n < N) {
-                if (OUT == kInt8OutF32)
-                  static_cast<float*>(p.y)[to] = f;
-                else
-                  static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack16<OUT == kInt8OutF16>(f, 0.0f) & 0xFFFFu);
+#pragma unroll 1
+            for (int j0 = warp - C::EPI_WARP; j0 < 32; j0 += 4 * C::EPI_WARPS) {
+              if (32 * c + j0 >= rows) break;
+              int4 v[4][4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                  // (a row past the last is read inside the tile and not stored)
+                  v[j][s] = make_int4(0, 0, 0, 0);
+                  if (s < split) v[j][s] = ld_shared_cluster_v4(from[s] + min(32 * c + j0 + j * C::EPI_WARPS, rows - 1) * (132 * 4));
+                }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float sa_j = __shfl_sync(0xffffffffu, sa[c], j0 + j * C::EPI_WARPS);
+                const int i = 32 * c + j0 + j * C::EPI_WARPS;
+                const float f[4] = {static_cast<float>(v[j][0].x + v[j][1].x + v[j][2].x + v[j][3].x) * sa_j * sb4[0],
+                                    static_cast<float>(v[j][0].y + v[j][1].y + v[j][2].y + v[j][3].y) * sa_j * sb4[1],
+                                    static_cast<float>(v[j][0].z + v[j][1].z + v[j][2].z + v[j][3].z) * sa_j * sb4[2],
+                                    static_cast<float>(v[j][0].w + v[j][1].w + v[j][2].w + v[j][3].w) * sa_j * sb4[3]};
+                if (i >= rows) continue;
+                const int64_t to = static_cast<int64_t>(own0 + i) * N + n;
+                if (OUT == kInt8OutF32) {
+                  float* y = static_cast<float*>(p.y) + to;
+                  if (whole)
+                    *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
+                  else
+                    for (int k = 0; k < 4; ++k)
+                      if (n + k < N) y[k] = f[k];
+                } else {
+                  constexpr bool H = OUT == kInt8OutF16;
+                  uint16_t* y = static_cast<uint16_t*>(p.y) + to;
+                  const uint2 w = make_uint2(pack16<H>(f[0], f[1]), pack16<H>(f[2], f[3]));
+                  if (whole) {
+                    *reinterpret_cast<uint2*>(y) = w;
+                  } else {
+                    for (int k = 0; k < 4; ++k)
+                      if (n + k < N) y[k] = static_cast<uint16_t>((k < 2 ? w.x : w.y) >> (k & 1 ? 16 : 0));
+                  }
+                }
               }
             }
         }
@@ -257,7 +329,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
         // 32 tokens x 32 channels at a time through the warp's box
 #pragma unroll
         for (int c = 0; c < C::COLS / 32; ++c) {
-          const int rows = min(32, M - row0 - 32 * c);
+          const int row0 = row_of(c), rows = min(32, M - row0);
           if (rows <= 0) continue;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -288,7 +360,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
             }
           }
           __syncwarp();
-          const int64_t at = static_cast<int64_t>(row0 + 32 * c) * N + col0;
+          const int64_t at = static_cast<int64_t>(row0) * N + col0;
           if (OUT == kInt8OutF32) {
             float* y = static_cast<float*>(p.y) + at;
             if (N % 4 == 0) {  // 16 bytes a lane, four tokens at a time
@@ -354,35 +426,70 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
         }
     } else if (warp == 1) {
       if (leader) {
-        const uint32_t idesc = idesc_f16(256, NT, false);
-        int s = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
+        int s = 0, x = 0;
+        uint32_t ph = 0, xph = 0, chunk = 0;
         for (int t = first; t < tiles && !*abort_flag; t += step) {
-          for (int kb = kb_begin; kb < kb_end; ++kb) {
-            const int in_chunk = (kb - kb_begin) % C::CHUNK;
-            if (!mbar_wait_warp(&ofull[s], ph, abort_flag, wd)) break;
-            if (WIDE && !mbar_wait_warp(&xfull[s], ph, abort_flag, wd)) break;
-            if (in_chunk == 0 && !mbar_wait_warp(&tempty[buf], bph ^ 1, abort_flag, wd)) break;
-            tc_fence_after();
-            const bool last = in_chunk == C::CHUNK - 1 || kb + 1 == kb_end;
-            if (elect_one()) {
-              const uint32_t xa = smem_u32(x_buf + s * C::X_BYTES);
+          for (int ob = kb_begin * C::PER; ob < kb_end * C::PER;) {
+            const int in_chunk = (ob - kb_begin * C::PER) % (C::CHUNK * C::PER);
+            // WIDE: a chunk's first operand blocks are summed half by half, the one in the free slot first, so that
+            // slot 1, which may still be read, is needed 1,024 cycles later; the others both halves at once.
+            const bool apart = WIDE && in_chunk == 0;
+            const int n = apart ? min(C::APART * C::PER, kb_end * C::PER - ob) : 1;
+            const int low = static_cast<int>(chunk & 1);  // slot of the first column
+            const uint32_t idesc = idesc_f16(256, apart ? C::HALF : NT, false);
+            bool go = true;
+            int bs = s, bx = x;
+            uint32_t bsph = ph, bxph = xph;
+            for (int pass = 0; pass < (apart ? 2 : 1) && go; ++pass) {
+              // apart: the half in slot 0 or 2, then the other in slot 1
+              const int half = apart ? (pass == 0 ? low : low ^ 1) : 0;
+              if (in_chunk == 0) {
+                const int slot = low + half;
+                const uint32_t use = WIDE && slot == 1 ? chunk : chunk >> 1;  // uses of this slot before
+                go = mbar_wait_warp(&tempty[slot], (use & 1) ^ 1, abort_flag, wd);
+              }
+              bs = s, bx = x, bsph = ph, bxph = xph;
+              for (int b = 0; b < n && go; ++b) {
+                const int in_block = (ob + b) % C::PER;
+                if (pass == 0) {
+                  go = mbar_wait_warp(&ofull[bs], bsph, abort_flag, wd);
+                  if (WIDE && in_block == 0) go = go && mbar_wait_warp(&xfull[bx], bxph, abort_flag, wd);
+                  if (!go) break;
+                }
+                tc_fence_after();
+                const bool last = in_chunk + b == C::CHUNK * C::PER - 1 || ob + b + 1 == kb_end * C::PER;
+                if (elect_one()) {
+                  // rows of this half in each CTA's tile: the MMA's N is split between the CTAs
+                  const uint32_t xa = smem_u32(x_buf + bx * C::X_BYTES) + half * (C::HALF / 2) * 128 + in_block * (C::X_BYTES / 2);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16_pair_ts(tmem + buf * NT, tmem + 256 + s * 64 + kk * 8,
-                                   desc_sw128(xa + (kk >> 2) * (C::X_BYTES / 2)) + 2 * (kk & 3), idesc, in_chunk != 0 || kk != 0);
-              tc_commit_pair(&oempty[s], 3u << lead);
-              if (last) tc_commit_pair(&tfull[buf], 3u << lead);
+                  for (int kk = 0; kk < C::OP_K / 16; ++kk)
+                    tc_mma_f16_pair_ts(tmem + (low + half) * C::HALF, tmem + C::A_COL + bs * (C::OP_K / 2) + kk * 8,
+                                       desc_sw128(xa + (kk >> 2) * (C::X_BYTES / 2)) + 2 * (kk & 3), idesc,
+                                       in_chunk + b != 0 || kk != 0);
+                  if (!apart || pass == 1) {
+                    tc_commit_pair(&oempty[bs], 3u << lead);
+                    if (WIDE && in_block == C::PER - 1) tc_commit_pair(&xempty[bx], 3u << lead);
+                    if (last) {
+                      tc_commit_pair(&tfull[low], 3u << lead);
+                      if (WIDE) tc_commit_pair(&tfull[low + 1], 3u << lead);
+                    }
+                  }
+                }
+                __syncwarp();
+                if (++bs == OPS) {
+                  bs = 0;
+                  bsph ^= 1;
+                }
+                if (in_block == C::PER - 1 && ++bx == XS) {
+                  bx = 0;
+                  bxph ^= 1;
+                }
+              }
             }
-            __syncwarp();
-            if (++s == OPS) {
-              s = 0;
-              ph ^= 1;
-            }
-            if (last && ++buf == BUFS) {
-              buf = 0;
-              bph ^= 1;
-            }
+            if (!go) break;
+            s = bs, x = bx, ph = bsph, xph = bxph;
+            ob += n;
+            if (in_chunk + n == C::CHUNK * C::PER || ob == kb_end * C::PER) ++chunk;
           }
         }
         if (elect_one()) tc_commit_pair(drain, 1u << lead);
@@ -398,51 +505,56 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
       for (int t = first; t < tiles && !*abort_flag; t += step) {
         const Int8Tile tl = int8_tile(p, t, NT);
         for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (!mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd)) break;
+          if (!mbar_wait_warp(&xempty[s], ph ^ 1, abort_flag, wd)) break;
           if (elect_one()) {
             uint8_t* st = x_buf + s * C::X_BYTES;
             const uint32_t bar = mapa_shared(smem_u32(&xfull[s]), lead);
             if (leader) mbar_arrive_expect_tx(&xfull[s], 2 * C::X_BYTES);
-            tma_load_2d_pair(st, &tmX, bar, kb * 128, tl.m0 + rank * C::XROWS, pol);
-            tma_load_2d_pair(st + C::X_BYTES / 2, &tmX, bar, kb * 128 + 64, tl.m0 + rank * C::XROWS, pol);
+            // [64 of K][two boxes of 64 tokens]. The MMA takes the even CTA's rows as its first columns: 128 of 256,
+            // or 64 of 128 where the halves are summed apart.
+            const bool apart = (kb - kb_begin) % C::CHUNK < C::APART;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tma_load_2d_pair(st + i * (C::X_BYTES / 4), &tmX, bar, kb * 128 + (i >> 1) * 64,
+                               tl.m0 + (apart ? (i & 1) * 128 + static_cast<int>(rank) * 64 : static_cast<int>(rank) * 128 + (i & 1) * 64),
+                               pol);
           }
           __syncwarp();
           used |= 1u << s;
           phases = (phases & ~(1u << s)) | ph << s;
-          if (++s == OPS) {
+          if (++s == XS) {
             s = 0;
             ph ^= 1;
           }
         }
       }
       if (leader)  // its barriers count both CTAs' bytes: let them all land
-        for (int i = 0; i < OPS; ++i)
+        for (int i = 0; i < XS; ++i)
           if (used >> i & 1) {
             volatile int32_t dummy = 0;
             mbar_wait_warp(&xfull[i], phases >> i & 1, &dummy, wd);
           }
-    } else if (warp >= 4 || !WIDE) {
-      // converters: a lane takes a channel's 128 bytes (warps 4-7), or with the other token warp the
-      // tokens', a row or half a row each
-      const bool weights = warp >= 4;
+    } else if (warp >= 4) {
+      // converters: a lane takes a channel's 128 bytes, then its share of the tokens
       const int q = warp & 3, group = (warp - 4) >> 2;
       const uint32_t ofull_leader = mapa_shared(smem_u32(ofull), lead);
       int r = 0, s = 0;
       uint32_t rph = 0, ph = 0, block = 0;
       for (int t = first; t < tiles && !*abort_flag; t += step) {
         for (int kb = kb_begin; kb < kb_end; ++kb, ++block) {
-          const bool turn = !weights || C::CONV_GROUPS == 1 || static_cast<int>(block & 1) == group;
-          if (turn && !mbar_wait_warp(&rfull[r], rph, abort_flag, wd)) break;
-          if (turn && !mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd)) break;
-          tc_fence_after();
-          const uint32_t raw = smem_u32(smem + r * C::RAW_BYTES);
-          if (!turn) {
-          } else if (weights) {
+          if (C::CONV_GROUPS == 1 || static_cast<int>(block & 1) == group) {
+            if (!mbar_wait_warp(&rfull[r], rph, abort_flag, wd)) break;
+            const uint32_t raw = smem_u32(smem + r * C::RAW_BYTES);
             const int row = q * 32 + lane;
             const uint32_t src = raw + row * 128;
-            const uint32_t dst = tmem + (static_cast<uint32_t>(q * 32) << 16) + 256 + s * 64;
+            bool go = true;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+              if (half == 0 || C::PER == 2) {
+                go = mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd);
+                if (!go) break;
+                tc_fence_after();
+              }
               uint32_t v[32];
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -452,43 +564,60 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
                 widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
                 widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
               }
-              tmem_st32(dst + half * 32, v);
+              tmem_st32(tmem + (static_cast<uint32_t>(q * 32) << 16) + C::A_COL + s * (C::OP_K / 2) + (C::PER == 2 ? 0 : half * 32), v);
+              if (C::PER == 2) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                  if (half == 1) mbar_arrive(&rempty[r]);
+                  mbar_arrive_operands(ofull_leader + 8 * s);
+                }
+                if (++s == OPS) {
+                  s = 0;
+                  ph ^= 1;
+                }
+              }
             }
-            tmem_st_wait();
-            tc_fence_before();
-          } else {
-            // 16-byte pieces of the XROWS x 128 bytes: piece c of row i becomes two of the fp16 tile, whose two
-            // boxes hold 64 of K each
-            const uint32_t src = raw + C::W_BYTES, dst = smem_u32(x_buf + s * C::X_BYTES);
-#pragma unroll 4
-            for (int i = (warp - 2) * 32 + lane; i < C::XROWS * 8; i += 64) {
-              const int row = i >> 3, c = i & 7;
-              const uint4 w = ld_shared_v4(src + row * 128 + ((c ^ (row & 7)) << 4));
-              uint32_t v[8];
-              widen4(w.x, v[0], v[1]);
-              widen4(w.y, v[2], v[3]);
-              widen4(w.z, v[4], v[5]);
-              widen4(w.w, v[6], v[7]);
-              const uint32_t to = dst + (c >> 2) * (C::X_BYTES / 2) + row * 128;
-              const int piece = 2 * (c & 3);
+            if (!go) break;
+            if (!WIDE) {
+              // 16-byte pieces of the XROWS x 128 bytes: piece c of row i becomes two of the fp16 tile, whose two
+              // boxes hold 64 of K each
+              const uint32_t xsrc = raw + C::W_BYTES, xdst = smem_u32(x_buf + s * C::X_BYTES);
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((piece + k) ^ (row & 7)) << 4)),
-                             "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
-                             : "memory");
+              for (int i = q * 32 + lane; i < C::XROWS * 8; i += 128) {
+                const int xrow = i >> 3, c = i & 7;
+                const uint4 w = ld_shared_v4(xsrc + xrow * 128 + ((c ^ (xrow & 7)) << 4));
+                uint32_t v[8];
+                widen4(w.x, v[0], v[1]);
+                widen4(w.y, v[2], v[3]);
+                widen4(w.z, v[4], v[5]);
+                widen4(w.w, v[6], v[7]);
+                const uint32_t to = xdst + (c >> 2) * (C::X_BYTES / 2) + xrow * 128;
+                const int piece = 2 * (c & 3);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((piece + k) ^ (xrow & 7)) << 4)),
+                               "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                               : "memory");
+              }
+              fence_proxy_async_shared();
             }
-            fence_proxy_async_shared();
-          }
-          __syncwarp();
-          if (turn && lane == 0) {
-            mbar_arrive(&rempty[r]);
-            mbar_arrive_operands(ofull_leader + 8 * s);
+            if (C::PER == 1) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&rempty[r]);
+                mbar_arrive_operands(ofull_leader + 8 * s);
+              }
+            }
           }
           if (++r == RAW) {
             r = 0;
             rph ^= 1;
           }
-          if (++s == OPS) {
+          if (C::PER == 1 && ++s == OPS) {
             s = 0;
             ph ^= 1;
           }

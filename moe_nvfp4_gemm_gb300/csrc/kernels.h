@@ -283,7 +283,7 @@ struct Int8GemmArgs {
   uint64_t watchdog_ns;  // limit of every pipeline wait
 };
 // tile_tokens 64 or 128: tmX over the codes [M, K], boxes of 128 x tile_tokens / 2; 256: over their fp16 values,
-// boxes of 64 x 128. tmW: boxes of 128 x 128.
+// boxes of 64 x 64. tmW: boxes of 128 x 128.
 cudaError_t launch_int8_gemm(const CUtensorMap& tmW, const CUtensorMap& tmX, const Int8GemmArgs& p, int tile_tokens, int sms,
                              cudaStream_t st);
 // n codes (a multiple of 16) to fp16

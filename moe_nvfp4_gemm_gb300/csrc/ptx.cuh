@@ -299,9 +299,11 @@ DEVI void mbar_arrive_operands(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Four bytes into any CTA's shared memory of the cluster.
-DEVI void st_shared_cluster_b32(uint32_t cluster_addr, int v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+// Sixteen bytes from any CTA's shared memory of the cluster.
+DEVI int4 ld_shared_cluster_v4(uint32_t cluster_addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(cluster_addr) : "memory");
+  return v;
 }
 
 // 2-D tiled TMA load issued for a CTA pair: lands in this CTA's shared memory and
