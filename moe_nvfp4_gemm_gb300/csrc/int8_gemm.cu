@@ -47,14 +47,16 @@ struct Int8Cfg {
   static constexpr int W_BYTES = 128 * 128;             // 128 channels x 128 of K
   static constexpr int RAW_BYTES = W_BYTES + (WIDE ? 0 : XROWS * 128);
   static constexpr int RAW = WIDE ? 4 : (NT == 128 ? 5 : 7);  // stages of 8-bit operands
-  // TMEM: the sums, then A in OPS operand blocks of OP_K. Up to 128 tokens: two buffers of NT columns, a chunk each.
+  // TMEM: the sums, then A in OPS operand blocks of 128 of K (64 columns). Up to 128 tokens: two buffers of NT columns, a chunk each.
   // 256: three slots of 128 columns; chunks take slots 0, 1 and 1, 2 in turn, the first half of the tokens in the
   // lower one, so that a chunk's first blocks can be summed into the free slot while slot 1 is still read.
   static constexpr int HALVES = WIDE ? 2 : 1, HALF = NT / HALVES, BUFS = WIDE ? 3 : 2;
-  static constexpr int OPS = WIDE ? 2 : 4, OP_K = 128, PER = 128 / OP_K;  // PER operand blocks to a block of 128
+  // (Operand blocks of 64 of K in WIDE, four of them, made prefill 1,550 us instead of 1,000: a block's hand-overs
+  // between converter and MMA cost as much as those of a block of 128.)
+  static constexpr int OPS = WIDE ? 2 : 4;
   static constexpr int APART = WIDE ? 2 : 0;  // a chunk's first blocks, summed half by half
   static constexpr int A_COL = BUFS * HALF;
-  static_assert(A_COL + OP_K / 2 * OPS <= 512 && APART * PER <= OPS, "TMEM columns");
+  static_assert(A_COL + 64 * OPS <= 512 && APART <= OPS, "TMEM columns");
   static constexpr int XS = 4;                          // tokens' fp16 tiles of 128 of K
   static constexpr int X_BYTES = XROWS * 256;           // two boxes of XROWS x 64 of K, fp16
   static constexpr int CHUNK = 8;                       // blocks of 128 between two readings of the sums
@@ -428,13 +430,47 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
       if (leader) {
         int s = 0, x = 0;
         uint32_t ph = 0, xph = 0, chunk = 0;
+        if constexpr (!WIDE) {
+          // A block's MMAs take 256 to 512 cycles: the loop around them is kept short.
+          constexpr uint32_t idesc = idesc_f16(256, NT, false);
+          const uint64_t xdesc = desc_sw128(smem_u32(x_buf));
+          const uint32_t a_tmem = tmem + C::A_COL;
+          for (int t = first; t < tiles && !*abort_flag; t += step) {
+            int left = C::CHUNK;  // blocks of this chunk
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
+              const uint32_t slot = chunk & 1;
+              if (!mbar_wait_warp(&ofull[s], ph, abort_flag, wd)) break;
+              if (left == C::CHUNK && !mbar_wait_warp(&tempty[slot], (chunk >> 1 & 1) ^ 1, abort_flag, wd)) break;
+              tc_fence_after();
+              const bool last = left == 1 || kb + 1 == kb_end;
+              if (elect_one()) {
+                const uint64_t xd = xdesc + static_cast<uint32_t>(s * (C::X_BYTES >> 4));
+                const uint32_t at = a_tmem + s * 64, dt = tmem + slot * NT;
+                const uint32_t more = left != C::CHUNK;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  tc_mma_f16_pair_ts(dt, at + kk * 8, xd + ((kk >> 2) * (C::X_BYTES >> 5) + 2 * (kk & 3)), idesc, kk == 0 ? more : 1);
+                tc_commit_pair(&oempty[s], 3u << lead);
+                if (last) tc_commit_pair(&tfull[slot], 3u << lead);
+              }
+              __syncwarp();
+              s = (s + 1) & (OPS - 1);
+              ph ^= s == 0;
+              --left;
+              if (last) {
+                left = C::CHUNK;
+                ++chunk;
+              }
+            }
+          }
+        } else
         for (int t = first; t < tiles && !*abort_flag; t += step) {
-          for (int ob = kb_begin * C::PER; ob < kb_end * C::PER;) {
-            const int in_chunk = (ob - kb_begin * C::PER) % (C::CHUNK * C::PER);
-            // WIDE: a chunk's first operand blocks are summed half by half, the one in the free slot first, so that
+          for (int kb = kb_begin; kb < kb_end;) {
+            const int in_chunk = (kb - kb_begin) % C::CHUNK;
+            // a chunk's first operand blocks are summed half by half, the one in the free slot first, so that
             // slot 1, which may still be read, is needed 1,024 cycles later; the others both halves at once.
-            const bool apart = WIDE && in_chunk == 0;
-            const int n = apart ? min(C::APART * C::PER, kb_end * C::PER - ob) : 1;
+            const bool apart = in_chunk == 0;
+            const int n = apart ? min(C::APART, kb_end - kb) : 1;
             const int low = static_cast<int>(chunk & 1);  // slot of the first column
             const uint32_t idesc = idesc_f16(256, apart ? C::HALF : NT, false);
             bool go = true;
@@ -445,33 +481,32 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
               const int half = apart ? (pass == 0 ? low : low ^ 1) : 0;
               if (in_chunk == 0) {
                 const int slot = low + half;
-                const uint32_t use = WIDE && slot == 1 ? chunk : chunk >> 1;  // uses of this slot before
+                const uint32_t use = slot == 1 ? chunk : chunk >> 1;  // uses of this slot before
                 go = mbar_wait_warp(&tempty[slot], (use & 1) ^ 1, abort_flag, wd);
               }
               bs = s, bx = x, bsph = ph, bxph = xph;
               for (int b = 0; b < n && go; ++b) {
-                const int in_block = (ob + b) % C::PER;
                 if (pass == 0) {
                   go = mbar_wait_warp(&ofull[bs], bsph, abort_flag, wd);
-                  if (WIDE && in_block == 0) go = go && mbar_wait_warp(&xfull[bx], bxph, abort_flag, wd);
+                  go = go && mbar_wait_warp(&xfull[bx], bxph, abort_flag, wd);
                   if (!go) break;
                 }
                 tc_fence_after();
-                const bool last = in_chunk + b == C::CHUNK * C::PER - 1 || ob + b + 1 == kb_end * C::PER;
+                const bool last = in_chunk + b == C::CHUNK - 1 || kb + b + 1 == kb_end;
                 if (elect_one()) {
                   // rows of this half in each CTA's tile: the MMA's N is split between the CTAs
-                  const uint32_t xa = smem_u32(x_buf + bx * C::X_BYTES) + half * (C::HALF / 2) * 128 + in_block * (C::X_BYTES / 2);
+                  const uint32_t xa = smem_u32(x_buf + bx * C::X_BYTES) + half * (C::HALF / 2) * 128;
 #pragma unroll
-                  for (int kk = 0; kk < C::OP_K / 16; ++kk)
-                    tc_mma_f16_pair_ts(tmem + (low + half) * C::HALF, tmem + C::A_COL + bs * (C::OP_K / 2) + kk * 8,
+                  for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_f16_pair_ts(tmem + (low + half) * C::HALF, tmem + C::A_COL + bs * 64 + kk * 8,
                                        desc_sw128(xa + (kk >> 2) * (C::X_BYTES / 2)) + 2 * (kk & 3), idesc,
                                        in_chunk + b != 0 || kk != 0);
                   if (!apart || pass == 1) {
                     tc_commit_pair(&oempty[bs], 3u << lead);
-                    if (WIDE && in_block == C::PER - 1) tc_commit_pair(&xempty[bx], 3u << lead);
+                    tc_commit_pair(&xempty[bx], 3u << lead);
                     if (last) {
                       tc_commit_pair(&tfull[low], 3u << lead);
-                      if (WIDE) tc_commit_pair(&tfull[low + 1], 3u << lead);
+                      tc_commit_pair(&tfull[low + 1], 3u << lead);
                     }
                   }
                 }
@@ -480,7 +515,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
                   bs = 0;
                   bsph ^= 1;
                 }
-                if (in_block == C::PER - 1 && ++bx == XS) {
+                if (++bx == XS) {
                   bx = 0;
                   bxph ^= 1;
                 }
@@ -488,8 +523,8 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
             }
             if (!go) break;
             s = bs, x = bx, ph = bsph, xph = bxph;
-            ob += n;
-            if (in_chunk + n == C::CHUNK * C::PER || ob == kb_end * C::PER) ++chunk;
+            kb += n;
+            if (in_chunk + n == C::CHUNK || kb == kb_end) ++chunk;
           }
         }
         if (elect_one()) tc_commit_pair(drain, 1u << lead);
@@ -538,89 +573,71 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
       // converters: a lane takes a channel's 128 bytes, then its share of the tokens
       const int q = warp & 3, group = (warp - 4) >> 2;
       const uint32_t ofull_leader = mapa_shared(smem_u32(ofull), lead);
-      int r = 0, s = 0;
-      uint32_t rph = 0, ph = 0, block = 0;
-      for (int t = first; t < tiles && !*abort_flag; t += step) {
-        for (int kb = kb_begin; kb < kb_end; ++kb, ++block) {
-          if (C::CONV_GROUPS == 1 || static_cast<int>(block & 1) == group) {
-            if (!mbar_wait_warp(&rfull[r], rph, abort_flag, wd)) break;
-            const uint32_t raw = smem_u32(smem + r * C::RAW_BYTES);
-            const int row = q * 32 + lane;
-            const uint32_t src = raw + row * 128;
-            bool go = true;
+      // this group's blocks of all of the pair's tiles, one after the other
+      const int blocks = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb_end - kb_begin) : 0;
+      int r = group, s = group;
+      uint32_t rph = 0, ph = 0;
+      const int row = q * 32 + lane;
+      // token rows that exist (one tile: the others' columns are never stored)
+      const int xrows = p.mt == 1 ? min(C::XROWS, max(0, M - static_cast<int>(rank) * C::XROWS)) : C::XROWS;
+      for (int block = group; block < blocks; block += C::CONV_GROUPS) {
+        if (!mbar_wait_warp(&rfull[r], rph, abort_flag, wd)) break;
+        if (!mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd)) break;
+        tc_fence_after();
+        const uint32_t raw = smem_u32(smem + r * C::RAW_BYTES);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (half == 0 || C::PER == 2) {
-                go = mbar_wait_warp(&oempty[s], ph ^ 1, abort_flag, wd);
-                if (!go) break;
-                tc_fence_after();
-              }
-              uint32_t v[32];
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[32];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 w = ld_shared_v4(src + (((half * 4 + c) ^ (row & 7)) << 4));
-                widen4(w.x, v[8 * c], v[8 * c + 1]);
-                widen4(w.y, v[8 * c + 2], v[8 * c + 3]);
-                widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
-                widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
-              }
-              tmem_st32(tmem + (static_cast<uint32_t>(q * 32) << 16) + C::A_COL + s * (C::OP_K / 2) + (C::PER == 2 ? 0 : half * 32), v);
-              if (C::PER == 2) {
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                  if (half == 1) mbar_arrive(&rempty[r]);
-                  mbar_arrive_operands(ofull_leader + 8 * s);
-                }
-                if (++s == OPS) {
-                  s = 0;
-                  ph ^= 1;
-                }
-              }
-            }
-            if (!go) break;
-            if (!WIDE) {
-              // 16-byte pieces of the XROWS x 128 bytes: piece c of row i becomes two of the fp16 tile, whose two
-              // boxes hold 64 of K each
-              const uint32_t xsrc = raw + C::W_BYTES, xdst = smem_u32(x_buf + s * C::X_BYTES);
-#pragma unroll
-              for (int i = q * 32 + lane; i < C::XROWS * 8; i += 128) {
-                const int xrow = i >> 3, c = i & 7;
-                const uint4 w = ld_shared_v4(xsrc + xrow * 128 + ((c ^ (xrow & 7)) << 4));
-                uint32_t v[8];
-                widen4(w.x, v[0], v[1]);
-                widen4(w.y, v[2], v[3]);
-                widen4(w.z, v[4], v[5]);
-                widen4(w.w, v[6], v[7]);
-                const uint32_t to = xdst + (c >> 2) * (C::X_BYTES / 2) + xrow * 128;
-                const int piece = 2 * (c & 3);
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((piece + k) ^ (xrow & 7)) << 4)),
-                               "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
-                               : "memory");
-              }
-              fence_proxy_async_shared();
-            }
-            if (C::PER == 1) {
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&rempty[r]);
-                mbar_arrive_operands(ofull_leader + 8 * s);
-              }
-            }
+          for (int c = 0; c < 4; ++c) {
+            const uint4 w = ld_shared_v4(raw + row * 128 + (((half * 4 + c) ^ (row & 7)) << 4));
+            widen4(w.x, v[8 * c], v[8 * c + 1]);
+            widen4(w.y, v[8 * c + 2], v[8 * c + 3]);
+            widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
+            widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
           }
-          if (++r == RAW) {
-            r = 0;
-            rph ^= 1;
+          tmem_st32(tmem + (static_cast<uint32_t>(q * 32) << 16) + C::A_COL + s * 64 + half * 32, v);
+        }
+        if (!WIDE) {
+          // 16-byte pieces of the XROWS x 128 bytes, 16 rows at a time: piece c of a row becomes two of the fp16 tile,
+          // whose two boxes hold 64 of K each
+          const uint32_t xsrc = raw + C::W_BYTES, xdst = smem_u32(x_buf + s * C::X_BYTES);
+          const int c = row & 7, piece = 2 * (c & 3);
+#pragma unroll
+          for (int i = 0; i < C::XROWS / 16; ++i) {
+            if (i * 16 >= xrows) break;
+            const int xrow = i * 16 + (row >> 3);
+            const uint4 w = ld_shared_v4(xsrc + xrow * 128 + ((c ^ (xrow & 7)) << 4));
+            uint32_t v[8];
+            widen4(w.x, v[0], v[1]);
+            widen4(w.y, v[2], v[3]);
+            widen4(w.z, v[4], v[5]);
+            widen4(w.w, v[6], v[7]);
+            const uint32_t to = xdst + (c >> 2) * (C::X_BYTES / 2) + xrow * 128;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((piece + k) ^ (xrow & 7)) << 4)),
+                           "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                           : "memory");
           }
-          if (C::PER == 1 && ++s == OPS) {
-            s = 0;
-            ph ^= 1;
-          }
+          fence_proxy_async_shared();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&rempty[r]);
+          mbar_arrive_operands(ofull_leader + 8 * s);
+        }
+        r += C::CONV_GROUPS;
+        if (r >= RAW) {
+          r -= RAW;
+          rph ^= 1;
+        }
+        s += C::CONV_GROUPS;
+        if (s >= OPS) {
+          s -= OPS;
+          ph ^= 1;
         }
       }
     }
