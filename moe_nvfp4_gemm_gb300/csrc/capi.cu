@@ -1294,11 +1294,28 @@ static int run_ffn_tile(FfnTileMaps& maps, FfnTileArgs& p, int mode, int sms, cu
   return from_cuda(launch_ffn_tile(maps, p, mode, sms, st));
 }
 
-// Few tokens: the weight-streaming kernel.
-static bool ffn_streams(int64_t M) { return M <= 64; }
+// Few tokens: the weight-streaming kernel, in tiles of 64 columns and up to 64 tokens. Returns its parts of K, or 0 for
+// the tile kernel. As many parts as fill the resident slots (two CTAs an SM), with at least four blocks of 64 each.
+// Of 65 to 128 tokens, two tiles that share the weights in L2: where all CTAs are resident and either fill the slots
+// or have little to do. Measured, us, streaming / tiles:
+//   tokens              80            128           192
+//   2816 x 1024     7.8 / 9.6     8.3 / 10.0    9.0 / 10.2
+//   1024 x 4096     8.5 / 11.7    9.3 / 12.9   15.0 / 12.8
+//   8192 x 4096    25.9 / 28.4   26.4 / 28.9   45.1 / 29.4  (192: not resident)
+//   5000 x 2056    22.6 / 15.6   23.6 / 17.2   23.4 / 17.3  (158 CTAs: hardly more than one an SM)
+//   14336 x 8192   91.4 / 92.2   94.5 / 94.2  127.0 / 93.2  (not resident)
+static int ffn_stream_split(int64_t M, int64_t I, int64_t K) {
+  if (M > 128) return 0;
+  const int64_t tiles = (I + 63) / 64 * ((M + 63) / 64), kb = (K + 63) / 64, slots = 4 * kPairs;
+  int64_t split = slots / tiles;
+  if (split > kb / 4) split = kb / 4;
+  split = split < 1 ? 1 : (split > 8 ? 8 : split);
+  if (M > 64 && (tiles > slots || (tiles * split < slots * 3 / 4 && kb / split > 16))) return 0;
+  return static_cast<int>(split);
+}
 
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K) {
-  if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0 || ffn_streams(M)) return 0;
+  if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0 || ffn_stream_split(M, I, K)) return 0;
   FfnTileArgs p = {};
   return ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
 }
@@ -1317,17 +1334,13 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
       !aligned16(workspace))
     return NVFP4_ERR_ALIGNMENT;
   DevInfo d;
-  if (ffn_streams(M)) {
+  if (const int split = ffn_stream_split(M, I, K)) {
     if ((rc = device_info(d))) return rc;
     FfnStreamArgs s = {h, gate, up, ldh, static_cast<int>(M), static_cast<int>(I), static_cast<int>((K + 63) / 64)};
-    // as many CTAs along K as fill the resident slots, with at least four blocks each
-    const int64_t tiles = (I + 63) / 64;
-    int64_t split = 2 * int64_t(d.sms) / tiles;
-    if (split > s.kblocks / 4) split = s.kblocks / 4;
-    s.split = static_cast<int>(split < 1 ? 1 : (split > 8 ? 8 : split));
+    s.split = split;
     s.act = activation;
     s.half = type == NVFP4_F16;
-    s.l2_prefetch = stream_l2_prefetch(tiles * s.split, d.sms, 16384);
+    s.l2_prefetch = stream_l2_prefetch((I + 63) / 64 * s.split, d.sms, 16384);
     s.drop_stage = g_tune.withhold_stage;
     s.status = dev_status;
     s.watchdog_ns = watchdog_ns();

@@ -23,11 +23,11 @@ template <int NT>
 struct FfnStreamCfg {
   // warps 0-3: weights' producer, MMA issuer, tokens' producer, idle; warps 4-7: epilogue
   static constexpr int THREADS = 256;
-  static constexpr int CTAS = NT <= 64 ? 2 : 1;  // per SM
+  static constexpr int CTAS = 2;  // per SM
   static constexpr int W_BYTES = 128 * 128, X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
   static constexpr int MAX_STAGES = 8;
-  static constexpr int ROOM = (CTAS == 2 ? 113 : 226) * 1024 - 1024 - 512;
+  static constexpr int ROOM = 113 * 1024 - 1024 - 512;
 };
 
 template <int NT, bool HALF>
@@ -50,10 +50,12 @@ __global__ void __launch_bounds__(FfnStreamCfg<NT>::THREADS, FfnStreamCfg<NT>::C
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t wd = p.watchdog_ns;
-  const int M = p.M, S = p.split;
+  // items: the token tiles of a weight tile one after the other, which share its bytes in L2; then the parts of K
+  const int S = p.split;
+  const int item = blockIdx.x / S, rank = static_cast<int>(blockIdx.x) - item * S;
+  const int m0 = item % p.mt * NT, n0 = item / p.mt * 64;
+  const int M = min(NT, p.M - m0);    // tokens of this tile
   const int m_own = (M + S - 1) / S;  // tokens per owner
-  const int tile = blockIdx.x / S, rank = static_cast<int>(blockIdx.x) - tile * S;
-  const int n0 = tile * 64;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / S);
   const int mine = min(m_own, M - rank * m_own);
@@ -135,22 +137,34 @@ __global__ void __launch_bounds__(FfnStreamCfg<NT>::THREADS, FfnStreamCfg<NT>::C
       named_sync(1, 128);
     }
     if (received && !*abort_flag) {
-      // a thread: two columns of h of every fourth token
+      // a thread: two columns of h; a warp: every fourth token, four of them at a time
       const int c = n0 + 2 * lane;
-      for (int i = q; i < mine; i += 4) {
-        float2 g = make_float2(0.0f, 0.0f), u = g;
-        for (int s = 0; s < S; ++s) {
-          const float* row = src + (s * m_own + i) * 128 + 2 * lane;
-          const float2 a = *reinterpret_cast<const float2*>(row), b = *reinterpret_cast<const float2*>(row + 64);
-          g.x += a.x, g.y += a.y, u.x += b.x, u.y += b.y;
-        }
-        const int64_t t = rank * m_own + i;
-        if (c < p.N) {  // N is even
-          const uint32_t h = pack16<HALF>(ffn_act(g.x, p.act) * u.x, ffn_act(g.y, p.act) * u.y);
-          *reinterpret_cast<uint32_t*>(p.h + t * p.ldh + c) = h;
-          if (p.gate) {
-            *reinterpret_cast<uint32_t*>(p.gate + t * p.N + c) = pack16<HALF>(g.x, g.y);
-            *reinterpret_cast<uint32_t*>(p.up + t * p.N + c) = pack16<HALF>(u.x, u.y);
+      const bool stored = c < p.N;  // N is even
+#pragma unroll 1
+      for (int i0 = q; i0 < mine; i0 += 16) {
+        float2 g[4], u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = u[j] = make_float2(0.0f, 0.0f);
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // (a token past the last is read as the last and not stored)
+            const float* row = src + (s * m_own + min(i0 + 4 * j, mine - 1)) * 128 + 2 * lane;
+            const float2 a = *reinterpret_cast<const float2*>(row), b = *reinterpret_cast<const float2*>(row + 64);
+            g[j].x += a.x, g[j].y += a.y, u[j].x += b.x, u[j].y += b.y;
+          }
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = pack16<HALF>(ffn_act(g[j].x, p.act) * u[j].x, ffn_act(g[j].y, p.act) * u[j].y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t t = m0 + rank * m_own + i0 + 4 * j;
+          if (i0 + 4 * j < mine && stored) {
+            *reinterpret_cast<uint32_t*>(p.h + t * p.ldh + c) = h[j];
+            if (p.gate) {
+              *reinterpret_cast<uint32_t*>(p.gate + t * p.N + c) = pack16<HALF>(g[j].x, g[j].y);
+              *reinterpret_cast<uint32_t*>(p.up + t * p.N + c) = pack16<HALF>(u[j].x, u[j].y);
+            }
           }
         }
       }
@@ -176,7 +190,7 @@ __global__ void __launch_bounds__(FfnStreamCfg<NT>::THREADS, FfnStreamCfg<NT>::C
       } else if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], boxes * 4096);
         for (int j = 0; j < boxes; ++j)
-          tma_load_2d(st + C::W_BYTES + j * 4096, &maps.x, &full[s], kb * 64, j * 32, pol);
+          tma_load_2d(st + C::W_BYTES + j * 4096, &maps.x, &full[s], kb * 64, m0 + j * 32, pol);
       }
       __syncwarp();
       used |= 1u << s;
@@ -237,7 +251,7 @@ cudaError_t launch_stream(const FfnStreamMaps& maps, FfnStreamArgs p, cudaStream
   auto kernel = k_ffn_stream<NT, HALF>;
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kernel));
   if (e != cudaSuccess) return e;
-  const int m_own = (p.M + p.split - 1) / p.split;
+  const int most = p.M < NT ? p.M : NT, m_own = (most + p.split - 1) / p.split;
   const int recv_bytes = p.split > 1 ? p.split * m_own * 512 : 0;  // at most (NT + 7) * 512: split <= 8
   int stages = (C::ROOM - recv_bytes) / C::STAGE_BYTES;
   if (stages > C::MAX_STAGES) stages = C::MAX_STAGES;
@@ -247,7 +261,8 @@ cudaError_t launch_stream(const FfnStreamMaps& maps, FfnStreamArgs p, cudaStream
   p.recv_at = stages * C::STAGE_BYTES;
   p.bars_at = p.recv_at + recv_bytes;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.N + 63) / 64 * p.split));
+  p.mt = (p.M + NT - 1) / NT;
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N + 63) / 64 * p.mt * p.split));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = p.bars_at + 1024 + 512;
   cfg.stream = st;
@@ -268,8 +283,7 @@ cudaError_t launch_stream(const FfnStreamMaps& maps, FfnStreamArgs p, cudaStream
 
 cudaError_t launch_ffn_stream(const FfnStreamMaps& maps, const FfnStreamArgs& p, cudaStream_t st) {
   if (p.M <= 32) return p.half ? launch_stream<32, true>(maps, p, st) : launch_stream<32, false>(maps, p, st);
-  if (p.M <= 64) return p.half ? launch_stream<64, true>(maps, p, st) : launch_stream<64, false>(maps, p, st);
-  return p.half ? launch_stream<128, true>(maps, p, st) : launch_stream<128, false>(maps, p, st);
+  return p.half ? launch_stream<64, true>(maps, p, st) : launch_stream<64, false>(maps, p, st);
 }
 
 }  // namespace nvfp4
