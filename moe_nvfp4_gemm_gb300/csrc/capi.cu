@@ -1260,11 +1260,25 @@ static int check_ld(int64_t ld, int64_t cols) {
   return ld % 8 != 0 || ld >= int64_t(1) << 38 ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
 }
 
-// Parts of a product's contraction: as many as give every CTA pair an item, of at least eight blocks of 64.
-static int ffn_split(int64_t items, int64_t kblocks) {
-  int64_t split = items < kPairs ? kPairs / items : 1;
-  if (split > kblocks / 8) split = kblocks / 8;
-  return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
+// Parts of a product's contraction, by an estimate of its time in us: the pairs' rounds (a block of 64 is 512 cycles, 0.27
+// us; four more fill and drain the pipeline) or the operands' bytes at 6.5 TB/s, and with parts their sums (fp32,
+// written and read back at about 10 TB/s out of L2) and the kernel that joins them, 2.5 us. At least eight blocks a part.
+static int ffn_split(int64_t mt, int64_t nt, int64_t weights, int64_t kblocks, int64_t values) {
+  const int64_t items = mt * nt * weights;
+  const double bytes = static_cast<double>((mt * weights + nt) * 256 * 128) * static_cast<double>(kblocks);
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 16 && (s == 1 || s * 8 <= kblocks); ++s) {
+    const double rounds = static_cast<double>((items * s + kPairs - 1) / kPairs);
+    const double math = rounds * static_cast<double>((kblocks + s - 1) / s) * 0.27, memory = bytes / 6.5e6;
+    const double cost = (math > memory ? math : memory) + rounds * 1.08 +
+                        (s > 1 ? 2.5 + static_cast<double>(values) * s * 8.0 / 10e6 : 0.0);
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // Sizes of one tile product, and the workspace bytes of its parts.
@@ -1275,7 +1289,7 @@ static size_t ffn_plan(FfnTileArgs& p, int64_t M, int64_t N, int64_t tile_cols, 
   p.nt = static_cast<int>((N + tile_cols - 1) / tile_cols);
   p.kblocks = static_cast<int>(kblocks);
   p.weights = weights;
-  p.split = ffn_split(static_cast<int64_t>(p.mt) * p.nt * weights, kblocks);
+  p.split = ffn_split(p.mt, p.nt, weights, kblocks, M * p.nt * 256 * weights);
   return p.split == 1 ? 0 : static_cast<size_t>(weights) * p.split * p.mt * p.nt * 256 * 256 * 4;
 }
 
@@ -1294,24 +1308,23 @@ static int run_ffn_tile(FfnTileMaps& maps, FfnTileArgs& p, int mode, int sms, cu
   return from_cuda(launch_ffn_tile(maps, p, mode, sms, st));
 }
 
-// Few tokens: the weight-streaming kernel, in tiles of 64 columns and up to 64 tokens. Returns its parts of K, or 0 for
-// the tile kernel. As many parts as fill the resident slots (two CTAs an SM), with at least four blocks of 64 each.
-// Of 65 to 128 tokens, two tiles that share the weights in L2: where all CTAs are resident and either fill the slots
-// or have little to do. Measured, us, streaming / tiles:
-//   tokens              80            128           192
-//   2816 x 1024     7.8 / 9.6     8.3 / 10.0    9.0 / 10.2
-//   1024 x 4096     8.5 / 11.7    9.3 / 12.9   15.0 / 12.8
-//   8192 x 4096    25.9 / 28.4   26.4 / 28.9   45.1 / 29.4  (192: not resident)
-//   5000 x 2056    22.6 / 15.6   23.6 / 17.2   23.4 / 17.3  (158 CTAs: hardly more than one an SM)
-//   14336 x 8192   91.4 / 92.2   94.5 / 94.2  127.0 / 93.2  (not resident)
+// Up to 128 tokens: the weight-streaming kernel, in tiles of 64 columns. Returns its parts of K, or 0 for the tile kernel: as
+// many as fill the resident slots (two CTAs an SM), with at least four blocks of 64 each. Measured, us, streaming / tiles:
+//   tokens              77            128           192 (two tiles of tokens)
+//   14336 x 8192   75.5 / 92.2   80.1 / 94.4    112 / 94
+//   10112 x 8192   59.1 / 81.7   63.7 / 85.2    105 / 86
+//   5000 x 2056    14.2 / 15.7   16.8 / 17.3   31.9 / 17.3
+//   8192 x 4096    24.1 / 26.9   25.7 / 27.9   33.8 / 29.9
+//   2816 x 1024     7.7 / 9.7     9.3 / 9.4    10.2 / 9.3
+//   4096 x 512      5.8 / 7.4     7.0 / 8.1     9.0 / 7.3
+//   14336 x 512    10.2 / 11.0   11.7 / 9.6    19.3 / 9.7   (many tokens, many tiles, little K: tiles)
+//   8192 x 256      5.8 / 5.7     7.4 / 6.2    10.0 / 7.2
 static int ffn_stream_split(int64_t M, int64_t I, int64_t K) {
-  if (M > 128) return 0;
-  const int64_t tiles = (I + 63) / 64 * ((M + 63) / 64), kb = (K + 63) / 64, slots = 4 * kPairs;
-  int64_t split = slots / tiles;
+  const int64_t tiles = (I + 63) / 64, kb = (K + 63) / 64;
+  if (M > 128 || (M > 96 && kb <= 8 && tiles >= 128)) return 0;
+  int64_t split = 4 * kPairs / tiles;
   if (split > kb / 4) split = kb / 4;
-  split = split < 1 ? 1 : (split > 8 ? 8 : split);
-  if (M > 64 && (tiles > slots || (tiles * split < slots * 3 / 4 && kb / split > 16))) return 0;
-  return static_cast<int>(split);
+  return static_cast<int>(split < 1 ? 1 : (split > 8 ? 8 : split));
 }
 
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K) {

@@ -230,7 +230,7 @@ struct FfnTileArgs {
   int64_t ldy;    // forward: row stride of h
 };
 cudaError_t launch_ffn_tile(const FfnTileMaps& maps, const FfnTileArgs& p, int mode, int sms, cudaStream_t st);
-// Forward pass for few tokens. w: gate and up, boxes of 64 x 64; x: boxes of 64 x 32.
+// Forward pass for up to 128 tokens. w: gate and up, boxes of 64 x 64; x: boxes of 64 x 32.
 struct FfnStreamMaps {
   CUtensorMap w[2], x;
 };
@@ -242,13 +242,11 @@ struct FfnStreamArgs {
   int M, N;
   int kblocks;     // blocks of 64 of K
   int split;       // cluster size along K
-  int mt;          // token tiles (set by the launcher)
   int act, half;
   int l2_prefetch;  // blocks of K prefetched into L2 at entry
   int drop_stage;   // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
   int32_t* status;
   uint64_t watchdog_ns;  // limit of every pipeline wait
-  int stages, recv_at, bars_at;  // set by the launcher: ring depth, shared-memory offsets
 };
 cudaError_t launch_ffn_stream(const FfnStreamMaps& maps, const FfnStreamArgs& p, cudaStream_t st);
 struct FfnGradArgs {

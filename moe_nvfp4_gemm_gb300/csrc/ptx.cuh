@@ -299,6 +299,13 @@ DEVI void mbar_arrive_operands(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Eight bytes from any CTA's shared memory of the cluster.
+DEVI float2 ld_shared_cluster_v2(uint32_t cluster_addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Sixteen bytes from any CTA's shared memory of the cluster.
 DEVI int4 ld_shared_cluster_v4(uint32_t cluster_addr) {
   int4 v;
