@@ -1251,7 +1251,7 @@ static int check_ffn_shape(int64_t M, int64_t I, int64_t K, int32_t type, int32_
   // 2^24: tiles are counted, and columns past the last addressed, in 32 bits
   if (I % 8 != 0 || K % 8 != 0 || M > kMaxFp8Dim || I > kMaxFfnWidth || K > kMaxFfnWidth) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const int64_t mt = (M + 255) / 256, it = (I + 127) / 128, kt = (K + 255) / 256;
-  if (mt * it > kMaxFp8Dim || mt * kt > kMaxFp8Dim || it * kt > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (mt * it > kMaxFp8Dim / 4 || mt * kt > kMaxFp8Dim / 4 || it * kt > kMaxFp8Dim / 4) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   return NVFP4_OK;
 }
 
@@ -1260,52 +1260,86 @@ static int check_ld(int64_t ld, int64_t cols) {
   return ld % 8 != 0 || ld >= int64_t(1) << 38 ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
 }
 
-// Parts of a product's contraction, by an estimate of its time in us: the pairs' rounds (a block of 64 is 512 cycles, 0.27
-// us; four more fill and drain the pipeline) or the operands' bytes at 6.5 TB/s, and with parts their sums (fp32,
-// written and read back at about 10 TB/s out of L2) and the kernel that joins them, 2.5 us. At least eight blocks a part.
-static int ffn_split(int64_t mt, int64_t nt, int64_t weights, int64_t kblocks, int64_t values) {
-  const int64_t items = mt * nt * weights;
-  const double bytes = static_cast<double>((mt * weights + nt) * 256 * 128) * static_cast<double>(kblocks);
-  int best = 1;
+// One of a launch's products: y [M, N] in tiles of 256 x tile_cols, `results` of them.
+static void ffn_product(FfnProduct& q, int64_t M, int64_t N, int64_t tile_cols, int64_t kblocks, int results) {
+  q.M = static_cast<int>(M);
+  q.N = static_cast<int>(N);
+  q.mt = static_cast<int>((M + 255) / 256);
+  q.nt = static_cast<int>((N + tile_cols - 1) / tile_cols);
+  q.kblocks = static_cast<int>(kblocks);
+  q.split = 1;
+  q.items = q.mt * q.nt * results;
+}
+
+// Parts of the products' contractions, by an estimate of the launch's time in us: all items' blocks spread over the pairs (a
+// block of 64 is 512 cycles, 0.27 us; four more fill and drain the pipeline), in whole rounds where one product has
+// them all, or the operands' bytes at 6.5 TB/s; and with parts their sums (fp32, written and read back at about 10 TB/s
+// out of L2) and the kernel that joins them, 2.5 us. At least eight blocks a part. Returns the workspace bytes of the parts.
+static size_t ffn_split(FfnTileArgs& p) {
+  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  double bytes = 0.0;
+  for (const FfnProduct& q : p.in)
+    if (q.items) bytes += static_cast<double>(q.items / q.nt + q.nt) * (256 * 128) * q.kblocks;
+  const double memory = bytes / 6.5e6;
   double least = 0.0;
-  for (int s = 1; s <= 16 && (s == 1 || s * 8 <= kblocks); ++s) {
-    const double rounds = static_cast<double>((items * s + kPairs - 1) / kPairs);
-    const double math = rounds * static_cast<double>((kblocks + s - 1) / s) * 0.27, memory = bytes / 6.5e6;
-    const double cost = (math > memory ? math : memory) + rounds * 1.08 +
-                        (s > 1 ? 2.5 + static_cast<double>(values) * s * 8.0 / 10e6 : 0.0);
-    if (s == 1 || cost < least) {
-      least = cost;
-      best = s;
+  int best[2] = {1, 1};
+  for (int s0 : kSplits)
+    for (int s1 : kSplits) {
+      const int s[2] = {s0, s1};
+      double work = 0.0, longest = 0.0, join = 0.0;
+      int64_t items = 0;
+      bool possible = true;
+      for (int i = 0; i < 2; ++i) {
+        const FfnProduct& q = p.in[i];
+        if (s[i] > 1 && (q.items == 0 || s[i] * 8 > q.kblocks)) possible = false;
+        if (q.items == 0) continue;
+        const double one = (q.kblocks + s[i] - 1) / s[i] + 4.0;
+        items += static_cast<int64_t>(q.items) * s[i];
+        work += one * q.items * s[i];
+        longest = one > longest ? one : longest;
+        if (s[i] > 1) join += static_cast<double>(q.M) * q.nt * 256 * (q.items / (q.mt * q.nt)) * s[i] * 8.0 / 10e6;
+      }
+      if (!possible) continue;
+      const double rounds = static_cast<double>((items + kPairs - 1) / kPairs) * longest;
+      const bool single = p.in[0].items == 0 || p.in[1].items == 0;
+      const double spread = work / kPairs + longest * 0.5;
+      double math = (single ? rounds : (spread > longest ? spread : longest)) * 0.27;
+      if (math < memory) math = memory;
+      const double cost = math + (join > 0.0 ? join + 2.5 : 0.0);
+      if (least == 0.0 || cost < least) {
+        least = cost;
+        best[0] = s0;
+        best[1] = s1;
+      }
     }
+  size_t ws = 0;
+  for (int i = 0; i < 2; ++i) {
+    FfnProduct& q = p.in[i];
+    q.split = best[i];
+    q.items *= best[i];
+    q.ws = reinterpret_cast<float*>(ws);  // an offset, until the workspace is known
+    if (q.split > 1) ws += static_cast<size_t>(q.items) * 256 * 256 * 4;
   }
-  return best;
+  return ws;
 }
 
-// Sizes of one tile product, and the workspace bytes of its parts.
-static size_t ffn_plan(FfnTileArgs& p, int64_t M, int64_t N, int64_t tile_cols, int64_t kblocks, int weights) {
-  p.M = static_cast<int>(M);
-  p.N = static_cast<int>(N);
-  p.mt = static_cast<int>((M + 255) / 256);
-  p.nt = static_cast<int>((N + tile_cols - 1) / tile_cols);
-  p.kblocks = static_cast<int>(kblocks);
-  p.weights = weights;
-  p.split = ffn_split(p.mt, p.nt, weights, kblocks, M * p.nt * 256 * weights);
-  return p.split == 1 ? 0 : static_cast<size_t>(weights) * p.split * p.mt * p.nt * 256 * 256 * 4;
-}
-
-static int run_ffn_tile(FfnTileMaps& maps, FfnTileArgs& p, int mode, int sms, cudaStream_t st) {
-  if (p.split > 1) {
-    const uint64_t rows = static_cast<uint64_t>(p.weights) * p.split * p.mt * 256;
-    int rc = encode_out(&maps.part, p.ws, rows, static_cast<uint64_t>(p.nt) * 256, true);
+static int run_ffn_tile(FfnTileMaps& maps, FfnTileArgs& p, void* parts, bool forward, int sms, cudaStream_t st) {
+  bool joined = false;
+  for (int i = 0; i < 2; ++i) {
+    FfnProduct& q = p.in[i];
+    maps.part[i] = maps.a[0];  // not used
+    if (q.items == 0 || q.split == 1) continue;
+    q.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(parts) + reinterpret_cast<size_t>(q.ws));
+    const uint64_t cols = static_cast<uint64_t>(q.nt) * 256;
+    const int rc = encode_out(&maps.part[i], q.ws, static_cast<uint64_t>(q.items) / q.nt * 256, cols, true);
     if (rc) return rc;
-  } else {
-    maps.part = maps.y[0];  // not used
+    joined = true;
   }
   p.raster = g_tune.dense_raster;
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
-  g_last_launches += p.split > 1 ? 2 : 1;
-  return from_cuda(launch_ffn_tile(maps, p, mode, sms, st));
+  g_last_launches += joined ? 2 : 1;
+  return from_cuda(launch_ffn_tile(maps, p, forward, sms, st));
 }
 
 // Up to 128 tokens: the weight-streaming kernel, in tiles of 64 columns. Returns its parts of K, or 0 for the tile kernel: as
@@ -1330,7 +1364,8 @@ static int ffn_stream_split(int64_t M, int64_t I, int64_t K) {
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K) {
   if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0 || ffn_stream_split(M, I, K)) return 0;
   FfnTileArgs p = {};
-  return ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
+  ffn_product(p.in[0], M, I, 128, (K + 63) / 64, 1);
+  return ffn_split(p);
 }
 
 int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
@@ -1365,7 +1400,8 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
     return from_cuda(launch_ffn_stream(maps, s, static_cast<cudaStream_t>(stream)));
   }
   FfnTileArgs p = {};
-  const size_t need = ffn_plan(p, M, I, 128, (K + 63) / 64, 1);
+  ffn_product(p.in[0], M, I, 128, (K + 63) / 64, 1);
+  const size_t need = ffn_split(p);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   rc = device_info(d);
   if (rc) return rc;
@@ -1374,6 +1410,7 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
   maps.a[1] = maps.a[0];
   if ((rc = encode_16(&maps.b[0], w_gate, I, K, ld_gate, 128))) return rc;
   if ((rc = encode_16(&maps.b[1], w_up, I, K, ld_up, 128))) return rc;
+  maps.b[2] = maps.b[0];
   if ((rc = encode_16(&maps.y[0], h, M, I, ldh, 32))) return rc;
   maps.y[1] = maps.y[2] = maps.y[0];
   if (gate && ((rc = encode_16(&maps.y[1], gate, M, I, I, 32)) || (rc = encode_16(&maps.y[2], up, M, I, I, 32)))) return rc;
@@ -1381,29 +1418,30 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
   p.save = gate != nullptr;
   p.half = type == NVFP4_F16;
   p.status = dev_status;
-  p.ws = static_cast<float*>(workspace);
   p.y[0] = h;
   p.y[1] = gate;
   p.y[2] = up;
   p.ldy = ldh;
-  return run_ffn_tile(maps, p, kFfnForward, d.sms, static_cast<cudaStream_t>(stream));
+  return run_ffn_tile(maps, p, workspace, true, d.sms, static_cast<cudaStream_t>(stream));
 }
 
-// The workspace: dg and du, [M, I] each, then the parts of the product that runs (one after the other).
-static size_t ffn_backward_plan(FfnTileArgs& input, FfnTileArgs& weight, int64_t M, int64_t I, int64_t K, int weights,
-                                size_t& parts_at) {
+// The workspace: dg and du, [M, I] each, then the products' parts.
+static size_t ffn_backward_plan(FfnTileArgs& p, int64_t M, int64_t I, int64_t K, bool input, int weights, size_t& parts_at) {
   parts_at = (static_cast<size_t>(M) * I * 4 + 255) / 256 * 256;
-  const size_t a = ffn_plan(input, M, K, 256, 2 * ((I + 63) / 64), 1);
-  const size_t b = weights ? ffn_plan(weight, I, K, 256, (M + 63) / 64, weights) : 0;
-  return parts_at + (a > b ? a : b);
+  if (input) ffn_product(p.in[0], M, K, 256, 2 * ((I + 63) / 64), 1);
+  if (weights) ffn_product(p.in[1], I, K, 256, (M + 63) / 64, weights);
+  return parts_at + ffn_split(p);
 }
 
 size_t nvfp4_gated_ffn_backward_workspace_bytes(int64_t M, int64_t I, int64_t K) {
   if (check_ffn_shape(M, I, K, NVFP4_BF16, NVFP4_SILU) || M == 0) return 0;
-  FfnTileArgs a = {}, b = {};
-  size_t at;
-  const size_t two = ffn_backward_plan(a, b, M, I, K, 2, at), one = ffn_backward_plan(a, b, M, I, K, 1, at);
-  return two > one ? two : one;
+  size_t most = 0, at;
+  for (int wanted = 1; wanted < 6; ++wanted) {  // whichever gradients are asked for
+    FfnTileArgs p = {};
+    const size_t need = ffn_backward_plan(p, M, I, K, wanted & 1, wanted >> 1, at);
+    most = need > most ? need : most;
+  }
+  return most;
 }
 
 int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
@@ -1430,48 +1468,36 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
     return NVFP4_OK;
   }
   if (!dx && !weights) return NVFP4_OK;
-  FfnTileArgs pi = {}, pw = {};
+  FfnTileArgs p = {};
   size_t parts_at;
-  const size_t need = ffn_backward_plan(pi, pw, M, I, K, weights, parts_at);
+  const size_t need = ffn_backward_plan(p, M, I, K, dx != nullptr, weights, parts_at);
   if (!workspace || workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
   rc = device_info(d);
   if (rc) return rc;
   uint16_t* dg = static_cast<uint16_t*>(workspace);
   uint16_t* du = dg + static_cast<size_t>(M) * I;
-  FfnGradArgs ga = {gate, up, dh, dg, du, M, lddh, static_cast<int>(I), activation, type == NVFP4_F16};
+  FfnTileMaps maps;
+  if ((rc = encode_16(&maps.a[0], dg, M, I, I, 64)) || (rc = encode_16(&maps.a[1], du, M, I, I, 64))) return rc;
+  for (CUtensorMap& m : maps.b) m = maps.a[0];  // where not wanted
+  for (CUtensorMap& m : maps.y) m = maps.a[0];
+  if (dx && ((rc = encode_16(&maps.b[0], w_gate, I, K, ld_gate, 64)) || (rc = encode_16(&maps.b[1], w_up, I, K, ld_up, 64)) ||
+             (rc = encode_16(&maps.y[0], dx, M, K, K, 32))))
+    return rc;
+  if (weights && (rc = encode_16(&maps.b[2], x, M, K, ldx, 64))) return rc;
+  p.up_first = dw_gate == nullptr;
+  uint16_t* dw[2] = {dw_gate ? dw_gate : dw_up, dw_gate ? dw_up : nullptr};
+  p.y[0] = dx;
+  for (int i = 0; i < 2; ++i) {
+    if (!dw[i]) continue;
+    p.y[1 + i] = dw[i];
+    if ((rc = encode_16(&maps.y[1 + i], dw[i], I, K, K, 32))) return rc;
+  }
+  p.half = type == NVFP4_F16;
+  p.status = dev_status;
+  FfnGradArgs ga = {gate, up, dh, dg, du, M, lddh, static_cast<int>(I), activation, p.half};
   if ((rc = from_cuda(launch_ffn_grad(ga, d.sms, st)))) return rc;
   g_last_launches = 1;
-  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + parts_at);
-  for (FfnTileArgs* p : {&pi, &pw}) {
-    p->half = type == NVFP4_F16;
-    p->status = dev_status;
-    p->ws = parts;
-  }
-  FfnTileMaps maps;
-  if (dx) {
-    if ((rc = encode_16(&maps.a[0], dg, M, I, I, 128)) || (rc = encode_16(&maps.a[1], du, M, I, I, 128)) ||
-        (rc = encode_16(&maps.b[0], w_gate, I, K, ld_gate, 64)) || (rc = encode_16(&maps.b[1], w_up, I, K, ld_up, 64)) ||
-        (rc = encode_16(&maps.y[0], dx, M, K, K, 32)))
-      return rc;
-    maps.y[1] = maps.y[2] = maps.y[0];
-    pi.y[0] = dx;
-    if ((rc = run_ffn_tile(maps, pi, kFfnInput, d.sms, st))) return rc;
-  }
-  if (weights) {
-    const int gate_first = dw_gate ? 0 : 1;  // what stands first
-    for (int i = 0; i < 2; ++i) {
-      const bool is_up = i == 1 || gate_first == 1;
-      uint16_t* dw = is_up ? dw_up : dw_gate;
-      if (!dw) dw = dw_gate;
-      if ((rc = encode_16(&maps.a[i], is_up ? du : dg, M, I, I, 64)) || (rc = encode_16(&maps.y[i], dw, I, K, K, 32))) return rc;
-      pw.y[i] = dw;
-    }
-    if ((rc = encode_16(&maps.b[0], x, M, K, ldx, 64))) return rc;
-    maps.b[1] = maps.b[0];
-    maps.y[2] = maps.y[0];
-    if ((rc = run_ffn_tile(maps, pw, kFfnWeight, d.sms, st))) return rc;
-  }
-  return NVFP4_OK;
+  return run_ffn_tile(maps, p, static_cast<uint8_t*>(workspace) + parts_at, false, d.sms, st);
 }
 
 // ---- 8-bit integers with a scale for each row ------------------------------------------------------

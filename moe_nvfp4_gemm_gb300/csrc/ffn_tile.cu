@@ -9,10 +9,14 @@
 // The forward tile has 128 gate and 128 up columns: the pair's even CTA loads rows of Wg, the odd one
 // rows of Wu, and both halves of the sums of a row meet in one thread, which applies the activation
 // to the fp32 sums. The gradients need no transposed copies: the products read W along its rows
-// (input) and all operands along theirs (weight) as MN-major tiles, two 64 x 64 boxes for 128 rows.
+// (input) and all operands along theirs (weight) as MN-major tiles, two 64 x 64 boxes for 128 rows. Both
+// gradients' tiles are one launch, so that the few tiles of the one fill the pairs that the other leaves.
 //
-// Products of few tiles are cut along their contraction into parts (p.split); the parts' fp32 sums go to
+// Products of few tiles are cut along their contraction into parts; the parts' fp32 sums go to
 // the workspace and are added, in the order of the contraction, by k_ffn_join.
+//
+// Bound by the tensor cores: 4096 x 14336 x 8192 forward 1.00-1.14 ms (1.92 PFLOP/s in a burst, less under the power cap),
+// 4099 x 8192 x 4096 forward 303 us, both gradients 620 us.
 #include <stdint.h>
 
 #include "ffn.cuh"
@@ -33,27 +37,29 @@ struct FfnCfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-// One item of the persistent walk: a tile and a part of the contraction.
+// One item of the persistent walk: a tile of a product and a part of its contraction.
 struct FfnItem {
-  int m0, n0;    // first row and column of the tile
-  int kb0, kb1;  // its blocks of 64
-  int which;     // weight gradients: 0 gate, 1 up
+  int product, which;  // of p.in; its result, 0 or 1
+  int m0, n0;          // first row and column of the tile
+  int kb0, kb1;        // its blocks of 64
   int part;
 };
 
 DEVI FfnItem ffn_item(const FfnTileArgs& p, int i) {
   FfnItem it;
-  const int tiles = p.mt * p.nt;
-  const int per_which = tiles * p.split;
-  it.which = i / per_which;
-  i -= it.which * per_which;
+  it.product = i >= p.in[0].items;
+  if (it.product) i -= p.in[0].items;
+  const FfnProduct& q = p.in[it.product];
+  const int tiles = q.mt * q.nt, per_result = tiles * q.split;
+  it.which = i / per_result;
+  i -= it.which * per_result;
   it.part = i / tiles;
   int mb, nb;
-  tile_coords(i - it.part * tiles, p.mt, p.nt, p.raster, mb, nb);
+  tile_coords(i - it.part * tiles, q.mt, q.nt, p.raster, mb, nb);
   it.m0 = mb * 256;
   it.n0 = nb * 256;
-  it.kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * it.part / p.split);
-  it.kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (it.part + 1) / p.split);
+  it.kb0 = static_cast<int>(static_cast<int64_t>(q.kblocks) * it.part / q.split);
+  it.kb1 = static_cast<int>(static_cast<int64_t>(q.kblocks) * (it.part + 1) / q.split);
   return it;
 }
 
@@ -77,12 +83,11 @@ DEVI void ffn_store_box(uint8_t* box, const CUtensorMap* tm, int col, int row, c
   }
 }
 
-template <int MODE, bool HALF, bool PARTIAL>
+template <bool FORWARD, bool HALF>
 __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     k_ffn_tile(const __grid_constant__ FfnTileMaps maps, const __grid_constant__ FfnTileArgs p) {
   using C = FfnCfg;
   constexpr int STAGES = C::STAGES;
-  constexpr bool A_MN = MODE == kFfnWeight, B_MN = MODE != kFfnForward;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out_buf = smem + STAGES * C::STAGE_BYTES;
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // set-up overlaps the previous kernel; every memory access waits for it
 
-  const int items = p.mt * p.nt * p.split * (MODE == kFfnWeight ? p.weights : 1);
+  const int items = p.in[0].items + p.in[1].items;
   const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
 
   if (warp >= 4) {
@@ -142,18 +147,19 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         __syncwarp();
         if (elect_one()) mbar_arrive_cluster(tempty_leader[buf]);
       };
-      if constexpr (PARTIAL) {
+      const FfnProduct& pr = p.in[it.product];
+      if (pr.split > 1) {
         // fp32 sums to [part][tile rows][tile columns] of the workspace
-        const int wrow = (it.which * p.split + it.part) * p.mt * 256 + row0;
+        const int wrow = (it.which * pr.split + it.part) * pr.mt * 256 + row0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           tmem_ld32(lanes + h * 128 + c * 32, r);
           tmem_ld_wait32(r);
           if (c == 3) release();
-          if (row0 < p.M) ffn_store_box(box, &maps.part, it.n0 + h * 128 + c * 32, wrow, r);
+          if (row0 < pr.M) ffn_store_box(box, &maps.part[it.product], it.n0 + h * 128 + c * 32, wrow, r);
         }
-      } else if constexpr (MODE == kFfnForward) {
+      } else if constexpr (FORWARD) {
         // 64 columns of h: their gate sums, and the up sums 128 columns further on
         const int col = it.n0 / 2 + h * 64;
         uint32_t hw[32], gw[32], uw[32];
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             }
           }
         }
-        if (row0 < p.M && col < p.N) {
+        if (row0 < pr.M && col < pr.N) {
           ffn_store_box(box, &maps.y[0], col, row0, hw);
           if (p.save) {
             ffn_store_box(box, &maps.y[1], col, row0, gw);
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
           }
         }
       } else {
-        const CUtensorMap* y = &maps.y[it.which];
+        const CUtensorMap* y = &maps.y[it.product + it.which];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int col = it.n0 + h * 128 + b * 64;
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             for (int j = 0; j < 16; ++j)
               w[16 * c + j] = pack16<HALF>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
           }
-          if (row0 < p.M && col < p.N) ffn_store_box(box, y, col, row0, w);
+          if (row0 < pr.M && col < pr.N) ffn_store_box(box, y, col, row0, w);
         }
       }
       buf ^= 1;
@@ -214,8 +220,9 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     uint32_t used = 0, phases = 0;  // per stage: requested at all, phase of the last request
     for (int i = pair; i < items && !*abort_flag; i += npairs) {
       const FfnItem it = ffn_item(p, i);
-      const int am = it.m0 + rank * 128;
-      const int bn = MODE == kFfnForward ? it.n0 / 2 : it.n0 + static_cast<int>(rank) * 128;
+      const int am = it.m0 + static_cast<int>(rank) * 128;
+      const int bn = FORWARD ? it.n0 / 2 : it.n0 + static_cast<int>(rank) * 128;
+      const int half = p.in[0].kblocks / 2;
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
         if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag, wd)) break;
         // test hook: the first CTA withholds its expect-tx arrival and loads
@@ -224,23 +231,20 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
           uint8_t* st = smem + s * C::STAGE_BYTES;
           const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
-          // the two halves of the input gradient's contraction: gate columns, then up columns
-          const int second = MODE == kFfnInput && kb >= p.kblocks / 2 ? 1 : 0;
-          const int k0 = (MODE == kFfnInput ? kb - second * (p.kblocks / 2) : kb) * 64;
-          const CUtensorMap* ta = &maps.a[MODE == kFfnWeight ? it.which : second];
-          const CUtensorMap* tb = &maps.b[MODE == kFfnForward ? rank : second];
-          if (A_MN) {
-            tma_load_2d_pair(st, ta, bar, am, k0, pol);
-            tma_load_2d_pair(st + C::TILE_BYTES / 2, ta, bar, am + 64, k0, pol);
+          if constexpr (FORWARD) {
+            tma_load_2d_pair(st, &maps.a[0], bar, kb * 64, am, pol);
+            tma_load_2d_pair(st + C::TILE_BYTES, &maps.b[rank], bar, kb * 64, bn, pol);
           } else {
-            tma_load_2d_pair(st, ta, bar, k0, am, pol);
-          }
-          st += C::TILE_BYTES;
-          if (B_MN) {
-            tma_load_2d_pair(st, tb, bar, bn, k0, pol);
-            tma_load_2d_pair(st + C::TILE_BYTES / 2, tb, bar, bn + 64, k0, pol);
-          } else {
-            tma_load_2d_pair(st, tb, bar, k0, bn, pol);
+            // boxes of 64 x 64. Input: the contraction is the gate's columns, then the up's; dg and du lie along it.
+            // Weight: all operands lie along their rows.
+            const int second = it.product ? it.which : kb >= half;
+            const int k0 = (it.product || !second ? kb : kb - half) * 64;
+            const CUtensorMap* ta = &maps.a[it.product ? p.up_first ^ second : second];
+            const CUtensorMap* tb = &maps.b[it.product ? 2 : second];
+            tma_load_2d_pair(st, ta, bar, it.product ? am : k0, it.product ? k0 : am, pol);
+            tma_load_2d_pair(st + C::TILE_BYTES / 2, ta, bar, it.product ? am + 64 : k0, it.product ? k0 : am + 64, pol);
+            tma_load_2d_pair(st + C::TILE_BYTES, tb, bar, bn, k0, pol);
+            tma_load_2d_pair(st + C::TILE_BYTES * 3 / 2, tb, bar, bn + 64, k0, pol);
           }
         }
         __syncwarp();
@@ -261,11 +265,14 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
           mbar_wait_warp(&full[j], phases >> j & 1, &dummy, wd);
         }
   } else if (warp == 1 && leader) {
-    const uint32_t idesc = idesc_f16(256, 256, !HALF, A_MN, B_MN);
     int s = 0, buf = 0;
     uint32_t ph = 0, bph = 0;
     for (int i = pair; i < items && !*abort_flag; i += npairs) {
       const FfnItem it = ffn_item(p, i);
+      const bool a_mn = !FORWARD && it.product == 1;
+      constexpr bool B_MN = !FORWARD;
+      const uint32_t idesc = a_mn ? idesc_f16(256, 256, !HALF, true, B_MN) : idesc_f16(256, 256, !HALF, false, B_MN);
+      const uint32_t a_step = a_mn ? 128 : 2;
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
         if (!mbar_wait_warp(&full[s], ph, abort_flag, wd)) break;
         if (kb == it.kb0 && !mbar_wait_warp(&tempty[buf], bph ^ 1, abort_flag, wd)) break;
@@ -273,11 +280,11 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         if (elect_one()) {
           const uint32_t addr = smem_u32(smem + s * C::STAGE_BYTES);
           // a step of 16: 32 bytes of a K-major row, two 8-row groups (2,048 bytes) of an MN-major tile
-          const uint64_t ad = A_MN ? desc_sw128_mn(addr, C::TILE_BYTES / 2) : desc_sw128(addr);
+          const uint64_t ad = a_mn ? desc_sw128_mn(addr, C::TILE_BYTES / 2) : desc_sw128(addr);
           const uint64_t bd = B_MN ? desc_sw128_mn(addr + C::TILE_BYTES, C::TILE_BYTES / 2) : desc_sw128(addr + C::TILE_BYTES);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16_pair(tmem + buf * 256, ad + (A_MN ? 128 : 2) * kk, bd + (B_MN ? 128 : 2) * kk, idesc,
+            tc_mma_f16_pair(tmem + buf * 256, ad + a_step * kk, bd + (B_MN ? 128 : 2) * kk, idesc,
                             kb != it.kb0 || kk != 0);
           tc_commit_pair(&empty[s], 3);
           if (kb + 1 == it.kb1) tc_commit_pair(&tfull[buf], 3);
@@ -311,48 +318,54 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 
 // y[r, c] = the parts' sums in the order of the contraction, eight columns a thread. Forward: columns
 // 256 b + j and 256 b + 128 + j of the workspace are gate and up of column 128 b + j of h.
-template <int MODE, bool HALF>
+template <bool FORWARD, bool HALF>
 __global__ void __launch_bounds__(256) k_ffn_join(const __grid_constant__ FfnTileArgs p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int groups = p.N / 8;
-  const int64_t total = static_cast<int64_t>(p.M) * groups * (MODE == kFfnWeight ? p.weights : 1);
-  const int64_t cols = static_cast<int64_t>(p.nt) * 256, part = static_cast<int64_t>(p.mt) * 256 * cols;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int c = static_cast<int>(i % groups) * 8;
-    const int64_t row = i / groups;
-    const int which = MODE == kFfnWeight ? static_cast<int>(row / p.M) : 0;
-    const int64_t r = row - static_cast<int64_t>(which) * p.M;
-    auto sum = [&](int64_t at, float (&v)[8]) {
+#pragma unroll 1
+  for (int product = 0; product < (FORWARD ? 1 : 2); ++product) {
+    const FfnProduct& q = p.in[product];
+    if (q.items == 0 || q.split == 1) continue;
+    const int groups = q.N / 8, results = q.items / (q.mt * q.nt * q.split);
+    const int64_t total = static_cast<int64_t>(q.M) * groups * results;
+    const int64_t cols = static_cast<int64_t>(q.nt) * 256, part = static_cast<int64_t>(q.mt) * 256 * cols;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+      const int c = static_cast<int>(i % groups) * 8;
+      const int64_t row = i / groups;
+      const int which = static_cast<int>(row / q.M);
+      const int64_t r = row - static_cast<int64_t>(which) * q.M;
+      auto sum = [&](int64_t at, float (&v)[8]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      const float* src = p.ws + which * p.split * part + r * cols + at;
-      for (int s = 0; s < p.split; ++s, src += part) {
-        const float4 lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
-        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
-      }
-    };
-    auto store = [&](void* y, int64_t ld, const float (&v)[8]) {
-      uint16_t* to = static_cast<uint16_t*>(y) + r * ld + c;
-      st_global_v4(to, pack16<HALF>(v[0], v[1]), pack16<HALF>(v[2], v[3]), pack16<HALF>(v[4], v[5]), pack16<HALF>(v[6], v[7]));
-    };
-    float v[8];
-    if (MODE == kFfnForward) {
-      const int64_t at = static_cast<int64_t>(c / 128) * 256 + c % 128;
-      float u[8];
-      sum(at, v);
-      sum(at + 128, u);
-      if (p.save) {
-        store(p.y[1], p.N, v);
-        store(p.y[2], p.N, u);
-      }
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        const float* src = q.ws + which * q.split * part + r * cols + at;
+#pragma unroll 4
+        for (int s = 0; s < q.split; ++s, src += part) {
+          const float4 lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
+          v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+          v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+        }
+      };
+      auto store = [&](void* y, int64_t ld, const float (&v)[8]) {
+        uint16_t* to = static_cast<uint16_t*>(y) + r * ld + c;
+        st_global_v4(to, pack16<HALF>(v[0], v[1]), pack16<HALF>(v[2], v[3]), pack16<HALF>(v[4], v[5]), pack16<HALF>(v[6], v[7]));
+      };
+      float v[8];
+      if (FORWARD) {
+        const int64_t at = static_cast<int64_t>(c / 128) * 256 + c % 128;
+        float u[8];
+        sum(at, v);
+        sum(at + 128, u);
+        if (p.save) {
+          store(p.y[1], q.N, v);
+          store(p.y[2], q.N, u);
+        }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = ffn_act(v[j], p.act) * u[j];
-    } else {
-      sum(c, v);
+        for (int j = 0; j < 8; ++j) v[j] = ffn_act(v[j], p.act) * u[j];
+      } else {
+        sum(c, v);
+      }
+      store(p.y[product + which], FORWARD ? p.ldy : q.N, v);
     }
-    store(p.y[which], MODE == kFfnForward ? p.ldy : p.N, v);
   }
 }
 
@@ -410,29 +423,25 @@ static cudaError_t launch_dependent(Kernel kernel, int grid, int block, int smem
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int MODE, bool HALF>
+template <bool FORWARD, bool HALF>
 static cudaError_t launch_tile(const FfnTileMaps& maps, const FfnTileArgs& p, int sms, cudaStream_t st) {
-  auto kernel = p.split > 1 ? k_ffn_tile<MODE, HALF, true> : k_ffn_tile<MODE, HALF, false>;
+  auto kernel = k_ffn_tile<FORWARD, HALF>;
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kernel));
   if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(p.mt) * p.nt * p.split * (MODE == kFfnWeight ? p.weights : 1);
-  const int64_t pairs = items < sms / 2 ? items : sms / 2;
-  e = launch_dependent(kernel, static_cast<int>(2 * pairs), FfnCfg::THREADS, FfnCfg::SMEM_BYTES, 2, st, maps, p);
-  if (e != cudaSuccess || p.split == 1) return e;
-  const int64_t threads = static_cast<int64_t>(p.M) * (p.N / 8) * (MODE == kFfnWeight ? p.weights : 1);
+  const int items = p.in[0].items + p.in[1].items, pairs = items < sms / 2 ? items : sms / 2;
+  e = launch_dependent(kernel, 2 * pairs, FfnCfg::THREADS, FfnCfg::SMEM_BYTES, 2, st, maps, p);
+  if (e != cudaSuccess) return e;
+  int64_t threads = 0;
+  for (const FfnProduct& q : p.in)
+    if (q.items > 0 && q.split > 1) threads += static_cast<int64_t>(q.M) * (q.N / 8) * (q.items / (q.mt * q.nt * q.split));
+  if (threads == 0) return cudaSuccess;
   const int64_t blocks = (threads + 255) / 256, most = 8 * static_cast<int64_t>(sms);
-  return launch_dependent(k_ffn_join<MODE, HALF>, static_cast<int>(blocks < most ? blocks : most), 256, 0, 1, st, p);
+  return launch_dependent(k_ffn_join<FORWARD, HALF>, static_cast<int>(blocks < most ? blocks : most), 256, 0, 1, st, p);
 }
 
-cudaError_t launch_ffn_tile(const FfnTileMaps& maps, const FfnTileArgs& p, int mode, int sms, cudaStream_t st) {
-  switch (mode) {
-    case kFfnForward:
-      return p.half ? launch_tile<kFfnForward, true>(maps, p, sms, st) : launch_tile<kFfnForward, false>(maps, p, sms, st);
-    case kFfnInput:
-      return p.half ? launch_tile<kFfnInput, true>(maps, p, sms, st) : launch_tile<kFfnInput, false>(maps, p, sms, st);
-    default:
-      return p.half ? launch_tile<kFfnWeight, true>(maps, p, sms, st) : launch_tile<kFfnWeight, false>(maps, p, sms, st);
-  }
+cudaError_t launch_ffn_tile(const FfnTileMaps& maps, const FfnTileArgs& p, bool forward, int sms, cudaStream_t st) {
+  if (forward) return p.half ? launch_tile<true, true>(maps, p, sms, st) : launch_tile<true, false>(maps, p, sms, st);
+  return p.half ? launch_tile<false, true>(maps, p, sms, st) : launch_tile<false, false>(maps, p, sms, st);
 }
 
 cudaError_t launch_ffn_grad(const FfnGradArgs& p, int sms, cudaStream_t st) {

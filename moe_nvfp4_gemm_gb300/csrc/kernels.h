@@ -207,29 +207,32 @@ cudaError_t launch_fp8_narrow(const CUtensorMap& tmW, const CUtensorMap& tmX, co
                                     cudaStream_t st);
 
 // ---- 16-bit gated feed-forward block ------------------------------------------------------
-enum { kFfnForward = 0, kFfnInput = 1, kFfnWeight = 2 };
+// Forward: a[0] x, b gate and up, y h, gate, up; boxes of 64 x 128. Gradients: a dg and du, b w_gate, w_up and x, y dx and
+// the weights' gradients; boxes of 64 x 64. part: the sums of a product in parts, fp32.
 struct FfnTileMaps {
-  CUtensorMap a[2], b[2];  // gate and up where the operand has both
-  CUtensorMap y[3];        // forward: h, gate, up; input: dx; weight: dw_gate, dw_up
-  CUtensorMap part;        // the parts' sums, fp32
+  CUtensorMap a[2], b[3], y[3], part[2];
+};
+struct FfnProduct {
+  int M, N;     // rows and columns of a result
+  int mt, nt;   // 256 x 256 tiles of sums (forward: 128 columns of h each)
+  int kblocks;  // blocks of 64 of the contraction
+  int split;    // its parts
+  int items;    // tiles x parts x results
+  float* ws;    // split > 1: fp32 [results][split][mt * 256][nt * 256]
 };
 struct FfnTileArgs {
-  int M, N;       // rows and columns of a result
-  int mt, nt;     // 256 x 256 tiles of sums (forward: 128 columns of h each)
-  int kblocks;    // blocks of 64 of the contraction
-  int split;      // parts of the contraction
-  int weights;    // weight gradients: results wanted, the first `weights` of y
-  int raster;     // tile order, see tile_coords
-  int act, save;  // forward: activation; also write gate and up
-  int half;       // fp16 instead of bf16
-  int drop_stage;  // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
+  FfnProduct in[2];  // forward: one; gradients: of the input and of the weights (no items: not wanted)
+  int raster;        // tile order, see tile_coords
+  int act, save;     // forward: activation; also write gate and up
+  int up_first;      // gradients: the weights' first result is w_up's
+  int half;          // fp16 instead of bf16
+  int drop_stage;    // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
   int32_t* status;
   uint64_t watchdog_ns;  // limit of every pipeline wait
-  float* ws;      // split > 1: fp32 [weights][split][mt * 256][nt * 256]
-  void* y[3];     // and the results, written by k_ffn_join
-  int64_t ldy;    // forward: row stride of h
+  void* y[3];        // the results, as maps.y, written by the kernel that joins parts
+  int64_t ldy;       // forward: row stride of h
 };
-cudaError_t launch_ffn_tile(const FfnTileMaps& maps, const FfnTileArgs& p, int mode, int sms, cudaStream_t st);
+cudaError_t launch_ffn_tile(const FfnTileMaps& maps, const FfnTileArgs& p, bool forward, int sms, cudaStream_t st);
 // Forward pass for up to 128 tokens. w: gate and up, boxes of 64 x 64; x: boxes of 64 x 32.
 struct FfnStreamMaps {
   CUtensorMap w[2], x;
