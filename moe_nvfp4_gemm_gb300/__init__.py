@@ -988,6 +988,14 @@ def nvfp4_grad_clip_workspace_bytes(count: int) -> int:
     return int(lib().nvfp4_grad_clip_workspace_bytes(count))
 
 
+_clip_workspace_bytes = functools.lru_cache(maxsize=128)(nvfp4_grad_clip_workspace_bytes)
+
+
+@functools.lru_cache(maxsize=128)
+def _list_types(n):  # of the host arrays of n gradients: making the types takes longer than filling them
+    return _vp * n, _i64 * n, _i32 * n
+
+
 def nvfp4_grad_clip(grads, max_norm=math.inf, out=None, norm=None, workspace=None, stream=None) -> torch.Tensor:
     """The norm over all values of `grads` (contiguous CUDA tensors, bf16, fp16 or fp32, mixed as they come), fp32 [1];
     the gradients are multiplied by min(1, max_norm / (norm + 1e-6)), in place or into the tensors `out` of the same
@@ -996,29 +1004,26 @@ def nvfp4_grad_clip(grads, max_norm=math.inf, out=None, norm=None, workspace=Non
         return _on_stream(stream, nvfp4_grad_clip, locals())
     grads = list(grads)
     n, here = len(grads), torch._C._cuda_getDevice()
-    types, sizes = [], []
+    dev, (pointers, counts, kinds) = grads[0].device if n else "cuda", _list_types(n)
     for t in grads:
-        kind = _GRAD_TYPES.get(t.dtype)
-        if kind is None or not t.is_cuda or not t.is_contiguous() or t.get_device() != here:
+        if not (t.dtype in _GRAD_TYPES and t.is_cuda and t.is_contiguous() and t.get_device() == here):
             raise TypeError("grads must be contiguous tensors of torch.bfloat16, float16 or float32 on the current CUDA device")
-        types.append(kind)
-        sizes.append(t.numel())
     to = None
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise TypeError(f"out has {len(out)} tensors, grads {n}")
         for t, o in zip(grads, out):
-            if not (o.is_cuda and o.dtype == t.dtype and o.shape == t.shape and o.is_contiguous() and o.get_device() == here):
+            if not (o.dtype == t.dtype and o.shape == t.shape and o.is_cuda and o.is_contiguous() and o.get_device() == here):
                 raise TypeError("out must hold tensors like grads")
-        to = (_vp * n)(*[o.data_ptr() for o in out])
+        to = pointers(*[o.data_ptr() for o in out])
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device="cuda")
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(nvfp4_grad_clip_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+        workspace = torch.empty(_clip_workspace_bytes(n), dtype=torch.uint8, device=dev)
     _check("nvfp4_grad_clip",
-           lib().nvfp4_grad_clip((_vp * n)(*[t.data_ptr() for t in grads]), to, (_i64 * n)(*sizes), (_i32 * n)(*types), n,
-                                 max_norm, _operand(norm, _F32, (1,), "norm"),
+           lib().nvfp4_grad_clip(pointers(*[t.data_ptr() for t in grads]), to, counts(*[t.numel() for t in grads]),
+                                 kinds(*[_GRAD_TYPES[t.dtype] for t in grads]), n, max_norm, _operand(norm, _F32, (1,), "norm"),
                                  _operand(workspace, _U8, (0,), "workspace"), workspace.numel(), _stream()))
     return norm
 

@@ -1564,10 +1564,15 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
   const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt, kb = (K + 127) / 128;
-  // parts of K: as many as have a place, of at least four blocks of 128
-  int64_t split = d.sms / 2 / tiles;
-  if (split > kb / 4) split = kb / 4;
-  p.split = static_cast<int>(split < 1 ? 1 : (split > 4 ? 4 : split));
+  // Parts of K, one to a pair of a cluster. Measured with K = 4096 (32 blocks), us, 1 / 2 / 3 / 4 parts:
+  //   tiles        14                  16                  22                  24                  36            38
+  //   64 tokens    14.9 10.8 10.0 9.2  14.9 11.0 10.1 17   14.9 11.4 10.5 17   14.9 11.4 19.5 18   15 12 20 26   15 22
+  //   300 tokens   28 21 20 18         28 21 20 28         28 22 21 31         29 22 32 32         29 23 36 46   29 38
+  // So as many as the tiles' clusters of 8, 6 or 4 CTAs are resident at once. Short K, 8 blocks: 64 tokens, 4 tiles 7.2 7.1
+  // 7.1 6.5; 300 tokens, 8 tiles 13.3 13.4 13.4 13.0; 1,000, 16 tiles 13.5 13.8 15.2.
+  int64_t split = tiles <= 14 ? 4 : (tiles <= 22 ? 3 : (tiles <= 36 ? 2 : 1));
+  if (split > kb / (tokens == 256 ? 8 : 2)) split = kb / (tokens == 256 ? 8 : 2);
+  p.split = static_cast<int>(split < 1 ? 1 : split);
   CUtensorMap tmW, tmX;
   if ((rc = encode_2d(&tmW, reinterpret_cast<const uint8_t*>(b), N, K, 128))) return rc;
   if (tokens == 256) {
