@@ -479,7 +479,8 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
  *   w_gate, w_up  device [I, K], of the same type, rows ld_gate and ld_up apart (the halves of one
  *              [2 I, K] tensor, for instance)
  *   h          [M, I] written, rows ldh apart
- *   gate, up   [M, I] contiguous, written: g and u rounded to the type, for the backward call; or both NULL
+ *   gate, up   fp32 [M, I] contiguous, 32-byte aligned, written: g and u as they are summed, for the backward call;
+ *              or both NULL
  *   workspace  nvfp4_gated_ffn_workspace_bytes(M, I, K) bytes, 16-byte aligned (NULL where that is 0)
  * I, K and the row strides are multiples of 8, pointers 16-byte aligned, I and K at most 2^24. A NaN or an
  * infinity stays in its token's row. dev_status as for nvfp4_gemm.
@@ -487,7 +488,7 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
 enum { NVFP4_SILU = 0, NVFP4_GELU_TANH = 1 };
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K);
 int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
-                    int64_t ld_up, int32_t type, int32_t activation, uint16_t* h, int64_t ldh, uint16_t* gate, uint16_t* up,
+                    int64_t ld_up, int32_t type, int32_t activation, uint16_t* h, int64_t ldh, float* gate, float* up,
                     int64_t M, int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                     void* stream);
 
@@ -496,7 +497,7 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
  *   dg = dh u act'(g),  du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
  * dg and du are rounded to the type (the tensor cores read them), the sums are fp32, the results are
  * rounded once.
- *   gate, up   device [M, I] contiguous;  dh [M, I], rows lddh apart
+ *   gate, up   device fp32 [M, I] contiguous;  dh [M, I], rows lddh apart
  *   dx         [M, K] contiguous, written, or NULL: not wanted (w_gate and w_up may then be NULL)
  *   dw_gate, dw_up  [I, K] contiguous, written, or NULL each (x may be NULL when both are). M == 0 writes zeros.
  *   workspace  nvfp4_gated_ffn_backward_workspace_bytes(M, I, K) bytes, 256-byte aligned
@@ -505,7 +506,7 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
  */
 size_t nvfp4_gated_ffn_backward_workspace_bytes(int64_t M, int64_t I, int64_t K);
 int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
-                             int64_t ld_up, const uint16_t* gate, const uint16_t* up, const uint16_t* dh, int64_t lddh,
+                             int64_t ld_up, const float* gate, const float* up, const uint16_t* dh, int64_t lddh,
                              int32_t type, int32_t activation, uint16_t* dx, uint16_t* dw_gate, uint16_t* dw_up, int64_t M,
                              int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 

@@ -866,7 +866,7 @@ def _ffn_inputs(x, w_gate, w_up, activation):
 
 def nvfp4_gated_ffn(x, w_gate, w_up, activation="silu", save=False, h=None, workspace=None, dev_status=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T), bf16 or fp16: x [M, K], w_gate and w_up [I, K], h [M, I]; activation
-    "silu" or "gelu_tanh". With save, returns (h, gate, up), what nvfp4_gated_ffn_backward needs. The rows of
+    "silu" or "gelu_tanh". With save, returns (h, gate, up): the two products in fp32, for nvfp4_gated_ffn_backward. The rows of
     x, the weights and h may lie apart (views of wider tensors); their strides, I and K are multiples of 8."""
     if stream is not None:
         return _on_stream(stream, nvfp4_gated_ffn, locals())
@@ -877,7 +877,7 @@ def nvfp4_gated_ffn(x, w_gate, w_up, activation="silu", save=False, h=None, work
     ph, ldh = _rows(h, dtype, (M, I), "h")
     gate = up = pg = pu = None
     if save:
-        gate, up = torch.empty((M, I), dtype=dtype, device=dev), torch.empty((M, I), dtype=dtype, device=dev)
+        gate, up = torch.empty((M, I), dtype=torch.float32, device=dev), torch.empty((M, I), dtype=torch.float32, device=dev)
         pg, pu = gate.data_ptr(), up.data_ptr()
     ws_bytes, pws = _ffn_workspace_bytes(M, I, K), None
     if workspace is not None:
@@ -900,7 +900,7 @@ def nvfp4_gated_ffn_backward(x, w_gate, w_up, gate, up, dh, activation="silu", n
     dtype, dev = x.dtype, x.device
     args = _rows(x, dtype, (M, K), "x") + _rows(w_gate, dtype, (I, K), "w_gate") + _rows(w_up, dtype, (I, K), "w_up")
     for t, n in ((gate, "gate"), (up, "up")):
-        if _rows(t, dtype, (M, I), n)[1] != I:
+        if _rows(t, torch.float32, (M, I), n)[1] != I:
             raise TypeError(f"{n} must be contiguous")
         args += (t.data_ptr(),)
     args += _rows(dh, dtype, (M, I), "dh")

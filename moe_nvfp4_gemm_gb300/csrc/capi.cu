@@ -92,6 +92,7 @@ int device_info(DevInfo& d) {
   return d.ok ? NVFP4_OK : NVFP4_ERR_ARCH;
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 2-D uint8 view [rows, cols] (cols bytes contiguous), 128-byte-swizzled boxes of
@@ -1369,7 +1370,7 @@ size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K) {
 }
 
 int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
-                    int64_t ld_up, int32_t type, int32_t activation, uint16_t* h, int64_t ldh, uint16_t* gate, uint16_t* up,
+                    int64_t ld_up, int32_t type, int32_t activation, uint16_t* h, int64_t ldh, float* gate, float* up,
                     int64_t M, int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                     void* stream) {
   g_last_launches = 0;
@@ -1378,7 +1379,7 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
   if ((rc = check_ld(ldx, K)) || (rc = check_ld(ld_gate, K)) || (rc = check_ld(ld_up, K)) || (rc = check_ld(ldh, I))) return rc;
   if (M == 0) return NVFP4_OK;
   if (!x || !w_gate || !w_up || !h || (gate == nullptr) != (up == nullptr)) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || !aligned16(gate) || !aligned16(up) ||
+  if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || !aligned32(gate) || !aligned32(up) ||
       !aligned16(workspace))
     return NVFP4_ERR_ALIGNMENT;
   DevInfo d;
@@ -1413,7 +1414,6 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
   maps.b[2] = maps.b[0];
   if ((rc = encode_16(&maps.y[0], h, M, I, ldh, 32))) return rc;
   maps.y[1] = maps.y[2] = maps.y[0];
-  if (gate && ((rc = encode_16(&maps.y[1], gate, M, I, I, 32)) || (rc = encode_16(&maps.y[2], up, M, I, I, 32)))) return rc;
   p.act = activation;
   p.save = gate != nullptr;
   p.half = type == NVFP4_F16;
@@ -1445,7 +1445,7 @@ size_t nvfp4_gated_ffn_backward_workspace_bytes(int64_t M, int64_t I, int64_t K)
 }
 
 int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int64_t ld_gate, const uint16_t* w_up,
-                             int64_t ld_up, const uint16_t* gate, const uint16_t* up, const uint16_t* dh, int64_t lddh,
+                             int64_t ld_up, const float* gate, const float* up, const uint16_t* dh, int64_t lddh,
                              int32_t type, int32_t activation, uint16_t* dx, uint16_t* dw_gate, uint16_t* dw_up, int64_t M,
                              int64_t I, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   g_last_launches = 0;

@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(FfnStreamCfg<NT>::THREADS, FfnStreamCfg<NT>::C
           const int64_t t = rank * m_own + i0 + 8 * j;
           *reinterpret_cast<uint32_t*>(p.h + t * p.ldh + c) = pack16<HALF>(ffn_act(gs.x, p.act) * us.x, ffn_act(gs.y, p.act) * us.y);
           if (p.gate) {
-            *reinterpret_cast<uint32_t*>(p.gate + t * p.N + c) = pack16<HALF>(gs.x, gs.y);
-            *reinterpret_cast<uint32_t*>(p.up + t * p.N + c) = pack16<HALF>(us.x, us.y);
+            *reinterpret_cast<float2*>(p.gate + t * p.N + c) = gs;
+            *reinterpret_cast<float2*>(p.up + t * p.N + c) = us;
           }
         }
       }

@@ -239,8 +239,8 @@ struct FfnStreamMaps {
 };
 struct FfnStreamArgs {
   uint16_t* h;     // rows ldh apart
-  uint16_t* gate;  // [M, N], with up: also written, or null
-  uint16_t* up;
+  float* gate;     // [M, N], with up: also written, or null
+  float* up;
   int64_t ldh;
   int M, N;
   int kblocks;     // blocks of 64 of K
@@ -253,8 +253,8 @@ struct FfnStreamArgs {
 };
 cudaError_t launch_ffn_stream(const FfnStreamMaps& maps, const FfnStreamArgs& p, cudaStream_t st);
 struct FfnGradArgs {
-  const uint16_t* gate;  // [M, I]
-  const uint16_t* up;    // [M, I]
+  const float* gate;     // [M, I]
+  const float* up;       // [M, I]
   const uint16_t* dh;    // rows lddh apart
   uint16_t* dg;          // [M, I]
   uint16_t* du;          // [M, I]

@@ -59,8 +59,8 @@ def check_forward(x, wg, wu, act, h, gate=None, up=None):
     # |act'| <= 1.13
     close(h, want, e * want.abs() * 1.01 + 1.13 * dg * (u.abs() + du) + a.abs() * du + FAST * want.abs(), "h")
     if gate is not None:
-        close(gate, g, e * g.abs() * 1.01 + dg, "gate")
-        close(up, u, e * u.abs() * 1.01 + du, "up")
+        close(gate, g, dg, "gate")
+        close(up, u, du, "up")
 
 
 def check_backward(x, wg, wu, gate, up, dh, act, dx, dwg, dwu):
@@ -176,11 +176,11 @@ def test_large_gate_values(m, act):
     wg = (gates / 8)[:, None].expand(8, 64).bfloat16().contiguous()
     wu = torch.full((8, 64), 0.125, dtype=torch.bfloat16, device="cuda")
     h, gate, up = m.nvfp4_gated_ffn(x, wg, wu, act, save=True)
-    assert torch.equal(h[:, 4:], gate[:, 4:]) and (h[:, :4].abs() < 1e-20).all()
+    assert torch.equal(h[:, 4:].float(), gate[:, 4:]) and (h[:, :4].abs() < 1e-20).all()
     dh = torch.ones_like(h)
     dx, dwg, dwu = m.nvfp4_gated_ffn_backward(x, wg, wu, gate, up, dh, act)
     assert torch.equal(dwg[4:], x.t()[:1].expand(4, 64) * 0 + 8) and (dwg[:4].abs() < 1e-20).all()
-    assert torch.equal(dwu[4:], gate[:1, 4:].t().expand(4, 64) * 8)
+    assert torch.equal(dwu[4:].float(), gate[:1, 4:].t().expand(4, 64) * 8)
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
@@ -253,7 +253,7 @@ def test_refusals(m):
         m.nvfp4_gated_ffn(wide[:, 4:36], wg, wu)  # rows that do not start at 16 bytes
     assert e.value.status == -3
     for bad in (dict(gate=gate[:, :56]), dict(dh=dh[:3]), dict(dx=torch.empty(4, 40, dtype=x.dtype, device="cuda")),
-                dict(up=torch.empty(4, 72, dtype=x.dtype, device="cuda")[:, :64])):
+                dict(up=torch.empty(4, 72, device="cuda")[:, :64]), dict(gate=gate.bfloat16())):
         with pytest.raises(TypeError):
             m.nvfp4_gated_ffn_backward(**{**dict(x=x, w_gate=wg, w_up=wu, gate=gate, up=up, dh=dh), **bad})
     with pytest.raises(m.NVFP4Error) as e:
