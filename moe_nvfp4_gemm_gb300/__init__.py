@@ -1003,19 +1003,18 @@ def nvfp4_grad_clip(grads, max_norm=math.inf, out=None, norm=None, workspace=Non
     if stream is not None:
         return _on_stream(stream, nvfp4_grad_clip, locals())
     grads = list(grads)
-    n, here = len(grads), torch._C._cuda_getDevice()
+    n = len(grads)
     dev, (pointers, counts, kinds) = grads[0].device if n else "cuda", _list_types(n)
-    for t in grads:
-        if not (t.dtype in _GRAD_TYPES and t.is_cuda and t.is_contiguous() and t.get_device() == here):
-            raise TypeError("grads must be contiguous tensors of torch.bfloat16, float16 or float32 on the current CUDA device")
+    # list by list: a list's check costs half of one tensor by tensor, and lists may be long
+    here, types = [torch._C._cuda_getDevice()] * n, [t.dtype for t in grads]
+    if [t.get_device() for t in grads] != here or not _GRAD_TYPES.keys() >= set(types) or not all([t.is_contiguous() for t in grads]):
+        raise TypeError("grads must be contiguous tensors of torch.bfloat16, float16 or float32 on the current CUDA device")
     to = None
     if out is not None:
         out = list(out)
-        if len(out) != n:
-            raise TypeError(f"out has {len(out)} tensors, grads {n}")
-        for t, o in zip(grads, out):
-            if not (o.dtype == t.dtype and o.shape == t.shape and o.is_cuda and o.is_contiguous() and o.get_device() == here):
-                raise TypeError("out must hold tensors like grads")
+        if ([o.dtype for o in out] != types or [o.get_device() for o in out] != here or [o.shape for o in out] != [t.shape for t in grads]
+                or not all([o.is_contiguous() for o in out])):
+            raise TypeError("out must hold contiguous tensors of the types and shapes of grads, on the same device")
         to = pointers(*[o.data_ptr() for o in out])
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
@@ -1023,7 +1022,7 @@ def nvfp4_grad_clip(grads, max_norm=math.inf, out=None, norm=None, workspace=Non
         workspace = torch.empty(_clip_workspace_bytes(n), dtype=torch.uint8, device=dev)
     _check("nvfp4_grad_clip",
            lib().nvfp4_grad_clip(pointers(*[t.data_ptr() for t in grads]), to, counts(*[t.numel() for t in grads]),
-                                 kinds(*[_GRAD_TYPES[t.dtype] for t in grads]), n, max_norm, _operand(norm, _F32, (1,), "norm"),
+                                 kinds(*[_GRAD_TYPES[t] for t in types]), n, max_norm, _operand(norm, _F32, (1,), "norm"),
                                  _operand(workspace, _U8, (0,), "workspace"), workspace.numel(), _stream()))
     return norm
 

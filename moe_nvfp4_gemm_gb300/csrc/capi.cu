@@ -1660,6 +1660,7 @@ int nvfp4_grad_clip(const void* const* grads, void* const* out, const int64_t* n
     int64_t chunks = 0;
     for (int32_t i = g.first; i < g.end; ++i) chunks += (numel[i] + kClipChunk - 1) / kClipChunk;
     if (chunks > kMaxDim) return false;
+    g.chunks = static_cast<int>(chunks);
     g.grid = static_cast<int>(chunks < kClipBlocks ? chunks : kClipBlocks);
     return true;
   };
@@ -1667,6 +1668,10 @@ int nvfp4_grad_clip(const void* const* grads, void* const* out, const int64_t* n
   for (int32_t i = 0; i < count; i += kClipGroup) {
     if (!group(i, a.slots, g)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     a.slots += g.grid;
+  }
+  if (count <= kClipGroup && group(0, 0, g) && g.chunks <= kClipFew) {
+    g_last_launches = 1;
+    return from_cuda(launch_clip_group(a, g, kClipAll, st));
   }
   for (int pass = 0; pass < 2; ++pass) {
     int slot0 = 0;
@@ -1677,7 +1682,7 @@ int nvfp4_grad_clip(const void* const* grads, void* const* out, const int64_t* n
       const bool wanted = pass == 0 ? g.grid > 0 : (first || (a.scale && g.grid > 0));
       if (wanted) {
         g.slot0 = pass == 1 ? !first : g.slot0;
-        if ((rc = from_cuda(launch_clip_group(a, g, pass == 1, st)))) return rc;
+        if ((rc = from_cuda(launch_clip_group(a, g, pass == 1 ? kClipScale : kClipNorm, st)))) return rc;
         ++g_last_launches;
       }
       first = false;

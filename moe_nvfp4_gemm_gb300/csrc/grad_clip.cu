@@ -5,7 +5,9 @@
 // more for the scaling, and written once. The list travels in the kernels' parameters (no copy to the
 // device, so that a captured graph carries it); it is cut into chunks of 16,384 values, which a fixed grid
 // walks in strides, so that the order of the sums, and with it every bit of the result, depends on the sizes
-// alone. The second kernel walks the chunks backwards: the last ones read are still in L2.
+// alone. The second kernel walks the chunks backwards: the last ones read are still in L2. Lists of up to 16
+// chunks take one launch: a cluster of eight CTAs, whose sums meet in distributed shared memory.
+// (0.8 billion bf16 values: norm 230 us, scaling 495 us, the bytes of both passes at 6.7 TB/s.)
 //
 // Squares: a thread adds those of a chunk (up to 64) in fp32 and joins chunks in fp64. Where that fp32 sum is
 // infinite (|g| > 2^63) or so small that squares fell below fp32's range, the thread's values are added
@@ -144,13 +146,11 @@ DEVI double chunk_squares(const void* p, int64_t i0, int64_t i1) {
   return d;
 }
 
+// Squares of the chunks first, first + step, ... of this thread.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ ClipTable<N> t) {
-  __shared__ double sh[kThreads / 32];
-  griddep_wait();
-  griddep_launch_dependents();
+DEVI double list_squares(const ClipTable<N>& t, int first, int step) {
   double sum = 0.0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  for (int c = first; c < t.chunks; c += step) {
     const ClipEntry& e = t.e[clip_entry(t, c)];
     const int64_t i0 = static_cast<int64_t>(c - e.first) * kChunk;
     const int64_t i1 = i0 + kChunk < e.numel ? i0 + kChunk : e.numel;
@@ -161,7 +161,15 @@ __global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ 
     else
       sum += chunk_squares<kClipBf16>(e.src, i0, i1);
   }
-  sum = block_sum(sum, sh);
+  return sum;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ ClipTable<N> t) {
+  __shared__ double sh[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const double sum = block_sum(list_squares(t, blockIdx.x, gridDim.x), sh);
   if (threadIdx.x == 0) t.partial[t.slot0 + blockIdx.x] = sum;
 }
 
@@ -212,19 +220,12 @@ DEVI void scale_chunk(const void* p, void* out, int64_t i0, int64_t i1, float f)
   if (tail + threadIdx.x < i1) scale_single<TYPE>(p, out, tail + threadIdx.x, f);
 }
 
+// The chunks of the list times min(1, max_norm / (norm + 1e-6)), the last ones first.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipTable<N> t) {
-  __shared__ double sh[kThreads / 32];
-  griddep_wait();
-  griddep_launch_dependents();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < t.slots; i += kThreads) sum += t.partial[i];
-  const float norm = static_cast<float>(sqrt(block_sum(sum, sh)));
-  if (blockIdx.x == 0 && threadIdx.x == 0 && t.slot0 == 0) *t.norm = norm;
-  if (!t.scale) return;
+DEVI void list_scale(const ClipTable<N>& t, float norm, int first, int step) {
   const float q = t.max_norm / (norm + 1e-6f);
   const float f = q > 1.0f ? 1.0f : q;  // NaN stays
-  for (int c = t.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+  for (int c = t.chunks - 1 - first; c >= 0; c -= step) {
     const ClipEntry& e = t.e[clip_entry(t, c)];
     if (f == 1.0f && e.src == e.dst) continue;  // nothing changes
     const int64_t i0 = static_cast<int64_t>(c - e.first) * kChunk;
@@ -238,24 +239,59 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   }
 }
 
+template <int N>
+__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipTable<N> t) {
+  __shared__ double sh[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < t.slots; i += kThreads) sum += t.partial[i];
+  const float norm = static_cast<float>(sqrt(block_sum(sum, sh)));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && t.slot0 == 0) *t.norm = norm;
+  if (t.scale) list_scale(t, norm, blockIdx.x, gridDim.x);
+}
+
+// The whole list in one cluster.
+template <int N>
+__global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant__ ClipTable<N> t) {
+  __shared__ double sh[kThreads / 32], mine;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rank = static_cast<int>(cluster_ctarank());
+  const double sum = block_sum(list_squares(t, rank, kClipCluster), sh);
+  if (threadIdx.x == 0) mine = sum;
+  cluster_sync();
+  double total = 0.0;
+#pragma unroll
+  for (int r = 0; r < kClipCluster; ++r) total += ld_shared_cluster_f64(mapa_shared(smem_u32(&mine), r));
+  const float norm = static_cast<float>(sqrt(total));
+  if (rank == 0 && threadIdx.x == 0) *t.norm = norm;
+  if (t.scale) list_scale(t, norm, rank, kClipCluster);
+  cluster_sync();  // no CTA leaves while another may still read its sum
+}
+
 template <typename Kernel, typename Table>
-cudaError_t launch_clip(Kernel kernel, int grid, cudaStream_t st, const Table& t) {
+cudaError_t launch_clip(Kernel kernel, int grid, int cluster, cudaStream_t st, const Table& t) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, t);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// One kernel of the pair for the entries [first, first + count) of the list.
+// One kernel for the entries of a group.
 template <int N>
-cudaError_t run_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaStream_t st) {
+cudaError_t run_group(const ClipArgs& a, const ClipGroup& g, ClipStep step, cudaStream_t st) {
   static_assert(sizeof(ClipTable<N>) <= 32764, "kernel parameters");
   ClipTable<N> t;
   t.count = 0;
@@ -273,16 +309,18 @@ cudaError_t run_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaSt
   t.norm = a.norm;
   t.max_norm = a.max_norm;
   t.scale = a.scale;
-  if (second) return launch_clip(k_clip_scale<N>, a.scale && g.grid > 0 ? g.grid : 1, st, t);
-  return launch_clip(k_clip_norm<N>, g.grid, st, t);
+  if (step == kClipAll) return launch_clip(k_clip_cluster<N>, kClipCluster, kClipCluster, st, t);
+  if (step == kClipScale) return launch_clip(k_clip_scale<N>, a.scale && g.grid > 0 ? g.grid : 1, 1, st, t);
+  return launch_clip(k_clip_norm<N>, g.grid, 1, st, t);
 }
 
 }  // namespace
 
-cudaError_t launch_clip_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaStream_t st) {
+cudaError_t launch_clip_group(const ClipArgs& a, const ClipGroup& g, ClipStep step, cudaStream_t st) {
   const int n = g.end - g.first;  // short lists in a short table: the parameters are copied with every launch
-  if (n <= 64) return run_group<64>(a, g, second, st);
-  return run_group<kClipGroup>(a, g, second, st);
+  if (n <= 16) return run_group<16>(a, g, step, st);
+  if (n <= 128) return run_group<128>(a, g, step, st);
+  return run_group<kClipGroup>(a, g, step, st);
 }
 
 }  // namespace nvfp4

@@ -296,6 +296,8 @@ cudaError_t launch_int8_quantize(const Int8QuantArgs& p, int sms, cudaStream_t s
 constexpr int kClipChunk = 16384;  // values that a block takes at a time
 constexpr int kClipGroup = 960;    // gradients a launch takes (its parameters hold the list)
 constexpr int kClipBlocks = 608;   // blocks of a launch at most: four on each SM
+constexpr int kClipCluster = 8;    // CTAs that take a short list, of up to kClipFew chunks, in one launch
+constexpr int kClipFew = 16;
 enum { kClipBf16 = 0, kClipF32 = 1, kClipF16 = 2 };
 struct ClipEntry {
   const void* src;
@@ -317,6 +319,7 @@ struct ClipArgs {
 };
 struct ClipGroup {
   int first, end;  // gradients of this launch
+  int chunks;
   int slot0, grid;
 };
 // Entry i of the list; false where it has no values.
@@ -327,8 +330,9 @@ inline bool clip_list_entry(const ClipArgs& a, int i, ClipEntry& e) {
   e.type = a.types[i];
   return e.numel > 0;
 }
-// `second`: the kernel that joins the sums and scales
-cudaError_t launch_clip_group(const ClipArgs& a, const ClipGroup& g, bool second, cudaStream_t st);
+// The sums of squares; the kernel that joins them and scales; or both, for a list of few chunks.
+enum ClipStep { kClipNorm, kClipScale, kClipAll };
+cudaError_t launch_clip_group(const ClipArgs& a, const ClipGroup& g, ClipStep step, cudaStream_t st);
 
 int stream_smem_bytes(int stages, int x_rows, int recv_bytes, bool sparse = false);
 // shared memory after the ring for one tile's token indices (and with qout the epilogue's

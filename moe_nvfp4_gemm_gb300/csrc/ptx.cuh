@@ -300,6 +300,11 @@ DEVI void mbar_arrive_operands(uint32_t cluster_addr) {
 }
 
 // Eight bytes from any CTA's shared memory of the cluster.
+DEVI double ld_shared_cluster_f64(uint32_t cluster_addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 DEVI float2 ld_shared_cluster_v2(uint32_t cluster_addr) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
