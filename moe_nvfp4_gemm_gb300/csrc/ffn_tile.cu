@@ -219,6 +219,8 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     __syncwarp();
   } else if (warp == 0) {
     const uint64_t pol = policy_evict_last();
+    // weights that one row of tiles reads once are not kept
+    const uint64_t pol_w = FORWARD && p.in[0].mt == 1 ? policy_evict_first() : pol;
     int s = 0, issued = 0;
     uint32_t ph = 0;
     uint32_t used = 0, phases = 0;  // per stage: requested at all, phase of the last request
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
           if constexpr (FORWARD) {
             tma_load_2d_pair(st, &maps.a[0], bar, kb * 64, am, pol);
-            tma_load_2d_pair(st + C::TILE_BYTES, &maps.b[rank], bar, kb * 64, bn, pol);
+            tma_load_2d_pair(st + C::TILE_BYTES, &maps.b[rank], bar, kb * 64, bn, pol_w);
           } else {
             // boxes of 64 x 64. Input: the contraction is the gate's columns, then the up's; dg and du lie along it.
             // Weight: all operands lie along their rows.
