@@ -3,10 +3,10 @@
 // (padded to 16) on its N side, so that no token is padded to a tile of 256.
 //
 // Bound by reading the weights, each once, in 64-column blocks by TMA; the tokens come from L2. A CTA
-// takes one tile of 64 columns of h (two CTAs share an SM, so that all tiles of a
-// layer of 19,456 are in flight at once and the uneven rest of a division by 152 costs nothing: an SM
-// with two tiles draws twice the bandwidth). The tensor core sums all of K in TMEM; the four epilogue warps put
+// takes one tile of 64 columns of h. Two CTAs share an SM, so that all tiles of a layer of up to 19,456 columns are in
+// flight at once and the uneven rest of a division by 152 costs nothing: an SM with two tiles draws twice the bandwidth. The tensor core sums all of K in TMEM; the four epilogue warps put
 // the sums into shared memory, where gate and up of a column, which lie in different lanes, meet.
+// One token of 14,336 x 8,192: 72 us, 6.5 TB/s; 128 tokens 78.
 // Few tiles: S CTAs of a cluster sum a part of K each, and each reads all parts' sums of its share of the tokens
 // through distributed shared memory.
 #include <stdint.h>

