@@ -482,8 +482,8 @@ int nvfp4_fp8_grouped_gemm(const uint8_t* a, const float* sa, const uint8_t* b, 
  *   gate, up   fp32 [M, I] contiguous, 32-byte aligned, written: g and u as they are summed, for the backward call;
  *              or both NULL
  *   workspace  nvfp4_gated_ffn_workspace_bytes(M, I, K) bytes, 16-byte aligned (NULL where that is 0)
- * I, K and the row strides are multiples of 8, pointers 16-byte aligned, I and K at most 2^24. A NaN or an
- * infinity stays in its token's row. dev_status as for nvfp4_gemm.
+ * I, K and the row strides are multiples of 8, pointers 16-byte aligned, I and K at most 2^24. h, gate and up share no
+ * element with an operand. A NaN or an infinity stays in its token's row. dev_status as for nvfp4_gemm.
  */
 enum { NVFP4_SILU = 0, NVFP4_GELU_TANH = 1 };
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K);
@@ -501,6 +501,7 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
  *   dx         [M, K] contiguous, written, or NULL: not wanted (w_gate and w_up may then be NULL)
  *   dw_gate, dw_up  [I, K] contiguous, written, or NULL each (x may be NULL when both are). M == 0 writes zeros.
  *   workspace  nvfp4_gated_ffn_backward_workspace_bytes(M, I, K) bytes, 256-byte aligned
+ * No result may share memory with another, with the workspace or with an operand: NVFP4_ERR_INVALID_ARG.
  * The weights' gradients sum over all M rows: a NaN in a row of x, gate, up or dh reaches all that it
  * meets, so padding rows must hold finite values (and dh zeros).
  */
@@ -516,7 +517,7 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
  * every step, 1/127 and 1/amax_row too, one IEEE fp32 operation (rows with amax below 2^-100 are first multiplied by 2^100). A row that holds
  * an infinity or NaN gets codes 0 and scale NaN: what is made of it is NaN.
  *   x     device [M, K], bf16 or fp16 (type), rows ldx elements apart (a multiple of 8), 16-byte aligned
- *   q, s  int8 [M, K], 16-byte aligned, and fp32 [M], written. K % 16 == 0.
+ *   q, s  int8 [M, K], 16-byte aligned, and fp32 [M], written. K % 16 == 0 (K == 0: scales of 1).
  */
 int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M, int64_t K, int8_t* q, float* s, void* stream);
 

@@ -852,6 +852,14 @@ def _rows(t, dtype, shape, name):
     return t.data_ptr(), ld
 
 
+def _here(*tensors):
+    """Refuses tensors that lie on another device than the current one."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise TypeError(f"a tensor is on {t.device}, not on the current device")
+
+
 def _ffn_inputs(x, w_gate, w_up, activation):
     """M, I, K, the codes of the type and of the activation."""
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _HALF_TYPES and x.dim() == 2):
@@ -880,6 +888,7 @@ def nvfp4_gated_ffn(x, w_gate, w_up, activation="silu", save=False, h=None, work
         gate, up = torch.empty((M, I), dtype=torch.float32, device=dev), torch.empty((M, I), dtype=torch.float32, device=dev)
         pg, pu = gate.data_ptr(), up.data_ptr()
     ws_bytes, pws = _ffn_workspace_bytes(M, I, K), None
+    _here(workspace, dev_status)
     if workspace is not None:
         pws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
     elif ws_bytes:
@@ -904,6 +913,9 @@ def nvfp4_gated_ffn_backward(x, w_gate, w_up, gate, up, dh, activation="silu", n
             raise TypeError(f"{n} must be contiguous")
         args += (t.data_ptr(),)
     args += _rows(dh, dtype, (M, I), "dh")
+    if len(need) != 3:
+        raise ValueError("need says for dx, dw_gate and dw_up whether they are wanted")
+    _here(workspace, dev_status)
     outs, ptrs = [], []
     for t, wanted, shape, n in zip((dx, dw_gate, dw_up), need, ((M, K), (I, K), (I, K)), ("dx", "dw_gate", "dw_up")):
         if wanted and t is None:
@@ -970,6 +982,7 @@ def nvfp4_int8_gemm(a, sa, b, sb, M: int, N: int, K: int, out_dtype=torch.bfloat
     except TypeError:  # sizes that the library refuses are its error
         _check("nvfp4_int8_gemm", lib().nvfp4_int8_gemm(None, None, None, None, None, y_type, min(M, 0), N, K, None, 0, None, None))
         raise
+    _here(a, sa, b, sb, y, workspace, dev_status)
     ws_bytes, pws = _int8_workspace_bytes(M, N, K), None
     if workspace is not None:
         pws, ws_bytes = _operand(workspace, _U8, (0,), "workspace"), workspace.numel()
@@ -1016,6 +1029,7 @@ def nvfp4_grad_clip(grads, max_norm=math.inf, out=None, norm=None, workspace=Non
                 or not all([o.is_contiguous() for o in out])):
             raise TypeError("out must hold contiguous tensors of the types and shapes of grads, on the same device")
         to = pointers(*[o.data_ptr() for o in out])
+    _here(norm, workspace)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     if workspace is None:

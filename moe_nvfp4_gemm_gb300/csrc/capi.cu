@@ -18,8 +18,8 @@ using namespace nvfp4;
 
 cudaError_t nvfp4::allow_max_smem(const void* func) {
   static std::mutex mu;
-  static const void* seen_fn[64];
-  static int seen_dev[64];
+  static const void* seen_fn[256];
+  static int seen_dev[256];
   static int n_seen = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -29,7 +29,7 @@ cudaError_t nvfp4::allow_max_smem(const void* func) {
     if (seen_fn[i] == func && seen_dev[i] == dev) return cudaSuccess;
   e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   if (e != cudaSuccess) return e;
-  if (n_seen < 64) {
+  if (n_seen < 256) {
     seen_fn[n_seen] = func;
     seen_dev[n_seen] = dev;
     ++n_seen;
@@ -1457,6 +1457,29 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
   if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(gate) || !aligned16(up) || !aligned16(dh) ||
       !aligned16(dx) || !aligned16(dw_gate) || !aligned16(dw_up) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return NVFP4_ERR_ALIGNMENT;
+  {
+    // the products run at the same time: what one writes the other may still read
+    const struct {
+      const void* p;
+      int64_t bytes;
+      bool written;
+    } spans[] = {{dx, M * K * 2, true},
+                 {dw_gate, I * K * 2, true},
+                 {dw_up, I * K * 2, true},
+                 {workspace, M * I * 4, true},
+                 {x, M > 0 ? ((M - 1) * ldx + K) * 2 : 0, false},
+                 {w_gate, ((I - 1) * ld_gate + K) * 2, false},
+                 {w_up, ((I - 1) * ld_up + K) * 2, false},
+                 {gate, M * I * 4, false},
+                 {up, M * I * 4, false},
+                 {dh, M > 0 ? ((M - 1) * lddh + I) * 2 : 0, false}};
+    for (const auto& a : spans)
+      for (const auto& b : spans) {
+        if (&a == &b || !a.written || !a.p || !b.p) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(a.p), bt = reinterpret_cast<uintptr_t>(b.p);
+        if (at < bt + static_cast<uintptr_t>(b.bytes) && bt < at + static_cast<uintptr_t>(a.bytes)) return NVFP4_ERR_INVALID_ARG;
+      }
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DevInfo d;
   if (M == 0) {  // no tokens: the weights' gradients are sums over none
@@ -1508,8 +1531,8 @@ int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M,
   if (K % 16 != 0 || M > kMaxFp8Dim || K > kMaxFp8Dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   int rc = check_ld(ldx, K);
   if (rc) return rc;
-  if (M == 0 || K == 0) return NVFP4_OK;
-  if (!x || !q || !s) return NVFP4_ERR_INVALID_ARG;
+  if (M == 0) return NVFP4_OK;
+  if (!s || (K > 0 && (!x || !q))) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned4(s)) return NVFP4_ERR_ALIGNMENT;
   DevInfo d;
   if ((rc = device_info(d))) return rc;

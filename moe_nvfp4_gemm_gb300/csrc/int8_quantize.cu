@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(1024) k_int8_quantize(const __grid_constant__ 
 cudaError_t launch_int8_quantize(const Int8QuantArgs& p, int sms, cudaStream_t st) {
   const bool is_long = p.K > 1024 * kVec * 8;
   int threads = is_long ? 1024 : static_cast<int>((p.K / 8 + kVec * 32 - 1) / (kVec * 32)) * 32;
+  if (threads == 0) threads = 32;  // rows without values: scale 1
   const int64_t resident = static_cast<int64_t>(sms) * (2048 / threads < 32 ? 2048 / threads : 32) * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.M < resident ? p.M : resident));

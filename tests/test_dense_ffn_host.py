@@ -45,8 +45,9 @@ def test_gated_workspaces(lib):
 
 def test_gated_backward_host_validation(lib):
     need = lib.nvfp4_gated_ffn_backward_workspace_bytes(300, 128, 256)
-    def call(x=64, ldx=256, wg=64, wu=64, gate=64, up=64, dh=64, lddh=128, kind=2, act=1, dx=64, dwg=64, dwu=64, M=300, I=128, K=256,
-             ws=256, wsb=need):
+    apart = 1 << 24  # bytes between two operands
+    def call(x=64, ldx=256, wg=64 + apart, wu=64 + 2 * apart, gate=64 + 3 * apart, up=64 + 4 * apart, dh=64 + 5 * apart, lddh=128, kind=2,
+             act=1, dx=64 + 6 * apart, dwg=64 + 7 * apart, dwu=64 + 8 * apart, M=300, I=128, K=256, ws=256 + 9 * apart, wsb=need):
         return lib.nvfp4_gated_ffn_backward(P(x), ldx, P(wg), 256, P(wu), 256, P(gate), P(up), P(dh), lddh, kind, act, P(dx), P(dwg),
                                             P(dwu), M, I, K, P(ws), wsb, None, None)
     assert call(dx=0, dwg=0, dwu=0) == 0 and call(M=0, dwg=0, dwu=0) == 0     # nothing to do
@@ -54,12 +55,16 @@ def test_gated_backward_host_validation(lib):
     assert call(gate=0) == -1 and call(dh=0) == -1 and call(x=0) == -1 and call(wg=0) == -1
     assert call(dh=72) == -3 and call(dx=8) == -3 and call(ws=128) == -3
     assert call(ws=0) == -6 and call(wsb=need - 1) == -6
+    # results over an operand, another result or the workspace: by a byte, or entirely
+    assert call(dx=64) == -1 and call(dx=64 + 300 * 512 - 16) == -1 and call(dx=64 + 300 * 512, wsb=0) == -6
+    assert call(dwg=64 + 8 * apart) == -1 and call(dwu=64 + apart) == -1 and call(ws=256 + 5 * apart) == -1
+    assert call(dx=64 + 3 * apart + 300 * 128 * 4 - 16) == -1
 
 
 def test_int8_host_validation(lib):
     def quantise(x=16, ldx=64, kind=0, M=4, K=64, q=16, s=16):
         return lib.nvfp4_int8_quantize(P(x), ldx, kind, M, K, P(q), P(s), None)
-    assert quantise(M=0) == 0 and quantise(K=0) == 0
+    assert quantise(M=0) == 0 and quantise(K=0, s=0) == -1
     assert quantise(M=-1) == -1 and quantise(kind=1) == -1 and quantise(ldx=56) == -1 and quantise(K=56) == -2 and quantise(ldx=68) == -2
     assert quantise(x=0) == -1 and quantise(s=0) == -1 and quantise(x=8) == -3 and quantise(q=8) == -3 and quantise(s=18) == -3
 

@@ -256,6 +256,11 @@ def test_refusals(m):
                 dict(up=torch.empty(4, 72, device="cuda")[:, :64]), dict(gate=gate.bfloat16())):
         with pytest.raises(TypeError):
             m.nvfp4_gated_ffn_backward(**{**dict(x=x, w_gate=wg, w_up=wu, gate=gate, up=up, dh=dh), **bad})
+    with pytest.raises(ValueError):
+        m.nvfp4_gated_ffn_backward(x, wg, wu, gate, up, dh, need=(True, True))
+    with pytest.raises(m.NVFP4Error) as e:  # over an operand that the other product still reads
+        m.nvfp4_gated_ffn_backward(x, wg, wu, gate, up, dh, dx=x)
+    assert e.value.status == -1
     with pytest.raises(m.NVFP4Error) as e:
         m.nvfp4_gated_ffn_backward(x, wg, wu, gate, up, dh, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -6

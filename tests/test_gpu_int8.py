@@ -222,4 +222,6 @@ def test_refusals(m):
         m.nvfp4_int8_quantize(x[:, :24])
     assert e.value.status == -2
     assert m.nvfp4_int8_quantize(x[:0])[0].shape == (0, 32)
+    q, s = m.nvfp4_int8_quantize(x[:, :0])  # rows without values are rows of zeros
+    assert q.shape == (4, 0) and (s == 1).all()
     assert math.isfinite(float(m.nvfp4_int8_quantize(x)[1][0]))
