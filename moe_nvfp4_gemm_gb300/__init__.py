@@ -1,4 +1,4 @@
-"""Thin Python binding of the NVFP4 C ABI (include/nvfp4.h).
+"""Thin Python binding of the NVFP4 C ABI (include/nvfp4.h, include/nvfp4_ffn.h).
 
 Argument marshalling only: every entry point takes torch CUDA tensors, passes
 their data pointers and the current CUDA stream to the function of the same
@@ -53,10 +53,11 @@ EXPORTS = ["nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_amax_workspace_byt
            "nvfp4_sparse_gemm", "nvfp4_grouped_sparse_gemm", "nvfp4_gemm_batched",
            "nvfp4_grouped_gemm_swiglu_quantize_out",
            "nvfp4_moe_route_workspace_bytes", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_fp8_quantize",
-           "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm_workspace_bytes", "nvfp4_fp8_grouped_gemm",
-           "nvfp4_gated_ffn_workspace_bytes", "nvfp4_gated_ffn", "nvfp4_gated_ffn_backward_workspace_bytes",
-           "nvfp4_gated_ffn_backward", "nvfp4_int8_quantize", "nvfp4_int8_gemm_workspace_bytes",
-           "nvfp4_int8_gemm", "nvfp4_grad_clip_workspace_bytes", "nvfp4_grad_clip"]
+           "nvfp4_fp8_gemm", "nvfp4_fp8_grouped_gemm_workspace_bytes", "nvfp4_fp8_grouped_gemm"]
+# of include/nvfp4_ffn.h
+EXPORTS_FFN = ["nvfp4_gated_ffn_workspace_bytes", "nvfp4_gated_ffn", "nvfp4_gated_ffn_backward_workspace_bytes",
+               "nvfp4_gated_ffn_backward", "nvfp4_int8_quantize", "nvfp4_int8_gemm_workspace_bytes", "nvfp4_int8_gemm",
+               "nvfp4_grad_clip_workspace_bytes", "nvfp4_grad_clip"]
 
 
 class NVFP4Error(RuntimeError):

@@ -19,8 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libnvfp4.so")
 SOURCES = ["capi.cu", "quantize.cu", "gemm_dense.cu", "gemm_stream.cu", "sparse.cu", "moe_route.cu",
-           "fp8_quantize.cu", "fp8_gemm.cu", "fp8_narrow.cu", "fp8_stream.cu", "ffn_tile.cu", "ffn_stream.cu", "int8_quantize.cu", "int8_gemm.cu",
-           "grad_clip.cu"]
+           "fp8_quantize.cu", "fp8_gemm.cu", "fp8_narrow.cu", "fp8_stream.cu", "ffn_tile.cu", "ffn_stream.cu",
+           "int8_quantize.cu", "int8_gemm.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -41,7 +41,7 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(INCLUDE, "nvfp4.h"))
+    headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     nvcc = _nvcc()
     common = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
               *ARCH, *extra_flags]

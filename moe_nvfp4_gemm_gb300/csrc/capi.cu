@@ -1,5 +1,5 @@
 // C ABI: argument validation, TMA descriptor encoding, plan selection and
-// launches. Declarations and the contract of every entry point: include/nvfp4.h.
+// launches. Declarations and the contract of every entry point: include/nvfp4.h and nvfp4_ffn.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -10,6 +10,7 @@
 #include <new>
 
 #include "nvfp4.h"
+#include "nvfp4_ffn.h"
 #include "kernels.h"
 #include "ptx.cuh"
 

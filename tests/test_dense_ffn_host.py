@@ -1,6 +1,9 @@
 """CPU checks of the gated block's, the int8 operators' and clipping's entry points: arguments rejected before the device is
 touched, and the workspace sizes."""
 import ctypes
+import inspect
+import os
+import re
 
 import pytest
 
@@ -14,6 +17,26 @@ def lib():
     build.build()
     import moe_nvfp4_gemm_gb300 as m
     return m.lib()
+
+
+def test_every_declared_symbol_is_exported(lib):
+    import moe_nvfp4_gemm_gb300 as m
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "nvfp4_ffn.h")
+    src = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(nvfp4_[a-z0-9_]+)\s*\(", src)))
+    assert sorted(m.EXPORTS_FFN) == names and all(hasattr(lib, n) for n in names) and all(hasattr(m, n) for n in names)
+
+
+def test_every_call_with_a_stream_runs_on_it(monkeypatch):
+    import moe_nvfp4_gemm_gb300 as m
+    monkeypatch.setattr(m, "_on_stream", lambda stream, fn, args: (stream, fn, args))
+    names = [n for n in m.EXPORTS_FFN if not n.endswith("_workspace_bytes")]
+    assert len(names) == 5
+    for n in names:
+        fn = getattr(m, n)
+        given = {p: i for i, p in enumerate(inspect.signature(fn).parameters)}
+        assert fn(**given) == (given["stream"], fn, given)  # before anything is looked at or allocated
+        assert "dev_status" not in given or "_status(dev_status)" in inspect.getsource(fn)
 
 
 def test_gated_host_validation(lib):
