@@ -55,7 +55,7 @@ DEVI FfnItem ffn_item(const FfnTileArgs& p, int i) {
   i -= it.which * per_result;
   it.part = i / tiles;
   int mb, nb;
-  tile_coords(i - it.part * tiles, q.mt, q.nt, p.raster, mb, nb);
+  tile_coords(i - it.part * tiles, q.mt, q.nt, q.raster, mb, nb);
   it.m0 = mb * 256;
   it.n0 = nb * 256;
   it.kb0 = static_cast<int>(static_cast<int64_t>(q.kblocks) * it.part / q.split);

@@ -77,8 +77,9 @@ struct Int8Tile {
 };
 
 DEVI Int8Tile int8_tile(const Int8GemmArgs& p, int t, int nt_tokens) {
-  // tokens fastest: the pairs that run at one time share the weights
-  return {t % p.mt * nt_tokens, t / p.mt * 256};
+  int mb, nb;
+  tile_coords(t, p.mt, p.nt, p.raster, mb, nb);
+  return {mb * nt_tokens, nb * 256};
 }
 
 // Four bytes, signed, as two pairs of fp16.

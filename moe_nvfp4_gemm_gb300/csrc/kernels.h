@@ -218,11 +218,11 @@ struct FfnProduct {
   int kblocks;  // blocks of 64 of the contraction
   int split;    // its parts
   int items;    // tiles x parts x results
+  int raster;   // tile order, see tile_coords
   float* ws;    // split > 1: fp32 [results][split][mt * 256][nt * 256]
 };
 struct FfnTileArgs {
   FfnProduct in[2];  // forward: one; gradients: of the input and of the weights (no items: not wanted)
-  int raster;        // tile order, see tile_coords
   int act, save;     // forward: activation; also write gate and up
   int up_first;      // gradients: the weights' first result is w_up's
   int half;          // fp16 instead of bf16
@@ -279,6 +279,7 @@ struct Int8GemmArgs {
   int64_t M, N, K;
   int mt, nt;       // tiles: tokens, 256 channels
   int split;        // pairs of a cluster, along K
+  int raster;       // tile order, see tile_coords
   int out;
   int drop_stage;   // test hook: k >= 1 withholds the k-th stage CTA 0 loads (0: none)
   int32_t* status;
