@@ -1271,11 +1271,20 @@ static void ffn_product(FfnProduct& q, int64_t M, int64_t N, int64_t tile_cols, 
   q.kblocks = static_cast<int>(kblocks);
   q.split = 1;
   q.items = q.mt * q.nt * results;
-  // The 76 pairs that run at one time take a block of 8 x 9 or 10 tiles, which reads the least of both operands, or, where one
-  // side has few tiles, all of these. Before (tokens or weights' rows first throughout) / so, us: forward
-  // 4,096 x 14,336 x 8,192 983 / 955, 8,192 x 2,816 x 8,192 479 / 441; with gradients 4,096 x 14,336 x 2,048 1,049 / 982,
-  // 8,192 x 4,096 x 4,096 1,061 / 1,008 (runs differ by 2 %).
-  q.raster = g_tune.dense_raster ? g_tune.dense_raster : (q.mt > 12 && q.nt > 12 ? 8 : (q.nt < q.mt ? -1 : 0));
+  // Order of the tiles: bands of rows of tiles, walked column by column, so that what a band reads stays in L2 while the other
+  // operand passes through once: as many as hold 42 MB, 8 to 24, the bands alike (with fewer than 8 or more than 24 the 76
+  // tiles of a moment read too many rows and columns). Products with a short side take all of it at once. Forward, us, all
+  // rows at once / bands of 8 / so: 4,096 x 8,192 x 4,096 271 / 281 / 272, 5,000 x 8,192 x 4,096 332 / 346 / 331,
+  // 7,000 x 5,000 x 5,120 400 / 377 / 370, 12,000 x 4,096 x 4,096 452 / 408 / 397, 4,096 x 14,336 x 8,192 989 / 971 / 971; with
+  // gradients 6,000 x 6,000 x 2,560 738 / 737 / 718 (runs differ by 2 %).
+  q.raster = g_tune.dense_raster;
+  if (q.raster == 0 && (q.mt <= 12 || q.nt <= 12)) {
+    q.raster = q.nt < q.mt ? -1 : 0;
+  } else if (q.raster == 0) {
+    const int most = kblocks >= 160 ? 8 : kblocks <= 53 ? 24 : static_cast<int>(1280 / kblocks);
+    const int bands = (q.mt + most - 1) / most;
+    q.raster = (q.mt + bands - 1) / bands;
+  }
 }
 
 // Parts of the products' contractions, by an estimate of the launch's time in us: all items' blocks spread over the pairs (a
