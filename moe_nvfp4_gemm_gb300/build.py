@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libnvfp4.so")
 SOURCES = ["capi.cu", "quantize.cu", "gemm_dense.cu", "gemm_stream.cu", "sparse.cu", "moe_route.cu",
            "fp8_quantize.cu", "fp8_gemm.cu", "fp8_narrow.cu", "fp8_stream.cu", "ffn_tile.cu", "ffn_stream.cu",
-           "int8_quantize.cu", "int8_gemm.cu", "grad_clip.cu"]
+           "int8_quantize.cu", "int8_gemm.cu", "int8_few.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

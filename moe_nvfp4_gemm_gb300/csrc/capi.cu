@@ -1570,6 +1570,24 @@ size_t nvfp4_int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return static_cast<size_t>(M) * K * 2;
 }
 
+// Warps that share a channel in the kernel of few tokens: rounds of resident CTAs times a CTA's steps of 512 of K and one for its
+// start and sums, at the least. Measured, us, 1 / 2 / 4 / 8 warps (the rule's is the first that is least, or within 5 %):
+//   one token    8,192 x 8,192 12.1 11.0 11.8 12.1   28,672 x 8,192 36.5 32.2 32.6 33.4   4,096 x 4,096 6.2 4.8 4.4 5.0
+//   8 tokens     8,192 x 8,192 16.6 17.9 18.9 21.5   14,336 x 4,096 17.7 16.9 19.6 26.6   1,024 x 8,192 15.4 8.5 5.4 4.4
+static int int8_few_split(int64_t M, int64_t N, int64_t K, int sms) {
+  const int64_t slots = static_cast<int64_t>(sms) * int8_few_resident(M), steps = (K + 511) / 512;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int split = 1; split <= 8; split *= 2) {
+    const int64_t rows = kInt8FewRows / split, ctas = (N + rows - 1) / rows;
+    const int64_t cost = (ctas + slots - 1) / slots * ((steps + split - 1) / split + 1);
+    if (cost >= least) continue;
+    least = cost;
+    best = split;
+  }
+  return best;
+}
+
 int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* y, int32_t y_type, int64_t M,
                     int64_t N, int64_t K, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   g_last_launches = 0;
@@ -1585,6 +1603,12 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
   DevInfo d;
   if ((rc = device_info(d))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M <= kInt8FewTokens && !g_tune.withhold_stage) {  // (the test hook wants a kernel with stages)
+    Int8FewArgs f = {a, b, sa, sb, y, M, N, K, 1, y_type};
+    f.split = int8_few_split(M, N, K, d.sms);
+    g_last_launches = 1;
+    return from_cuda(launch_int8_few(f, st));
+  }
   const int tokens = int8_tile_tokens(M);
   const uint8_t* a8 = reinterpret_cast<const uint8_t*>(a);
   Int8GemmArgs p = {};

@@ -289,6 +289,20 @@ struct Int8GemmArgs {
 // boxes of 64 x 64. tmW: boxes of 128 x 128.
 cudaError_t launch_int8_gemm(const CUtensorMap& tmW, const CUtensorMap& tmX, const Int8GemmArgs& p, int tile_tokens, int sms,
                              cudaStream_t st);
+constexpr int kInt8FewTokens = 8;  // most tokens of the kernel without tensor cores
+constexpr int kInt8FewRows = 32;   // channels of one of its CTAs, over split
+constexpr int int8_few_resident(int64_t M) { return M <= 2 ? 4 : (M <= 4 ? 3 : 2); }  // its CTAs on an SM, by their registers
+struct Int8FewArgs {
+  const int8_t* a;  // [M, K]
+  const int8_t* b;  // [N, K]
+  const float* sa;
+  const float* sb;
+  void* y;
+  int64_t M, N, K;
+  int split;        // warps that share a channel: 1, 2, 4 or 8
+  int out;
+};
+cudaError_t launch_int8_few(const Int8FewArgs& p, cudaStream_t st);
 // n codes (a multiple of 16) to fp16
 cudaError_t launch_int8_widen(const uint8_t* a, void* out, int64_t n, int sms, cudaStream_t st);
 cudaError_t launch_int8_quantize(const Int8QuantArgs& p, int sms, cudaStream_t st);

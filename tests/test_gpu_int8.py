@@ -133,6 +133,54 @@ def test_largest_sums(m, M, K):
     assert torch.equal(y, (a.double() @ b.double().t()).float())
 
 
+# a few tokens take a kernel of their own, up to 8: each number of tokens; channels and K on both sides of its pieces (4
+# channels, 16 bytes, steps of 512 of K), K shared by one to eight warps
+@pytest.mark.parametrize("M", range(1, 10))
+@pytest.mark.parametrize("N,K", [(1, 16), (3, 48), (4, 512), (5, 528), (33, 1040), (257, 4112), (2050, 6160), (29000, 1552), (30000, 512)])
+def test_few_tokens(m, M, N, K):
+    a, b, r = codes(M, M, K), codes(N + K, N, K), rand(M * N)
+    sa, sb = r(M).abs() + 1e-3, r(N).abs() + 1e-4
+    want = product(a, sa, b, sb)
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        y = torch.full((M + 1, N), 7.0, dtype=dtype, device="cuda")
+        m.nvfp4_int8_gemm(a, sa, b, sb, M, N, K, out_dtype=dtype, y=y)
+        assert torch.equal(y[:M], want.to(dtype)) and (y[M] == 7).all()
+    sa[M - 1], sb[N - 1] = float("nan"), float("inf")
+    y = m.nvfp4_int8_gemm(a, sa, b, sb, M, N, K, out_dtype=torch.float32)
+    assert y[M - 1].isnan().all() and torch.equal(y[:M - 1, :N - 1], want[:M - 1, :N - 1])
+    assert torch.equal(y[:, N - 1].isfinite(), torch.zeros(M, dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [2, 7, 12])
+def test_weights_past_32_bits(m, M):
+    N, K, times = 1003, 8192, 540  # 4.4 GB of weights
+    a, b, r = codes(M, M, K), codes(N, N, K), rand(M)
+    sa, sb = r(M).abs() + 1e-3, r(N).abs() + 1e-4
+    y = m.nvfp4_int8_gemm(a, sa, b.repeat(times, 1), sb.repeat(times), M, N * times, K, out_dtype=torch.float32)
+    assert torch.equal(y.view(M, times, N), product(a, sa, b, sb)[:, None].expand(M, times, N))
+
+
+def test_few_tokens_in_a_graph(m):
+    """Quantise and multiply, captured and replayed with other tokens: what the call reads is of this replay."""
+    r = rand(3)
+    x, w = r(4, 2048).bfloat16(), r(3000, 2048).bfloat16()
+    b, sb = m.nvfp4_int8_quantize(w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m.nvfp4_int8_gemm(*m.nvfp4_int8_quantize(x), b, sb, 4, 3000, 2048)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = [m.nvfp4_int8_gemm(*m.nvfp4_int8_quantize(x), b, sb, 4, 3000, 2048, out_dtype=torch.float32) for _ in range(3)]
+    for _ in range(3):
+        x.copy_(r(4, 2048))
+        g.replay()
+        q, s = formula(x)
+        want = product(q, s, b, sb)
+        assert all(torch.equal(t, want) for t in y)
+
+
 def test_longest_sum(m):
     K = 131056
     a, b = (torch.full((n, K), -128, dtype=torch.int8, device="cuda") for n in (2, 3))
