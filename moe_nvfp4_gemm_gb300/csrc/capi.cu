@@ -1555,9 +1555,6 @@ int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M,
   return from_cuda(launch_int8_quantize(a, d.sms, static_cast<cudaStream_t>(stream)));
 }
 
-// Tokens of a tile: two sizes of tiles on the CTAs' own conversion, then 256 from the workspace.
-static int int8_tile_tokens(int64_t M) { return M <= 64 ? 64 : (M <= 128 ? 128 : 256); }
-
 static int check_int8_shape(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N <= 0 || K <= 0) return NVFP4_ERR_INVALID_ARG;
   // 131,071 products of at most 2^14 fit 32 bits
@@ -1565,8 +1562,50 @@ static int check_int8_shape(int64_t M, int64_t N, int64_t K) {
   return ((M + 255) / 256) * ((N + 255) / 256) > kMaxFp8Dim ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
 }
 
+// Tokens of a tile and the parts that its K is cut into (one to a pair of a cluster). Tiles of 256 tokens read the tokens as fp16, which
+// a kernel before writes to the workspace; smaller ones convert them on the way, in every CTA that needs them.
+struct Int8Plan {
+  int tokens, split;
+};
+
+// Parts of K, measured with K = 4096 (32 blocks), us, 1 / 2 / 3 / 4 parts:
+//   tiles        14                  16                  22                  24                  36            38
+//   64 tokens    14.9 10.8 10.0 9.2  14.9 11.0 10.1 17   14.9 11.4 10.5 17   14.9 11.4 19.5 18   15 12 20 26   15 22
+//   300 tokens   28 21 20 18         28 21 20 28         28 22 21 31         29 22 32 32         29 23 36 46   29 38
+// So as many as the tiles' clusters of 8, 6 or 4 CTAs are resident at once. Short K, 8 blocks: 64 tokens, 4 tiles 7.2 7.1
+// 7.1 6.5; 300 tokens, 8 tiles 13.3 13.4 13.4 13.0; 1,000, 16 tiles 13.5 13.8 15.2.
+static int int8_split(int64_t tiles, int64_t kb, int tokens) {
+  const int64_t most = kb / (tokens == 256 ? 8 : 2);
+  const int64_t split = tiles <= 14 ? 4 : (tiles <= 22 ? 3 : (tiles <= 36 ? 2 : 1));
+  return static_cast<int>(split < most ? split : (most < 1 ? 1 : most));
+}
+
+// More than 128 tokens: tiles of 128 or 256, by estimates of the time in us, rounds of the 76 pairs' tiles: 128 tokens 5 and
+// 4.5 a round and 0.36 a block of K; 256 tokens 7, the tokens' bytes as 8 and 16 bits at 5 TB/s, 4 a round and 0.58 a
+// block. Measured, us, 128 / 256 tokens, at 1,024 x 4,096 (channels x K): 256 tokens 12.5 / 16.8, 1,024 16.3 / 22.0; 4,096 x 4,096:
+// 256 16.3 / 20.7, 512 21.0 / 24.0, 727 34.4 / 31.3, 1,536 48.1 / 52.1; 8,192 x 8,192: 256 36.0 / 33.9, 512 61.6 / 51.7, 727
+// 87.1 / 92.4, 1,536 166 / 138.
+static Int8Plan int8_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t nt = (N + 255) / 256, kb = (K + 127) / 128;
+  if (M <= 128) {
+    const int tokens = M <= 64 ? 64 : 128;
+    return {tokens, int8_split(nt, kb, tokens)};
+  }
+  Int8Plan plan[2];
+  double cost[2];
+  for (int i = 0; i < 2; ++i) {
+    const int tokens = 128 << i;
+    const int64_t tiles = (M + tokens - 1) / tokens * nt;
+    plan[i] = {tokens, int8_split(tiles, kb, tokens)};
+    const int64_t rounds = plan[i].split > 1 ? 1 : (tiles + kPairs - 1) / kPairs;
+    const double blocks = static_cast<double>((kb + plan[i].split - 1) / plan[i].split);
+    cost[i] = i == 0 ? 5.0 + rounds * (4.5 + 0.36 * blocks) : 7.0 + 3.0 * M * K / 5e6 + rounds * (4.0 + 0.58 * blocks);
+  }
+  return plan[cost[1] <= cost[0]];
+}
+
 size_t nvfp4_int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (check_int8_shape(M, N, K) || int8_tile_tokens(M) != 256) return 0;
+  if (check_int8_shape(M, N, K) || M == 0 || int8_plan(M, N, K).tokens != 256) return 0;
   return static_cast<size_t>(M) * K * 2;
 }
 
@@ -1609,7 +1648,8 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
     g_last_launches = 1;
     return from_cuda(launch_int8_few(f, st));
   }
-  const int tokens = int8_tile_tokens(M);
+  const Int8Plan plan = int8_plan(M, N, K);
+  const int tokens = plan.tokens;
   const uint8_t* a8 = reinterpret_cast<const uint8_t*>(a);
   Int8GemmArgs p = {};
   p.sa = sa;
@@ -1624,16 +1664,7 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
   p.status = dev_status;
   p.watchdog_ns = watchdog_ns();
   p.drop_stage = g_tune.withhold_stage;
-  const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt, kb = (K + 127) / 128;
-  // Parts of K, one to a pair of a cluster. Measured with K = 4096 (32 blocks), us, 1 / 2 / 3 / 4 parts:
-  //   tiles        14                  16                  22                  24                  36            38
-  //   64 tokens    14.9 10.8 10.0 9.2  14.9 11.0 10.1 17   14.9 11.4 10.5 17   14.9 11.4 19.5 18   15 12 20 26   15 22
-  //   300 tokens   28 21 20 18         28 21 20 28         28 22 21 31         29 22 32 32         29 23 36 46   29 38
-  // So as many as the tiles' clusters of 8, 6 or 4 CTAs are resident at once. Short K, 8 blocks: 64 tokens, 4 tiles 7.2 7.1
-  // 7.1 6.5; 300 tokens, 8 tiles 13.3 13.4 13.4 13.0; 1,000, 16 tiles 13.5 13.8 15.2.
-  int64_t split = tiles <= 14 ? 4 : (tiles <= 22 ? 3 : (tiles <= 36 ? 2 : 1));
-  if (split > kb / (tokens == 256 ? 8 : 2)) split = kb / (tokens == 256 ? 8 : 2);
-  p.split = static_cast<int>(split < 1 ? 1 : split);
+  p.split = plan.split;
   // blocks of 8 x 9 or 10 tiles at one time, as for the gated block (4,096 x 8,192 x 8,192: 326 -> 314 us)
   p.raster = g_tune.dense_raster ? g_tune.dense_raster : (p.mt > 12 && p.nt > 12 ? 8 : 0);
   CUtensorMap tmW, tmX;

@@ -97,8 +97,8 @@ def test_int8_host_validation(lib):
     assert gemm(M=-1) == -1 and gemm(N=0) == -1 and gemm(kind=3) == -1 and gemm(a=0) == -1 and gemm(y=0) == -1
     assert gemm(K=100) == -2 and gemm(K=131072) == -2 and gemm(M=(1 << 30) + 1) == -2
     assert gemm(a=24) == -3 and gemm(y=24) == -3 and gemm(sa=18) == -3 and gemm(ws=8) == -3
-    assert lib.nvfp4_int8_gemm_workspace_bytes(128, 64, 256) == 0 and lib.nvfp4_int8_gemm_workspace_bytes(129, 64, 256) == 129 * 512
-    assert gemm(M=129, ws=0) == -6 and gemm(M=129, wsb=129 * 512 - 1) == -6
+    assert lib.nvfp4_int8_gemm_workspace_bytes(128, 64, 256) == 0 and lib.nvfp4_int8_gemm_workspace_bytes(1025, 8192, 256) == 1025 * 512
+    assert gemm(M=1025, N=8192, ws=0) == -6 and gemm(M=1025, N=8192, wsb=1025 * 512 - 1) == -6
 
 
 def test_clip_host_validation(lib):

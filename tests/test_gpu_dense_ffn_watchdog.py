@@ -57,7 +57,8 @@ def test_gradients(withhold, M, I, K, stage):
 
 
 # each size of token tiles, in four parts and whole
-@pytest.mark.parametrize("M,N,K", [(3, 300, 2048), (3, 9800, 512), (100, 300, 2048), (100, 9800, 512), (300, 300, 4096), (300, 5003, 512)])
+@pytest.mark.parametrize("M,N,K", [(3, 300, 2048), (3, 9800, 512), (100, 300, 2048), (100, 9800, 512), (300, 300, 4096), (300, 5003, 512),
+                                   (512, 2579, 8192), (1100, 5003, 512)])
 @pytest.mark.parametrize("stage", [1, 3])
 def test_int8(withhold, M, N, K, stage):
     a, b = codes(1, M, K), codes(2, N, K)

@@ -113,6 +113,27 @@ def test_product(m, M, N, K):
     assert int(status) == 0
 
 
+# tiles of 256 tokens (fp16 through the workspace), whole and in two and three parts; the others above take smaller ones
+@pytest.mark.parametrize("M,N,K", [(129, 12175, 496), (256, 8192, 8192), (300, 4000, 8192), (512, 2579, 8192), (513, 8200, 1040), (600, 5003, 2064),
+                                   (700, 7000, 80), (1100, 5003, 512), (1111, 2300, 272), (5000, 4100, 1040)])
+def test_product_of_wide_tiles(m, M, N, K):
+    assert m.nvfp4_int8_gemm_workspace_bytes(M, N, K) == 2 * M * K
+    test_product(m, M, N, K)
+
+
+@pytest.mark.parametrize("M,N", [(3, 200), (100, 200), (300, 200), (600, 5300)])
+@pytest.mark.parametrize("K", [1024, 4096, 20000])
+def test_largest_sums_in_each_kernel(m, M, N, K):
+    """Sums of equal signs and odd ones beside them, in the kernels of up to 8, 64, 128 and 256 tokens a tile."""
+    assert (m.nvfp4_int8_gemm_workspace_bytes(M, N, K) > 0) == (N == 5300)
+    a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    b = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    a[1], b[1] = 127, 127
+    b[2, ::2], a[2, ::3], b[5], a[0, K - 1], b[0, K - 1], b[N - 1, 0] = 127, 1, codes(5, K), 1, 1, 3
+    y = m.nvfp4_int8_gemm(a, torch.ones(M, device="cuda"), b, torch.ones(N, device="cuda"), M, N, K, out_dtype=torch.float32)
+    assert torch.equal(y, (a.double() @ b.double().t()).float())
+
+
 @pytest.mark.parametrize("M", [3, 100, 300])
 @pytest.mark.parametrize("K", [1024, 4096, 20000])
 def test_largest_sums(m, M, K):
@@ -258,9 +279,9 @@ def test_refusals(m):
             m.nvfp4_int8_gemm(**{**ok, "K": K})
         assert e.value.status == status
     assert m.nvfp4_int8_gemm(a[:0], sa[:0], b, sb, 0, 8, 32).shape == (0, 8)
-    big = codes(3, 300, 32)
+    big, wide = codes(3, 1025, 32), codes(4, 8192, 32)
     with pytest.raises(m.NVFP4Error) as e:
-        m.nvfp4_int8_gemm(big, torch.ones(300, device="cuda"), b, sb, 300, 8, 32, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        m.nvfp4_int8_gemm(big, torch.ones(1025, device="cuda"), wide, torch.ones(8192, device="cuda"), 1025, 8192, 32, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -6
     x = torch.zeros(4, 32, device="cuda").bfloat16()
     for bad in (x.float(), x.cpu(), x.t(), x[0]):
