@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
         float sb[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sb[i] = __shfl_sync(0xffffffffu, sb_lane, 8 * i + (lane >> 2));
-        // 32 tokens x 32 channels at a time through the warp's box
+        // 32 tokens x 32 channels at a time through the warp's box (rows of odd lengths are stored value by value, eight
+        // tokens under way: 4,925 x 14,555 x 512 122 -> 115 us)
 #pragma unroll
         for (int c = 0; c < C::COLS / 32; ++c) {
           const int row0 = row_of(c), rows = min(32, M - row0);
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
                   *reinterpret_cast<uint4*>(y + static_cast<int64_t>(i) * N + 4 * (lane & 7)) =
                       *reinterpret_cast<const uint4*>(box + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
             } else if (col0 + lane < N) {
+#pragma unroll 8
               for (int i = 0; i < rows; ++i)
                 y[static_cast<int64_t>(i) * N + lane] =
                     reinterpret_cast<const float*>(box)[i * 32 + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)];
@@ -387,6 +389,7 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
                   *reinterpret_cast<uint4*>(y + static_cast<int64_t>(i) * N + 8 * (lane & 3)) =
                       *reinterpret_cast<const uint4*>(box + i * 64 + (((lane & 3) ^ (i >> 1 & 3)) << 4));
             } else if (col0 + lane < N) {
+#pragma unroll 8
               for (int i = 0; i < rows; ++i)
                 y[static_cast<int64_t>(i) * N + lane] =
                     reinterpret_cast<const uint16_t*>(box)[i * 32 + (((lane >> 3) ^ (i >> 1 & 3)) << 3) + (lane & 7)];
