@@ -665,19 +665,24 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
   if (threadIdx.x == 0 && *abort_flag) report_status(p.status, kStatusTimeout);
 }
 
-// Tokens' codes to fp16, 16 a thread.
-__global__ void __launch_bounds__(256) k_int8_widen(const uint4* a, uint4* out, int64_t n) {
+// Tokens' codes to fp16: 8 of them a thread, so that loads and stores are whole lines, four such pieces under way.
+__global__ void __launch_bounds__(256) k_int8_widen(const uint2* a, uint4* out, int64_t n) {
   griddep_wait();
   griddep_launch_dependents();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const uint4 w = a[i];
-    uint4 lo, hi;
-    widen4(w.x, lo.x, lo.y);
-    widen4(w.y, lo.z, lo.w);
-    widen4(w.z, hi.x, hi.y);
-    widen4(w.w, hi.z, hi.w);
-    out[2 * i] = lo;
-    out[2 * i + 1] = hi;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += 4 * step) {
+    uint2 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * step < n) w[j] = a[i + j * step];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i + j * step >= n) break;
+      uint4 v;
+      widen4(w[j].x, v.x, v.y);
+      widen4(w[j].y, v.z, v.w);
+      out[i + j * step] = v;
+    }
   }
 }
 
@@ -724,7 +729,7 @@ cudaError_t launch_int8_gemm(const CUtensorMap& tmW, const CUtensorMap& tmX, con
 }
 
 cudaError_t launch_int8_widen(const uint8_t* a, void* out, int64_t n, int sms, cudaStream_t st) {
-  const int64_t groups = n / 16, blocks = (groups + 255) / 256, most = 8 * static_cast<int64_t>(sms);
+  const int64_t groups = n / 8, blocks = (groups + 1023) / 1024, most = 8 * static_cast<int64_t>(sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most));
   cfg.blockDim = dim3(256);
@@ -734,7 +739,7 @@ cudaError_t launch_int8_widen(const uint8_t* a, void* out, int64_t n, int sms, c
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_int8_widen, reinterpret_cast<const uint4*>(a), static_cast<uint4*>(out), groups);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_int8_widen, reinterpret_cast<const uint2*>(a), static_cast<uint4*>(out), groups);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
