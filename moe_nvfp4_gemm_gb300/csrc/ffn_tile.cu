@@ -15,8 +15,8 @@
 // Products of few tiles are cut along their contraction into parts; the parts' fp32 sums go to
 // the workspace and are added, in the order of the contraction, by k_ffn_join.
 //
-// Bound by the tensor cores: 4096 x 14336 x 8192 forward 1.00-1.14 ms (1.92 PFLOP/s in a burst, less under the power cap),
-// 4099 x 8192 x 4096 forward 308 us, both gradients 627 us.
+// Bound by the tensor cores: 4096 x 14336 x 8192 forward 0.94-1.14 ms (up to 2.04 PFLOP/s in a burst, less under the power
+// cap), 4096 x 8192 x 4096 forward 272 us, both gradients 594-616 us (1.78-1.85 PFLOP/s).
 #include <stdint.h>
 
 #include "ffn.cuh"

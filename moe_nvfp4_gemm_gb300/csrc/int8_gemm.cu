@@ -12,11 +12,11 @@
 // they would fill. Tokens: up to 128 are converted by the same warps into the swizzled shared-memory tile that the
 // MMA reads; tiles of 256 come as fp16 from the workspace, converted once by k_int8_widen.
 //
-// Few tiles: the pairs of a cluster (p.split of them) sum a tile's parts of K, exchange the integer sums through
+// Up to 8 tokens have a kernel without tensor cores (int8_few.cu). Few tiles: the pairs of a cluster (p.split of them) sum a tile's parts of K, exchange the integer sums through
 // distributed shared memory and store a share of the tokens each.
 //
-// Bound by the tensor cores with many tokens (4,096 x 28,672 x 8,192: 1.00 ms, 1.92 PFLOP/s, the fp16 rate; under the power
-// cap 1.06), by the loop around a block with few (one token, 8,192 x 8,192: 15.8 us, 4.2 TB/s of weights).
+// Bound by the tensor cores with many tokens (4,096 x 28,672 x 8,192: 0.99 ms, 1.94 PFLOP/s, the fp16 rate; under the power
+// cap 1.06), by the loop around a block with few (9 tokens, 8,192 x 8,192: 17.4 us, 3.9 TB/s of weights).
 #include <stdint.h>
 
 #include <cuda_fp16.h>
