@@ -43,7 +43,8 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
  *   dx         [M, K] contiguous, written, or NULL: not wanted (w_gate and w_up may then be NULL)
  *   dw_gate, dw_up  [I, K] contiguous, written, or NULL each (x may be NULL when both are). M == 0 writes zeros.
  *   workspace  nvfp4_gated_ffn_backward_workspace_bytes(M, I, K) bytes, 256-byte aligned
- * No result may share memory with another, with the workspace or with an operand: NVFP4_ERR_INVALID_ARG.
+ * No result may share memory with another, with the workspace or with an operand, nor the workspace with an operand:
+ * NVFP4_ERR_INVALID_ARG. (Between rows that lie apart there may be other tensors.)
  * The weights' gradients sum over all M rows: a NaN in a row of x, gate, up or dh reaches all that it
  * meets, so padding rows must hold finite values (and dh zeros).
  */

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <mutex>
 #include <new>
+#include <utility>
 
 #include "nvfp4.h"
 #include "nvfp4_ffn.h"
@@ -185,6 +186,49 @@ int pow2_at_least(int v) {
   int p = 32;
   while (p < v) p <<= 1;
   return p;
+}
+
+// `rows` rows of `bytes` bytes, `pitch` bytes apart (at least `bytes`).
+struct Region {
+  const void* p;
+  int64_t rows, bytes, pitch;
+};
+
+// Whether two regions share a byte: by their ends; where both have gaps, row by row of the one with fewer rows, or once
+// where the rows of both lie as far apart.
+bool shared(Region a, Region b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.bytes <= 0 || b.bytes <= 0) return false;
+  for (Region* r : {&a, &b})
+    if (r->rows == 1 || r->pitch == r->bytes) *r = {r->p, 1, r->rows * r->bytes, r->rows * r->bytes};
+  if (a.rows > b.rows) std::swap(a, b);
+  // 128 bits: strides that no operand has may leave 64
+  using Wide = __int128;
+  const Wide a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const Wide a1 = a0 + static_cast<Wide>(a.rows - 1) * a.pitch + a.bytes, b1 = b0 + static_cast<Wide>(b.rows - 1) * b.pitch + b.bytes;
+  if (a1 <= b0 || b1 <= a0) return false;
+  const bool alike = a.rows > 1 && a.pitch == b.pitch;
+  for (int64_t i = 0; i < (alike ? 1 : a.rows); ++i) {
+    // the last row of b that starts before this row of a ends; alike: of any row of a, counted from the first
+    const Wide lo = a0 + static_cast<Wide>(i) * a.pitch, hi = lo + a.bytes;
+    if (!alike && lo >= b1) break;
+    const int64_t first = alike ? 1 - a.rows : 0;
+    const Wide room = hi - 1 - b0;
+    Wide j = room >= 0 ? room / b.pitch : -((-room + b.pitch - 1) / b.pitch);
+    if (j > b.rows - 1) j = b.rows - 1;
+    if (j >= first && b0 + j * b.pitch + b.bytes > lo) return true;
+  }
+  return false;
+}
+
+// Whether one of the regions that a call writes shares a byte with another one or with one that it reads.
+bool any_shared(const Region* written, int n, const Region* read, int m) {
+  for (int i = 0; i < n; ++i) {
+    for (int j = i + 1; j < n; ++j)
+      if (shared(written[i], written[j])) return true;
+    for (int j = 0; j < m; ++j)
+      if (shared(written[i], read[j])) return true;
+  }
+  return false;
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
@@ -1471,28 +1515,18 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
   if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(gate) || !aligned16(up) || !aligned16(dh) ||
       !aligned16(dx) || !aligned16(dw_gate) || !aligned16(dw_up) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return NVFP4_ERR_ALIGNMENT;
+  FfnTileArgs p = {};
+  size_t parts_at = 0;
+  const size_t need = M > 0 && (dx || weights) ? ffn_backward_plan(p, M, I, K, dx != nullptr, weights, parts_at) : 0;
   {
     // the products run at the same time: what one writes the other may still read
-    const struct {
-      const void* p;
-      int64_t bytes;
-      bool written;
-    } spans[] = {{dx, M * K * 2, true},
-                 {dw_gate, I * K * 2, true},
-                 {dw_up, I * K * 2, true},
-                 {workspace, M * I * 4, true},
-                 {x, M > 0 ? ((M - 1) * ldx + K) * 2 : 0, false},
-                 {w_gate, ((I - 1) * ld_gate + K) * 2, false},
-                 {w_up, ((I - 1) * ld_up + K) * 2, false},
-                 {gate, M * I * 4, false},
-                 {up, M * I * 4, false},
-                 {dh, M > 0 ? ((M - 1) * lddh + I) * 2 : 0, false}};
-    for (const auto& a : spans)
-      for (const auto& b : spans) {
-        if (&a == &b || !a.written || !a.p || !b.p) continue;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(a.p), bt = reinterpret_cast<uintptr_t>(b.p);
-        if (at < bt + static_cast<uintptr_t>(b.bytes) && bt < at + static_cast<uintptr_t>(a.bytes)) return NVFP4_ERR_INVALID_ARG;
-      }
+    const Region written[] = {{dx, M, K * 2, K * 2},
+                              {dw_gate, I, K * 2, K * 2},
+                              {dw_up, I, K * 2, K * 2},
+                              {workspace, 1, static_cast<int64_t>(need), static_cast<int64_t>(need)}};
+    const Region read[] = {{x, M, K * 2, ldx * 2},        {w_gate, I, K * 2, ld_gate * 2}, {w_up, I, K * 2, ld_up * 2},
+                           {gate, M, I * 4, I * 4},       {up, M, I * 4, I * 4},           {dh, M, I * 2, lddh * 2}};
+    if (any_shared(written, 4, read, 6)) return NVFP4_ERR_INVALID_ARG;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DevInfo d;
@@ -1505,9 +1539,6 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
     return NVFP4_OK;
   }
   if (!dx && !weights) return NVFP4_OK;
-  FfnTileArgs p = {};
-  size_t parts_at;
-  const size_t need = ffn_backward_plan(p, M, I, K, dx != nullptr, weights, parts_at);
   if (!workspace || workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
   rc = device_info(d);
   if (rc) return rc;

@@ -1,0 +1,53 @@
+"""CPU checks of what may share memory in the dense feed-forward calls: every result and workspace over every operand and
+every other result is refused before the device is touched. (Calls that are let through are in
+test_gpu_dense_ffn_overlap.py, on memory that exists; here they end at a workspace that is too small.)"""
+import ctypes
+
+import pytest
+
+P = ctypes.c_void_p
+APART = 1 << 28  # bytes between two operands
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from moe_nvfp4_gemm_gb300 import build
+    build.build()
+    import moe_nvfp4_gemm_gb300 as m
+    return m.lib()
+
+
+def place(names):
+    """An address of its own for each name."""
+    return {n: 4096 + (i + 1) * APART for i, n in enumerate(names.split())}
+
+
+def backward(lib, M, I, K, wsb, ldx=None, lddh=None, **over):
+    a = {**place("x wg wu gate up dh dx dwg dwu ws"), **over}
+    return lib.nvfp4_gated_ffn_backward(P(a["x"]), ldx or K, P(a["wg"]), K, P(a["wu"]), K, P(a["gate"]), P(a["up"]), P(a["dh"]), lddh or I,
+                                        0, 0, P(a["dx"]), P(a["dwg"]), P(a["dwu"]), M, I, K, P(a["ws"]), wsb, None, None)
+
+
+def test_gradients_and_the_parts_in_the_workspace(lib):
+    """Few tiles: the workspace holds dg and du, 4 M I bytes, and behind them the fp32 sums of the products' parts."""
+    M, I, K = 8, 4096, 256
+    need = lib.nvfp4_gated_ffn_backward_workspace_bytes(M, I, K)
+    parts = 4 * M * I
+    assert need >= parts + 2 * 256 * 256 * 4
+    ws = place("x wg wu gate up dh dx dwg dwu ws")["ws"]
+    for at in (ws, ws + parts, ws + parts + 65536):
+        for name in ("dx", "dwg", "dwu", "x", "wg", "wu", "gate", "up", "dh"):
+            assert backward(lib, M, I, K, need, **{name: at}) == -1, (name, at - ws)
+    for name in ("dx", "dwg", "dwu", "x", "wg", "wu", "gate", "up", "dh"):  # behind the workspace: let through
+        assert backward(lib, M, I, K, 0, **{name: ws + need + 256}) == -6, name
+
+
+def test_gradients_between_rows_that_lie_apart(lib):
+    """A result in the gap between two rows of an operand shares nothing with it."""
+    M, I, K, ld = 2, 64, 256, 4096
+    x = place("x")["x"]
+    assert backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * K) == -6            # dx takes 1,024 of the 7,680 bytes of the gap
+    assert backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld - 1024) == -6    # up to the second row
+    assert backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld - 1008) == -1 and backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * K - 16) == -1
+    assert backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld + 2 * K - 16) == -1 and backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld + 2 * K) == -6
+    assert backward(lib, M, I, K, 0, lddh=ld, dwg=place("x wg wu gate up dh")["dh"] + 128) == -1  # 32,768 bytes: over the second row
