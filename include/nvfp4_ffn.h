@@ -24,8 +24,9 @@ extern "C" {
  *   gate, up   fp32 [M, I] contiguous, 32-byte aligned, written: g and u as they are summed, for the backward call;
  *              or both NULL
  *   workspace  nvfp4_gated_ffn_workspace_bytes(M, I, K) bytes, 16-byte aligned (NULL where that is 0)
- * I, K and the row strides are multiples of 8, pointers 16-byte aligned, I and K at most 2^24. h, gate and up share no
- * element with an operand. A NaN or an infinity stays in its token's row. dev_status as for nvfp4_gemm.
+ * I, K and the row strides are positive multiples of 8, pointers 16-byte aligned, I and K at most 2^24. h, gate, up and the
+ * workspace share no byte with each other or with an operand: NVFP4_ERR_INVALID_ARG (columns of one buffer beside each
+ * other are fine). A NaN or an infinity stays in its token's row. dev_status as for nvfp4_gemm.
  */
 enum { NVFP4_SILU = 0, NVFP4_GELU_TANH = 1 };
 size_t nvfp4_gated_ffn_workspace_bytes(int64_t M, int64_t I, int64_t K);

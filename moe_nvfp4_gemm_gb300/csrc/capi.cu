@@ -1440,9 +1440,24 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
   if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || !aligned32(gate) || !aligned32(up) ||
       !aligned16(workspace))
     return NVFP4_ERR_ALIGNMENT;
+  const int split = ffn_stream_split(M, I, K);
+  FfnTileArgs p = {};
+  size_t need = 0;
+  if (!split) {
+    ffn_product(p.in[0], M, I, 128, (K + 63) / 64, 1);
+    need = ffn_split(p);
+  }
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  // a tile's results are stored while others still read the operands
+  const Region written[] = {{h, M, I * 2, ldh * 2},
+                            {gate, M, I * 4, I * 4},
+                            {up, M, I * 4, I * 4},
+                            {workspace, 1, static_cast<int64_t>(need), static_cast<int64_t>(need)}};
+  const Region read[] = {{x, M, K * 2, ldx * 2}, {w_gate, I, K * 2, ld_gate * 2}, {w_up, I, K * 2, ld_up * 2}};
+  if (any_shared(written, 4, read, 3)) return NVFP4_ERR_INVALID_ARG;
   DevInfo d;
-  if (const int split = ffn_stream_split(M, I, K)) {
-    if ((rc = device_info(d))) return rc;
+  if ((rc = device_info(d))) return rc;
+  if (split) {
     FfnStreamArgs s = {h, gate, up, ldh, static_cast<int>(M), static_cast<int>(I), static_cast<int>((K + 63) / 64)};
     s.split = split;
     s.act = activation;
@@ -1458,12 +1473,6 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
     g_last_launches = 1;
     return from_cuda(launch_ffn_stream(maps, s, static_cast<cudaStream_t>(stream)));
   }
-  FfnTileArgs p = {};
-  ffn_product(p.in[0], M, I, 128, (K + 63) / 64, 1);
-  const size_t need = ffn_split(p);
-  if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
-  rc = device_info(d);
-  if (rc) return rc;
   FfnTileMaps maps;
   if ((rc = encode_16(&maps.a[0], x, M, K, ldx, 128))) return rc;
   maps.a[1] = maps.a[0];

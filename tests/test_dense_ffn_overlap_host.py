@@ -51,3 +51,45 @@ def test_gradients_between_rows_that_lie_apart(lib):
     assert backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld - 1008) == -1 and backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * K - 16) == -1
     assert backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld + 2 * K - 16) == -1 and backward(lib, M, I, K, 0, ldx=ld, dx=x + 2 * ld + 2 * K) == -6
     assert backward(lib, M, I, K, 0, lddh=ld, dwg=place("x wg wu gate up dh")["dh"] + 128) == -1  # 32,768 bytes: over the second row
+
+
+def forward(lib, M, I, K, wsb=1 << 27, ldx=None, ldh=None, save=True, **over):
+    a = {**place("x wg wu h gate up ws"), **over}
+    gate, up = (a["gate"], a["up"]) if save else (0, 0)
+    return lib.nvfp4_gated_ffn(P(a["x"]), ldx or K, P(a["wg"]), K, P(a["wu"]), K, 0, 0, P(a["h"]), ldh or I, P(gate), P(up), M, I, K,
+                               P(a["ws"]), wsb, None, None)
+
+
+# streamed, in whole tiles, in parts
+@pytest.mark.parametrize("M,I,K", [(5, 256, 256), (300, 256, 256), (256, 256, 8192)])
+def test_forward(lib, M, I, K):
+    at = place("x wg wu h gate up ws")
+    row = 2 * K
+    for name, size in (("x", M * row), ("wg", I * row), ("wu", I * row), ("gate", 4 * M * I), ("up", 4 * M * I)):
+        assert forward(lib, M, I, K, h=at[name]) == -1, name
+        assert forward(lib, M, I, K, h=at[name] + size - 16) == -1, name
+        assert forward(lib, M, I, K, h=at[name] - 2 * M * I + 16) == -1, name
+    for name, size in (("x", M * row), ("wg", I * row), ("wu", I * row), ("h", 2 * M * I), ("up", 4 * M * I)):
+        assert forward(lib, M, I, K, gate=at[name]) == -1 and forward(lib, M, I, K, gate=at[name] + size - 32) == -1, name
+    for name in ("x", "wg", "wu", "h", "gate"):
+        assert forward(lib, M, I, K, up=at[name]) == -1, name
+    assert forward(lib, M, I, K, save=False, h=at["x"]) == -1
+    if lib.nvfp4_gated_ffn_workspace_bytes(M, I, K):
+        need = lib.nvfp4_gated_ffn_workspace_bytes(M, I, K)
+        for name in ("x", "wg", "wu", "h", "gate", "up"):
+            assert forward(lib, M, I, K, ws=at[name]) == -1 and forward(lib, M, I, K, ws=at[name] - need + 16) == -1, name
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_forward_rows_that_lie_apart(lib, M):
+    """h and x as columns of one buffer, eight columns too near; and with strides of their own, where some rows meet."""
+    I, K, ld = 128, 256, 512
+    x = place("x")["x"]
+    assert forward(lib, M, I, K, ldx=ld, ldh=ld, h=x + 2 * (K - 8)) == -1            # over the end of each row of x
+    assert forward(lib, M, I, K, ldx=ld, ldh=ld, h=x + 2 * (ld - I + 8)) == -1       # over the start of the next row
+    assert forward(lib, M, I, K, ldx=ld, ldh=ld, h=x + 2 * (ld * (M - 1) + K - 8)) == -1  # one row alone meets the last of x
+    assert forward(lib, M, I, K, ldx=ld, ldh=ld, h=x - 2 * (ld * (M - 1) + I - 8)) == -1  # the last of h meets the first of x
+    # rows of h 520 apart: the fourth ends eight columns into the next row of x
+    assert forward(lib, M, I, K, ldx=ld, ldh=520, h=x + 2 * 368) == -1
+    # rows of h twice as far apart as those of x
+    assert forward(lib, M, I, K, ldx=ld, ldh=2 * ld, h=x + 2 * (K - 8)) == -1

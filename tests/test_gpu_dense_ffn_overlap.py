@@ -4,9 +4,28 @@ import pytest
 import torch
 
 import moe_nvfp4_gemm_gb300 as m
-from tests.test_gpu_gated_ffn import check_backward, make
+from tests.test_gpu_gated_ffn import check_backward, check_forward, make
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M", [1, 5, 300])
+def test_columns_of_one_buffer(M):
+    """x and h side by side in each row, and h in rows four times as far apart as it needs behind every second row of x."""
+    I, K = 136, 200
+    x, wg, wu, _ = make(M, I, K, torch.bfloat16, seed=M)
+    buf = torch.full((M, K + I), 7.0, dtype=torch.bfloat16, device="cuda")
+    buf[:, :K] = x
+    m.nvfp4_gated_ffn(buf[:, :K], wg, wu, h=buf[:, K:])
+    assert torch.equal(buf[:, :K], x)
+    check_forward(x, wg, wu, "silu", buf[:, K:])
+    pitch = K + I + 8
+    flat = torch.full((2 * M * pitch,), 7.0, dtype=torch.bfloat16, device="cuda")
+    near, far = flat[:M * pitch].view(M, pitch), flat.view(M, 2 * pitch)
+    near[:, :K] = x
+    m.nvfp4_gated_ffn(near[:, :K], wg, wu, h=far[:, K:K + I])
+    assert torch.equal(near[:, :K], x)
+    check_forward(x, wg, wu, "silu", far[:, K:K + I])
 
 
 def test_gradient_between_the_rows_of_an_operand():
@@ -19,3 +38,14 @@ def test_gradient_between_the_rows_of_an_operand():
     got = m.nvfp4_gated_ffn_backward(wide[:, :K], wg, wu, gate, up, dh, dx=dx)
     assert got[0] is dx and torch.equal(wide[:, :K], x) and (wide[0, K + M * K:] == 7).all() and (wide[1, K:] == 7).all()
     check_backward(x, wg, wu, gate, up, dh, "silu", *got)
+
+
+@pytest.mark.parametrize("M", [5, 200])
+def test_refused(M):
+    x, wg, wu, _ = make(M, 256, 256, torch.bfloat16)
+    kept = [t.clone() for t in (x, wg)]
+    for call in (lambda: m.nvfp4_gated_ffn(x, wg, wu, h=x), lambda: m.nvfp4_gated_ffn(x, wg, wu, h=wg[:M])):
+        with pytest.raises(m.NVFP4Error) as e:
+            call()
+        assert e.value.status == -1
+    assert all(torch.equal(t, k) for t, k in zip((x, wg), kept))
