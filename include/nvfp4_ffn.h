@@ -72,8 +72,9 @@ int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M,
  *           any codes, -128 included
  *   y       [M, N] row-major, bf16, fp16 or fp32 (y_type), 16-byte aligned (a, b and the workspace too)
  *   workspace  nvfp4_int8_gemm_workspace_bytes(M, N, K) bytes (NULL where that is 0)
- * K % 16 == 0, K <= 131,056 (the sums fit 32 bits); any M >= 0, N >= 1. y shares no memory with an operand or the
- * workspace. dev_status as for nvfp4_gemm (calls of up to 8 tokens wait for nothing and never write it).
+ * K % 16 == 0, 16 <= K <= 131,056 (the sums fit 32 bits); any M >= 0, N >= 1. y and the workspace share no memory with
+ * each other or with an operand: NVFP4_ERR_INVALID_ARG. dev_status as for nvfp4_gemm (calls of up to 8 tokens wait for
+ * nothing and never write it).
  */
 size_t nvfp4_int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* y, int32_t y_type, int64_t M,

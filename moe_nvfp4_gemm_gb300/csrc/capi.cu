@@ -1679,6 +1679,10 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
     return NVFP4_ERR_ALIGNMENT;
   const size_t need = nvfp4_int8_gemm_workspace_bytes(M, N, K);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  const int64_t row = N * (y_type == NVFP4_F32 ? 4 : 2), ws = static_cast<int64_t>(need);
+  const Region written[] = {{y, M, row, row}, {workspace, 1, ws, ws}};
+  const Region read[] = {{a, M, K, K}, {b, N, K, K}, {sa, M, 4, 4}, {sb, N, 4, 4}};
+  if (any_shared(written, 2, read, 4)) return NVFP4_ERR_INVALID_ARG;
   DevInfo d;
   if ((rc = device_info(d))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

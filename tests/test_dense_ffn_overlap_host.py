@@ -93,3 +93,20 @@ def test_forward_rows_that_lie_apart(lib, M):
     assert forward(lib, M, I, K, ldx=ld, ldh=520, h=x + 2 * 368) == -1
     # rows of h twice as far apart as those of x
     assert forward(lib, M, I, K, ldx=ld, ldh=2 * ld, h=x + 2 * (K - 8)) == -1
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 512, 256), (40, 512, 256), (1025, 8192, 256)])
+def test_int8_product(lib, M, N, K):
+    at = place("a sa b sb y ws")
+    need = lib.nvfp4_int8_gemm_workspace_bytes(M, N, K)
+
+    def call(kind=1, **over):
+        a = {**at, **over}
+        return lib.nvfp4_int8_gemm(P(a["a"]), P(a["sa"]), P(a["b"]), P(a["sb"]), P(a["y"]), kind, M, N, K, P(a["ws"]), need, None, None)
+    for name, size in (("a", M * K), ("sa", 4 * M), ("b", N * K), ("sb", 4 * N)):
+        assert call(y=at[name]) == -1 and call(y=at[name] + (size - 1) // 16 * 16) == -1, name
+        assert call(y=at[name] - 4 * M * N + 16) == -1 and call(kind=0, y=at[name] - 2 * M * N + 16) == -1, name
+        if need:
+            assert call(ws=at[name]) == -1 and call(ws=at[name] - need + 16) == -1, name
+    if need:
+        assert call(ws=at["y"]) == -1

@@ -43,9 +43,13 @@ def test_gradient_between_the_rows_of_an_operand():
 @pytest.mark.parametrize("M", [5, 200])
 def test_refused(M):
     x, wg, wu, _ = make(M, 256, 256, torch.bfloat16)
-    kept = [t.clone() for t in (x, wg)]
-    for call in (lambda: m.nvfp4_gated_ffn(x, wg, wu, h=x), lambda: m.nvfp4_gated_ffn(x, wg, wu, h=wg[:M])):
+    a, sa = m.nvfp4_int8_quantize(x)
+    b, sb = m.nvfp4_int8_quantize(wg)
+    over = sb.view(torch.bfloat16)[:2 * M].view(M, 2)  # two channels' results over the channels' scales
+    kept = [t.clone() for t in (x, wg, sb)]
+    for call in (lambda: m.nvfp4_gated_ffn(x, wg, wu, h=x), lambda: m.nvfp4_gated_ffn(x, wg, wu, h=wg[:M]),
+                 lambda: m.nvfp4_int8_gemm(a, sa, b[:2], sb[:2], M, 2, 256, y=over)):
         with pytest.raises(m.NVFP4Error) as e:
             call()
         assert e.value.status == -1
-    assert all(torch.equal(t, k) for t, k in zip((x, wg), kept))
+    assert all(torch.equal(t, k) for t, k in zip((x, wg, sb), kept))
