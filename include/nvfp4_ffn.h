@@ -61,7 +61,8 @@ int nvfp4_gated_ffn_backward(const uint16_t* x, int64_t ldx, const uint16_t* w_g
  * every step, 1/127 and 1/amax_row too, one IEEE fp32 operation (rows with amax below 2^-100 are first multiplied by 2^100). A row that holds
  * an infinity or NaN gets codes 0 and scale NaN: what is made of it is NaN.
  *   x     device [M, K], bf16 or fp16 (type), rows ldx elements apart (a multiple of 8), 16-byte aligned
- *   q, s  int8 [M, K], 16-byte aligned, and fp32 [M], written. K % 16 == 0 (K == 0: scales of 1).
+ *   q, s  int8 [M, K], 16-byte aligned, and fp32 [M], written. K % 16 == 0 (K == 0: scales of 1). They share no memory
+ *         with each other or with x: NVFP4_ERR_INVALID_ARG.
  */
 int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M, int64_t K, int8_t* q, float* s, void* stream);
 

@@ -1588,6 +1588,8 @@ int nvfp4_int8_quantize(const uint16_t* x, int64_t ldx, int32_t type, int64_t M,
   if (M == 0) return NVFP4_OK;
   if (!s || (K > 0 && (!x || !q))) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned4(s)) return NVFP4_ERR_ALIGNMENT;
+  const Region written[] = {{q, M, K, K}, {s, M, 4, 4}}, read = {x, M, K * 2, ldx * 2};
+  if (any_shared(written, 2, &read, 1)) return NVFP4_ERR_INVALID_ARG;
   DevInfo d;
   if ((rc = device_info(d))) return rc;
   Int8QuantArgs a = {x, M, K, ldx, reinterpret_cast<uint8_t*>(q), s, type == NVFP4_F16};

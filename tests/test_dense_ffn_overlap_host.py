@@ -110,3 +110,16 @@ def test_int8_product(lib, M, N, K):
             assert call(ws=at[name]) == -1 and call(ws=at[name] - need + 16) == -1, name
     if need:
         assert call(ws=at["y"]) == -1
+
+
+def test_int8_quantiser(lib):
+    M, K, ld = 8, 256, 1024
+    at = place("x q s")
+
+    def call(ldx=K, **over):
+        a = {**at, **over}
+        return lib.nvfp4_int8_quantize(P(a["x"]), ldx, 0, M, K, P(a["q"]), P(a["s"]), None)
+    assert call(q=at["x"]) == -1 and call(q=at["x"] + 2 * M * K - 16) == -1 and call(q=at["x"] - M * K + 16) == -1
+    assert call(s=at["x"]) == -1 and call(s=at["x"] + 2 * M * K - 4) == -1
+    assert call(s=at["q"]) == -1 and call(q=at["s"]) == -1 and call(s=at["q"] + M * K - 4) == -1
+    assert call(ldx=ld, q=at["x"] + 2 * K) == -1 and call(ldx=ld, s=at["x"] + 2 * ld - 4) == -1  # over the second row of x
