@@ -94,7 +94,7 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
  *   norm       device fp32 [1], written (0 for an empty list)
  *   workspace  nvfp4_grad_clip_workspace_bytes(count) bytes, 16-byte aligned
  * Results must not share memory with each other or with another gradient (the same tensor twice, for
- * instance): NVFP4_ERR_INVALID_ARG.
+ * instance), nor the norm or the workspace with any of them or each other: NVFP4_ERR_INVALID_ARG.
  */
 size_t nvfp4_grad_clip_workspace_bytes(int32_t count);
 int nvfp4_grad_clip(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* types, int32_t count,

@@ -200,6 +200,8 @@ bool shared(Region a, Region b) {
   if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.bytes <= 0 || b.bytes <= 0) return false;
   for (Region* r : {&a, &b})
     if (r->rows == 1 || r->pitch == r->bytes) *r = {r->p, 1, r->rows * r->bytes, r->rows * r->bytes};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.p), bt = reinterpret_cast<uintptr_t>(b.p);
+  if (a.rows == 1 && b.rows == 1) return at < bt + static_cast<uintptr_t>(b.bytes) && bt < at + static_cast<uintptr_t>(a.bytes);
   if (a.rows > b.rows) std::swap(a, b);
   // 128 bits: strides that no operand has may leave 64
   using Wide = __int128;
@@ -1781,6 +1783,19 @@ int nvfp4_grad_clip(const void* const* grads, void* const* out, const int64_t* n
     if ((reinterpret_cast<uintptr_t>(grads[i]) | (out ? reinterpret_cast<uintptr_t>(out[i]) : 0)) & mask) return NVFP4_ERR_ALIGNMENT;
   }
   if (!workspace || workspace_bytes < nvfp4_grad_clip_workspace_bytes(count)) return NVFP4_ERR_WORKSPACE;
+  // the norm and the partial sums over a gradient, a result or each other
+  const uintptr_t nt = reinterpret_cast<uintptr_t>(norm), wt = reinterpret_cast<uintptr_t>(workspace);
+  const uintptr_t partials = nvfp4_grad_clip_workspace_bytes(count);
+  auto mine = [=](const void* p, uintptr_t bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return (at < nt + 4 && nt < at + bytes) || (at < wt + partials && wt < at + bytes);
+  };
+  if (nt < wt + partials && wt < nt + 4) return NVFP4_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t bytes = static_cast<uintptr_t>(numel[i]) * (types[i] == NVFP4_F32 ? 4 : 2);
+    if (mine(grads[i], bytes) || (out && mine(out[i], bytes))) return NVFP4_ERR_INVALID_ARG;
+  }
   ClipArgs a = {grads, out, numel, types, static_cast<double*>(workspace), norm, 0, max_norm, 0};
   // in place without a limit only the norm is wanted
   a.scale = out != nullptr || max_norm < HUGE_VALF;

@@ -123,3 +123,23 @@ def test_int8_quantiser(lib):
     assert call(s=at["x"]) == -1 and call(s=at["x"] + 2 * M * K - 4) == -1
     assert call(s=at["q"]) == -1 and call(q=at["s"]) == -1 and call(s=at["q"] + M * K - 4) == -1
     assert call(ldx=ld, q=at["x"] + 2 * K) == -1 and call(ldx=ld, s=at["x"] + 2 * ld - 4) == -1  # over the second row of x
+
+
+@pytest.mark.parametrize("limit", [1.0, float("inf")])
+@pytest.mark.parametrize("scaled", [False, True])
+def test_clipping(lib, limit, scaled):
+    """The norm and the workspace over a gradient, a result or each other."""
+    src = [(1 << 24) + i * 65536 for i in range(70)]
+    dst = [(1 << 25) + i * 65536 for i in range(70)]
+    n = len(src)
+    need = lib.nvfp4_grad_clip_workspace_bytes(n)
+
+    def call(norm=1 << 20, ws=1 << 21):
+        return lib.nvfp4_grad_clip((P * n)(*src), (P * n)(*dst) if scaled else None, (ctypes.c_int64 * n)(*[1000] * n),
+                                   (ctypes.c_int32 * n)(*[i % 3 for i in range(n)]), n, limit, P(norm), P(ws), need, None)
+    for i in (0, 33, 69):
+        size = (2, 4, 2)[i % 3] * 1000
+        for at in (src, dst) if scaled else (src,):
+            assert call(norm=at[i]) == -1 and call(norm=at[i] + size - 4) == -1
+            assert call(ws=at[i]) == -1 and call(ws=at[i] + (size - 1) // 16 * 16) == -1 and call(ws=at[i] - need + 16) == -1
+    assert call(norm=1 << 21) == -1 and call(norm=(1 << 21) + need - 4) == -1

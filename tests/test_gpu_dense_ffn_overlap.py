@@ -46,10 +46,20 @@ def test_refused(M):
     a, sa = m.nvfp4_int8_quantize(x)
     b, sb = m.nvfp4_int8_quantize(wg)
     over = sb.view(torch.bfloat16)[:2 * M].view(M, 2)  # two channels' results over the channels' scales
-    kept = [t.clone() for t in (x, wg, sb)]
+    g = torch.ones(100, device="cuda")
+    kept = [t.clone() for t in (x, wg, sb, g)]
     for call in (lambda: m.nvfp4_gated_ffn(x, wg, wu, h=x), lambda: m.nvfp4_gated_ffn(x, wg, wu, h=wg[:M]),
-                 lambda: m.nvfp4_int8_gemm(a, sa, b[:2], sb[:2], M, 2, 256, y=over)):
+                 lambda: m.nvfp4_int8_gemm(a, sa, b[:2], sb[:2], M, 2, 256, y=over),
+                 lambda: m.nvfp4_grad_clip([g], 1.0, norm=g[3:4]), lambda: m.nvfp4_grad_clip([g], norm=g[3:4])):
         with pytest.raises(m.NVFP4Error) as e:
             call()
         assert e.value.status == -1
-    assert all(torch.equal(t, k) for t, k in zip((x, wg, sb), kept))
+    assert all(torch.equal(t, k) for t, k in zip((x, wg, sb, g), kept))
+
+
+def test_norm_behind_the_gradients():
+    """A norm that is the next value of the gradients' buffer shares nothing with them."""
+    flat = torch.full((101,), 2.0, device="cuda")
+    norm = m.nvfp4_grad_clip([flat[:100]], 10.0, norm=flat[100:])
+    assert norm.data_ptr() == flat[100:].data_ptr() and float(norm) == 20.0
+    assert ((flat[:100] - 1).abs() < 1e-6).all()
