@@ -90,7 +90,7 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
  *   grads, out, numel, types  HOST arrays of `count` device pointers, element counts and types (NVFP4_BF16,
  *              NVFP4_F16, NVFP4_F32), read before the call returns. out NULL: in place. Pointers need
  *              their elements' alignment only. Empty gradients may have null pointers.
- *   max_norm   >= 0; infinity: nothing is scaled (in place: only the norm is computed)
+ *   max_norm   >= 0; infinity: nothing is scaled, whatever the norm (in place: only the norm is computed; else copied)
  *   norm       device fp32 [1], written (0 for an empty list)
  *   workspace  nvfp4_grad_clip_workspace_bytes(count) bytes, 16-byte aligned
  * Results must not share memory with each other or with another gradient (the same tensor twice, for

@@ -220,11 +220,11 @@ DEVI void scale_chunk(const void* p, void* out, int64_t i0, int64_t i1, float f)
   if (tail + threadIdx.x < i1) scale_single<TYPE>(p, out, tail + threadIdx.x, f);
 }
 
-// The chunks of the list times min(1, max_norm / (norm + 1e-6)), the last ones first.
+// The chunks of the list times min(1, max_norm / (norm + 1e-6)), 1 without a limit, the last ones first.
 template <int N>
 DEVI void list_scale(const ClipTable<N>& t, float norm, int first, int step) {
   const float q = t.max_norm / (norm + 1e-6f);
-  const float f = q > 1.0f ? 1.0f : q;  // NaN stays
+  const float f = q > 1.0f || t.max_norm == __int_as_float(0x7F800000) ? 1.0f : q;  // NaN stays
   for (int c = t.chunks - 1 - first; c >= 0; c -= step) {
     const ClipEntry& e = t.e[clip_entry(t, c)];
     if (f == 1.0f && e.src == e.dst) continue;  // nothing changes
