@@ -11,7 +11,8 @@
 //
 // Squares: a thread adds those of a chunk (up to 64) in fp32 and joins chunks in fp64. Where that fp32 sum is
 // infinite (|g| > 2^63) or so small that squares fell below fp32's range, the thread's values are added
-// again in fp64: the norm is right for every finite input (and infinite or NaN for the others).
+// again in fp64: the norm is right for every finite input (and infinite or NaN for the others). One beyond fp32's largest number
+// is written as infinity, but the factor comes from its fp64 value.
 #include <stdint.h>
 
 #include "ffn.cuh"
@@ -173,20 +174,41 @@ __global__ void __launch_bounds__(kThreads) k_clip_norm(const __grid_constant__ 
   if (threadIdx.x == 0) t.partial[t.slot0 + blockIdx.x] = sum;
 }
 
+// The factor min(1, max_norm / (norm + 1e-6)) as first * second; first is 1 but for factors below fp32's normal numbers, where
+// it is a power of two that keeps both the second and all products whose result counts in range (a result of 2^-149 has
+// a value of at least 2^-23 with a factor below 2^-126, of 2^41 with one below 2^-190). The norm that no fp32 number holds
+// makes the fp32 quotient 0 and comes here in fp64.
+struct ClipFactor {
+  float first, second;
+};
+
+DEVI ClipFactor clip_factor(double norm64, float max_norm) {
+  if (max_norm == __int_as_float(0x7F800000)) return {1.0f, 1.0f};
+  const float q = max_norm / (static_cast<float>(norm64) + 1e-6f);
+  if (q < 0x1p-126f && norm64 <= 0x1p1000) {  // an infinite norm's factor is 0
+    const double d = max_norm / (norm64 + 1e-6);
+    const float first = d < 0x1p-190 ? 0x1p-126f : (d < 0x1p-126 ? 0x1p-64f : 1.0f);
+    return {first, static_cast<float>(d / first)};
+  }
+  return {1.0f, q > 1.0f ? 1.0f : q};  // NaN stays
+}
+
+DEVI float clip_scaled(float v, ClipFactor f) { return v * f.first * f.second; }
+
 template <int TYPE>
-DEVI uint4 scaled(uint4 v, float f) {
+DEVI uint4 scaled(uint4 v, ClipFactor f) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    w[j] = TYPE == kClipF32 ? __float_as_uint(__uint_as_float(w[j]) * f)
-                            : pack16<TYPE == kClipF16>(unpack16<TYPE == kClipF16>(w[j], 0) * f,
-                                                       unpack16<TYPE == kClipF16>(w[j], 1) * f);
+    w[j] = TYPE == kClipF32 ? __float_as_uint(clip_scaled(__uint_as_float(w[j]), f))
+                            : pack16<TYPE == kClipF16>(clip_scaled(unpack16<TYPE == kClipF16>(w[j], 0), f),
+                                                       clip_scaled(unpack16<TYPE == kClipF16>(w[j], 1), f));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int TYPE>
-DEVI void scale_single(const void* p, void* out, int64_t i, float f) {
-  const float v = clip_value(p, i, TYPE) * f;
+DEVI void scale_single(const void* p, void* out, int64_t i, ClipFactor f) {
+  const float v = clip_scaled(clip_value(p, i, TYPE), f);
   if (TYPE == kClipF32)
     static_cast<float*>(out)[i] = v;
   else
@@ -194,7 +216,7 @@ DEVI void scale_single(const void* p, void* out, int64_t i, float f) {
 }
 
 template <int TYPE>
-DEVI void scale_chunk(const void* p, void* out, int64_t i0, int64_t i1, float f) {
+DEVI void scale_chunk(const void* p, void* out, int64_t i0, int64_t i1, ClipFactor f) {
   constexpr int SIZE = TYPE == kClipF32 ? 4 : 2, PER = 16 / SIZE;
   if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15u) != 0) {
     for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) scale_single<TYPE>(p, out, i, f);
@@ -222,12 +244,11 @@ DEVI void scale_chunk(const void* p, void* out, int64_t i0, int64_t i1, float f)
 
 // The chunks of the list times min(1, max_norm / (norm + 1e-6)), 1 without a limit, the last ones first.
 template <int N>
-DEVI void list_scale(const ClipTable<N>& t, float norm, int first, int step) {
-  const float q = t.max_norm / (norm + 1e-6f);
-  const float f = q > 1.0f || t.max_norm == __int_as_float(0x7F800000) ? 1.0f : q;  // NaN stays
+DEVI void list_scale(const ClipTable<N>& t, double norm, int first, int step) {
+  const ClipFactor f = clip_factor(norm, t.max_norm);
   for (int c = t.chunks - 1 - first; c >= 0; c -= step) {
     const ClipEntry& e = t.e[clip_entry(t, c)];
-    if (f == 1.0f && e.src == e.dst) continue;  // nothing changes
+    if (f.first * f.second == 1.0f && e.src == e.dst) continue;  // nothing changes
     const int64_t i0 = static_cast<int64_t>(c - e.first) * kChunk;
     const int64_t i1 = i0 + kChunk < e.numel ? i0 + kChunk : e.numel;
     if (e.type == kClipF32)
@@ -246,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   griddep_launch_dependents();
   double sum = 0.0;
   for (int i = threadIdx.x; i < t.slots; i += kThreads) sum += t.partial[i];
-  const float norm = static_cast<float>(sqrt(block_sum(sum, sh)));
-  if (blockIdx.x == 0 && threadIdx.x == 0 && t.slot0 == 0) *t.norm = norm;
+  const double norm = sqrt(block_sum(sum, sh));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && t.slot0 == 0) *t.norm = static_cast<float>(norm);
   if (t.scale) list_scale(t, norm, blockIdx.x, gridDim.x);
 }
 
@@ -264,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) k_clip_cluster(const __grid_constant
   double total = 0.0;
 #pragma unroll
   for (int r = 0; r < kClipCluster; ++r) total += ld_shared_cluster_f64(mapa_shared(smem_u32(&mine), r));
-  const float norm = static_cast<float>(sqrt(total));
-  if (rank == 0 && threadIdx.x == 0) *t.norm = norm;
+  const double norm = sqrt(total);
+  if (rank == 0 && threadIdx.x == 0) *t.norm = static_cast<float>(norm);
   if (t.scale) list_scale(t, norm, rank, kClipCluster);
   cluster_sync();  // no CTA leaves while another may still read its sum
 }
