@@ -1,13 +1,15 @@
-"""Clipping at its edges: no limit, and norms beyond fp32."""
+"""Clipping at its edges: no limit, norms beyond fp32, and the same values at other addresses."""
 import math
 
 import pytest
 import torch
 
 import moe_nvfp4_gemm_gb300 as m
-from tests.test_gpu_grad_clip import TYPES, norm64, tensors
+from tests.test_gpu_grad_clip import TYPES, check, norm64, tensors
 
 pytestmark = pytest.mark.gpu
+
+IDS = ["bf16", "fp16", "fp32"]
 
 
 # one launch, and two
@@ -52,3 +54,40 @@ def test_norm_beyond_fp32(n, dtype, limit, largest):
     tol += 1.01 * (2.0 ** -134 if dtype == torch.bfloat16 else 2.0 ** -150) + 2.0 ** -148
     for r in (t, out):
         assert ((r.double() - value).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("sizes", [[20011], [1], [7], [8], [9], [15, 17, 16384, 16385, 16391], [3, 33001, 300007, 5]],
+                         ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("scale", [1e-2, 1e-30])
+def test_addresses_change_no_bit(dtype, sizes, scale):
+    """The same gradients at every offset from a 16-byte boundary: the same norm and the same results, bit for bit. (At
+    1e-30 the squares leave fp32's range and are added again in fp64.)"""
+    if dtype == torch.float16:
+        scale = max(scale, 1e-4)
+    grads = tensors(len(sizes), sizes, [dtype] * len(sizes), scale)
+    limit = 0.3 * norm64(grads)
+    first = None
+    for off in range(16 // grads[0].element_size()):
+        views = []
+        for i, t in enumerate(grads):  # each gradient at another offset, NaN around it
+            flat = torch.full((t.numel() + 32,), float("nan"), dtype=dtype, device="cuda")
+            at = (off * (2 * i + 1)) % 8
+            flat[at:at + t.numel()] = t
+            views.append(flat[at:at + t.numel()])
+        out = [torch.empty_like(t) for t in grads]
+        norm = m.nvfp4_grad_clip(views, limit, out=out)
+        alone = m.nvfp4_grad_clip(views)
+        assert torch.equal(norm, alone)
+        first = first or (norm, out)
+        assert torch.equal(norm, first[0]) and all(torch.equal(a, b) for a, b in zip(out, first[1])), off
+    check(m, grads, limit)
+
+
+def test_short_gradients_at_every_offset():
+    flat = tensors(5, [4096], [torch.bfloat16], 1.0)[0]
+    for n in range(1, 41):
+        for at in range(8):
+            g = flat[at:at + n]
+            want = norm64([g])
+            assert abs(float(m.nvfp4_grad_clip([g])) - want) <= 33 * 2.0 ** -24 * want, (n, at)
