@@ -1,7 +1,8 @@
 // Product of 8-bit integers with a scale for each token and each channel:
 //   y[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k],  the sum exact.
 //
-// sm_103a has no integer kind of tcgen05.mma, so the sums run through kind::f16: an 8-bit integer is exact in
+// sm_103a has no integer kind of tcgen05.mma, and mma.sync multiplies integers at 158 TOP/s (fp16 at 603): 16 tokens on
+// 8,192 x 8,192 would take 13.6 us, the weights' bytes 9.9. So the sums run through kind::f16: an 8-bit integer is exact in
 // fp16, a product of two in fp32, and a sum of 1,024 products, at most 1,024 * 128^2 = 2^24, too. After every
 // 1,024 of K (a chunk) the epilogue warps read the sums back, convert them and add them as 32-bit integers.
 //
@@ -12,8 +13,8 @@
 // they would fill. Tokens: up to 128 are converted by the same warps into the swizzled shared-memory tile that the
 // MMA reads; tiles of 256 come as fp16 from the workspace, converted once by k_int8_widen.
 //
-// Up to 8 tokens have a kernel without tensor cores (int8_few.cu). Few tiles: the pairs of a cluster (p.split of them) sum a tile's parts of K, exchange the integer sums through
-// distributed shared memory and store a share of the tokens each.
+// Up to 8 tokens have a kernel without tensor cores (int8_few.cu). Few tiles: the pairs of a cluster (p.split of them)
+// sum a tile's parts of K, exchange the integer sums through distributed shared memory and store a share of the tokens each.
 //
 // Bound by the tensor cores with many tokens (4,096 x 28,672 x 8,192: 0.99 ms, 1.94 PFLOP/s, the fp16 rate; under the power
 // cap 1.06), by the loop around a block with few (9 tokens, 8,192 x 8,192: 17.4 us, 3.9 TB/s of weights).
@@ -470,68 +471,69 @@ __global__ void __launch_bounds__(Int8Cfg<NT>::THREADS, 1)
               }
             }
           }
-        } else
-        for (int t = first; t < tiles && !*abort_flag; t += step) {
-          for (int kb = kb_begin; kb < kb_end;) {
-            const int in_chunk = (kb - kb_begin) % C::CHUNK;
-            // a chunk's first operand blocks are summed half by half, the one in the free slot first, so that
-            // slot 1, which may still be read, is needed 1,024 cycles later; the others both halves at once.
-            const bool apart = in_chunk == 0;
-            const int n = apart ? min(C::APART, kb_end - kb) : 1;
-            const int low = static_cast<int>(chunk & 1);  // slot of the first column
-            const uint32_t idesc = idesc_f16(256, apart ? C::HALF : NT, false);
-            bool go = true;
-            int bs = s, bx = x;
-            uint32_t bsph = ph, bxph = xph;
-            for (int pass = 0; pass < (apart ? 2 : 1) && go; ++pass) {
-              // apart: the half in slot 0 or 2, then the other in slot 1
-              const int half = apart ? (pass == 0 ? low : low ^ 1) : 0;
-              if (in_chunk == 0) {
-                const int slot = low + half;
-                const uint32_t use = slot == 1 ? chunk : chunk >> 1;  // uses of this slot before
-                go = mbar_wait_warp(&tempty[slot], (use & 1) ^ 1, abort_flag, wd);
-              }
-              bs = s, bx = x, bsph = ph, bxph = xph;
-              for (int b = 0; b < n && go; ++b) {
-                if (pass == 0) {
-                  go = mbar_wait_warp(&ofull[bs], bsph, abort_flag, wd);
-                  go = go && mbar_wait_warp(&xfull[bx], bxph, abort_flag, wd);
-                  if (!go) break;
+        } else {
+          for (int t = first; t < tiles && !*abort_flag; t += step) {
+            for (int kb = kb_begin; kb < kb_end;) {
+              const int in_chunk = (kb - kb_begin) % C::CHUNK;
+              // a chunk's first operand blocks are summed half by half, the one in the free slot first, so that
+              // slot 1, which may still be read, is needed 1,024 cycles later; the others both halves at once.
+              const bool apart = in_chunk == 0;
+              const int n = apart ? min(C::APART, kb_end - kb) : 1;
+              const int low = static_cast<int>(chunk & 1);  // slot of the first column
+              const uint32_t idesc = idesc_f16(256, apart ? C::HALF : NT, false);
+              bool go = true;
+              int bs = s, bx = x;
+              uint32_t bsph = ph, bxph = xph;
+              for (int pass = 0; pass < (apart ? 2 : 1) && go; ++pass) {
+                // apart: the half in slot 0 or 2, then the other in slot 1
+                const int half = apart ? (pass == 0 ? low : low ^ 1) : 0;
+                if (in_chunk == 0) {
+                  const int slot = low + half;
+                  const uint32_t use = slot == 1 ? chunk : chunk >> 1;  // uses of this slot before
+                  go = mbar_wait_warp(&tempty[slot], (use & 1) ^ 1, abort_flag, wd);
                 }
-                tc_fence_after();
-                const bool last = in_chunk + b == C::CHUNK - 1 || kb + b + 1 == kb_end;
-                if (elect_one()) {
-                  // rows of this half in each CTA's tile: the MMA's N is split between the CTAs
-                  const uint32_t xa = smem_u32(x_buf + bx * C::X_BYTES) + half * (C::HALF / 2) * 128;
+                bs = s, bx = x, bsph = ph, bxph = xph;
+                for (int b = 0; b < n && go; ++b) {
+                  if (pass == 0) {
+                    go = mbar_wait_warp(&ofull[bs], bsph, abort_flag, wd);
+                    go = go && mbar_wait_warp(&xfull[bx], bxph, abort_flag, wd);
+                    if (!go) break;
+                  }
+                  tc_fence_after();
+                  const bool last = in_chunk + b == C::CHUNK - 1 || kb + b + 1 == kb_end;
+                  if (elect_one()) {
+                    // rows of this half in each CTA's tile: the MMA's N is split between the CTAs
+                    const uint32_t xa = smem_u32(x_buf + bx * C::X_BYTES) + half * (C::HALF / 2) * 128;
 #pragma unroll
-                  for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_f16_pair_ts(tmem + (low + half) * C::HALF, tmem + C::A_COL + bs * 64 + kk * 8,
-                                       desc_sw128(xa + (kk >> 2) * (C::X_BYTES / 2)) + 2 * (kk & 3), idesc,
-                                       in_chunk + b != 0 || kk != 0);
-                  if (!apart || pass == 1) {
-                    tc_commit_pair(&oempty[bs], 3u << lead);
-                    tc_commit_pair(&xempty[bx], 3u << lead);
-                    if (last) {
-                      tc_commit_pair(&tfull[low], 3u << lead);
-                      tc_commit_pair(&tfull[low + 1], 3u << lead);
+                    for (int kk = 0; kk < 8; ++kk)
+                      tc_mma_f16_pair_ts(tmem + (low + half) * C::HALF, tmem + C::A_COL + bs * 64 + kk * 8,
+                                         desc_sw128(xa + (kk >> 2) * (C::X_BYTES / 2)) + 2 * (kk & 3), idesc,
+                                         in_chunk + b != 0 || kk != 0);
+                    if (!apart || pass == 1) {
+                      tc_commit_pair(&oempty[bs], 3u << lead);
+                      tc_commit_pair(&xempty[bx], 3u << lead);
+                      if (last) {
+                        tc_commit_pair(&tfull[low], 3u << lead);
+                        tc_commit_pair(&tfull[low + 1], 3u << lead);
+                      }
                     }
                   }
-                }
-                __syncwarp();
-                if (++bs == OPS) {
-                  bs = 0;
-                  bsph ^= 1;
-                }
-                if (++bx == XS) {
-                  bx = 0;
-                  bxph ^= 1;
+                  __syncwarp();
+                  if (++bs == OPS) {
+                    bs = 0;
+                    bsph ^= 1;
+                  }
+                  if (++bx == XS) {
+                    bx = 0;
+                    bxph ^= 1;
+                  }
                 }
               }
+              if (!go) break;
+              s = bs, x = bx, ph = bsph, xph = bxph;
+              kb += n;
+              if (in_chunk + n == C::CHUNK || kb == kb_end) ++chunk;
             }
-            if (!go) break;
-            s = bs, x = bx, ph = bsph, xph = bxph;
-            kb += n;
-            if (in_chunk + n == C::CHUNK || kb == kb_end) ++chunk;
           }
         }
         if (elect_one()) tc_commit_pair(drain, 1u << lead);
