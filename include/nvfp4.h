@@ -516,6 +516,9 @@ int nvfp4_encode_e4m3(const float* v, int64_t n, uint8_t* out, void* stream);
  *   NVFP4_TUNE_DENSE_RASTER    order in which the persistent large-M kernels walk the output
  *                              tiles: 0 (default) m-blocks fastest, -1 n-blocks fastest, G > 0
  *                              bands of G m-blocks (m fastest inside a band). Results unchanged.
+ *                              The gated block's, its gradients' and the int8 product's tile
+ *                              kernels choose an order by the sizes with 0; a G of at least the
+ *                              number of m-blocks is m-blocks fastest.
  *   NVFP4_TUNE_WATCHDOG_US     limit, in microseconds, after which a GEMM kernel's pipeline
  *                              wait gives up, stops the CTA's other roles, frees its tensor
  *                              memory and reports NVFP4_ERR_TIMEOUT in *dev_status (0: the
@@ -538,7 +541,8 @@ int nvfp4_encode_e4m3(const float* v, int64_t n, uint8_t* out, void* stream);
  * The FP8 GEMMs follow DENSE_GRID (their tile kernels), STREAM_MAX_M (the dense one: streaming up to
  * that many rows, at most 64, and 256 x 256 tiles above), STREAM_SPLIT (the dense one: cluster size along
  * K of the streaming kernel, or 1, 2 or 4 parts of K of the tile kernel), STREAM_L2_PREFETCH (blocks of 128 K elements),
- * WATCHDOG_US and TEST_WITHHOLD_STAGE.
+ * WATCHDOG_US and TEST_WITHHOLD_STAGE. The calls of nvfp4_ffn.h follow DENSE_RASTER, WATCHDOG_US, TEST_WITHHOLD_STAGE and,
+ * the gated block up to 128 tokens, STREAM_L2_PREFETCH (blocks of 64 K elements).
  * Returns NVFP4_OK or NVFP4_ERR_INVALID_ARG.
  */
 enum {

@@ -39,7 +39,8 @@ int nvfp4_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w_gate, int6
  * Its gradients, from the forward call's gate and up and the gradient dh of h:
  *   dg = dh u act'(g),  du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
  * dg and du are rounded to the type (the tensor cores read them), the sums are fp32, the results are
- * rounded once.
+ * rounded once. With fp16 a dg or du beyond 65,504 is infinite, and with it what it is summed into, and one below 2^-25 is
+ * zero: dh is scaled as for any fp16 backward pass.
  *   gate, up   device fp32 [M, I] contiguous;  dh [M, I], rows lddh apart
  *   dx         [M, K] contiguous, written, or NULL: not wanted (w_gate and w_up may then be NULL)
  *   dw_gate, dw_up  [I, K] contiguous, written, or NULL each (x may be NULL when both are). M == 0 writes zeros.

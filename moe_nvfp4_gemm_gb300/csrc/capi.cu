@@ -236,7 +236,9 @@ bool any_shared(const Region* written, int n, const Region* read, int m) {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxFp8Dim = int64_t(1) << 30;
 constexpr int64_t kMaxFfnWidth = int64_t(1) << 24;
-constexpr int64_t kPairs = 76;  // CTA pairs of a GB300; workspace sizes follow it
+// CTA pairs of a GB300. The dense feed-forward calls choose their parts by it and not by the device's count, because workspace
+// sizes follow the parts and are asked for without a device; results do not depend on it beyond the order of sums.
+constexpr int64_t kPairs = 76;
 constexpr int64_t kFp8MinTileRows = 32;  // smallest token tile of the grouped FP8 kernels
 
 }  // namespace

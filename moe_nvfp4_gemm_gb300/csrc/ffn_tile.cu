@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(256) k_ffn_join(const __grid_constant__ FfnTil
 // dg = dh u act'(g), du = dh act(g) for eight neighbouring values a thread, from the forward call's fp32 sums: bound by
 // its 14 bytes an element. dg and du are rounded to 16 bits, as the tensor cores read them: half a step of the type,
 // like the rounding of the results, and with it all that the gradients lose (kept as 16-bit values, g and u
-// would bring the gradients' error from 1.4 to 1.8 times that of the one rounding of a result).
+// would bring the gradients' error from 1.4 to 1.8 times that of the one rounding of a result). In fp16 one beyond 65,504
+// becomes infinite and one below 2^-25 zero, as in any fp16 backward pass; bf16 has fp32's range.
 template <bool HALF>
 __global__ void __launch_bounds__(256) k_ffn_grad(const __grid_constant__ FfnGradArgs p) {
   griddep_wait();

@@ -1,9 +1,11 @@
 // Product of 8-bit integers for a few tokens, sums in 32-bit integers on the ordinary cores:
 //   y[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k],  M <= 8.
 //
-// Bound by the weights' bytes with one or two tokens (8,192 x 8,192: one 11.0 us, 6.1 TB/s, two 11.6; in tiles of the tensor cores, which
-// convert every weight, 17.1), by the tokens' reads from L1 and the products with more (four 15.7, eight 16.5; nine, in
-// tiles, 17.4). A warp takes four channels, a lane 16 bytes of each at every 512 of K, with two such steps under
+// Bound by the weights' bytes with up to four tokens, given whole rounds of CTAs (28,672 x 8,192, 35 us of bytes: one 35.8 us, two 38.4,
+// four 39.6; 8,192 x 8,192, 9.9: one 11.0, two 11.6; in tiles of the tensor cores, which convert every weight, 17.1). With five to
+// eight the tokens' reads from L1 and the products count, two CTAs an SM (28,672 channels: 48). Three and more tokens
+// do not split K at 8,192 channels: 256 CTAs put two on 104 SMs and one on 48, and the call takes as long as two on each would
+// (four tokens 16.5 us; 9,728 channels, exactly two an SM, 17.6; 14,592, three, 21.4 of 17.6). A warp takes four channels, a lane 16 bytes of each at every 512 of K, with two such steps under
 // way (a step is asked for as soon as the one two before it is summed): 16 to 32 warps and 64 to 128 KB an SM. The
 // tokens' bytes, the same for all warps, stay in L1. Products of four bytes add to 32 bits (dp4a).
 // Few channels: `split` warps of a CTA take a channel's steps in turn and add their sums through shared memory (whole
