@@ -86,9 +86,10 @@ int nvfp4_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const flo
  * Norm over a list of gradients, and clipping to a largest norm:
  *   norm = sqrt(sum of all squares),  out_i = grads_i min(1, max_norm / (norm + 1e-6))
  * (one fp32 factor, or where it is below 2^-126 a power of two times one; a NaN or infinite norm gives the factor that this
- * formula gives; a finite norm that fp32 does not hold is written as infinity, its factor is that of the fp64 value). Squares are added in fp32
- * over at most 64 values of a thread, everything else in fp64; where such a sum leaves fp32's range its values
- * are added in fp64 again. The order of the sums depends on the sizes alone, not on addresses: results repeat bit for bit.
+ * formula gives; a finite norm that fp32 does not hold is written as infinity, its factor is that of the fp64 value).
+ * Squares are added in fp32 over at most 64 values of a thread, everything else in fp64; where such a sum leaves fp32's
+ * range its values are added in fp64 again. The order of the sums depends on the list's sizes and types alone, not on
+ * addresses: results repeat bit for bit.
  *   grads, out, numel, types  HOST arrays of `count` device pointers, element counts and types (NVFP4_BF16,
  *              NVFP4_F16, NVFP4_F32), read before the call returns. out NULL: in place. Pointers need
  *              their elements' alignment only. Empty gradients may have null pointers.
